@@ -307,6 +307,89 @@ tq_status tq_decode_attention_asym(const tq_attn_desc* desc, const tq_codec* vc,
                                    const uint16_t* v_tail, const int32_t* tail_lens, void* out,
                                    void* workspace, size_t workspace_bytes, tq_stream_t stream);
 
+/* Decode attention of a batch whose sequences share a prefix (a system prompt, a document):
+ * each query attends the prefix's tokens and then its own sequence's tokens in one softmax,
+ *   out = Σ_t p_t v̂_t,  p = softmax over prefix_len + seq_lens[b] estimator scores ([QJL] §五,
+ *   §六),
+ * with the prefix's codes read once for all sequences: the queries of up to 128 (sequence,
+ * head) rows of a KV head are multiplied with a tile of it at a time on the tensor cores.
+ *   prefix_k, prefix_v : caches with batch = 1 and prefix_capacity slots (flat or paged; they may
+ *              be pages of the same pool as k and v), coded by kc and vc.
+ *   prefix_len : device int32[1], tokens of the prefix (0 is allowed); prefix_max_len bounds it
+ *              (≤ prefix_capacity) and sizes the grid.  A longer length is clamped and flagged.
+ *   k, v, seq_lens : each sequence's own tokens, behind the prefix; desc->max_seq_len bounds
+ *              seq_lens (longer ones are clamped and flagged).  A sequence with no token at all
+ *              gives a zero row.
+ *   kc, vc   : key codecs of 2 to 5 bits, value codecs of 1 to 4; created on the current device.
+ *   desc->out_dtype is F16 or BF16: the products run on fp16 operands (F32 returns
+ *   TQ_ERR_UNSUPPORTED).  Value vectors with norms below 2^-60 count as zero vectors.
+ *   workspace: ≥ tq_prefix_workspace_bytes(desc, prefix_max_len) bytes, 256-byte aligned, no
+ *              initialisation needed; calls that share it must be serialised on one stream.
+ *   Other arguments as tq_decode_attention. */
+size_t tq_prefix_workspace_bytes(const tq_attn_desc* desc, int32_t prefix_max_len);
+tq_status tq_prefix_attention(const tq_attn_desc* desc, const tq_codec* kc, const tq_codec* vc,
+                              const void* q, tq_prod_cache prefix_k, tq_mse_cache prefix_v,
+                              int32_t prefix_capacity, int32_t prefix_max_len,
+                              const int32_t* prefix_len, tq_prod_cache k, tq_mse_cache v,
+                              const int32_t* seq_lens, void* out, void* workspace,
+                              size_t workspace_bytes, tq_stream_t stream);
+
+/* ------------------------------------------------------------------ block-sparse attention */
+
+/* A long cache can be read in part: the keys of every block of TQ_BLOCK_TOKENS tokens have
+ * bounds (their smallest and largest value in each of the 128 channels), an upper bound of a
+ * query's product with any key of a block follows from them, and the query attends the blocks
+ * whose bounds are largest.  Bounds are kept beside the cache in the same layout, with blocks in
+ * place of slots. */
+#define TQ_BLOCK_TOKENS 64
+
+typedef struct {
+  uint16_t* bounds;        /* device, bf16 [batch][heads][capacity/64][2][128]: lower, upper */
+  const tq_pages* pages;   /* as in tq_prod_cache; the pool has num_pages
+                            * pages of page_tokens/64 blocks for each head */
+} tq_block_cache;
+
+/* Folds keys into the bounds of their blocks, as they are written to the cache: arguments as
+ * tq_quantize_prod (the same call for a prefill, a chunk or a decode step's tokens).  A token in
+ * the first slot of a block begins its bounds anew; other tokens widen what is there, so a
+ * block's bounds are those of the tokens written since its first slot.  Keys that bf16 does not
+ * hold are rounded outward (the bounds stay bounds); NaN values are left out.  Blocks without a
+ * token of the call are left as they are.  x needs the alignment of its type only. */
+tq_status tq_block_bounds(const void* x, tq_dtype x_dtype, int32_t batch, int32_t heads,
+                          int32_t tokens, int64_t stride_b, int64_t stride_h, int64_t stride_t,
+                          const int32_t* pos, const int32_t* count, tq_block_cache blocks,
+                          int32_t capacity, tq_stream_t stream);
+
+/* Selects the blocks that each (sequence, KV head) attends.  The score of a block is the largest,
+ * over the query heads g of the KV head's group, of Σ_j max(q_gj·lo_j, q_gj·hi_j); the last
+ * block's bounds may cover only its first tokens.  Of the n = ⌈seq_lens[b]/64⌉ blocks of a
+ * sequence all are kept if n ≤ max_blocks; else the first first_blocks, the last last_blocks and,
+ * of those between, the ones with the largest scores, equal scores by the lower number.  The
+ * scores are compared as in 64 bits: the result does not depend on any order of summation.  A
+ * query head whose sum is NaN is left out; a block left with none scores −∞.
+ *   list     : device int32 [batch][kv_heads][max_blocks], the kept blocks ascending, then −1.
+ *   first_blocks + last_blocks ≤ max_blocks.
+ *   desc     : batch, q_heads, kv_heads, capacity, max_seq_len (bounds seq_lens) and q_dtype.
+ *   workspace: ≥ tq_block_select_workspace_bytes(desc) bytes, 256-byte aligned, no
+ *              initialisation needed; calls that share it must be serialised on one stream. */
+size_t tq_block_select_workspace_bytes(const tq_attn_desc* desc);
+tq_status tq_block_select(const tq_attn_desc* desc, const void* q, tq_block_cache blocks,
+                          const int32_t* seq_lens, int32_t first_blocks, int32_t last_blocks,
+                          int32_t max_blocks, int32_t* list, void* workspace,
+                          size_t workspace_bytes, tq_stream_t stream);
+
+/* Decode attention over the listed blocks only: query head h of sequence b attends the tokens
+ * t < seq_lens[b] of the blocks list[b][h / G][0 .. max_blocks), in any order.  Entries outside
+ * the sequence's blocks (−1 among them) are passed over; a block that is listed twice counts
+ * twice.  No block at all gives a zero row.  Arguments, types and limits as
+ * tq_prefix_attention; workspace ≥ tq_sparse_workspace_bytes(desc, max_blocks) bytes. */
+size_t tq_sparse_workspace_bytes(const tq_attn_desc* desc, int32_t max_blocks);
+tq_status tq_sparse_attention(const tq_attn_desc* desc, const tq_codec* kc, const tq_codec* vc,
+                              const void* q, tq_prod_cache k, tq_mse_cache v,
+                              const int32_t* seq_lens, const int32_t* list, int32_t max_blocks,
+                              void* out, void* workspace, size_t workspace_bytes,
+                              tq_stream_t stream);
+
 /* ------------------------------------------------------------------ store with an FP16 tail */
 
 /* Bytes of workspace tq_store_append needs for `batch` sequences (0 if batch ≤ 0). */

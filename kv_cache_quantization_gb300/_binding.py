@@ -19,6 +19,7 @@ TQ_PROD, TQ_MSE = 0, 1
 TQ_HEAD_DIM = 128
 TQ_MAX_GROUP = 8
 TQ_CAPACITY_ALIGN = 64
+TQ_BLOCK_TOKENS = 64
 TQ_FLAG_POS_OVERFLOW, TQ_FLAG_LEN_OVERFLOW, TQ_FLAG_TIMEOUT, TQ_FLAG_PAGE = 1, 2, 4, 8
 
 _vp = ctypes.c_void_p
@@ -38,6 +39,10 @@ class tq_prod_cache(ctypes.Structure):
 
 class tq_mse_cache(ctypes.Structure):
     _fields_ = [("idx", _vp), ("xnorm", _vp), ("pages", ctypes.POINTER(tq_pages))]
+
+
+class tq_block_cache(ctypes.Structure):
+    _fields_ = [("bounds", _vp), ("pages", ctypes.POINTER(tq_pages))]
 
 
 class tq_attn_desc(ctypes.Structure):
@@ -88,6 +93,20 @@ SIGNATURES = {
                                             _vp, _vp]),
     "tq_store_append": (ctypes.c_int, [_vp, _i32, _i32, _vp, _vp, ctypes.c_int, _vp, tq_mse_cache,
                                        _i32, _vp, _vp, _i32, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "tq_prefix_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(tq_attn_desc), _i32]),
+    "tq_prefix_attention": (ctypes.c_int, [ctypes.POINTER(tq_attn_desc), _vp, _vp, _vp,
+                                           tq_prod_cache, tq_mse_cache, _i32, _i32, _vp,
+                                           tq_prod_cache, tq_mse_cache, _vp, _vp, _vp,
+                                           ctypes.c_size_t, _vp]),
+    "tq_block_bounds": (ctypes.c_int, [_vp, ctypes.c_int, _i32, _i32, _i32, _i64, _i64, _i64, _vp,
+                                       _vp, tq_block_cache, _i32, _vp]),
+    "tq_block_select_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(tq_attn_desc)]),
+    "tq_block_select": (ctypes.c_int, [ctypes.POINTER(tq_attn_desc), _vp, tq_block_cache, _vp,
+                                       _i32, _i32, _i32, _vp, _vp, ctypes.c_size_t, _vp]),
+    "tq_sparse_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(tq_attn_desc), _i32]),
+    "tq_sparse_attention": (ctypes.c_int, [ctypes.POINTER(tq_attn_desc), _vp, _vp, _vp,
+                                           tq_prod_cache, tq_mse_cache, _vp, _vp, _i32, _vp, _vp,
+                                           ctypes.c_size_t, _vp]),
     "tq_check_bounded_wait": (ctypes.c_int, [ctypes.c_uint32, _vp]),
 }
 
@@ -229,6 +248,49 @@ def tq_decode_attention_noalloc(desc: tq_attn_desc, kc, vc, q, k: tq_prod_cache,
 
 def tq_decode_noalloc_scratch_bytes() -> int:
     return load().tq_decode_noalloc_scratch_bytes()
+
+
+def tq_prefix_workspace_bytes(desc: tq_attn_desc, prefix_max_len: int) -> int:
+    return load().tq_prefix_workspace_bytes(ctypes.byref(desc), prefix_max_len)
+
+
+def tq_prefix_attention(desc: tq_attn_desc, kc, vc, q, prefix_k: tq_prod_cache,
+                        prefix_v: tq_mse_cache, prefix_capacity, prefix_max_len, prefix_len,
+                        k: tq_prod_cache, v: tq_mse_cache, seq_lens, out, workspace,
+                        workspace_bytes, stream) -> int:
+    return load().tq_prefix_attention(ctypes.byref(desc), kc, vc, ptr(q), prefix_k, prefix_v,
+                                      prefix_capacity, prefix_max_len, ptr(prefix_len), k, v,
+                                      ptr(seq_lens), ptr(out), ptr(workspace), workspace_bytes,
+                                      ptr(stream))
+
+
+def tq_block_bounds(x, x_dtype, batch, heads, tokens, stride_b, stride_h, stride_t, pos, count,
+                    blocks: tq_block_cache, capacity, stream) -> int:
+    return load().tq_block_bounds(ptr(x), x_dtype, batch, heads, tokens, stride_b, stride_h,
+                                  stride_t, ptr(pos), ptr(count), blocks, capacity, ptr(stream))
+
+
+def tq_block_select_workspace_bytes(desc: tq_attn_desc) -> int:
+    return load().tq_block_select_workspace_bytes(ctypes.byref(desc))
+
+
+def tq_block_select(desc: tq_attn_desc, q, blocks: tq_block_cache, seq_lens, first_blocks,
+                    last_blocks, max_blocks, out_list, workspace, workspace_bytes, stream) -> int:
+    return load().tq_block_select(ctypes.byref(desc), ptr(q), blocks, ptr(seq_lens), first_blocks,
+                                  last_blocks, max_blocks, ptr(out_list), ptr(workspace),
+                                  workspace_bytes, ptr(stream))
+
+
+def tq_sparse_workspace_bytes(desc: tq_attn_desc, max_blocks: int) -> int:
+    return load().tq_sparse_workspace_bytes(ctypes.byref(desc), max_blocks)
+
+
+def tq_sparse_attention(desc: tq_attn_desc, kc, vc, q, k: tq_prod_cache, v: tq_mse_cache,
+                        seq_lens, block_list, max_blocks, out, workspace, workspace_bytes,
+                        stream) -> int:
+    return load().tq_sparse_attention(ctypes.byref(desc), kc, vc, ptr(q), k, v, ptr(seq_lens),
+                                      ptr(block_list), max_blocks, ptr(out), ptr(workspace),
+                                      workspace_bytes, ptr(stream))
 
 
 def tq_check_bounded_wait(limit_us: int, stream) -> int:

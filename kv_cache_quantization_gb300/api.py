@@ -348,6 +348,201 @@ class PrefillPlan:
         return out
 
 
+# ------------------------------------------------------------------ long contexts
+
+def _on_device(*tensors):
+    """The library works on the current device: tensors of another one are refused."""
+    d = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != d:
+            raise ValueError(f"expected tensors on the current device cuda:{d}, got one on {t.device}")
+
+
+def _expect(t: torch.Tensor, shape, dtype, name):
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}, "
+                         f"got {t.dtype} {list(t.shape)}")
+
+
+def _expect_caches(k: "ProdCache", v: "MSECache", rows, heads, capacity, kc, vc, name):
+    """Shapes of a pair of caches (or pools) for `rows` sequences of `capacity` slots."""
+    for c, what in ((k, "key"), (v, "value")):
+        norms = c.xnorm
+        if c.capacity != capacity or norms.shape[1] != heads:
+            raise ValueError(f"{name}: {what} cache of {norms.shape[1]} heads and {c.capacity} slots, "
+                             f"expected {heads} and {capacity}")
+        if c.pages is None and norms.shape[0] < rows or \
+                c.pages is not None and (c.pages.block_table.shape[0] < rows or
+                                         norms.shape[0] < c.pages.num_pages):
+            raise ValueError(f"{name}: {what} cache has too few sequences or pages")
+    if k.idx.shape[2] != kc.index_bits or v.bits != vc.bits:
+        raise ValueError(f"{name}: the caches hold codes of other widths than the codecs'")
+
+
+@dataclasses.dataclass
+class BlockBounds:
+    """Per-block bounds of a cache's keys (include/tq.h, tq_block_cache): lower and upper bounds
+    of the 128 channels over each block of 64 tokens; with `pages` a pool as for ProdCache."""
+    bounds: torch.Tensor   # bfloat16 [B, H, cap / 64, 2, 128]
+    pages: Optional[Pages] = None
+
+    @classmethod
+    def empty(cls, batch, heads, capacity, device="cuda"):
+        return cls(torch.zeros(batch, heads, _cap(capacity) // B.TQ_BLOCK_TOKENS, 2, HEAD_DIM,
+                               dtype=torch.bfloat16, device=device))
+
+    @classmethod
+    def empty_paged(cls, pages: Pages, heads, device="cuda"):
+        if pages.page_tokens % B.TQ_CAPACITY_ALIGN:
+            raise ValueError("page_tokens must be a multiple of TQ_CAPACITY_ALIGN")
+        b = cls.empty(pages.num_pages, heads, pages.page_tokens, device)
+        b.pages = pages
+        return b
+
+    @property
+    def capacity(self):
+        return self.pages.capacity if self.pages is not None \
+            else self.bounds.shape[2] * B.TQ_BLOCK_TOKENS
+
+    def c(self):
+        return B.tq_block_cache(self.bounds.data_ptr(), _pages_ptr(self.pages))
+
+    def expect(self, rows, heads):
+        s = self.bounds.shape
+        blocks = self.bounds.shape[2] if self.pages is None \
+            else self.pages.page_tokens // B.TQ_BLOCK_TOKENS
+        _expect(self.bounds, (s[0], heads, blocks, 2, HEAD_DIM), torch.bfloat16, "bounds")
+        if s[0] < (rows if self.pages is None else self.pages.num_pages) or \
+                self.pages is not None and self.pages.block_table.shape[0] < rows:
+            raise ValueError("bounds have too few sequences or pages")
+
+
+def block_bounds(x: torch.Tensor, blocks: BlockBounds, pos=None, count=None, stream=None):
+    """Folds keys x [batch, heads, tokens, 128] into their blocks' bounds, at the cache positions
+    pos[b].. (0) and count[b] tokens each (all): the arguments of quantize_prod."""
+    bsz, h, t, sb, sh, st = _x_args(x)
+    _on_device(x, blocks.bounds, pos, count)
+    blocks.expect(bsz, h)
+    for n, v in (("pos", pos), ("count", count)):
+        if v is not None:
+            _expect(v, (bsz,), torch.int32, n)
+    B.check(B.tq_block_bounds(x, tq_dtype(x.dtype), bsz, h, t, sb, sh, st, pos, count, blocks.c(),
+                              blocks.capacity, _stream(stream)), "tq_block_bounds")
+
+
+class SparsePlan:
+    """Block-sparse decode attention: which blocks a query attends (tq_block_select) and attention
+    over them (tq_sparse_attention), with the workspace of both (allocated once, reused; calls of
+    a plan are to be serialised on one stream).  Of each sequence at most max_blocks blocks of 64
+    tokens are attended, the first first_blocks and the last last_blocks always."""
+
+    def __init__(self, batch, q_heads, kv_heads, capacity, max_seq_len, max_blocks,
+                 first_blocks=1, last_blocks=2, q_dtype=torch.bfloat16, out_dtype=torch.bfloat16,
+                 softmax_scale=None, device="cuda"):
+        self.desc = B.tq_attn_desc(batch, q_heads, kv_heads, HEAD_DIM, _cap(capacity),
+                                   max_seq_len, 0, softmax_scale if softmax_scale else 0.0,
+                                   tq_dtype(q_dtype), tq_dtype(out_dtype))
+        sizes = (B.tq_block_select_workspace_bytes(self.desc),
+                 B.tq_sparse_workspace_bytes(self.desc, max_blocks))
+        if 0 in sizes or first_blocks < 0 or last_blocks < 0 or \
+                first_blocks + last_blocks > max_blocks:
+            raise ValueError("invalid sparse-attention configuration")
+        self.workspace = torch.empty(max(sizes), dtype=torch.uint8, device=device)
+        self.max_blocks, self.first_blocks, self.last_blocks = max_blocks, first_blocks, last_blocks
+        self.batch, self.kv_heads, self.capacity = batch, kv_heads, _cap(capacity)
+        self.q_dtype, self.out_dtype = q_dtype, out_dtype
+        self.shape = (batch, q_heads, HEAD_DIM)
+
+    def new_out(self, device="cuda"):
+        return torch.empty(self.shape, dtype=self.out_dtype, device=device)
+
+    def new_list(self, device="cuda"):
+        return torch.empty(self.batch, self.kv_heads, self.max_blocks, dtype=torch.int32,
+                           device=device)
+
+    def select(self, q, blocks: BlockBounds, seq_lens, out, stream=None):
+        """The blocks of each (sequence, KV head) that q [batch, q_heads, 128] attends, ascending,
+        −1 behind them, into out [batch, kv_heads, max_blocks] int32."""
+        _on_device(q, blocks.bounds, seq_lens, out, self.workspace)
+        _expect(q, self.shape, self.q_dtype, "q")
+        _expect(seq_lens, (self.batch,), torch.int32, "seq_lens")
+        _expect(out, (self.batch, self.kv_heads, self.max_blocks), torch.int32, "out")
+        blocks.expect(self.batch, self.kv_heads)
+        if blocks.capacity != self.capacity:
+            raise ValueError(f"bounds of {blocks.capacity} slots, expected {self.capacity}")
+        B.check(B.tq_block_select(self.desc, q, blocks.c(), seq_lens, self.first_blocks,
+                                  self.last_blocks, self.max_blocks, out, self.workspace,
+                                  self.workspace.numel(), _stream(stream)), "tq_block_select")
+        return out
+
+    def run(self, kc: Codec, vc: Codec, q, k: ProdCache, v: MSECache, seq_lens, block_list, out,
+            stream=None):
+        """Attention of q over the listed blocks of the cache, into out [batch, q_heads, 128]."""
+        _on_device(q, k.idx, v.idx, seq_lens, block_list, out, self.workspace)
+        _expect(q, self.shape, self.q_dtype, "q")
+        _expect(seq_lens, (self.batch,), torch.int32, "seq_lens")
+        _expect(block_list, (self.batch, self.kv_heads, self.max_blocks), torch.int32, "block_list")
+        _expect(out, self.shape, self.out_dtype, "out")
+        _expect_caches(k, v, self.batch, self.kv_heads, self.capacity, kc, vc, "cache")
+        B.check(B.tq_sparse_attention(self.desc, kc.handle, vc.handle, q, k.c(), v.c(), seq_lens,
+                                      block_list, self.max_blocks, out, self.workspace,
+                                      self.workspace.numel(), _stream(stream)),
+                "tq_sparse_attention")
+        return out
+
+    def step(self, kc: Codec, vc: Codec, q, k_new, v_new, k: ProdCache, v: MSECache,
+             blocks: BlockBounds, pos, seq_lens, block_list, out, stream=None):
+        """One decode step: appends k_new, v_new [batch, kv_heads, 128] at pos[b] (codes and
+        bounds), selects blocks and attends them.  seq_lens holds pos + 1."""
+        quantize_prod(kc, k_new.unsqueeze(2), k, pos=pos, stream=stream)
+        quantize_mse(vc, v_new.unsqueeze(2), v, pos=pos, stream=stream)
+        block_bounds(k_new.unsqueeze(2), blocks, pos=pos, stream=stream)
+        self.select(q, blocks, seq_lens, block_list, stream=stream)
+        return self.run(kc, vc, q, k, v, seq_lens, block_list, out, stream=stream)
+
+
+class PrefixPlan:
+    """Decode attention of a batch whose sequences share a prefix (tq_prefix_attention), with its
+    workspace (allocated once, reused; calls of a plan are to be serialised on one stream)."""
+
+    def __init__(self, batch, q_heads, kv_heads, capacity, max_seq_len, prefix_capacity,
+                 prefix_max_len, q_dtype=torch.bfloat16, out_dtype=torch.bfloat16,
+                 softmax_scale=None, device="cuda"):
+        self.desc = B.tq_attn_desc(batch, q_heads, kv_heads, HEAD_DIM, _cap(capacity),
+                                   max_seq_len, 0, softmax_scale if softmax_scale else 0.0,
+                                   tq_dtype(q_dtype), tq_dtype(out_dtype))
+        nbytes = B.tq_prefix_workspace_bytes(self.desc, prefix_max_len)
+        if nbytes == 0 or prefix_max_len > _cap(prefix_capacity):
+            raise ValueError("invalid prefix-attention configuration")
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.batch, self.kv_heads, self.capacity = batch, kv_heads, _cap(capacity)
+        self.prefix_capacity, self.prefix_max_len = _cap(prefix_capacity), prefix_max_len
+        self.q_dtype, self.out_dtype = q_dtype, out_dtype
+        self.shape = (batch, q_heads, HEAD_DIM)
+
+    def new_out(self, device="cuda"):
+        return torch.empty(self.shape, dtype=self.out_dtype, device=device)
+
+    def run(self, kc: Codec, vc: Codec, q, prefix_k: ProdCache, prefix_v: MSECache, prefix_len,
+            k: ProdCache, v: MSECache, seq_lens, out, stream=None):
+        """Attention of q [batch, q_heads, 128] over the prefix's prefix_len (int32 [1]) tokens and
+        each sequence's own seq_lens[b] tokens."""
+        _on_device(q, prefix_k.idx, prefix_v.idx, prefix_len, k.idx, v.idx, seq_lens, out,
+                   self.workspace)
+        _expect(q, self.shape, self.q_dtype, "q")
+        _expect(prefix_len, (1,), torch.int32, "prefix_len")
+        _expect(seq_lens, (self.batch,), torch.int32, "seq_lens")
+        _expect(out, self.shape, self.out_dtype, "out")
+        _expect_caches(prefix_k, prefix_v, 1, self.kv_heads, self.prefix_capacity, kc, vc, "prefix")
+        _expect_caches(k, v, self.batch, self.kv_heads, self.capacity, kc, vc, "cache")
+        B.check(B.tq_prefix_attention(self.desc, kc.handle, vc.handle, q, prefix_k.c(),
+                                      prefix_v.c(), self.prefix_capacity, self.prefix_max_len,
+                                      prefix_len, k.c(), v.c(), seq_lens, out, self.workspace,
+                                      self.workspace.numel(), _stream(stream)),
+                "tq_prefix_attention")
+        return out
+
+
 class TailStore:
     """A cache in the asymmetric layout: a compressed part (FP16 keys, MSE-coded values) and an
     FP16 tail of the most recent tokens that compacts into the compressed part when it fills

@@ -1,0 +1,588 @@
+// Which parts of a long cache a decode query should read: bounds of the keys of each 64-token
+// block, kept beside the cache as the keys are written (tq_block_bounds), and the selection of
+// blocks by an upper bound of the query's products with their keys (tq_block_select).
+//
+// Mathematics.  With lo_j ≤ k_j ≤ hi_j for every key k of a block,
+//   ⟨q, k⟩ = Σ_j q_j k_j ≤ Σ_j max(q_j lo_j, q_j hi_j) = ⟨min(q, 0), lo⟩ + ⟨max(q, 0), hi⟩,
+// one product of length 256 with the block's bounds.  The bounds are bf16, rounded outward, so
+// the inequality survives the rounding; minima and maxima do not depend on an order.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "tq_internal.h"
+
+TQ_DEFINE_FLAGS(tq_take_flags_blocks)
+
+namespace {
+
+constexpr int kBlock = TQ_BLOCK_TOKENS;
+constexpr int kRow = 2 * TQ_D;          // bf16 values per block: 128 lower, 128 upper bounds
+
+// ---------------------------------------------------------------- bounds
+struct BoundsArgs {
+  const void* x;
+  int batch, heads, tokens;
+  long long sb, sh, st;
+  const int* pos;
+  const int* count;
+  __nv_bfloat16* bounds;
+  tq_rowmap map;
+  int capacity;
+  int nt;                  // blocks that a chunk of `tokens` tokens can touch
+  long long units;         // batch · heads · nt
+};
+
+// bf16 bits of the nearest number not above (up = false) or not below (up = true) x
+__device__ __forceinline__ uint32_t outward(float x, bool up) {
+  const uint32_t u = __float_as_uint(x);
+  const bool away = (u & 0xffffu) && (up ? !(u >> 31) : (u >> 31));
+  return (u + (away ? 0x10000u : 0u)) >> 16;
+}
+
+// Lane's view of the rows of one block: 16 bytes of a row per load (8 values of 16 bits and two
+// rows a warp, or 4 values of 32 bits and one row).
+template <typename T>
+struct Rows {
+  static constexpr int kPer = 16 / sizeof(T);        // values per lane
+  static constexpr int kLanes = TQ_D / kPer;         // lanes per row
+  static constexpr int kStep = 32 / kLanes;          // rows per load
+};
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// One warp per (sequence, head, block): it reads the chunk's rows that fall in the block, 16
+// loads of 512 bytes in flight, and owns the block's bounds, so there is nothing atomic.
+// Bound by reading the keys.  kVec: rows are 16-byte aligned.
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(256) block_bounds_kernel(const BoundsArgs a) {
+  using R = Rows<T>;
+  const long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (unit >= a.units) return;
+  const int i = (int)(unit % a.nt);
+  const int h = (int)(unit / a.nt % a.heads), b = (int)(unit / a.nt / a.heads);
+  const long long pos = a.pos ? a.pos[b] : 0;
+  long long n = a.count ? min(max(a.count[b], 0), a.tokens) : a.tokens;
+  if (n > 0 && (pos < 0 || pos + n > a.capacity)) {
+    if (i == 0 && h == 0 && lane == 0) atomicOr(&g_tq_flags, TQ_FLAG_POS_OVERFLOW);
+    if (pos < 0) return;
+    n = min(n, (long long)a.capacity - pos);
+  }
+  const long long blk = pos / kBlock + i;
+  const long long first = max(blk * kBlock - pos, 0LL);               // the chunk's tokens in
+  const long long last = min((blk + 1) * kBlock - pos, n);            // this block
+  if (first >= last) return;
+  long long row;
+  int slot;
+  if (!tq_map_slot(a.map, a.heads, b, h, (int)(blk * kBlock), row, slot)) {
+    if (lane == 0) atomicOr(&g_tq_flags, TQ_FLAG_PAGE);
+    return;
+  }
+  const T* x = static_cast<const T*>(a.x) + b * a.sb + h * a.sh + (lane % R::kLanes) * R::kPer;
+  float lo[R::kPer], hi[R::kPer];
+#pragma unroll
+  for (int j = 0; j < R::kPer; ++j) {
+    lo[j] = INFINITY;
+    hi[j] = -INFINITY;
+  }
+  constexpr int kFlight = 16;
+  for (long long t0 = first; t0 < last; t0 += kFlight * R::kStep) {
+    alignas(16) T v[kFlight][R::kPer];
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      // rows past the end repeat the last one
+      const long long t = min(t0 + k * R::kStep + lane / R::kLanes, last - 1);
+      if (kVec) {
+        *reinterpret_cast<uint4*>(v[k]) = __ldg(reinterpret_cast<const uint4*>(x + t * a.st));
+      } else {
+#pragma unroll
+        for (int j = 0; j < R::kPer; ++j) v[k][j] = x[t * a.st + j];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k)
+#pragma unroll
+      for (int j = 0; j < R::kPer; ++j) {
+        const float f = to_float(v[k][j]);
+        lo[j] = fminf(lo[j], f);
+        hi[j] = fmaxf(hi[j], f);
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < R::kPer; ++j)
+#pragma unroll
+    for (int o = R::kLanes; o < 32; o *= 2) {
+      lo[j] = fminf(lo[j], __shfl_xor_sync(0xffffffffu, lo[j], o));
+      hi[j] = fmaxf(hi[j], __shfl_xor_sync(0xffffffffu, hi[j], o));
+    }
+  const int slots = tq_row_slots(a.map, a.capacity);
+  uint16_t* dst = reinterpret_cast<uint16_t*>(a.bounds) +
+                  (row * (slots / kBlock) + slot / kBlock) * kRow + (lane % R::kLanes) * R::kPer;
+  // a block that this chunk does not begin goes on: fold its bounds in
+  const bool goes_on = blk * kBlock < pos;
+  if (lane < R::kLanes) {
+#pragma unroll
+    for (int j = 0; j < R::kPer; j += 2) {
+      uint32_t l[2], u[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[e] = outward(lo[j + e], false);
+        u[e] = outward(hi[j + e], true);
+        if (goes_on) {
+          l[e] = __float_as_uint(fminf(__uint_as_float(l[e] << 16),
+                                       __uint_as_float((uint32_t)dst[j + e] << 16))) >> 16;
+          u[e] = __float_as_uint(fmaxf(__uint_as_float(u[e] << 16),
+                                       __uint_as_float((uint32_t)dst[TQ_D + j + e] << 16))) >> 16;
+        }
+      }
+      *reinterpret_cast<uint32_t*>(dst + j) = l[0] | l[1] << 16;
+      *reinterpret_cast<uint32_t*>(dst + TQ_D + j) = u[0] | u[1] << 16;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- selection
+struct SelectArgs {
+  const void* q;
+  int q_dtype;
+  const __nv_bfloat16* bounds;
+  tq_rowmap map;
+  int capacity, max_len;
+  const int* seq_lens;
+  int Hkv, G;
+  int nb;                 // blocks of max_len tokens (row stride of the workspace arrays)
+  int chunks;             // CTAs per row of the scoring kernel
+  int first, last, keep;
+  float* score;           // [B·Hkv][nb]
+  float* err;             // [B·Hkv][chunks] bounds of Σ|terms| of a chunk's blocks
+  unsigned long long* exact;   // [B·Hkv][nb] ordered 64-bit scores of the blocks in doubt
+  int* doubt;             // [B·Hkv][nb] their numbers
+  int* list;              // [B·Hkv][keep]
+};
+
+constexpr int kPerCta = 64;      // blocks per CTA of the scoring kernel
+
+__device__ __forceinline__ float load_elem(const void* base, int dtype, long long i) {
+  if (dtype == TQ_F32) return static_cast<const float*>(base)[i];
+  const uint16_t u = static_cast<const uint16_t*>(base)[i];
+  if (dtype == TQ_BF16) return __uint_as_float((uint32_t)u << 16);
+  return __half2float(__ushort_as_half(u));
+}
+
+// Pointer to the 256 bounds of block blk; null where its page is bad.
+__device__ __forceinline__ const __nv_bfloat16* bounds_at(const SelectArgs& a, int b, int h, int blk) {
+  long long row;
+  int slot;
+  if (!tq_map_slot(a.map, a.Hkv, b, h, blk * kBlock, row, slot)) return nullptr;
+  return a.bounds + (row * (tq_row_slots(a.map, a.capacity) / kBlock) + slot / kBlock) * kRow;
+}
+
+__device__ __forceinline__ int blocks_of(const SelectArgs& a, int b) {
+  return (min(max(a.seq_lens[b], 0), a.max_len) + kBlock - 1) / kBlock;
+}
+
+// Scores in 32 bits of the blocks of one (sequence, KV head): the largest over the group's
+// query heads.  A warp takes a block at a time, lanes 0–15 its lower and lanes 16–31 its upper
+// bounds (one 512-byte load), each with its half of the query rows.
+template <int kG>
+__global__ void __launch_bounds__(256) block_score_kernel(const SelectArgs a) {
+  __shared__ float s_err[8];
+  const int row = blockIdx.y, b = row / a.Hkv, h = row % a.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int len = a.seq_lens[b];
+  if (len > a.max_len && blockIdx.x == 0 && h == 0 && threadIdx.x == 0)
+    atomicOr(&g_tq_flags, TQ_FLAG_LEN_OVERFLOW);
+  const int nblk = blocks_of(a, b);
+  const int begin = blockIdx.x * kPerCta, end = min(begin + kPerCta, nblk);
+  if (nblk <= a.keep || begin >= end) return;   // nothing to choose, or nothing here
+  float q[kG][8], most[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) most[j] = 0.f;
+#pragma unroll
+  for (int g = 0; g < kG; ++g)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      // absent heads repeat head 0: the maximum over them is the same
+      const float v = load_elem(a.q, a.q_dtype, ((long long)row * a.G + (g < a.G ? g : 0)) * TQ_D +
+                                                    (lane & 15) * 8 + j);
+      q[g][j] = (lane < 16 ? v > 0.f : v < 0.f) ? 0.f : v;   // NaN goes to both
+      most[j] = fmaxf(most[j], fabsf(q[g][j]));
+    }
+  float err = 0.f;
+  for (int blk = begin + warp; blk < end; blk += 8) {
+    const __nv_bfloat16* p = bounds_at(a, b, h, blk);
+    float s = -INFINITY;
+    if (p) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(p) + lane);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      float v[8], t[kG], e = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+        e = fmaf(most[j], fabsf(v[j]), e);
+      }
+      err = e <= err ? err : e;   // NaN stays
+#pragma unroll
+      for (int g = 0; g < kG; ++g) {
+        t[g] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[g] = fmaf(q[g][j], v[j], t[g]);
+      }
+#pragma unroll
+      for (int g = 0; g < kG; ++g) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) t[g] += __shfl_xor_sync(0xffffffffu, t[g], o);
+        s = fmaxf(s, t[g]);
+      }
+    } else if (lane == 0) {
+      atomicOr(&g_tq_flags, TQ_FLAG_PAGE);
+    }
+    if (lane == 0) a.score[(long long)row * a.nb + blk] = s;
+  }
+  // Σ over lanes of each lane's largest partial sum: at least every block's Σ|terms|
+#pragma unroll
+  for (int o = 16; o; o >>= 1) err += __shfl_xor_sync(0xffffffffu, err, o);
+  if (lane == 0) s_err[warp] = err;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float e = 0.f;
+    for (int i = 0; i < 8; ++i) e = s_err[i] <= e ? e : s_err[i];
+    a.err[(long long)row * a.chunks + blockIdx.x] = e;
+  }
+}
+
+// Integers in the order of the numbers (no NaN reaches them: a maximum leaves it out).
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t u = __float_as_uint(x + 0.f);              // −0 as +0
+  return u >> 31 ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t k) {
+  return __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~k);
+}
+__device__ __forceinline__ unsigned long long ordered(double x) {
+  const unsigned long long u = __double_as_longlong(x + 0.0);
+  return u >> 63 ? ~u : u | 0x8000000000000000ull;
+}
+
+constexpr int kSelThreads = 1024;
+
+// Sum over the CTA of one int per thread (every thread gets it).
+__device__ __forceinline__ int cta_sum(int v, int* scratch) {
+  v = __reduce_add_sync(0xffffffffu, v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const int w = threadIdx.x & 31;
+  return __reduce_add_sync(0xffffffffu, w < (int)(blockDim.x >> 5) ? scratch[w] : 0);
+}
+
+// The largest t with at least `want` of the n keys ≥ t (want ≥ 1, want ≤ n): bit by bit, one
+// count of the CTA per bit, stopping early at a count that is `want` exactly.
+template <typename K, typename F>
+__device__ __forceinline__ K kth_key(int n, int want, int bits, F key, int* scratch) {
+  K t = 0;
+  for (int bit = bits - 1; bit >= 0; --bit) {
+    const K c = t | ((K)1 << bit);
+    int mine = 0;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) mine += key(i) >= c;
+    const int got = cta_sum(mine, scratch);
+    if (got >= want) t = c;
+    if (got == want) break;
+  }
+  return t;
+}
+
+// One CTA per (sequence, KV head).  The 32-bit scores are off by at most E each; with v the
+// smallest score among the `want` largest, blocks above v + 2E are kept and blocks below v − 2E
+// are not, whatever the rounding.  Those between are scored again in 64 bits (the products are
+// exact there) and ranked, ties to the lowest number: the selection does not depend on the
+// order of any sum.
+__global__ void __launch_bounds__(kSelThreads) block_select_kernel(const SelectArgs a) {
+  extern __shared__ uint32_t s_dyn[];     // keep bits, then per-word offsets
+  __shared__ int s_red[32];
+  const int row = blockIdx.x, b = row / a.Hkv, h = row % a.Hkv;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarps = blockDim.x >> 5;
+  const int nblk = blocks_of(a, b);
+  int* list = a.list + (long long)row * a.keep;
+  if (nblk <= a.keep) {
+    for (int i = tid; i < a.keep; i += blockDim.x) list[i] = i < nblk ? i : -1;
+    return;
+  }
+  const int words = (nblk + 31) / 32;
+  uint32_t* bits = s_dyn;
+  const float* score = a.score + (long long)row * a.nb;
+  const int lo = a.first, n = nblk - a.first - a.last;      // candidates lo .. lo + n − 1
+  const int want = a.keep - a.first - a.last;
+  for (int i = tid; i < words; i += blockDim.x) bits[i] = 0;
+  float err = 0.f;
+  for (int i = tid; i < (nblk + kPerCta - 1) / kPerCta; i += blockDim.x) {
+    const float e = a.err[(long long)row * a.chunks + i];
+    err = e <= err ? err : e;
+  }
+  // the largest bound of the row, NaN above all
+  const uint32_t worst = __reduce_max_sync(0xffffffffu, err != err ? ~0u : __float_as_uint(err));
+  if (lane == 0) s_red[warp] = (int)worst;
+  __syncthreads();
+  const uint32_t wall = __reduce_max_sync(0xffffffffu, lane < nwarps ? (uint32_t)s_red[lane] : 0u);
+  // eight multiply-adds and five additions per lane and shuffle, half a step of 32 bits each:
+  // 13·2^-24·Σ|terms|; 2^-20 leaves room for the rounding of the bound itself
+  const float E = wall == ~0u ? INFINITY : __uint_as_float(wall) * 9.5367431640625e-7f;
+  for (int i = tid; i < a.first; i += blockDim.x) atomicOr(&bits[i >> 5], 1u << (i & 31));
+  for (int i = nblk - a.last + tid; i < nblk; i += blockDim.x) atomicOr(&bits[i >> 5], 1u << (i & 31));
+  if (want > 0) {
+    auto key = [&](int i) { return ordered(score[lo + i]); };
+    const uint32_t t = kth_key<uint32_t>(n, want, 32, key, s_red);
+    // v: the smallest key ≥ t
+    uint32_t v = ~0u;
+    for (int i = tid; i < n; i += blockDim.x) {
+      const uint32_t k = key(i);
+      if (k >= t) v = min(v, k);
+    }
+    v = __reduce_min_sync(0xffffffffu, v);
+    __syncthreads();
+    if (lane == 0) s_red[warp] = (int)v;
+    __syncthreads();
+    v = __reduce_min_sync(0xffffffffu, lane < nwarps ? (uint32_t)s_red[lane] : ~0u);
+    const float vf = unordered(v);
+    const float up = vf + 2.f * E, down = vf - 2.f * E;
+    // kept whatever the rounding; in doubt (with an infinite E every block is)
+    int sure = 0, open = 0;
+    for (int i = tid; i < n; i += blockDim.x) {
+      const float s = score[lo + i];
+      const bool in = s > up, out = s < down;
+      sure += in;
+      open += !in && !out;
+      if (in) atomicOr(&bits[(lo + i) >> 5], 1u << ((lo + i) & 31));
+    }
+    sure = cta_sum(sure, s_red);
+    open = cta_sum(open, s_red);
+    const int need = want - sure;
+    int* doubt = a.doubt + (long long)row * a.nb;
+    unsigned long long* exact = a.exact + (long long)row * a.nb;
+    if (open <= need) {
+      for (int i = tid; i < n; i += blockDim.x) {
+        const float s = score[lo + i];
+        if (!(s > up) && !(s < down)) atomicOr(&bits[(lo + i) >> 5], 1u << ((lo + i) & 31));
+      }
+    } else {
+      // the blocks in doubt, in ascending order, each warp of 32 candidates at a time
+      int base = 0;
+      for (int i0 = 0; i0 < n; i0 += blockDim.x) {
+        const int i = i0 + tid;
+        const float s = i < n ? score[lo + i] : 0.f;
+        const bool d = i < n && !(s > up) && !(s < down);
+        const uint32_t vote = __ballot_sync(0xffffffffu, d);
+        __syncthreads();
+        if (lane == 0) s_red[warp] = __popc(vote);
+        __syncthreads();
+        const int c = lane < nwarps ? s_red[lane] : 0;
+        const int before = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
+        if (d) doubt[base + before + __popc(vote & ((1u << lane) - 1))] = lo + i;
+        base += __reduce_add_sync(0xffffffffu, c);
+      }
+      __syncthreads();
+      // (a row of zero queries has nothing to score: every term is 0)
+      for (int i = tid; wall == 0u && i < open; i += blockDim.x) exact[i] = ordered(0.0);
+      for (int i = warp; wall != 0u && i < open; i += nwarps) {
+        const __nv_bfloat16* p = bounds_at(a, b, h, doubt[i]);
+        double best = -INFINITY;
+        for (int g = 0; p && g < a.G; ++g) {
+          double s = 0.0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int c = 4 * lane + j;
+            const double x = load_elem(a.q, a.q_dtype, ((long long)row * a.G + g) * TQ_D + c);
+            const double l = __bfloat162float(p[c]), u = __bfloat162float(p[TQ_D + c]);
+            s += x < 0.0 ? x * l : x * u;
+          }
+#pragma unroll
+          for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          best = fmax(best, s);   // a NaN head is left out
+        }
+        if (lane == 0) exact[i] = ordered(best);
+      }
+      __syncthreads();
+      auto key64 = [&](int i) { return exact[i]; };
+      const unsigned long long t64 = kth_key<unsigned long long>(open, need, 64, key64, s_red);
+      // above t64, and of those at it (or from it on, where the count was exact) the first
+      int above = 0;
+      for (int i = tid; i < open; i += blockDim.x) above += exact[i] > t64;
+      above = cta_sum(above, s_red);
+      int left = need - above, at = 0;    // places for keys equal to t64, in ascending order
+      for (int i0 = 0; i0 < open; i0 += blockDim.x) {
+        const int i = i0 + tid;
+        const unsigned long long k = i < open ? exact[i] : 0ull;
+        const bool eq = i < open && k == t64;
+        const uint32_t vote = __ballot_sync(0xffffffffu, eq);
+        __syncthreads();
+        if (lane == 0) s_red[warp] = __popc(vote);
+        __syncthreads();
+        const int c = lane < nwarps ? s_red[lane] : 0;
+        const int before = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
+        const bool in = i < open && (k > t64 || (eq && at + before + __popc(vote & ((1u << lane) - 1)) < left));
+        if (in) atomicOr(&bits[doubt[i] >> 5], 1u << (doubt[i] & 31));
+        at += __reduce_add_sync(0xffffffffu, c);
+      }
+    }
+  }
+  // the kept blocks in ascending order: words of 32 blocks, counted then written
+  int base = 0;
+  for (int w0 = 0; w0 < words; w0 += blockDim.x) {
+    __syncthreads();
+    const int w = w0 + tid;
+    uint32_t m = w < words ? bits[w] : 0u;
+    const int c = __popc(m);
+    int incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) s_red[warp] = incl;
+    __syncthreads();
+    const int ws = lane < nwarps ? s_red[lane] : 0;
+    int at = base + __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0) + incl - c;
+    base += __reduce_add_sync(0xffffffffu, ws);
+    while (m) {
+      list[at++] = 32 * w + __ffs((int)m) - 1;
+      m &= m - 1;
+    }
+  }
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+template <typename T>
+void launch_bounds_t(const BoundsArgs& a, bool vec, unsigned grid, cudaStream_t stream) {
+  if (vec) block_bounds_kernel<T, true><<<grid, 256, 0, stream>>>(a);
+  else block_bounds_kernel<T, false><<<grid, 256, 0, stream>>>(a);
+}
+
+struct SelPlan {
+  int G, nb, chunks;
+  size_t err_off, exact_off, doubt_off, bytes;
+};
+
+tq_status select_plan(const tq_attn_desc* d, SelPlan* p) {
+  if (!d) return TQ_ERR_INVALID_ARG;
+  if (d->head_dim != TQ_HEAD_DIM) return TQ_ERR_UNSUPPORTED;
+  if (d->batch < 0 || d->q_heads <= 0 || d->kv_heads <= 0) return TQ_ERR_INVALID_ARG;
+  if (d->q_heads % d->kv_heads) return TQ_ERR_INVALID_ARG;
+  if (d->q_heads / d->kv_heads > TQ_MAX_GROUP) return TQ_ERR_UNSUPPORTED;
+  if (d->capacity <= 0 || d->capacity % TQ_CAPACITY_ALIGN) return TQ_ERR_INVALID_ARG;
+  if (d->max_seq_len < 0 || d->max_seq_len > d->capacity) return TQ_ERR_INVALID_ARG;
+  if (d->q_dtype != TQ_F32 && d->q_dtype != TQ_F16 && d->q_dtype != TQ_BF16) return TQ_ERR_UNSUPPORTED;
+  // rows of the scoring grid, and keep bits of a row in shared memory (1.5 M blocks)
+  if ((long long)d->batch * d->kv_heads > 65535 || d->max_seq_len > (1 << 26)) return TQ_ERR_UNSUPPORTED;
+  p->G = d->q_heads / d->kv_heads;
+  p->nb = std::max((d->max_seq_len + kBlock - 1) / kBlock, 1);
+  p->chunks = (p->nb + kPerCta - 1) / kPerCta;
+  const size_t rows = (size_t)d->batch * d->kv_heads;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  p->err_off = up(rows * p->nb * sizeof(float));
+  p->exact_off = p->err_off + up(rows * p->chunks * sizeof(float));
+  p->doubt_off = p->exact_off + up(rows * p->nb * sizeof(unsigned long long));
+  p->bytes = p->doubt_off + up(rows * p->nb * sizeof(int)) + 256;
+  return TQ_OK;
+}
+
+}  // namespace
+
+extern "C" tq_status tq_block_bounds(const void* x, tq_dtype x_dtype, int32_t batch, int32_t heads,
+                                     int32_t tokens, int64_t stride_b, int64_t stride_h,
+                                     int64_t stride_t, const int32_t* pos, const int32_t* count,
+                                     tq_block_cache blocks, int32_t capacity, tq_stream_t stream_) {
+  if (batch < 0 || heads <= 0 || tokens < 0) return TQ_ERR_INVALID_ARG;
+  if (stride_b < 0 || stride_h < 0 || stride_t < 0) return TQ_ERR_INVALID_ARG;
+  if (capacity <= 0 || capacity % TQ_CAPACITY_ALIGN) return TQ_ERR_INVALID_ARG;
+  if (x_dtype != TQ_F32 && x_dtype != TQ_F16 && x_dtype != TQ_BF16) return TQ_ERR_UNSUPPORTED;
+  if (!x || !blocks.bounds || !aligned16(blocks.bounds)) return TQ_ERR_INVALID_ARG;
+  const int elem = x_dtype == TQ_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(x) % elem) return TQ_ERR_INVALID_ARG;
+  BoundsArgs a{};
+  tq_status st = tq_rowmap_of(blocks.pages, capacity, &a.map);
+  if (st != TQ_OK) return st;
+  if (batch == 0 || tokens == 0) return TQ_OK;
+  a.x = x;
+  a.batch = batch; a.heads = heads; a.tokens = tokens;
+  a.sb = stride_b; a.sh = stride_h; a.st = stride_t;
+  a.pos = pos; a.count = count;
+  a.bounds = reinterpret_cast<__nv_bfloat16*>(blocks.bounds);
+  a.capacity = capacity;
+  a.nt = (int)(pos ? (tokens + (kBlock - 2LL)) / kBlock + 1 : (tokens + (kBlock - 1LL)) / kBlock);
+  a.units = (long long)batch * heads * a.nt;
+  if ((a.units + 7) / 8 > 0x7fffffffLL) return TQ_ERR_UNSUPPORTED;
+  const bool vec = aligned16(x) && stride_b * elem % 16 == 0 && stride_h * elem % 16 == 0 &&
+                   stride_t * elem % 16 == 0;
+  const unsigned grid = (unsigned)((a.units + 7) / 8);
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (x_dtype == TQ_F32) launch_bounds_t<float>(a, vec, grid, stream);
+  else if (x_dtype == TQ_F16) launch_bounds_t<__half>(a, vec, grid, stream);
+  else launch_bounds_t<__nv_bfloat16>(a, vec, grid, stream);
+  return tq_cuda_status(cudaGetLastError());
+}
+
+extern "C" size_t tq_block_select_workspace_bytes(const tq_attn_desc* desc) {
+  SelPlan p;
+  return select_plan(desc, &p) == TQ_OK ? p.bytes : 0;
+}
+
+extern "C" tq_status tq_block_select(const tq_attn_desc* desc, const void* q, tq_block_cache blocks,
+                                     const int32_t* seq_lens, int32_t first_blocks,
+                                     int32_t last_blocks, int32_t max_blocks, int32_t* list,
+                                     void* workspace, size_t workspace_bytes, tq_stream_t stream_) {
+  SelPlan p;
+  tq_status st = select_plan(desc, &p);
+  if (st != TQ_OK) return st;
+  if (first_blocks < 0 || last_blocks < 0 || max_blocks <= 0 || max_blocks > (1 << 24) ||
+      (long long)first_blocks + last_blocks > max_blocks)
+    return TQ_ERR_INVALID_ARG;
+  if (!q || !blocks.bounds || !aligned16(blocks.bounds) || !seq_lens || !list || !workspace)
+    return TQ_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < p.bytes)
+    return TQ_ERR_INVALID_ARG;
+  SelectArgs a{};
+  if ((st = tq_rowmap_of(blocks.pages, desc->capacity, &a.map)) != TQ_OK) return st;
+  if (desc->batch == 0) return TQ_OK;
+  char* ws = static_cast<char*>(workspace);
+  a.q = q; a.q_dtype = desc->q_dtype;
+  a.bounds = reinterpret_cast<const __nv_bfloat16*>(blocks.bounds);
+  a.capacity = desc->capacity; a.max_len = desc->max_seq_len;
+  a.seq_lens = seq_lens;
+  a.Hkv = desc->kv_heads; a.G = p.G;
+  a.nb = p.nb; a.chunks = p.chunks;
+  a.first = first_blocks; a.last = last_blocks; a.keep = max_blocks;
+  a.score = reinterpret_cast<float*>(ws);
+  a.err = reinterpret_cast<float*>(ws + p.err_off);
+  a.exact = reinterpret_cast<unsigned long long*>(ws + p.exact_off);
+  a.doubt = reinterpret_cast<int*>(ws + p.doubt_off);
+  a.list = list;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const int rows = desc->batch * desc->kv_heads;
+  const dim3 grid(p.chunks, rows);
+  if (p.G <= 1) block_score_kernel<1><<<grid, 256, 0, stream>>>(a);
+  else if (p.G <= 2) block_score_kernel<2><<<grid, 256, 0, stream>>>(a);
+  else if (p.G <= 4) block_score_kernel<4><<<grid, 256, 0, stream>>>(a);
+  else block_score_kernel<8><<<grid, 256, 0, stream>>>(a);
+  if ((st = tq_cuda_status(cudaGetLastError())) != TQ_OK) return st;
+  // about four blocks a thread
+  const int want = (p.nb + 3) / 4;
+  const int threads = std::min(kSelThreads, std::max(128, (want + 31) / 32 * 32));
+  const size_t smem = (size_t)(p.nb + 31) / 32 * sizeof(uint32_t);
+  static bool configured[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return TQ_ERR_CUDA;
+  if (!configured[dev]) {
+    if (cudaFuncSetAttribute(block_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             200 * 1024) != cudaSuccess)
+      return TQ_ERR_CUDA;
+    configured[dev] = true;
+  }
+  block_select_kernel<<<rows, threads, smem, stream>>>(a);
+  return tq_cuda_status(cudaGetLastError());
+}

@@ -506,8 +506,10 @@ extern "C" tq_status tq_device_status(uint32_t* flags) {
   const unsigned int a = tq_take_flags_quantize(), b = tq_take_flags_attention();
   const unsigned int d = tq_take_flags_quantize_tc(), e = tq_take_flags_decode_tc();
   const unsigned int f = tq_take_flags_decode_asym(), g = tq_take_flags_store();
-  if (a == ~0u || b == ~0u || d == ~0u || e == ~0u || f == ~0u || g == ~0u) return TQ_ERR_CUDA;
-  *flags = a | b | d | e | f | g;
+  const unsigned int h = tq_take_flags_rows(), i = tq_take_flags_blocks();
+  if (a == ~0u || b == ~0u || d == ~0u || e == ~0u || f == ~0u || g == ~0u || h == ~0u || i == ~0u)
+    return TQ_ERR_CUDA;
+  *flags = a | b | d | e | f | g | h | i;
   if (*flags & TQ_FLAG_TIMEOUT) return TQ_ERR_TIMEOUT;
   return *flags ? TQ_ERR_DEVICE_STATUS : TQ_OK;
 }

@@ -1,0 +1,1029 @@
+// Decode attention of many query rows over one token stream of the compressed cache: over a
+// prefix that a whole batch shares (tq_prefix_attention) and over the blocks that a selection
+// kept of each sequence (tq_sparse_attention).
+//
+// Mathematics.  With y = Π q, z = S q and a token's code (i, s, ‖x‖, ‖r‖), the estimator of
+// ⟨q, k⟩ (QJL deep-dive §五) is
+//   ‖x‖·( ⟨y, c[i]⟩ + ρ·⟨z, s⟩ ),   ρ = ‖r‖/‖x‖·√(π/2)/d,
+// one product of length 256 of the row [y, z] with the token's operand [c[i], ±ρ].  A value is
+// ‖v‖·Πᵀc[j], so the output row is Πᵀ·Σ_t p_t‖v_t‖c[j_t] / Σ_t p_t.  The weights of the value
+// product are w_t = 2^(e_t − m) with e_t = score + log2‖v_t‖ and m a reference near the running
+// maximum of e (not of the score): they are at most 2^kGrow whatever the norms, so fp16 holds
+// them; the denominator is Σ w_t/‖v_t‖ in 32 bits.
+//
+// One CTA works on one item: up to 128 query rows × a run of 128-token tiles.
+//   8 expander warps  turn the codes of a tile into fp16 operands in shared memory (a byte
+//                     permute looks four levels up at a time; codes of the next tile are in
+//                     flight in registers meanwhile),
+//   1 issuer warp     D = [y, z]·[c, ±ρ]ᵀ (128 × 128 × 256, rows in TMEM as the A operand) and
+//                     O += W·V (128 × 128 × 128, W in TMEM over the scores it came from),
+//   8 softmax warps   one thread per (row, half of the tile's tokens).
+// D has two buffers, so tile t + 1 is scored while tile t's softmax runs.
+// The items' (m, l, O) records are merged, and rotated back once per row, by rows_merge_kernel.
+//
+// Roundings to 16 bits: the rotated query and sketch, ρ, the levels (scaled so that fp16 holds
+// them best) and the weights, each half a step of fp16 (2^-12 relative): together below the
+// half step of a bf16 output (2^-9) and near that of an fp16 one.  Scores, maxima, sums and
+// accumulators are 32 bits.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "tc_ptx.h"
+#include "tq_internal.h"
+
+TQ_DEFINE_FLAGS(tq_take_flags_rows)
+
+namespace {
+
+using tq::mbar_arrive;
+using tq::s32;
+using tq::tc_after;
+using tq::tc_before;
+
+constexpr int kTile = 128;              // tokens per tile, and query rows per item
+constexpr int kExpThreads = 256;        // 8 softmax warps, 8 expander warps, 1 issuer warp
+constexpr int kThreads = 544;
+constexpr int kRecFloats = 132;         // acc[128], m, l, padding
+constexpr int kLBO = 2048;              // bytes between 8-position chunks of an operand image
+constexpr int kKBytes = 32 * kLBO;      // key operand: 128 tokens × 256 positions, fp16
+constexpr int kVBytes = 16 * kLBO;
+constexpr int kQCol = 0, kDCol = 128, kOCol = 384;   // TMEM columns
+constexpr int kFacSlots = 4;
+constexpr float kAlpha = 64.f, kBeta = 4.f;   // scales of y and z in the fp16 row operand
+constexpr float kGrow = 8.f;            // the reference follows the maximum when 2^8 above it
+constexpr float kTiny = 8.6736174e-19f; // 2^-60: smaller value norms count as zero
+constexpr float kQjl = 1.2533141373155003f / 128.f;   // √(π/2)/d
+
+// fp16 levels as byte tables for a byte permute: levels 0–7 in lo[0..1], hi[0..1], 8–15 behind.
+struct LevelBytes {
+  uint32_t lo[4], hi[4];
+};
+
+struct CacheSide {
+  const uint8_t* kidx;
+  const uint8_t* ksgn;
+  const float* kxn;
+  const float* krn;
+  const uint8_t* vidx;
+  const float* vxn;
+  tq_rowmap kmap, vmap;
+  int cap;
+};
+
+struct RowsArgs {
+  CacheSide own, pre;
+  const int* seq_lens;
+  const int* pre_len;
+  const int* list;          // [B][Hkv][max_blocks] block numbers, or null
+  int max_blocks;
+  int max_len, max_pre;     // bounds of the lengths that the split is made for
+  int B, Hq, Hkv, G;
+  int row_tiles, pre_splits, own_splits;
+  LevelBytes kt, vt;
+  float rho_scale;          // ρ's scale in the key operand
+  const uint4* qop;         // [B·Hq][256] fp16 row operands
+  const float* qf;          // [B·Hq] factor of the products
+  float* rec;               // [pre_splits + own_splits][B·Hq][kRecFloats]
+};
+
+struct alignas(1024) Smem {
+  unsigned char k[2][kKBytes];
+  unsigned char v[2][kVBytes];
+  float fac[kFacSlots][3][kTile];    // ‖x‖, log2‖v‖, 1/‖v‖ of a tile's tokens
+  float tmax[2][kTile];
+  float lsum[kTile];
+  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], ffull[kFacSlots];
+  uint64_t pvdone, qfull, drain;
+  uint32_t tmem;
+  int tiles;
+};
+
+__device__ __forceinline__ float load_elem(const void* base, int dtype, long long i) {
+  if (dtype == TQ_F32) return static_cast<const float*>(base)[i];
+  const uint16_t u = static_cast<const uint16_t*>(base)[i];
+  if (dtype == TQ_BF16) return __uint_as_float((uint32_t)u << 16);
+  return __half2float(__ushort_as_half(u));
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(s));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr __host__ __device__ uint32_t shr(uint32_t x, int n) { return n >= 0 ? x >> n : x << -n; }
+
+// Coordinate of operand position p.  Planes: chunk 4w + r of eight positions holds bits
+// r, r + 4, ..., r + 28 of word w (one AND spreads them over eight nibbles).  Signs: chunk
+// 4w + c holds the bit pairs (j, j + 16), j = 4c..4c + 3 (one AND leaves both at the sign bits
+// of an fp16 pair).  Nibble codes keep their order.
+__host__ __device__ constexpr int plane_coord(int p) {
+  return (p & ~31) + 4 * (p & 7) + ((p >> 3) & 3);
+}
+__host__ __device__ constexpr int sign_coord(int p) {
+  return (p & ~31) + 4 * ((p >> 3) & 3) + ((p & 7) >> 1) + 16 * (p & 1);
+}
+
+// Eight fp16 levels of eight 3-bit indices (one per nibble of s; with 16 levels `top` holds the
+// fourth bit, 8 | bit per nibble: a permute in sign-replicating mode makes it a byte mask).
+template <bool k16>
+__device__ __forceinline__ uint4 levels8(const LevelBytes& t, uint32_t s, uint32_t top) {
+  uint32_t w[4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t sh = h ? s >> 16 : s;
+    uint32_t lo = prmt(t.lo[0], t.lo[1], sh), hi = prmt(t.hi[0], t.hi[1], sh);
+    if (k16) {
+      const uint32_t m = prmt(0x8000u, 0u, h ? top >> 16 : top);
+      lo = (lo & ~m) | (prmt(t.lo[2], t.lo[3], sh) & m);
+      hi = (hi & ~m) | (prmt(t.hi[2], t.hi[3], sh) & m);
+    }
+    w[2 * h] = prmt(lo, hi, 0x5140u);
+    w[2 * h + 1] = prmt(lo, hi, 0x7362u);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Chunk r of a word of NB planes.
+template <int NB>
+__device__ __forceinline__ uint4 plane_chunk(const LevelBytes& t, const uint32_t (&w)[NB], int r) {
+  uint32_t s = shr(w[0], r) & 0x11111111u, top = 0;
+  if (NB >= 2) s |= shr(w[NB >= 2 ? 1 : 0], r - 1) & 0x22222222u;
+  if (NB >= 3) s |= shr(w[NB >= 3 ? 2 : 0], r - 2) & 0x44444444u;
+  if (NB >= 4) top = (shr(w[NB >= 4 ? 3 : 0], r) & 0x11111111u) | 0x88888888u;
+  return levels8<NB == 4>(t, s, top);
+}
+
+// The codes of half a token (64 coordinates) as an expander thread holds them.
+template <int IB, int VB>
+struct Codes {
+  uint2 k[IB], s;
+  uint2 v[VB == 4 ? 4 : VB];
+  float xn, rn, vn;
+  bool ok;
+};
+
+template <int IB, int VB>
+__device__ __forceinline__ void fetch(const CacheSide& c, int Hkv, int b, int h, long long token,
+                                      bool ok, int half, Codes<IB, VB>& o) {
+  long long krow = 0, vrow = 0;
+  int kslot = 0, vslot = 0;
+  if (ok) {
+    const bool kin = tq_map_slot(c.kmap, Hkv, b, h, (int)token, krow, kslot);
+    const bool vin = tq_map_slot(c.vmap, Hkv, b, h, (int)token, vrow, vslot);
+    if (!kin || !vin) {
+      atomicOr(&g_tq_flags, TQ_FLAG_PAGE);
+      ok = false;
+    }
+  }
+  o.ok = ok;
+  o.xn = o.rn = o.vn = 0.f;
+  o.s = make_uint2(0, 0);
+#pragma unroll
+  for (int p = 0; p < IB; ++p) o.k[p] = make_uint2(0, 0);
+#pragma unroll
+  for (int p = 0; p < (VB == 4 ? 4 : VB); ++p) o.v[p] = make_uint2(0, 0);
+  if (!ok) return;
+  const long long ks = tq_row_slots(c.kmap, c.cap), vs = tq_row_slots(c.vmap, c.cap);
+#pragma unroll
+  for (int p = 0; p < IB; ++p)
+    o.k[p] = __ldg(reinterpret_cast<const uint2*>(c.kidx + ((krow * IB + p) * ks + kslot) * 16 + 8 * half));
+  o.s = __ldg(reinterpret_cast<const uint2*>(c.ksgn + (krow * ks + kslot) * 16 + 8 * half));
+  o.xn = __ldg(c.kxn + krow * ks + kslot);
+  o.rn = __ldg(c.krn + krow * ks + kslot);
+  if (VB == 4) {
+    const uint4* p = reinterpret_cast<const uint4*>(c.vidx + (vrow * vs + vslot) * 64 + 32 * half);
+    const uint4 x = __ldg(p), y = __ldg(p + 1);
+    o.v[0] = make_uint2(x.x, x.y);
+    o.v[1 % (VB == 4 ? 4 : VB)] = make_uint2(x.z, x.w);
+    o.v[2 % (VB == 4 ? 4 : VB)] = make_uint2(y.x, y.y);
+    o.v[3 % (VB == 4 ? 4 : VB)] = make_uint2(y.z, y.w);
+  } else {
+#pragma unroll
+    for (int p = 0; p < VB; ++p)
+      o.v[p] = __ldg(reinterpret_cast<const uint2*>(c.vidx + ((vrow * VB + p) * vs + vslot) * 16 + 8 * half));
+  }
+  o.vn = __ldg(c.vxn + vrow * vs + vslot);
+}
+
+// Key operand of half a token: level chunks 8·half.. and sign chunks 16 + 8·half...
+template <int IB, int VB>
+__device__ __forceinline__ void expand_key(const RowsArgs& a, const Codes<IB, VB>& c, int half,
+                                           unsigned char* dst) {
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    uint32_t x[IB];
+#pragma unroll
+    for (int p = 0; p < IB; ++p) x[p] = w ? c.k[p].y : c.k[p].x;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      *reinterpret_cast<uint4*>(dst + (8 * half + 4 * w + r) * kLBO) = plane_chunk<IB>(a.kt, x, r);
+  }
+  // ρ ≤ 1 or so for codes of any key (‖r‖ is the norm of a quantisation residual); a zero key
+  // has both norms 0
+  const float rho = c.xn > 0.f ? c.rn / c.xn * a.rho_scale : 0.f;
+  const __half2 r2 = __float2half2_rn(rho);
+  const uint32_t neg = *reinterpret_cast<const uint32_t*>(&r2) ^ 0x80008000u;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const uint32_t x = w ? c.s.y : c.s.x;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint4 o;
+      o.x = (shr(x, 4 * q + 0 - 15) & 0x80008000u) ^ neg;
+      o.y = (shr(x, 4 * q + 1 - 15) & 0x80008000u) ^ neg;
+      o.z = (shr(x, 4 * q + 2 - 15) & 0x80008000u) ^ neg;
+      o.w = (shr(x, 4 * q + 3 - 15) & 0x80008000u) ^ neg;
+      *reinterpret_cast<uint4*>(dst + (16 + 8 * half + 4 * w + q) * kLBO) = o;
+    }
+  }
+}
+
+template <int IB, int VB>
+__device__ __forceinline__ void expand_value(const RowsArgs& a, const Codes<IB, VB>& c, int half,
+                                             unsigned char* dst) {
+  LevelBytes t = a.vt;
+  if (!(c.vn >= kTiny)) {   // a zero vector adds nothing, whatever its code
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t.lo[i] = t.hi[i] = 0;
+  }
+  if constexpr (VB == 4) {
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      const uint32_t x = (w & 1) ? c.v[w / 2].y : c.v[w / 2].x;
+      *reinterpret_cast<uint4*>(dst + (8 * half + w) * kLBO) =
+          levels8<true>(t, x & 0x77777777u, ((x >> 3) & 0x11111111u) | 0x88888888u);
+    }
+  } else {
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      uint32_t x[VB];
+#pragma unroll
+      for (int p = 0; p < VB; ++p) x[p] = w ? c.v[p].y : c.v[p].x;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<uint4*>(dst + (8 * half + 4 * w + r) * kLBO) = plane_chunk<VB>(t, x, r);
+    }
+  }
+}
+
+// Valid length of a sequence: clamped to what the call was sized for, flagged if longer.
+__device__ __forceinline__ int clamp_len(int len, int most) {
+  if (len > most) {
+    atomicOr(&g_tq_flags, TQ_FLAG_LEN_OVERFLOW);
+    return most;
+  }
+  return len < 0 ? 0 : len;
+}
+
+template <int IB, int VB>
+__global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_constant__ RowsArgs a) {
+  extern __shared__ unsigned char smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // ---- the item: prefix items first (they are the long ones)
+  int item = blockIdx.x;
+  const int npre = a.pre_splits * a.Hkv * a.row_tiles;
+  const bool pre = item < npre;
+  int split, h, b = 0, rt = 0;
+  if (pre) {
+    rt = item % a.row_tiles;
+    h = item / a.row_tiles % a.Hkv;
+    split = item / (a.row_tiles * a.Hkv);
+  } else {
+    item -= npre;
+    h = item % a.Hkv;
+    b = item / a.Hkv % a.B;
+    split = item / (a.Hkv * a.B);
+  }
+  CacheSide side;   // field by field: a reference into either would put both in local memory
+  side.kidx = pre ? a.pre.kidx : a.own.kidx;
+  side.ksgn = pre ? a.pre.ksgn : a.own.ksgn;
+  side.kxn = pre ? a.pre.kxn : a.own.kxn;
+  side.krn = pre ? a.pre.krn : a.own.krn;
+  side.vidx = pre ? a.pre.vidx : a.own.vidx;
+  side.vxn = pre ? a.pre.vxn : a.own.vxn;
+  side.kmap.table = pre ? a.pre.kmap.table : a.own.kmap.table;
+  side.kmap.max_pages = pre ? a.pre.kmap.max_pages : a.own.kmap.max_pages;
+  side.kmap.page_tokens = pre ? a.pre.kmap.page_tokens : a.own.kmap.page_tokens;
+  side.kmap.num_pages = pre ? a.pre.kmap.num_pages : a.own.kmap.num_pages;
+  side.vmap.table = pre ? a.pre.vmap.table : a.own.vmap.table;
+  side.vmap.max_pages = pre ? a.pre.vmap.max_pages : a.own.vmap.max_pages;
+  side.vmap.page_tokens = pre ? a.pre.vmap.page_tokens : a.own.vmap.page_tokens;
+  side.vmap.num_pages = pre ? a.pre.vmap.num_pages : a.own.vmap.num_pages;
+  side.cap = pre ? a.pre.cap : a.own.cap;
+  const int rows = pre ? min(kTile, a.B * a.G - rt * kTile) : a.G;
+  const int len = pre ? clamp_len(*a.pre_len, a.max_pre) : clamp_len(a.seq_lens[b], a.max_len);
+  const int splits = pre ? a.pre_splits : a.own_splits;
+  const int* list = a.list ? a.list + ((long long)b * a.Hkv + h) * a.max_blocks : nullptr;
+  const int nblk = (len + 63) / 64;
+  const int total = list ? (a.max_blocks + 1) / 2 : (len + kTile - 1) / kTile;
+  const int t0 = (int)((long long)total * split / splits);
+  int tiles = (int)((long long)total * (split + 1) / splits) - t0;
+  if (list) {
+    // leave out the tiles behind the last block of this run that is there
+    if (tid == 0) sm.tiles = 0;
+    __syncthreads();
+    int last = 0;
+    for (int i = tid; i < 2 * tiles; i += kThreads) {
+      const int at = 2 * t0 + i;
+      const int blk = at < a.max_blocks ? list[at] : -1;
+      if (blk >= 0 && blk < nblk) last = i / 2 + 1;
+    }
+    if (last) atomicMax(&sm.tiles, last);
+    __syncthreads();
+    tiles = sm.tiles;
+  }
+  const int rec_split = pre ? split : a.pre_splits + split;
+  auto qrow_of = [&](int r) -> long long {   // query row (b·Hq + head) of item row r
+    if (!pre) return (long long)b * a.Hq + h * a.G + r;
+    const int rr = rt * kTile + r;
+    return (long long)(rr / a.G) * a.Hq + h * a.G + rr % a.G;
+  };
+  if (tiles <= 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (tid < rows) {
+      float* rec = a.rec + ((long long)rec_split * a.B * a.Hq + qrow_of(tid)) * kRecFloats;
+      rec[128] = -INFINITY;
+      rec[129] = 0.f;
+    }
+    return;
+  }
+  const int active = (rows + 31) / 32;   // softmax warp pairs with a row to work on
+
+  if (warp == 16) tq::tmem_alloc(&sm.tmem, 512);
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tq::mbar_init(&sm.kfull[i], 8);
+      tq::mbar_init(&sm.vfull[i], 8);
+      tq::mbar_init(&sm.kempty[i], 1);
+      tq::mbar_init(&sm.vempty[i], 1);
+      tq::mbar_init(&sm.sfull[i], 1);
+      tq::mbar_init(&sm.pfull[i], 2 * active);
+    }
+    for (int i = 0; i < kFacSlots; ++i) tq::mbar_init(&sm.ffull[i], 8);
+    tq::mbar_init(&sm.pvdone, 1);
+    tq::mbar_init(&sm.qfull, 2 * active);
+    tq::mbar_init(&sm.drain, 1);
+    tq::mbar_init_fence();
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = sm.tmem;
+  bool ok = true;   // false once a bounded wait gave up: every role then leaves its loop
+  auto wait = [&](uint64_t* bar, unsigned parity) {
+    return ok = __all_sync(0xffffffffu, ok && tq::mbar_wait(bar, parity));
+  };
+
+  if (warp < 8) {
+    // ================================================================ softmax
+    const int wl = warp & 3, hf = warp >> 2;
+    const int r = 32 * wl + lane;
+    if (wl < active) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      const uint32_t lane_base = tmem + ((uint32_t)(32 * wl) << 16);
+      float f = 0.f;
+      {
+        uint32_t q[64];
+        if (r < rows) {
+          const long long qr = qrow_of(r);
+          const uint4* src = a.qop + qr * 32 + 16 * hf;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint4 x = __ldg(src + i);
+            q[4 * i] = x.x; q[4 * i + 1] = x.y; q[4 * i + 2] = x.z; q[4 * i + 3] = x.w;
+          }
+          f = __ldg(a.qf + qr);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) q[i] = 0;
+        }
+        tq::tmem_st_32x32b_x32(lane_base + kQCol + 64 * hf, q);
+        tq::tmem_st_32x32b_x32(lane_base + kQCol + 64 * hf + 32, q + 32);
+        tq::tmem_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.qfull);
+      }
+      float m = -INFINITY, l = 0.f;
+      bool alive = true;
+      for (int t = 0; t < tiles; ++t) {
+        const int buf = t & 1;
+        wait(&sm.ffull[t % kFacSlots], (t / kFacSlots) & 1);
+        wait(&sm.sfull[buf], (t >> 1) & 1);
+        tc_after();
+        const uint32_t dcol = lane_base + kDCol + 128 * buf;
+        float e[64];
+        tq::tmem_ld_32x32b_x32(dcol + 64 * hf, reinterpret_cast<uint32_t*>(e));
+        tq::tmem_ld_32x32b_x32(dcol + 64 * hf + 32, reinterpret_cast<uint32_t*>(e + 32));
+        tq::tmem_wait_ld();
+        const float* fx = sm.fac[t % kFacSlots][0] + 64 * hf;
+        float mt = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float4 xn = *reinterpret_cast<const float4*>(fx + 4 * i);
+          const float4 lv = *reinterpret_cast<const float4*>(fx + kTile + 4 * i);
+          e[4 * i] = fmaf(e[4 * i] * f, xn.x, lv.x);
+          e[4 * i + 1] = fmaf(e[4 * i + 1] * f, xn.y, lv.y);
+          e[4 * i + 2] = fmaf(e[4 * i + 2] * f, xn.z, lv.z);
+          e[4 * i + 3] = fmaf(e[4 * i + 3] * f, xn.w, lv.w);
+          mt = fmaxf(mt, fmaxf(fmaxf(e[4 * i], e[4 * i + 1]), fmaxf(e[4 * i + 2], e[4 * i + 3])));
+        }
+        sm.tmax[hf][r] = mt;
+        // both halves have read D: it may be overwritten by the weights.  A wait that gave up
+        // ends both halves' loops here, together (neither then waits for the other)
+        if (!(alive = tq::named_sync_and(1 + wl, 64, ok))) break;
+        mt = fmaxf(mt, sm.tmax[hf ^ 1][r]);
+        const float m_new = mt > m + kGrow ? mt : m;
+        if (t > 0 && __any_sync(0xffffffffu, m_new != m)) {
+          // O (this half of its columns) follows the reference
+          wait(&sm.pvdone, (t - 1) & 1);
+          tc_after();
+          const float corr = m == -INFINITY ? 0.f : ex2(m - m_new);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float o[32];
+            const uint32_t at = lane_base + kOCol + 64 * hf + 32 * c;
+            tq::tmem_ld_32x32b_x32(at, reinterpret_cast<uint32_t*>(o));
+            tq::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= corr;
+            tq::tmem_st_32x32b_x32(at, reinterpret_cast<uint32_t*>(o));
+          }
+          l *= corr;
+        }
+        m = m_new;
+        const float ref = m == -INFINITY ? 0.f : m;
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float4 iv = *reinterpret_cast<const float4*>(fx + 2 * kTile + 4 * i);
+          const float w0 = ex2(e[4 * i] - ref), w1 = ex2(e[4 * i + 1] - ref);
+          const float w2 = ex2(e[4 * i + 2] - ref), w3 = ex2(e[4 * i + 3] - ref);
+          l = fmaf(w0, iv.x, l);
+          l = fmaf(w1, iv.y, l);
+          l = fmaf(w2, iv.z, l);
+          l = fmaf(w3, iv.w, l);
+          const __half2 p0 = __floats2half2_rn(w0, w1), p1 = __floats2half2_rn(w2, w3);
+          w[2 * i] = *reinterpret_cast<const uint32_t*>(&p0);
+          w[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&p1);
+        }
+        tq::tmem_st_32x32b_x32(dcol + 32 * hf, w);
+        tq::tmem_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.pfull[buf]);
+        // tmax is written again only after the partner's next wait on sfull, which needs both
+        // arrivals above
+      }
+      if (alive) {
+        wait(&sm.pvdone, (tiles - 1) & 1);
+        if (hf) sm.lsum[r] = l;
+        alive = tq::named_sync_and(1 + wl, 64, ok);
+      }
+      ok = ok && alive;
+      if (ok) {
+        tc_after();
+        if (!hf) l += sm.lsum[r];
+        float* rec = r < rows
+            ? a.rec + ((long long)rec_split * a.B * a.Hq + qrow_of(r)) * kRecFloats : nullptr;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float o[32];
+          tq::tmem_ld_32x32b_x32(lane_base + kOCol + 64 * hf + 32 * c, reinterpret_cast<uint32_t*>(o));
+          tq::tmem_wait_ld();
+          if (rec) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(rec + 64 * hf + 32 * c + 4 * i) =
+                  make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+        if (rec && !hf) {
+          rec[128] = m;
+          rec[129] = l;
+        }
+      }
+    }
+  } else if (warp < 16) {
+    // ================================================================ expanders
+    const int e = tid - kExpThreads, tt = e & 127, half = e >> 7;
+    auto get = [&](int t, Codes<IB, VB>& c) {
+      long long token;
+      bool there;
+      if (list) {
+        const int at = 2 * (t0 + t) + (tt >> 6);
+        const int blk = at < a.max_blocks ? __ldg(list + at) : -1;
+        there = blk >= 0 && blk < nblk;
+        token = (long long)blk * 64 + (tt & 63);
+      } else {
+        token = (long long)(t0 + t) * kTile + tt;
+        there = true;
+      }
+      there = there && token < len;
+      fetch<IB, VB>(side, a.Hkv, b, h, token, there, half, c);
+    };
+    unsigned char* at_row = nullptr;
+    const int row_off = (tt >> 3) * 128 + (tt & 7) * 16;
+    Codes<IB, VB> next;
+    get(0, next);
+    for (int t = 0; t < tiles; ++t) {
+      const Codes<IB, VB> c = next;
+      if (t + 1 < tiles) get(t + 1, next);
+      const int st = t & 1, fs = t % kFacSlots;
+      if (t >= 2 && !wait(&sm.kempty[st], ((t >> 1) - 1) & 1)) break;
+      if (half == 0) {
+        const bool some = c.vn >= kTiny;
+        sm.fac[fs][0][tt] = c.ok ? c.xn : 0.f;
+        sm.fac[fs][1][tt] = !c.ok ? -INFINITY : some ? log2f(c.vn) : c.vn < kTiny ? -60.f : c.vn;
+        sm.fac[fs][2][tt] = !c.ok ? 0.f : some ? 1.f / c.vn : 1.152921504606847e18f;   // 2^60
+      }
+      at_row = sm.k[st] + row_off;
+      expand_key<IB, VB>(a, c, half, at_row);
+      tq::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sm.ffull[fs]);
+        mbar_arrive(&sm.kfull[st]);
+      }
+      if (t >= 2 && !wait(&sm.vempty[st], ((t >> 1) - 1) & 1)) break;
+      at_row = sm.v[st] + row_off;
+      expand_value<IB, VB>(a, c, half, at_row);
+      tq::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.vfull[st]);
+    }
+  } else {
+    // ================================================================ MMA issuer
+    constexpr uint32_t kIdescS = tq::idesc_f16(128, 128);
+    constexpr uint32_t kIdescO = kIdescS | (1u << 16);   // B (values) is N-major
+    auto weigh = [&](int t) {   // O += W(t)·V(t)
+      const int st = t & 1;
+      if (!wait(&sm.vfull[st], (t >> 1) & 1) || !wait(&sm.pfull[st], (t >> 1) & 1)) return;
+      tc_after();
+      if (lane == 0) {
+        const uint32_t v = s32(sm.v[st]);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          tq::mma_ts(tmem + kOCol, tmem + kDCol + 128 * st + 8 * ks,
+                     tq::smem_desc(v + ks * 256, 128, kLBO), kIdescO, t > 0 || ks > 0);
+        tq::mma_commit(&sm.vempty[st]);
+        tq::mma_commit(&sm.pvdone);
+      }
+      __syncwarp();
+    };
+    wait(&sm.qfull, 0);
+    for (int t = 0; t < tiles && ok; ++t) {
+      const int st = t & 1;
+      if (!wait(&sm.kfull[st], (t >> 1) & 1)) break;
+      tc_after();
+      if (lane == 0) {
+        const uint32_t k = s32(sm.k[st]);
+#pragma unroll
+        for (int ks = 0; ks < 16; ++ks)
+          tq::mma_ts(tmem + kDCol + 128 * st, tmem + kQCol + 8 * ks,
+                     tq::smem_desc(k + ks * 2 * kLBO, kLBO, 128), kIdescS, ks > 0);
+        tq::mma_commit(&sm.sfull[st]);
+        tq::mma_commit(&sm.kempty[st]);
+      }
+      __syncwarp();
+      if (t > 0) weigh(t - 1);
+    }
+    if (ok) weigh(tiles - 1);
+    // whatever was issued has ended before the tensor memory is given back
+    if (lane == 0) tq::mma_commit(&sm.drain);
+    __syncwarp();
+    if (!tq::mbar_wait(&sm.drain, 0)) ok = false;
+  }
+  if (!ok && lane == 0) atomicOr(&g_tq_flags, TQ_FLAG_TIMEOUT);
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == 16) tq::tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- row operands
+// y = Π q and z = S q of kRows query rows per CTA, in the operand's order, scaled by a power of
+// two of the row so that fp16 holds them.  1024 threads: 256 outputs × 4 quarters of k.
+constexpr int kPrepThreads = 1024;
+template <int kRows>
+__global__ void __launch_bounds__(kPrepThreads)
+rows_prep_kernel(const void* q, int q_dtype, int nrows, const float* __restrict__ piT,
+                 const float* __restrict__ sT, float factor, __half* qop, float* qf) {
+  __shared__ float qs[kRows][TQ_D];
+  __shared__ float part[4][kRows][256];
+  __shared__ float scale[kRows];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, row0 = blockIdx.x * kRows;
+  const int p = tid & 255, kq = tid >> 8;
+  // position p < 128: y at plane_coord(p); else z at sign_coord(p − 128)
+  const float* mat = (p < 128 ? piT + plane_coord(p) : sT + sign_coord(p - 128)) + 32 * kq * TQ_D;
+  float w[32];
+#pragma unroll
+  for (int k = 0; k < 32; ++k) w[k] = __ldg(mat + k * TQ_D);
+  for (int i = tid; i < kRows * TQ_D; i += kPrepThreads) {
+    const int r = i / TQ_D;
+    qs[r][i % TQ_D] = row0 + r < nrows ? load_elem(q, q_dtype, (long long)row0 * TQ_D + i) : 0.f;
+  }
+  __syncthreads();
+  if (tid < 32 * kRows) {
+    const int r = tid >> 5, lane = tid & 31;
+    float m = 0.f;
+    for (int j = lane; j < TQ_D; j += 32) m = fmaxf(m, fabsf(qs[r][j]));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) {
+      // ‖q‖ ≤ √128·max|q_j| < 2^(e + 4) with max|q_j| < 2^e
+      int e = 0;
+      if (m > 0.f && m < INFINITY) frexpf(m, &e);
+      e = min(max(e + 4, -110), 120);
+      scale[r] = ldexpf(1.f, -e);
+      if (row0 + r < nrows) qf[row0 + r] = ldexpf(factor, e);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(&qs[r][32 * kq + k]);
+      s = fmaf(w[k], x.x, s);
+      s = fmaf(w[k + 1], x.y, s);
+      s = fmaf(w[k + 2], x.z, s);
+      s = fmaf(w[k + 3], x.w, s);
+    }
+    part[kq][r][p] = s;
+  }
+  __syncthreads();
+  for (int i = tid; i < kRows * 256; i += kPrepThreads) {
+    const int r = i >> 8, c = i & 255;
+    if (row0 + r >= nrows) continue;
+    const float s = (part[0][r][c] + part[1][r][c]) + (part[2][r][c] + part[3][r][c]);
+    qop[(long long)(row0 + r) * 256 + c] =
+        __float2half_rn(s * scale[r] * (c < 128 ? kAlpha : kBeta));
+  }
+}
+
+// ---------------------------------------------------------------- merge
+// Rows' records added up with their log-sum-exp weights, then out = Πᵀ·acc / l.  kRows rows per
+// CTA share the reads of Π; 512 threads: 128 columns × 4 quarters (of the records, then of k).
+constexpr int kMergeThreads = 512;
+template <int kRows>
+__global__ void __launch_bounds__(kMergeThreads)
+rows_merge_kernel(const float* rec, int nrec, int nrows, const float* __restrict__ pi, int nibbles,
+                  float unscale, void* out, int out_dtype) {
+  __shared__ float acc[4][kRows][TQ_D];
+  __shared__ float sum[kRows][TQ_D];
+  __shared__ float ref[kRows], total[kRows];
+  const int tid = threadIdx.x, j = tid & 127, kq = tid >> 7, row0 = blockIdx.x * kRows;
+  float w[32];   // Π does not depend on the launch before
+#pragma unroll
+  for (int k = 0; k < 32; ++k) w[k] = __ldg(pi + (32 * kq + k) * TQ_D + j);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long stride = (long long)nrows * kRecFloats;
+  if (tid < 32 * kRows) {
+    const int r = tid >> 5, lane = tid & 31;
+    if (row0 + r < nrows) {
+      const float* p = rec + (long long)(row0 + r) * kRecFloats + 128;
+      float m = -INFINITY;
+      for (int s = lane; s < nrec; s += 32)
+        if (p[s * stride + 1] != 0.f) m = fmaxf(m, p[s * stride]);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      float l = 0.f;
+      for (int s = lane; s < nrec; s += 32) {
+        const float ls = p[s * stride + 1];
+        if (ls != 0.f) l += ls * ex2(p[s * stride] - m);
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (lane == 0) {
+        ref[r] = m;
+        total[r] = l;
+      }
+    }
+  }
+  __syncthreads();
+  // the position that column j is read at (the value operand's order)
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    float s = 0.f;
+    if (row0 + r < nrows) {
+      const float* p = rec + (long long)(row0 + r) * kRecFloats;
+      for (int i = kq; i < nrec; i += 4) {
+        const float ls = p[i * stride + 129];
+        if (ls != 0.f) s = fmaf(p[i * stride + j], ex2(p[i * stride + 128] - ref[r]), s);
+      }
+    }
+    acc[kq][r][j] = s;
+  }
+  __syncthreads();
+  for (int i = tid; i < kRows * TQ_D; i += kMergeThreads) {
+    const int r = i >> 7, c = i & 127;
+    sum[r][nibbles ? c : plane_coord(c)] =
+        (acc[0][r][c] + acc[1][r][c]) + (acc[2][r][c] + acc[3][r][c]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(&sum[r][32 * kq + k]);
+      s = fmaf(w[k], x.x, s);
+      s = fmaf(w[k + 1], x.y, s);
+      s = fmaf(w[k + 2], x.z, s);
+      s = fmaf(w[k + 3], x.w, s);
+    }
+    acc[kq][r][j] = s;
+  }
+  __syncthreads();
+  for (int i = tid; i < kRows * TQ_D; i += kMergeThreads) {
+    const int r = i >> 7, c = i & 127;
+    if (row0 + r >= nrows) continue;
+    const float l = total[r];
+    const float s = (acc[0][r][c] + acc[1][r][c]) + (acc[2][r][c] + acc[3][r][c]);
+    const float o = l == 0.f ? 0.f : s * unscale / l;
+    const long long at = (long long)(row0 + r) * TQ_D + c;
+    if (out_dtype == TQ_BF16) static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(o);
+    else static_cast<__half*>(out)[at] = __float2half_rn(o);
+  }
+}
+
+// ---------------------------------------------------------------- host
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+struct Plan {
+  int G, rows, row_tiles, pre_splits, own_splits;
+  size_t qf_off, rec_off, bytes;
+};
+
+// Splits that make the estimated time least: an item costs its tiles and about kFixed tiles of
+// start and end; items that fit one wave take as long as the longest, more of them as long as
+// an even share of the SMs and half an item.
+constexpr int kFixed = 4;
+tq_status make_plan(const tq_attn_desc* d, long long pre_tiles, long long own_tiles, Plan* p) {
+  if (!d) return TQ_ERR_INVALID_ARG;
+  if (d->head_dim != TQ_HEAD_DIM) return TQ_ERR_UNSUPPORTED;
+  if (d->batch < 0 || d->q_heads <= 0 || d->kv_heads <= 0) return TQ_ERR_INVALID_ARG;
+  if (d->q_heads % d->kv_heads) return TQ_ERR_INVALID_ARG;
+  if (d->q_heads / d->kv_heads > TQ_MAX_GROUP) return TQ_ERR_UNSUPPORTED;
+  if (d->capacity <= 0 || d->capacity % TQ_CAPACITY_ALIGN) return TQ_ERR_INVALID_ARG;
+  if (d->max_seq_len < 0 || d->max_seq_len > d->capacity) return TQ_ERR_INVALID_ARG;
+  if (d->tail_capacity != 0) return TQ_ERR_INVALID_ARG;
+  if (d->q_dtype != TQ_F32 && d->q_dtype != TQ_F16 && d->q_dtype != TQ_BF16) return TQ_ERR_UNSUPPORTED;
+  if (d->out_dtype != TQ_F16 && d->out_dtype != TQ_BF16) return TQ_ERR_UNSUPPORTED;
+  if ((long long)d->batch * d->q_heads > (1 << 24)) return TQ_ERR_UNSUPPORTED;
+  p->G = d->q_heads / d->kv_heads;
+  p->rows = d->batch * d->q_heads;
+  p->row_tiles = (int)(((long long)d->batch * p->G + kTile - 1) / kTile);
+  const int n = tq_num_sms();
+  const long long sms = n > 0 ? n : 152;
+  const long long pu = (long long)p->row_tiles * d->kv_heads, ou = (long long)d->batch * d->kv_heads;
+  double best = 0;
+  p->pre_splits = p->own_splits = 1;
+  bool first = true;
+  const long long longest = std::max<long long>(std::max(pre_tiles, own_tiles), 1);
+  for (long long L = 1;; L += std::max<long long>(1, L / 8)) {
+    L = std::min(L, longest);
+    const long long sp = std::max<long long>((pre_tiles + L - 1) / L, pre_tiles > 0 ? 1 : 0);
+    const long long so = std::max<long long>((own_tiles + L - 1) / L, 1);
+    if (sp + so <= 512 || L == longest) {
+      const long long items = pu * sp + ou * so;
+      const double lp = sp ? (double)((pre_tiles + sp - 1) / sp) : 0, lo = (double)((own_tiles + so - 1) / so);
+      const double most = std::max(lp, lo) + kFixed;
+      const double work = (double)pu * pre_tiles + (double)ou * own_tiles + (double)items * kFixed;
+      const double est = items <= sms ? most : std::max(most, work / sms + 0.5 * most);
+      if (first || est < best) {
+        best = est;
+        first = false;
+        p->pre_splits = (int)sp;
+        p->own_splits = (int)so;
+      }
+    }
+    if (L >= longest) break;
+  }
+  if (pu * p->pre_splits + ou * p->own_splits > 0x7fffffffLL) return TQ_ERR_UNSUPPORTED;
+  p->qf_off = (size_t)p->rows * 512;
+  p->rec_off = (p->qf_off + (size_t)p->rows * sizeof(float) + 255) / 256 * 256;
+  p->bytes = p->rec_off + (size_t)(p->pre_splits + p->own_splits) * p->rows * kRecFloats * sizeof(float);
+  return TQ_OK;
+}
+
+LevelBytes level_bytes(const tq_codec* c) {
+  LevelBytes t{};
+  for (int i = 0; i < 16; ++i) {
+    const __half h = __float2half_rn(i < c->levels ? c->lut_scale * c->centroids[i] : 0.f);
+    const uint16_t u = __half_raw(h).x;
+    t.lo[i / 4] |= (uint32_t)(u & 255u) << (8 * (i % 4));
+    t.hi[i / 4] |= (uint32_t)(u >> 8) << (8 * (i % 4));
+  }
+  return t;
+}
+
+tq_status cache_side(const tq_prod_cache& k, const tq_mse_cache& v, int capacity, CacheSide* s) {
+  if (!k.idx || !k.sgn || !k.xnorm || !k.rnorm || !v.idx || !v.xnorm) return TQ_ERR_INVALID_ARG;
+  if (!aligned16(k.idx) || !aligned16(k.sgn) || !aligned16(k.xnorm) || !aligned16(k.rnorm) ||
+      !aligned16(v.idx) || !aligned16(v.xnorm))
+    return TQ_ERR_INVALID_ARG;
+  s->kidx = k.idx; s->ksgn = k.sgn; s->kxn = k.xnorm; s->krn = k.rnorm;
+  s->vidx = v.idx; s->vxn = v.xnorm;
+  s->cap = capacity;
+  tq_status st = tq_rowmap_of(k.pages, capacity, &s->kmap);
+  if (st != TQ_OK) return st;
+  return tq_rowmap_of(v.pages, capacity, &s->vmap);
+}
+
+cudaLaunchConfig_t config(unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
+                          cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(block);
+  c.dynamicSmemBytes = smem;
+  c.stream = stream;
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = attr;
+  c.numAttrs = 1;
+  return c;
+}
+
+template <int IB, int VB>
+tq_status launch_attn(const RowsArgs& a, unsigned items, cudaStream_t stream) {
+  constexpr int smem = (int)sizeof(Smem) + 1024;
+  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+  static bool configured[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return TQ_ERR_CUDA;
+  if (!configured[dev]) {
+    if (cudaFuncSetAttribute(rows_attn_kernel<IB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem) != cudaSuccess)
+      return TQ_ERR_CUDA;
+    configured[dev] = true;
+  }
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = config(items, kThreads, smem, stream, attr);
+  return tq_cuda_status(cudaLaunchKernelEx(&cfg, rows_attn_kernel<IB, VB>, a));
+}
+
+template <int IB>
+tq_status launch_k(const RowsArgs& a, int vbits, unsigned items, cudaStream_t stream) {
+  switch (vbits) {
+    case 1: return launch_attn<IB, 1>(a, items, stream);
+    case 2: return launch_attn<IB, 2>(a, items, stream);
+    case 3: return launch_attn<IB, 3>(a, items, stream);
+    case 4: return launch_attn<IB, 4>(a, items, stream);
+  }
+  return TQ_ERR_UNSUPPORTED;
+}
+
+// Rows per CTA of the two kernels around: the fewest (1, 2, 4, 8) that keep about one CTA per SM.
+int rows_per_cta(int rows) {
+  const int sms = std::max(tq_num_sms(), 1);
+  for (int r = 1; r < 8; r *= 2)
+    if ((rows + r - 1) / r <= sms) return r;
+  return 8;
+}
+
+tq_status launch_prep(const void* q, int q_dtype, int rows, const tq_codec* kc, float factor,
+                      void* qop, float* qf, cudaStream_t stream) {
+  const int rp = rows_per_cta(rows);
+  auto kern = rp == 1 ? rows_prep_kernel<1> : rp == 2 ? rows_prep_kernel<2>
+            : rp == 4 ? rows_prep_kernel<4> : rows_prep_kernel<8>;
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = config((rows + rp - 1) / rp, kPrepThreads, 0, stream, attr);
+  return tq_cuda_status(cudaLaunchKernelEx(&cfg, kern, q, q_dtype, rows, (const float*)kc->d_piT,
+                                           (const float*)kc->d_sT, factor,
+                                           static_cast<__half*>(qop), qf));
+}
+
+tq_status launch_merge(const float* rec, int nrec, int rows, const tq_codec* vc, void* out,
+                       int out_dtype, cudaStream_t stream) {
+  const int rp = rows_per_cta(rows);
+  auto kern = rp == 1 ? rows_merge_kernel<1> : rp == 2 ? rows_merge_kernel<2>
+            : rp == 4 ? rows_merge_kernel<4> : rows_merge_kernel<8>;
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = config((rows + rp - 1) / rp, kMergeThreads, 0, stream, attr);
+  return tq_cuda_status(cudaLaunchKernelEx(&cfg, kern, rec, nrec, rows, (const float*)vc->d_pi,
+                                           vc->ibits == 4 ? 1 : 0, 1.f / vc->lut_scale, out,
+                                           out_dtype));
+}
+
+tq_status run(const tq_attn_desc* d, const Plan& p, const tq_codec* kc, const tq_codec* vc,
+              const void* q, RowsArgs& a, void* out, void* workspace, size_t workspace_bytes,
+              tq_stream_t stream_) {
+  tq_status st;
+  if ((st = tq_check_codec(kc, TQ_PROD)) != TQ_OK) return st;
+  if ((st = tq_check_codec(vc, TQ_MSE)) != TQ_OK) return st;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return TQ_ERR_CUDA;
+  if (kc->device != dev || vc->device != dev) return TQ_ERR_INVALID_ARG;
+  if (!q || !a.seq_lens || !out || !workspace) return TQ_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < p.bytes)
+    return TQ_ERR_INVALID_ARG;
+  if (d->batch == 0) return TQ_OK;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  char* ws = static_cast<char*>(workspace);
+  const float scale = d->softmax_scale > 0.f ? d->softmax_scale : 1.0f / sqrtf((float)TQ_D);
+  a.B = d->batch; a.Hq = d->q_heads; a.Hkv = d->kv_heads; a.G = p.G;
+  a.max_len = d->max_seq_len;
+  a.row_tiles = p.row_tiles; a.pre_splits = p.pre_splits; a.own_splits = p.own_splits;
+  a.kt = level_bytes(kc);
+  a.vt = level_bytes(vc);
+  a.rho_scale = kAlpha / kBeta * kc->lut_scale * kQjl;
+  a.qop = reinterpret_cast<const uint4*>(ws);
+  a.qf = reinterpret_cast<const float*>(ws + p.qf_off);
+  a.rec = reinterpret_cast<float*>(ws + p.rec_off);
+  const float factor = scale * 1.4426950408889634f / (kAlpha * kc->lut_scale);
+  st = launch_prep(q, d->q_dtype, p.rows, kc, factor, ws, reinterpret_cast<float*>(ws + p.qf_off),
+                   stream);
+  if (st != TQ_OK) return st;
+  const unsigned items = (unsigned)((long long)p.pre_splits * a.Hkv * p.row_tiles +
+                                    (long long)p.own_splits * a.Hkv * a.B);
+  switch (kc->ibits) {
+    case 1: st = launch_k<1>(a, vc->ibits, items, stream); break;
+    case 2: st = launch_k<2>(a, vc->ibits, items, stream); break;
+    case 3: st = launch_k<3>(a, vc->ibits, items, stream); break;
+    case 4: st = launch_k<4>(a, vc->ibits, items, stream); break;
+    default: st = TQ_ERR_UNSUPPORTED;
+  }
+  if (st != TQ_OK) return st;
+  return launch_merge(a.rec, p.pre_splits + p.own_splits, p.rows, vc, out, d->out_dtype, stream);
+}
+
+long long tiles_of(long long tokens) { return (tokens + kTile - 1) / kTile; }
+
+tq_status plan_sparse(const tq_attn_desc* d, int max_blocks, Plan* p) {
+  if (max_blocks <= 0 || max_blocks > (1 << 24)) return TQ_ERR_INVALID_ARG;
+  return make_plan(d, 0, (max_blocks + 1) / 2, p);
+}
+
+tq_status plan_prefix(const tq_attn_desc* d, int prefix_max_len, Plan* p) {
+  if (!d || prefix_max_len < 0) return TQ_ERR_INVALID_ARG;
+  return make_plan(d, tiles_of(prefix_max_len), tiles_of(d->max_seq_len), p);
+}
+
+}  // namespace
+
+extern "C" size_t tq_sparse_workspace_bytes(const tq_attn_desc* desc, int32_t max_blocks) {
+  Plan p;
+  return plan_sparse(desc, max_blocks, &p) == TQ_OK ? p.bytes : 0;
+}
+
+extern "C" tq_status tq_sparse_attention(const tq_attn_desc* desc, const tq_codec* kc,
+                                         const tq_codec* vc, const void* q, tq_prod_cache k,
+                                         tq_mse_cache v, const int32_t* seq_lens,
+                                         const int32_t* blocks, int32_t max_blocks, void* out,
+                                         void* workspace, size_t workspace_bytes,
+                                         tq_stream_t stream) {
+  Plan p;
+  tq_status st = plan_sparse(desc, max_blocks, &p);
+  if (st != TQ_OK) return st;
+  RowsArgs a{};
+  if (!blocks) return TQ_ERR_INVALID_ARG;
+  if ((st = cache_side(k, v, desc->capacity, &a.own)) != TQ_OK) return st;
+  a.seq_lens = seq_lens;
+  a.list = blocks;
+  a.max_blocks = max_blocks;
+  return run(desc, p, kc, vc, q, a, out, workspace, workspace_bytes, stream);
+}
+
+extern "C" size_t tq_prefix_workspace_bytes(const tq_attn_desc* desc, int32_t prefix_max_len) {
+  Plan p;
+  return plan_prefix(desc, prefix_max_len, &p) == TQ_OK ? p.bytes : 0;
+}
+
+extern "C" tq_status tq_prefix_attention(const tq_attn_desc* desc, const tq_codec* kc,
+                                         const tq_codec* vc, const void* q,
+                                         tq_prod_cache prefix_k, tq_mse_cache prefix_v,
+                                         int32_t prefix_capacity, int32_t prefix_max_len,
+                                         const int32_t* prefix_len, tq_prod_cache k,
+                                         tq_mse_cache v, const int32_t* seq_lens, void* out,
+                                         void* workspace, size_t workspace_bytes,
+                                         tq_stream_t stream) {
+  Plan p;
+  tq_status st = plan_prefix(desc, prefix_max_len, &p);
+  if (st != TQ_OK) return st;
+  if (prefix_capacity <= 0 || prefix_capacity % TQ_CAPACITY_ALIGN || prefix_max_len > prefix_capacity)
+    return TQ_ERR_INVALID_ARG;
+  RowsArgs a{};
+  if (!prefix_len) return TQ_ERR_INVALID_ARG;
+  if ((st = cache_side(prefix_k, prefix_v, prefix_capacity, &a.pre)) != TQ_OK) return st;
+  if ((st = cache_side(k, v, desc->capacity, &a.own)) != TQ_OK) return st;
+  a.seq_lens = seq_lens;
+  a.pre_len = prefix_len;
+  a.max_pre = prefix_max_len;
+  return run(desc, p, kc, vc, q, a, out, workspace, workspace_bytes, stream);
+}

@@ -95,6 +95,8 @@ unsigned int tq_take_flags_quantize_tc();
 unsigned int tq_take_flags_decode_tc();
 unsigned int tq_take_flags_decode_asym();
 unsigned int tq_take_flags_store();
+unsigned int tq_take_flags_rows();
+unsigned int tq_take_flags_blocks();
 
 static inline tq_status tq_cuda_status(cudaError_t e) {
   return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;

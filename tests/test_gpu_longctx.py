@@ -1,0 +1,454 @@
+"""Operators of long contexts (include/tq.h: tq_prefix_attention, tq_block_bounds,
+tq_block_select, tq_sparse_attention) against their definitions in 64 bits (longctx_ref.py)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import longctx_ref as ref
+from kv_cache_quantization_gb300 import _binding as B
+from kv_cache_quantization_gb300 import api
+
+pytestmark = pytest.mark.gpu
+
+D = 128
+_codecs = {}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    B.load()
+    yield
+    torch.cuda.synchronize()
+
+
+def codec(kind, bits):
+    if (kind, bits) not in _codecs:
+        _codecs[kind, bits] = api.Codec.prod(bits) if kind == "k" else api.Codec.mse(bits)
+    return _codecs[kind, bits]
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def flags():
+    return api.device_status()[1]
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def table(rows, per_row, page, seed, spare=3):
+    """A block table of rows × per_row pages in a shuffled order."""
+    n = rows * per_row + spare
+    t = np.random.default_rng(seed).permutation(n)[:rows * per_row].reshape(rows, per_row)
+    return api.Pages(i32(t), page, n)
+
+
+def caches(rows, heads, cap, kbits, vbits, seed, pages=None, used=None):
+    """Caches of random codes: every bit pattern, norms as Gaussian keys have them; norms of slots
+    at or past used[b] are NaN (they must not be read into anything)."""
+    g = gen(seed)
+    if pages is None:
+        k, v = api.ProdCache.empty(rows, heads, cap, kbits), api.MSECache.empty(rows, heads, cap, vbits)
+    else:
+        k, v = api.ProdCache.empty_paged(pages, heads, kbits), api.MSECache.empty_paged(pages, heads, vbits)
+    for t in (k.idx, k.sgn, v.idx):
+        t.copy_(torch.randint(0, 256, t.shape, generator=g, device="cuda", dtype=torch.uint8))
+    for t, low, high in ((k.xnorm, 6, 16), (k.rnorm, 2, 5), (v.xnorm, 6, 16)):
+        t.copy_(low + (high - low) * torch.rand(t.shape, generator=g, device="cuda"))
+    if used is not None:
+        for b, n in enumerate(used):
+            for t in (k.xnorm, k.rnorm, v.xnorm):
+                if pages is None:
+                    t[b, :, n:] = math.nan
+                else:
+                    pt = pages.page_tokens
+                    for i, p in enumerate(pages.block_table[b].tolist()):
+                        t[p, :, max(0, n - i * pt):] = math.nan
+    return k, v
+
+
+def queries(batch, heads, dtype, seed, size=1.0):
+    return (size * torch.randn(batch, heads, D, generator=gen(seed), device="cuda")).to(dtype)
+
+
+def parts(k, v, kc, vc, b, h, at):
+    return (*ref.key_parts(k, kc, b, h, at), *ref.value_parts(v, vc, b, h, at))
+
+
+def up64(n):
+    return max(-(-n // 64) * 64, 64)
+
+
+# ------------------------------------------------------------------ shared prefix
+
+def run_prefix(kbits, vbits, batch, kv, group, plen, lens, paged=0, q_dtype=torch.bfloat16,
+               out_dtype=torch.float16, seed=0, size=1.0, scale=None):
+    kc, vc = codec("k", kbits), codec("v", vbits)
+    pcap, cap = up64(plen), up64(max(lens))
+    pp = po = None
+    if paged:
+        pcap, cap = -(-pcap // paged) * paged, -(-cap // paged) * paged
+        pp, po = table(1, pcap // paged, paged, seed + 1), table(batch, cap // paged, paged, seed + 2)
+    pk, pv = caches(1, kv, pcap, kbits, vbits, seed + 3, pp, [plen])
+    k, v = caches(batch, kv, cap, kbits, vbits, seed + 4, po, lens)
+    q = queries(batch, kv * group, q_dtype, seed + 5, size)
+    plan = api.PrefixPlan(batch, kv * group, kv, cap, max(lens), pcap, plen, q_dtype, out_dtype, scale)
+    out = plan.run(kc, vc, q, pk, pv, i32([plen]), k, v, i32(lens), plan.new_out())
+    return kc, vc, q, (pk, pv), (k, v), plan, out
+
+
+def check_prefix(kc, vc, q, pre, mine, out, plen, lens, kv, group, scale=None):
+    worst = 0.0
+    for h in range(kv):
+        shared = parts(*pre, kc, vc, 0, h, torch.arange(plen, device="cuda"))
+        for b, n in enumerate(lens):
+            own = parts(*mine, kc, vc, b, h, torch.arange(n, device="cuda"))
+            rows = slice(h * group, (h + 1) * group)
+            r, err = ref.attend(q[b, rows], [torch.cat(p) for p in zip(shared, own)], kc, vc, scale)
+            worst = max(worst, ref.check_rows(out[b, rows], r, err, f"sequence {b}, KV head {h}"))
+    return worst
+
+
+@pytest.mark.parametrize("kbits,vbits", [(k, v) for k in (2, 3, 4, 5) for v in (1, 2, 3, 4)])
+def test_prefix_bit_widths(kbits, vbits):
+    lens = [5, 130]
+    a = run_prefix(kbits, vbits, 2, 1, 3, 200, lens, seed=10 * kbits + vbits)
+    check_prefix(*a[:5], a[6], 200, lens, 1, 3)
+    assert flags() == 0
+
+
+@pytest.mark.parametrize("batch,kv,group,plen,lens", [
+    (1, 1, 1, 1, [0]),
+    (1, 2, 8, 0, [1]),
+    (2, 1, 5, 0, [0, 64]),                                      # a row with no token at all
+    (3, 2, 7, 127, [127, 128, 129]),
+    (1, 4, 4, 129, [0]),
+    (19, 2, 7, 1000, [(37 * i) % 300 for i in range(19)]),      # 133 rows: two row tiles
+    (5, 1, 8, 20011, [1, 0, 700, 63, 65]),                      # many splits
+])
+@pytest.mark.parametrize("paged", [0, 64, 192])
+def test_prefix_shapes(batch, kv, group, plen, lens, paged):
+    a = run_prefix(3, 4, batch, kv, group, plen, lens, paged, seed=plen + paged)
+    check_prefix(*a[:5], a[6], plen, lens, kv, group)
+    assert flags() == 0
+
+
+@pytest.mark.parametrize("q_dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("out_dtype", [torch.float16, torch.bfloat16])
+def test_prefix_types(q_dtype, out_dtype):
+    lens = [9, 70]
+    a = run_prefix(4, 2, 2, 2, 4, 300, lens, 0, q_dtype, out_dtype, seed=7, scale=0.05)
+    check_prefix(*a[:5], a[6], 300, lens, 2, 4, 0.05)
+
+
+@pytest.mark.parametrize("size", [1e-12, 30.0, 1e15])
+def test_prefix_query_sizes(size):
+    """Queries of any size: the operand is scaled by a power of two of the row (tiny queries
+    attend evenly; large ones pick single tokens)."""
+    lens = [40]
+    scale = 1.0 / size
+    a = run_prefix(3, 2, 1, 1, 2, 300, lens, 0, torch.float32, seed=3, size=size, scale=scale)
+    check_prefix(*a[:5], a[6], 300, lens, 1, 2, scale)
+
+
+def test_prefix_value_norms():
+    """Value norms from 2^-50 to 2^16 side by side, zeros among them: the weights of the value
+    product are taken relative to score + log2 of the norm, so fp16 holds them."""
+    kc, vc = codec("k", 3), codec("v", 4)
+    k, v = caches(2, 1, 512, 3, 4, 1)
+    pk, pv = caches(1, 1, 512, 3, 4, 2)
+    e = torch.randint(-50, 17, v.xnorm.shape, generator=gen(3), device="cuda").float()
+    v.xnorm.copy_(torch.exp2(e) * (torch.rand(e.shape, generator=gen(4), device="cuda") > 0.2))
+    v.xnorm[1] = 0
+    pv.xnorm[:, :, :] = 0
+    q = queries(2, 4, torch.bfloat16, 5)
+    plan = api.PrefixPlan(2, 4, 1, 512, 512, 512, 512, out_dtype=torch.bfloat16)
+    lens = [500, 300]
+    out = plan.run(kc, vc, q, pk, pv, i32([400]), k, v, i32(lens), plan.new_out())
+    check_prefix(kc, vc, q, (pk, pv), (k, v), out, 400, lens, 1, 4)
+    assert not out[1].any()      # zero values only: exactly zero
+    assert flags() == 0
+
+
+def test_prefix_equals_decode_over_one_cache():
+    """Prefix and own tokens in one paged cache attended by tq_decode_attention (fp32 output, its
+    own kernel) give the rows that the prefix call gives."""
+    kc, vc = codec("k", 3), codec("v", 2)
+    kv, group, page = 2, 4, 64
+    plen, lens = 640, [64, 100, 1]
+    pp = table(1, 10, page, 1, spare=10)
+    free = [p for p in range(pp.num_pages) if p not in pp.block_table[0].tolist()]
+    own = i32(free[:6]).view(3, 2)
+    po = api.Pages(own, page, pp.num_pages)
+    both = api.Pages(torch.cat([pp.block_table.expand(3, -1), own], 1), page, pp.num_pages)
+    k, v = caches(None, kv, None, 3, 2, 4, pp)
+    q = queries(3, kv * group, torch.float16, 6)
+
+    def at(pages):
+        return (api.ProdCache(k.idx, k.sgn, k.xnorm, k.rnorm, pages), api.MSECache(v.idx, v.xnorm, 2, pages))
+
+    plan = api.PrefixPlan(3, kv * group, kv, 128, 100, 640, 640, torch.float16, torch.float16)
+    got = plan.run(kc, vc, q, *at(pp), i32([plen]), *at(po), i32(lens), plan.new_out())
+    dec = api.DecodePlan(3, kv * group, kv, 768, 768, torch.float16, torch.float32)
+    want = dec.run(kc, vc, q, *at(both), i32([plen + n for n in lens]), dec.new_out())
+    check_prefix(kc, vc, q, at(pp), at(po), got, plen, lens, kv, group)
+    # both are within 1e-3 of the definition (the decode's bound, and fp16's operands here)
+    off = (got.double() - want.double()).norm(dim=-1) / want.double().norm(dim=-1)
+    assert float(off.max()) < 4e-3
+
+
+def test_prefix_lengths_over_the_plan_are_clamped_and_flagged():
+    a = run_prefix(3, 2, 2, 1, 2, 256, [64, 64], seed=5)
+    kc, vc, q, pre, mine, plan, out = a
+    assert flags() == 0
+    again = plan.run(kc, vc, q, *pre, i32([300]), *mine, i32([64, 65]), plan.new_out())
+    assert flags() == B.TQ_FLAG_LEN_OVERFLOW
+    assert torch.equal(out, again)
+
+
+# ------------------------------------------------------------------ sparse attention
+
+def check_sparse(kc, vc, q, k, v, lists, lens, out, group):
+    for b, n in enumerate(lens):
+        for h in range(lists.shape[1]):
+            at = [np.arange(64 * i, min(64 * i + 64, n)) for i in lists[b, h].tolist()
+                  if 0 <= i and 64 * i < n]
+            at = torch.tensor(np.concatenate(at) if at else [], dtype=torch.long, device="cuda")
+            rows = slice(h * group, (h + 1) * group)
+            r, err = ref.attend(q[b, rows], parts(k, v, kc, vc, b, h, at), kc, vc)
+            ref.check_rows(out[b, rows], r, err, f"sequence {b}, KV head {h}")
+
+
+def lists_of(lens, kv, keep, seed):
+    """Random lists: any order, absent entries anywhere, out-of-range numbers, repeats."""
+    rng = np.random.default_rng(seed)
+    x = np.full((len(lens), kv, keep), -1)
+    for b, n in enumerate(lens):
+        nb = -(-n // 64)
+        for h in range(kv):
+            m = int(rng.integers(0, min(keep, nb) + 1))
+            x[b, h, rng.permutation(keep)[:m]] = rng.permutation(nb)[:m]
+            if keep > 3:
+                x[b, h, 1] = x[b, h, 0]
+                x[b, h, 2] = [nb, 1 << 30, -7][(b + h) % 3]
+    return i32(x)
+
+
+@pytest.mark.parametrize("batch,kv,group,lens,keep,paged,kbits,vbits", [
+    (1, 1, 1, [1], 1, 0, 3, 4),
+    (1, 1, 3, [100], 1, 0, 2, 1),
+    (2, 2, 8, [0, 4000], 5, 0, 3, 2),
+    (3, 4, 7, [129, 700, 5000], 16, 64, 4, 4),
+    (3, 4, 7, [129, 700, 5000], 17, 256, 5, 3),
+    (1, 8, 4, [70001], 300, 0, 3, 2),
+    (40, 2, 5, [61 * i for i in range(40)], 9, 128, 4, 1),
+])
+def test_sparse_attention(batch, kv, group, lens, keep, paged, kbits, vbits):
+    kc, vc = codec("k", kbits), codec("v", vbits)
+    cap = up64(max(lens))
+    pages = None
+    if paged:
+        cap = -(-cap // paged) * paged
+        pages = table(batch, cap // paged, paged, 9)
+    k, v = caches(batch, kv, cap, kbits, vbits, keep, pages, lens)
+    q = queries(batch, kv * group, torch.bfloat16, 1)
+    lst = lists_of(lens, kv, keep, 2)
+    plan = api.SparsePlan(batch, kv * group, kv, cap, max(lens), keep, 0, 0, out_dtype=torch.float16)
+    out = plan.run(kc, vc, q, k, v, i32(lens), lst, plan.new_out())
+    check_sparse(kc, vc, q, k, v, lst, lens, out, group)
+    assert flags() == 0
+
+
+def test_sparse_bad_page_is_skipped_and_flagged():
+    kc, vc = codec("k", 3), codec("v", 2)
+    pages = table(1, 4, 64, 1)
+    k, v = caches(1, 1, 256, 3, 2, 3, pages)
+    pages.block_table[0, 2] = pages.num_pages + 5
+    q = queries(1, 2, torch.bfloat16, 1)
+    plan = api.SparsePlan(1, 2, 1, 256, 256, 4, 0, 0, out_dtype=torch.float16)
+    lens = i32([256])
+    out = plan.run(kc, vc, q, k, v, lens, i32([[[0, 1, 3, -1]]]), plan.new_out())
+    assert flags() == 0      # an entry that no listed token needs is not read
+    got = plan.run(kc, vc, q, k, v, lens, i32([[[0, 1, 2, 3]]]), plan.new_out())
+    assert flags() == B.TQ_FLAG_PAGE
+    assert torch.allclose(got.float(), out.float(), rtol=4e-3, atol=4e-3)
+
+
+# ------------------------------------------------------------------ block bounds
+
+def special_(x, seed):
+    """NaN, infinities and zeros of both signs among the values."""
+    r = torch.rand(x.shape, generator=gen(seed), device="cuda")
+    for i, v in enumerate((math.nan, math.inf, -math.inf, 0.0, -0.0)):
+        x[(r > 0.01 * i) & (r < 0.01 * i + 0.01)] = v
+    return x
+
+
+def blank(batch, heads, cap, pages, seed):
+    b = api.BlockBounds.empty(batch, heads, cap) if pages is None else \
+        api.BlockBounds.empty_paged(pages, heads)
+    b.bounds.copy_(torch.randn(b.bounds.shape, generator=gen(seed), device="cuda"))
+    return b
+
+
+def flat_bounds(b):
+    if b.pages is None:
+        return b.bounds
+    return b.bounds[b.pages.block_table.long()].movedim(1, 2).flatten(2, 3)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("batch,heads,tokens,pos,count,paged", [
+    (1, 1, 1, None, None, 0),
+    (1, 2, 640, None, None, 0),
+    (2, 3, 300, None, [0, 300], 0),
+    (4, 2, 1, [0, 63, 64, 200], None, 64),
+    (3, 4, 130, [1, 63, 700], [130, 2, 65], 192),
+    (2, 1, 66, [62, 127], [66, 1], 0),
+])
+def test_block_bounds(dtype, batch, heads, tokens, pos, count, paged):
+    cap = up64(max(pos or [0]) + tokens)
+    pages = None
+    if paged:
+        cap = -(-cap // paged) * paged
+        pages = table(batch, cap // paged, paged, 5)
+    x = special_(3 * torch.randn(batch, heads, tokens, D, generator=gen(1), device="cuda"), 2).to(dtype)
+    blocks = blank(batch, heads, cap, pages, 3)
+    want = ref.bounds(x, pos or [0] * batch, count or [tokens] * batch, flat_bounds(blocks))
+    spare = blocks.bounds.clone()
+    api.block_bounds(x, blocks, None if pos is None else i32(pos), None if count is None else i32(count))
+    assert torch.equal(flat_bounds(blocks), want)
+    if pages is not None:      # pages outside the table are left alone
+        free = sorted(set(range(pages.num_pages)) - set(pages.block_table.flatten().tolist()))
+        assert torch.equal(blocks.bounds[free], spare[free])
+    assert flags() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_block_bounds_strides_and_alignment(dtype):
+    """Token-major inputs, views that start at an odd element, and rows at an odd stride."""
+    base = torch.randn(2 * 100 * 3 * 131 + 1, generator=gen(1), device="cuda").to(dtype)
+    x = base[1:].view(2, 100, 3, 131)[..., 2:130].transpose(1, 2)      # [2, 3, 100, 128]
+    for v in (x, torch.randn(2, 100, 3, D, generator=gen(2), device="cuda").to(dtype).transpose(1, 2),
+              x[:1].expand(2, -1, -1, -1)):                            # a broadcast batch
+        blocks = blank(2, 3, 128, None, 3)
+        want = ref.bounds(v, [20, 0], [100, 100], blocks.bounds)
+        api.block_bounds(v, blocks, i32([20, 0]))
+        assert torch.equal(blocks.bounds, want)
+
+
+def test_block_bounds_one_by_one_equal_a_prefill():
+    x = torch.randn(2, 2, 200, D, generator=gen(1), device="cuda").half()
+    a, b = blank(2, 2, 256, None, 2), blank(2, 2, 256, None, 2)
+    api.block_bounds(x, a)
+    at = i32([0, 0])
+    for t in range(200):
+        api.block_bounds(x[:, :, t:t + 1], b, pos=at)
+        at += 1
+    assert torch.equal(a.bounds, b.bounds)
+
+
+def test_block_bounds_past_the_capacity():
+    x = torch.randn(3, 1, 100, D, generator=gen(1), device="cuda").bfloat16()
+    blocks = blank(3, 1, 128, None, 2)
+    want = ref.bounds(x, [100, 0, 0], [28, 100, 0], blocks.bounds)
+    api.block_bounds(x, blocks, i32([100, 0, -5]), i32([100, 1000, 100]))
+    assert flags() == B.TQ_FLAG_POS_OVERFLOW
+    assert torch.equal(blocks.bounds, want)
+
+
+# ------------------------------------------------------------------ block selection
+
+def run_select(q, blocks, lens, keep, first, last, group, kv, cap, max_len=None):
+    plan = api.SparsePlan(len(lens), kv * group, kv, cap, max_len or max(max(lens), 1), keep, first,
+                          last, q_dtype=q.dtype)
+    out = plan.new_list()
+    out.fill_(12345)
+    return plan, plan.select(q, blocks, i32(lens), out)
+
+
+def check_select(q, blocks, lens, keep, first, last, group, kv, got):
+    flat = flat_bounds(blocks)
+    for b, n in enumerate(lens):
+        for h in range(kv):
+            want = ref.select(q[b, h * group:(h + 1) * group], flat[b, h], -(-n // 64), keep, first, last)
+            assert got[b, h].tolist() == want, (b, h)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("batch,kv,group,lens,keep,first,last,paged", [
+    (1, 1, 1, [64 * 7], 3, 0, 0, 0),
+    (1, 2, 7, [64 * 40 - 5], 7, 1, 2, 0),
+    (4, 2, 8, [0, 1, 640, 6400], 10, 3, 7, 64),      # all forced
+    (4, 3, 3, [63, 64, 65, 64 * 300 + 1], 100, 0, 1, 128),
+    (2, 1, 2, [64 * 5000, 64 * 131 + 2], 130, 2, 0, 0),
+    (1, 1, 5, [64 * 33], 32, 1, 0, 0),
+])
+def test_block_select(dtype, batch, kv, group, lens, keep, first, last, paged):
+    cap = up64(max(lens))
+    pages = None
+    if paged:
+        cap = -(-cap // paged) * paged
+        pages = table(batch, cap // paged, paged, 5)
+    blocks = blank(batch, kv, cap, pages, 1)
+    blocks.bounds[..., 1, :] += 2
+    q = queries(batch, kv * group, dtype, 2)
+    _, got = run_select(q, blocks, lens, keep, first, last, group, kv, cap)
+    check_select(q, blocks, lens, keep, first, last, group, kv, got)
+    assert flags() == 0
+
+
+def test_block_select_ties_and_near_ties():
+    """Scores that differ by less than 32 bits hold, and blocks that are the same: the order is
+    that of 64 bits, equal ones by the lower number."""
+    n = 700
+    blocks = blank(1, 2, 64 * n, None, 1)
+    blocks.bounds[:, :, :] = blocks.bounds[:, :, :1]                 # every block alike
+    blocks.bounds[0, 1, :, :, 0] = 256.0
+    blocks.bounds[0, 1, :, :, 1] = torch.linspace(0, 699, n, device="cuda")[torch.randperm(
+        n, generator=gen(3), device="cuda")][:, None].bfloat16()
+    q = queries(1, 4, torch.float32, 2)
+    q[0, 2:, 0] = 4096.0
+    q[0, 2:, 1] = 2.0 ** -22
+    _, got = run_select(q, blocks, [64 * n], 50, 2, 3, 2, 2, 64 * n)
+    check_select(q, blocks, [64 * n], 50, 2, 3, 2, 2, got)
+    assert got[0, 0].tolist() == list(range(47)) + [697, 698, 699]
+
+
+@pytest.mark.parametrize("kind", ["zero queries", "infinite bounds", "NaN", "tiny"])
+def test_block_select_odd_values(kind):
+    n = 300
+    blocks = blank(1, 1, 64 * n, None, 1)
+    q = queries(1, 3, torch.float32, 2)
+    if kind == "zero queries":
+        q.zero_()
+    elif kind == "infinite bounds":
+        blocks.bounds[0, 0, 100:150, 1, 5] = math.inf
+        blocks.bounds[0, 0, 120:180, 0, 9] = -math.inf
+    elif kind == "NaN":
+        blocks.bounds[0, 0, 10:60, 1] = math.nan
+        blocks.bounds[0, 0, 10:60, 0] = math.nan
+        q[0, 1, 3] = math.nan
+    else:
+        q *= 1e-30
+        blocks.bounds *= 1e-8
+    _, got = run_select(q, blocks, [64 * n], 64, 1, 1, 3, 1, 64 * n)
+    check_select(q, blocks, [64 * n], 64, 1, 1, 3, 1, got)
+
+
+def test_block_select_length_over_the_plan():
+    blocks = blank(2, 1, 64 * 40, None, 1)
+    q = queries(2, 2, torch.bfloat16, 2)
+    plan, got = run_select(q, blocks, [64 * 30, 64 * 30], 8, 0, 1, 2, 1, 64 * 40)
+    assert flags() == 0
+    more = plan.select(q, blocks, i32([64 * 30, 64 * 31]), plan.new_list())
+    assert flags() == B.TQ_FLAG_LEN_OVERFLOW
+    assert torch.equal(got, more)
