@@ -45,7 +45,10 @@ using tq::tc_before;
 
 constexpr int kTile = 128;              // tokens per tile, and query rows per item
 constexpr int kExpThreads = 256;        // 8 softmax warps, 8 expander warps, 1 issuer warp
-constexpr int kThreads = 544;
+constexpr int kThreads = 640;           // (five warpgroups: the last holds the issuer warp alone)
+// Registers per thread: 96 at launch (61,440 of the block); the issuer's warpgroup gives up what
+// the softmax warps take: 128·24 + 256·96 + 256·128 = 60,416.
+constexpr int kRegsLaunch = 96, kRegsIssue = 24, kRegsSoftmax = 128;
 constexpr int kRecFloats = 132;         // acc[128], m, l, padding
 constexpr int kLBO = 2048;              // bytes between 8-position chunks of an operand image
 constexpr int kKBytes = 32 * kLBO;      // key operand: 128 tokens × 256 positions, fp16
@@ -70,7 +73,8 @@ struct CacheSide {
   const uint8_t* vidx;
   const float* vxn;
   tq_rowmap kmap, vmap;
-  int cap;
+  int kslots, vslots;       // slots of a row: the capacity (flat) or the page's
+  int same_map;             // keys and values lie alike
 };
 
 struct RowsArgs {
@@ -93,10 +97,10 @@ struct alignas(1024) Smem {
   unsigned char k[2][kKBytes];
   unsigned char v[2][kVBytes];
   float fac[kFacSlots][3][kTile];    // ‖x‖, log2‖v‖, 1/‖v‖ of a tile's tokens
-  float tmax[2][kTile];
+  float tmax[2][2][kTile];           // [tile parity][half of the tokens][row]
   float lsum[kTile];
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], ffull[kFacSlots];
-  uint64_t pvdone, qfull, drain;
+  uint64_t qfull, drain;
   uint32_t tmem;
   int tiles;
 };
@@ -117,6 +121,15 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
 constexpr __host__ __device__ uint32_t shr(uint32_t x, int n) { return n >= 0 ? x >> n : x << -n; }
 
@@ -170,15 +183,21 @@ struct Codes {
   bool ok;
 };
 
+// Row and slot of a token in a cache's arrays; 64-bit slot offsets follow from them.
+struct Place {
+  long long row;
+  int slot;
+};
+
 template <int IB, int VB>
-__device__ __forceinline__ void fetch(const CacheSide& c, int Hkv, int b, int h, long long token,
-                                      bool ok, int half, Codes<IB, VB>& o) {
-  long long krow = 0, vrow = 0;
-  int kslot = 0, vslot = 0;
+__device__ __forceinline__ void fetch(const CacheSide& c, int Hkv, int b, int h, int token, bool ok,
+                                      int half, Codes<IB, VB>& o) {
+  Place k{0, 0}, v{0, 0};
   if (ok) {
-    const bool kin = tq_map_slot(c.kmap, Hkv, b, h, (int)token, krow, kslot);
-    const bool vin = tq_map_slot(c.vmap, Hkv, b, h, (int)token, vrow, vslot);
-    if (!kin || !vin) {
+    bool in = tq_map_slot(c.kmap, Hkv, b, h, token, k.row, k.slot);
+    if (c.same_map) v = k;
+    else in &= tq_map_slot(c.vmap, Hkv, b, h, token, v.row, v.slot);
+    if (!in) {
       atomicOr(&g_tq_flags, TQ_FLAG_PAGE);
       ok = false;
     }
@@ -191,26 +210,27 @@ __device__ __forceinline__ void fetch(const CacheSide& c, int Hkv, int b, int h,
 #pragma unroll
   for (int p = 0; p < (VB == 4 ? 4 : VB); ++p) o.v[p] = make_uint2(0, 0);
   if (!ok) return;
-  const long long ks = tq_row_slots(c.kmap, c.cap), vs = tq_row_slots(c.vmap, c.cap);
+  const int ks = c.kslots, vs = c.vslots;
+  const uint8_t* kp = c.kidx + (k.row * IB * ks + k.slot) * 16 + 8 * half;
 #pragma unroll
-  for (int p = 0; p < IB; ++p)
-    o.k[p] = __ldg(reinterpret_cast<const uint2*>(c.kidx + ((krow * IB + p) * ks + kslot) * 16 + 8 * half));
-  o.s = __ldg(reinterpret_cast<const uint2*>(c.ksgn + (krow * ks + kslot) * 16 + 8 * half));
-  o.xn = __ldg(c.kxn + krow * ks + kslot);
-  o.rn = __ldg(c.krn + krow * ks + kslot);
-  if (VB == 4) {
-    const uint4* p = reinterpret_cast<const uint4*>(c.vidx + (vrow * vs + vslot) * 64 + 32 * half);
+  for (int p = 0; p < IB; ++p) o.k[p] = __ldg(reinterpret_cast<const uint2*>(kp + (long long)p * ks * 16));
+  const long long kt = k.row * ks + k.slot, vt = v.row * vs + v.slot;
+  o.s = __ldg(reinterpret_cast<const uint2*>(c.ksgn + kt * 16 + 8 * half));
+  o.xn = __ldg(c.kxn + kt);
+  o.rn = __ldg(c.krn + kt);
+  if constexpr (VB == 4) {
+    const uint4* p = reinterpret_cast<const uint4*>(c.vidx + vt * 64 + 32 * half);
     const uint4 x = __ldg(p), y = __ldg(p + 1);
     o.v[0] = make_uint2(x.x, x.y);
-    o.v[1 % (VB == 4 ? 4 : VB)] = make_uint2(x.z, x.w);
-    o.v[2 % (VB == 4 ? 4 : VB)] = make_uint2(y.x, y.y);
-    o.v[3 % (VB == 4 ? 4 : VB)] = make_uint2(y.z, y.w);
+    o.v[1] = make_uint2(x.z, x.w);
+    o.v[2] = make_uint2(y.x, y.y);
+    o.v[3] = make_uint2(y.z, y.w);
   } else {
+    const uint8_t* vp = c.vidx + (v.row * VB * vs + v.slot) * 16 + 8 * half;
 #pragma unroll
-    for (int p = 0; p < VB; ++p)
-      o.v[p] = __ldg(reinterpret_cast<const uint2*>(c.vidx + ((vrow * VB + p) * vs + vslot) * 16 + 8 * half));
+    for (int p = 0; p < VB; ++p) o.v[p] = __ldg(reinterpret_cast<const uint2*>(vp + (long long)p * vs * 16));
   }
-  o.vn = __ldg(c.vxn + vrow * vs + vslot);
+  o.vn = __ldg(c.vxn + vt);
 }
 
 // Key operand of half a token: level chunks 8·half.. and sign chunks 16 + 8·half...
@@ -274,6 +294,64 @@ __device__ __forceinline__ void expand_value(const RowsArgs& a, const Codes<IB, 
   }
 }
 
+// The tokens that an item attends.
+struct Item {
+  int t0, tiles, len, nblk, b, h;
+  const int* list;
+};
+
+// An expander thread's work: half a token of every tile.  False once a wait gave up.
+template <int IB, int VB, bool kList>
+__device__ __forceinline__ bool expand(const RowsArgs& a, const CacheSide& side, Smem& sm,
+                                       const Item& it) {
+  const int e = threadIdx.x - kExpThreads, tt = e & 127, half = e >> 7, lane = e & 31;
+  auto get = [&](int t, Codes<IB, VB>& c) {
+    int token;
+    bool there = true;
+    if (kList) {
+      const int at = 2 * (it.t0 + t) + (tt >> 6);
+      const int blk = at < a.max_blocks ? __ldg(it.list + at) : -1;
+      there = blk >= 0 && blk < it.nblk;
+      token = blk * 64 + (tt & 63);
+    } else {
+      token = (it.t0 + t) * kTile + tt;
+    }
+    fetch<IB, VB>(side, a.Hkv, it.b, it.h, token, there && token < it.len, half, c);
+  };
+  const int row_off = (tt >> 3) * 128 + (tt & 7) * 16;
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, unsigned parity) {
+    return ok = __all_sync(0xffffffffu, tq::mbar_wait(bar, parity));
+  };
+  Codes<IB, VB> next;
+  get(0, next);
+  for (int t = 0; t < it.tiles; ++t) {
+    const Codes<IB, VB> c = next;
+    if (t + 1 < it.tiles) get(t + 1, next);
+    const int st = t & 1, fs = t % kFacSlots;
+    if (t >= 2 && !wait(&sm.kempty[st], ((t >> 1) - 1) & 1)) break;
+    if (half == 0) {
+      const bool some = c.vn >= kTiny;
+      sm.fac[fs][0][tt] = c.ok ? c.xn : 0.f;
+      sm.fac[fs][1][tt] = !c.ok ? -INFINITY : some ? log2f(c.vn) : c.vn < kTiny ? -60.f : c.vn;
+      sm.fac[fs][2][tt] = !c.ok ? 0.f : some ? 1.f / c.vn : 1.152921504606847e18f;   // 2^60
+    }
+    expand_key<IB, VB>(a, c, half, sm.k[st] + row_off);
+    tq::fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&sm.ffull[fs]);
+      mbar_arrive(&sm.kfull[st]);
+    }
+    if (t >= 2 && !wait(&sm.vempty[st], ((t >> 1) - 1) & 1)) break;
+    expand_value<IB, VB>(a, c, half, sm.v[st] + row_off);
+    tq::fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.vfull[st]);
+  }
+  return ok;
+}
+
 // Valid length of a sequence: clamped to what the call was sized for, flagged if longer.
 __device__ __forceinline__ int clamp_len(int len, int most) {
   if (len > most) {
@@ -291,6 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+  static_assert(128 * kRegsIssue + 256 * (kRegsLaunch + kRegsSoftmax) <= kThreads * kRegsLaunch, "register split");
+
   // ---- the item: prefix items first (they are the long ones)
   int item = blockIdx.x;
   const int npre = a.pre_splits * a.Hkv * a.row_tiles;
@@ -306,22 +386,6 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
     b = item / a.Hkv % a.B;
     split = item / (a.Hkv * a.B);
   }
-  CacheSide side;   // field by field: a reference into either would put both in local memory
-  side.kidx = pre ? a.pre.kidx : a.own.kidx;
-  side.ksgn = pre ? a.pre.ksgn : a.own.ksgn;
-  side.kxn = pre ? a.pre.kxn : a.own.kxn;
-  side.krn = pre ? a.pre.krn : a.own.krn;
-  side.vidx = pre ? a.pre.vidx : a.own.vidx;
-  side.vxn = pre ? a.pre.vxn : a.own.vxn;
-  side.kmap.table = pre ? a.pre.kmap.table : a.own.kmap.table;
-  side.kmap.max_pages = pre ? a.pre.kmap.max_pages : a.own.kmap.max_pages;
-  side.kmap.page_tokens = pre ? a.pre.kmap.page_tokens : a.own.kmap.page_tokens;
-  side.kmap.num_pages = pre ? a.pre.kmap.num_pages : a.own.kmap.num_pages;
-  side.vmap.table = pre ? a.pre.vmap.table : a.own.vmap.table;
-  side.vmap.max_pages = pre ? a.pre.vmap.max_pages : a.own.vmap.max_pages;
-  side.vmap.page_tokens = pre ? a.pre.vmap.page_tokens : a.own.vmap.page_tokens;
-  side.vmap.num_pages = pre ? a.pre.vmap.num_pages : a.own.vmap.num_pages;
-  side.cap = pre ? a.pre.cap : a.own.cap;
   const int rows = pre ? min(kTile, a.B * a.G - rt * kTile) : a.G;
   const int len = pre ? clamp_len(*a.pre_len, a.max_pre) : clamp_len(a.seq_lens[b], a.max_len);
   const int splits = pre ? a.pre_splits : a.own_splits;
@@ -372,7 +436,6 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
       tq::mbar_init(&sm.pfull[i], 2 * active);
     }
     for (int i = 0; i < kFacSlots; ++i) tq::mbar_init(&sm.ffull[i], 8);
-    tq::mbar_init(&sm.pvdone, 1);
     tq::mbar_init(&sm.qfull, 2 * active);
     tq::mbar_init(&sm.drain, 1);
     tq::mbar_init_fence();
@@ -388,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
 
   if (warp < 8) {
     // ================================================================ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int wl = warp & 3, hf = warp >> 2;
     const int r = 32 * wl + lane;
     if (wl < active) {
@@ -395,22 +459,18 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
       const uint32_t lane_base = tmem + ((uint32_t)(32 * wl) << 16);
       float f = 0.f;
       {
-        uint32_t q[64];
-        if (r < rows) {
-          const long long qr = qrow_of(r);
-          const uint4* src = a.qop + qr * 32 + 16 * hf;
+        const long long qr = r < rows ? qrow_of(r) : 0;
+        if (r < rows) f = __ldg(a.qf + qr);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint4 x = __ldg(src + i);
+        for (int c = 0; c < 2; ++c) {
+          uint32_t q[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 x = r < rows ? __ldg(a.qop + qr * 32 + 16 * hf + 8 * c + i) : make_uint4(0, 0, 0, 0);
             q[4 * i] = x.x; q[4 * i + 1] = x.y; q[4 * i + 2] = x.z; q[4 * i + 3] = x.w;
           }
-          f = __ldg(a.qf + qr);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 64; ++i) q[i] = 0;
+          tq::tmem_st_32x32b_x32(lane_base + kQCol + 64 * hf + 32 * c, q);
         }
-        tq::tmem_st_32x32b_x32(lane_base + kQCol + 64 * hf, q);
-        tq::tmem_st_32x32b_x32(lane_base + kQCol + 64 * hf + 32, q + 32);
         tq::tmem_wait_st();
         tc_before();
         __syncwarp();
@@ -440,26 +500,28 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
           e[4 * i + 3] = fmaf(e[4 * i + 3] * f, xn.w, lv.w);
           mt = fmaxf(mt, fmaxf(fmaxf(e[4 * i], e[4 * i + 1]), fmaxf(e[4 * i + 2], e[4 * i + 3])));
         }
-        sm.tmax[hf][r] = mt;
+        sm.tmax[buf][hf][r] = mt;
         // both halves have read D: it may be overwritten by the weights.  A wait that gave up
         // ends both halves' loops here, together (neither then waits for the other)
         if (!(alive = tq::named_sync_and(1 + wl, 64, ok))) break;
-        mt = fmaxf(mt, sm.tmax[hf ^ 1][r]);
+        mt = fmaxf(mt, sm.tmax[buf][hf ^ 1][r]);
         const float m_new = mt > m + kGrow ? mt : m;
         if (t > 0 && __any_sync(0xffffffffu, m_new != m)) {
-          // O (this half of its columns) follows the reference
-          wait(&sm.pvdone, (t - 1) & 1);
+          // O (this half of its columns) follows the reference, once O += W(t − 1)·V(t − 1) is
+          // done (vempty).  Its barrier is that of every other tile: the phase before, tile
+          // t − 3's, ended before tile t was scored, so the parity says which tile is meant
+          wait(&sm.vempty[buf ^ 1], ((t - 1) >> 1) & 1);
           tc_after();
           const float corr = m == -INFINITY ? 0.f : ex2(m - m_new);
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float o[32];
-            const uint32_t at = lane_base + kOCol + 64 * hf + 32 * c;
-            tq::tmem_ld_32x32b_x32(at, reinterpret_cast<uint32_t*>(o));
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 16) {   // 16 columns at a time: e stays in registers
+            uint32_t o[16];
+            const uint32_t at = lane_base + kOCol + 64 * hf + c;
+            tmem_ld_x16(at, o);
             tq::tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= corr;
-            tq::tmem_st_32x32b_x32(at, reinterpret_cast<uint32_t*>(o));
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
+            tq::tmem_st_32x32b_x16(at, o);
           }
           l *= corr;
         }
@@ -484,11 +546,11 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
         tc_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.pfull[buf]);
-        // tmax is written again only after the partner's next wait on sfull, which needs both
-        // arrivals above
+        // tile t + 2 is scored after both halves have arrived here: until then this tile's tmax
+        // and factors may still be read (tile t + 1 may be scored already)
       }
       if (alive) {
-        wait(&sm.pvdone, (tiles - 1) & 1);
+        wait(&sm.vempty[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1);
         if (hf) sm.lsum[r] = l;
         alive = tq::named_sync_and(1 + wl, 64, ok);
       }
@@ -518,54 +580,14 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
     }
   } else if (warp < 16) {
     // ================================================================ expanders
-    const int e = tid - kExpThreads, tt = e & 127, half = e >> 7;
-    auto get = [&](int t, Codes<IB, VB>& c) {
-      long long token;
-      bool there;
-      if (list) {
-        const int at = 2 * (t0 + t) + (tt >> 6);
-        const int blk = at < a.max_blocks ? __ldg(list + at) : -1;
-        there = blk >= 0 && blk < nblk;
-        token = (long long)blk * 64 + (tt & 63);
-      } else {
-        token = (long long)(t0 + t) * kTile + tt;
-        there = true;
-      }
-      there = there && token < len;
-      fetch<IB, VB>(side, a.Hkv, b, h, token, there, half, c);
-    };
-    unsigned char* at_row = nullptr;
-    const int row_off = (tt >> 3) * 128 + (tt & 7) * 16;
-    Codes<IB, VB> next;
-    get(0, next);
-    for (int t = 0; t < tiles; ++t) {
-      const Codes<IB, VB> c = next;
-      if (t + 1 < tiles) get(t + 1, next);
-      const int st = t & 1, fs = t % kFacSlots;
-      if (t >= 2 && !wait(&sm.kempty[st], ((t >> 1) - 1) & 1)) break;
-      if (half == 0) {
-        const bool some = c.vn >= kTiny;
-        sm.fac[fs][0][tt] = c.ok ? c.xn : 0.f;
-        sm.fac[fs][1][tt] = !c.ok ? -INFINITY : some ? log2f(c.vn) : c.vn < kTiny ? -60.f : c.vn;
-        sm.fac[fs][2][tt] = !c.ok ? 0.f : some ? 1.f / c.vn : 1.152921504606847e18f;   // 2^60
-      }
-      at_row = sm.k[st] + row_off;
-      expand_key<IB, VB>(a, c, half, at_row);
-      tq::fence_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sm.ffull[fs]);
-        mbar_arrive(&sm.kfull[st]);
-      }
-      if (t >= 2 && !wait(&sm.vempty[st], ((t >> 1) - 1) & 1)) break;
-      at_row = sm.v[st] + row_off;
-      expand_value<IB, VB>(a, c, half, at_row);
-      tq::fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.vfull[st]);
-    }
+    const Item it{t0, tiles, len, nblk, b, h, list};
+    if (pre) ok = expand<IB, VB, false>(a, a.pre, sm, it);
+    else if (list) ok = expand<IB, VB, true>(a, a.own, sm, it);
+    else ok = expand<IB, VB, false>(a, a.own, sm, it);
   } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     // ================================================================ MMA issuer
+    if (warp == 16) {
     constexpr uint32_t kIdescS = tq::idesc_f16(128, 128);
     constexpr uint32_t kIdescO = kIdescS | (1u << 16);   // B (values) is N-major
     auto weigh = [&](int t) {   // O += W(t)·V(t)
@@ -579,7 +601,6 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
           tq::mma_ts(tmem + kOCol, tmem + kDCol + 128 * st + 8 * ks,
                      tq::smem_desc(v + ks * 256, 128, kLBO), kIdescO, t > 0 || ks > 0);
         tq::mma_commit(&sm.vempty[st]);
-        tq::mma_commit(&sm.pvdone);
       }
       __syncwarp();
     };
@@ -605,6 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
     if (lane == 0) tq::mma_commit(&sm.drain);
     __syncwarp();
     if (!tq::mbar_wait(&sm.drain, 0)) ok = false;
+    }
   }
   if (!ok && lane == 0) atomicOr(&g_tq_flags, TQ_FLAG_TIMEOUT);
   tc_before();
@@ -840,10 +862,14 @@ tq_status cache_side(const tq_prod_cache& k, const tq_mse_cache& v, int capacity
     return TQ_ERR_INVALID_ARG;
   s->kidx = k.idx; s->ksgn = k.sgn; s->kxn = k.xnorm; s->krn = k.rnorm;
   s->vidx = v.idx; s->vxn = v.xnorm;
-  s->cap = capacity;
   tq_status st = tq_rowmap_of(k.pages, capacity, &s->kmap);
+  if (st == TQ_OK) st = tq_rowmap_of(v.pages, capacity, &s->vmap);
   if (st != TQ_OK) return st;
-  return tq_rowmap_of(v.pages, capacity, &s->vmap);
+  s->kslots = tq_row_slots(s->kmap, capacity);
+  s->vslots = tq_row_slots(s->vmap, capacity);
+  s->same_map = s->kmap.table == s->vmap.table && s->kmap.max_pages == s->vmap.max_pages &&
+                s->kmap.page_tokens == s->vmap.page_tokens && s->kmap.num_pages == s->vmap.num_pages;
+  return TQ_OK;
 }
 
 cudaLaunchConfig_t config(unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
@@ -871,6 +897,10 @@ tq_status launch_attn(const RowsArgs& a, unsigned items, cudaStream_t stream) {
     if (cudaFuncSetAttribute(rows_attn_kernel<IB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smem) != cudaSuccess)
       return TQ_ERR_CUDA;
+    // the warpgroups' shares add up to what the block is launched with: more would wait forever
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, rows_attn_kernel<IB, VB>) != cudaSuccess) return TQ_ERR_CUDA;
+    if (fa.numRegs != kRegsLaunch) return TQ_ERR_UNSUPPORTED;
     configured[dev] = true;
   }
   cudaLaunchAttribute attr[1];
