@@ -12,9 +12,10 @@
 // them; the denominator is Σ w_t/‖v_t‖ in 32 bits.
 //
 // One CTA works on one item: up to 128 query rows × a run of 128-token tiles.
-//   8 expander warps  turn the codes of a tile into fp16 operands in shared memory (a byte
-//                     permute looks four levels up at a time; codes of the next tile are in
-//                     flight in registers meanwhile),
+//   12 expander warps turn the codes of a tile into fp16 operands in shared memory, four for
+//                     the key levels, four for the signs and norms, four for the value levels
+//                     (a byte permute looks four levels up at a time; codes of the next tile
+//                     are in flight in registers meanwhile),
 //   1 issuer warp     D = [y, z]·[c, ±ρ]ᵀ (128 × 128 × 256, rows in TMEM as the A operand) and
 //                     O += W·V (128 × 128 × 128, W in TMEM over the scores it came from),
 //   8 softmax warps   one thread per (row, half of the tile's tokens).
@@ -44,11 +45,12 @@ using tq::tc_after;
 using tq::tc_before;
 
 constexpr int kTile = 128;              // tokens per tile, and query rows per item
-constexpr int kExpThreads = 256;        // 8 softmax warps, 8 expander warps, 1 issuer warp
-constexpr int kThreads = 640;           // (five warpgroups: the last holds the issuer warp alone)
-// Registers per thread: 96 at launch (61,440 of the block); the issuer's warpgroup gives up what
-// the softmax warps take: 128·24 + 256·96 + 256·128 = 60,416.
-constexpr int kRegsLaunch = 96, kRegsIssue = 24, kRegsSoftmax = 128;
+// 8 softmax warps, 3 × 4 expander warps, and a warpgroup that holds the issuer warp alone
+constexpr int kKeyWarp = 8, kSignWarp = 12, kValueWarp = 16, kIssueWarp = 20;
+constexpr int kThreads = 768;
+// Registers per thread: 80 at launch (61,440 of the block); the softmax warps take what the
+// others give up: 256·104 + 384·72 + 128·56 = 61,440.
+constexpr int kRegsLaunch = 80, kRegsSoftmax = 104, kRegsExpand = 72, kRegsIssue = 56;
 constexpr int kRecFloats = 132;         // acc[128], m, l, padding
 constexpr int kLBO = 2048;              // bytes between 8-position chunks of an operand image
 constexpr int kKBytes = 32 * kLBO;      // key operand: 128 tokens × 256 positions, fp16
@@ -98,7 +100,6 @@ struct alignas(1024) Smem {
   unsigned char v[2][kVBytes];
   float fac[kFacSlots][3][kTile];    // ‖x‖, log2‖v‖, 1/‖v‖ of a tile's tokens
   float tmax[2][2][kTile];           // [tile parity][half of the tokens][row]
-  float lsum[kTile];
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], ffull[kFacSlots];
   uint64_t qfull, drain;
   uint32_t tmem;
@@ -112,6 +113,16 @@ __device__ __forceinline__ float load_elem(const void* base, int dtype, long lon
   return __half2float(__ushort_as_half(u));
 }
 
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+// Bounded wait of a whole warp: false for all lanes once any gave up.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity) {
+  return __all_sync(0xffffffffu, tq::mbar_wait(bar, parity));
+}
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) {
   uint32_t r;
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(s));
@@ -122,14 +133,38 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+// N consecutive TMEM columns of the thread's lane, for N = 8, 16, 32 or 64.
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t at, uint32_t* r) {
+  if constexpr (N == 64) {
+    tq::tmem_ld_32x32b_x32(at, r);
+    tq::tmem_ld_32x32b_x32(at + 32, r + 32);
+  } else if constexpr (N == 32) {
+    tq::tmem_ld_32x32b_x32(at, r);
+  } else {
+    static_assert(N == 16, "columns");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(at));
+  }
+}
+template <int N>
+__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t* v) {
+  if constexpr (N == 32) {
+    tq::tmem_st_32x32b_x32(at, v);
+  } else if constexpr (N == 16) {
+    tq::tmem_st_32x32b_x16(at, v);
+  } else {
+    static_assert(N == 8, "columns");
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
+                 "r"(v[7])
+                 : "memory");
+  }
 }
 constexpr __host__ __device__ uint32_t shr(uint32_t x, int n) { return n >= 0 ? x >> n : x << -n; }
 
@@ -174,182 +209,237 @@ __device__ __forceinline__ uint4 plane_chunk(const LevelBytes& t, const uint32_t
   return levels8<NB == 4>(t, s, top);
 }
 
-// The codes of half a token (64 coordinates) as an expander thread holds them.
-template <int IB, int VB>
-struct Codes {
-  uint2 k[IB], s;
-  uint2 v[VB == 4 ? 4 : VB];
-  float xn, rn, vn;
-  bool ok;
-};
-
-// Row and slot of a token in a cache's arrays; 64-bit slot offsets follow from them.
-struct Place {
-  long long row;
-  int slot;
-};
-
-template <int IB, int VB>
-__device__ __forceinline__ void fetch(const CacheSide& c, int Hkv, int b, int h, int token, bool ok,
-                                      int half, Codes<IB, VB>& o) {
-  Place k{0, 0}, v{0, 0};
-  if (ok) {
-    bool in = tq_map_slot(c.kmap, Hkv, b, h, token, k.row, k.slot);
-    if (c.same_map) v = k;
-    else in &= tq_map_slot(c.vmap, Hkv, b, h, token, v.row, v.slot);
-    if (!in) {
-      atomicOr(&g_tq_flags, TQ_FLAG_PAGE);
-      ok = false;
-    }
-  }
-  o.ok = ok;
-  o.xn = o.rn = o.vn = 0.f;
-  o.s = make_uint2(0, 0);
-#pragma unroll
-  for (int p = 0; p < IB; ++p) o.k[p] = make_uint2(0, 0);
-#pragma unroll
-  for (int p = 0; p < (VB == 4 ? 4 : VB); ++p) o.v[p] = make_uint2(0, 0);
-  if (!ok) return;
-  const int ks = c.kslots, vs = c.vslots;
-  const uint8_t* kp = c.kidx + (k.row * IB * ks + k.slot) * 16 + 8 * half;
-#pragma unroll
-  for (int p = 0; p < IB; ++p) o.k[p] = __ldg(reinterpret_cast<const uint2*>(kp + (long long)p * ks * 16));
-  const long long kt = k.row * ks + k.slot, vt = v.row * vs + v.slot;
-  o.s = __ldg(reinterpret_cast<const uint2*>(c.ksgn + kt * 16 + 8 * half));
-  o.xn = __ldg(c.kxn + kt);
-  o.rn = __ldg(c.krn + kt);
-  if constexpr (VB == 4) {
-    const uint4* p = reinterpret_cast<const uint4*>(c.vidx + vt * 64 + 32 * half);
-    const uint4 x = __ldg(p), y = __ldg(p + 1);
-    o.v[0] = make_uint2(x.x, x.y);
-    o.v[1] = make_uint2(x.z, x.w);
-    o.v[2] = make_uint2(y.x, y.y);
-    o.v[3] = make_uint2(y.z, y.w);
-  } else {
-    const uint8_t* vp = c.vidx + (v.row * VB * vs + v.slot) * 16 + 8 * half;
-#pragma unroll
-    for (int p = 0; p < VB; ++p) o.v[p] = __ldg(reinterpret_cast<const uint2*>(vp + (long long)p * vs * 16));
-  }
-  o.vn = __ldg(c.vxn + vt);
-}
-
-// Key operand of half a token: level chunks 8·half.. and sign chunks 16 + 8·half...
-template <int IB, int VB>
-__device__ __forceinline__ void expand_key(const RowsArgs& a, const Codes<IB, VB>& c, int half,
-                                           unsigned char* dst) {
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    uint32_t x[IB];
-#pragma unroll
-    for (int p = 0; p < IB; ++p) x[p] = w ? c.k[p].y : c.k[p].x;
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      *reinterpret_cast<uint4*>(dst + (8 * half + 4 * w + r) * kLBO) = plane_chunk<IB>(a.kt, x, r);
-  }
-  // ρ ≤ 1 or so for codes of any key (‖r‖ is the norm of a quantisation residual); a zero key
-  // has both norms 0
-  const float rho = c.xn > 0.f ? c.rn / c.xn * a.rho_scale : 0.f;
-  const __half2 r2 = __float2half2_rn(rho);
-  const uint32_t neg = *reinterpret_cast<const uint32_t*>(&r2) ^ 0x80008000u;
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const uint32_t x = w ? c.s.y : c.s.x;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint4 o;
-      o.x = (shr(x, 4 * q + 0 - 15) & 0x80008000u) ^ neg;
-      o.y = (shr(x, 4 * q + 1 - 15) & 0x80008000u) ^ neg;
-      o.z = (shr(x, 4 * q + 2 - 15) & 0x80008000u) ^ neg;
-      o.w = (shr(x, 4 * q + 3 - 15) & 0x80008000u) ^ neg;
-      *reinterpret_cast<uint4*>(dst + (16 + 8 * half + 4 * w + q) * kLBO) = o;
-    }
-  }
-}
-
-template <int IB, int VB>
-__device__ __forceinline__ void expand_value(const RowsArgs& a, const Codes<IB, VB>& c, int half,
-                                             unsigned char* dst) {
-  LevelBytes t = a.vt;
-  if (!(c.vn >= kTiny)) {   // a zero vector adds nothing, whatever its code
-#pragma unroll
-    for (int i = 0; i < 4; ++i) t.lo[i] = t.hi[i] = 0;
-  }
-  if constexpr (VB == 4) {
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      const uint32_t x = (w & 1) ? c.v[w / 2].y : c.v[w / 2].x;
-      *reinterpret_cast<uint4*>(dst + (8 * half + w) * kLBO) =
-          levels8<true>(t, x & 0x77777777u, ((x >> 3) & 0x11111111u) | 0x88888888u);
-    }
-  } else {
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      uint32_t x[VB];
-#pragma unroll
-      for (int p = 0; p < VB; ++p) x[p] = w ? c.v[p].y : c.v[p].x;
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        *reinterpret_cast<uint4*>(dst + (8 * half + 4 * w + r) * kLBO) = plane_chunk<VB>(t, x, r);
-    }
-  }
-}
-
 // The tokens that an item attends.
 struct Item {
   int t0, tiles, len, nblk, b, h;
   const int* list;
 };
 
-// An expander thread's work: half a token of every tile.  False once a wait gave up.
+// Where the 32 tokens of a warp lie in a cache's arrays: all in one 64-token block, so the row
+// (and the page) is the warp's.  Slots past the sequence's length but in its last block are in
+// the cache: they are read, and masked where it matters.
+struct Spot {
+  bool some;      // at least the first token is attended
+  int token0;
+  long long row;
+  int slot;
+};
+
+// first: the warp's first token in a tile of 128.
+template <bool kList>
+__device__ __forceinline__ Spot locate(const RowsArgs& a, const tq_rowmap& map, const Item& it,
+                                       int t, int first, bool flag) {
+  Spot s;
+  s.row = 0;
+  s.slot = 0;
+  if (kList) {
+    const int at = 2 * (it.t0 + t) + (first >> 6);
+    const int blk = at < a.max_blocks ? __ldg(it.list + at) : -1;
+    s.token0 = blk >= 0 && blk < it.nblk ? blk * 64 + (first & 63) : -1;
+  } else {
+    s.token0 = (it.t0 + t) * kTile + first;
+  }
+  s.some = s.token0 >= 0 && s.token0 < it.len;
+  if (s.some) {
+    s.some = tq_map_slot(map, a.Hkv, it.b, it.h, s.token0, s.row, s.slot);
+    if (!s.some && flag) atomicOr(&g_tq_flags, TQ_FLAG_PAGE);
+  }
+  return s;
+}
+
+// Loads of the next tile's codes: volatile, so that they are issued here and not where the values
+// are used, a tile later (the compiler may sink a plain read-only load that far).
+__device__ __forceinline__ uint4 load_early(const uint4* p) {
+  uint4 x;
+  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "l"(p));
+  return x;
+}
+__device__ __forceinline__ float load_early(const float* p) {
+  float x;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(x) : "l"(p));
+  return x;
+}
+
+__device__ __forceinline__ uint32_t word(const uint4& x, int w) {
+  return w == 0 ? x.x : w == 1 ? x.y : w == 2 ? x.z : x.w;
+}
+
+// NB planes of 16 bytes of one token.  Offsets within a row stay below 2^32 bytes (the host
+// checks).  Where the warp has no token the registers keep what they hold: any code is a finite
+// operand.
+template <int NB>
+__device__ __forceinline__ void load_planes(const uint8_t* base, const Spot& s, int slots, int lane,
+                                            uint4 (&o)[NB]) {
+  if (!s.some) return;
+  const uint8_t* row = base + s.row * ((long long)NB * slots * 16);
+#pragma unroll
+  for (int p = 0; p < NB; ++p)
+    o[p] = load_early(reinterpret_cast<const uint4*>(row + ((uint32_t)(p * slots + s.slot + lane) * 16u)));
+}
+
+// Level chunks 0–15 of a token from its NB planes.
+template <int NB>
+__device__ __forceinline__ void put_planes(const LevelBytes& t, const uint4 (&c)[NB], unsigned char* dst) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    uint32_t x[NB];
+#pragma unroll
+    for (int p = 0; p < NB; ++p) x[p] = word(c[p], w);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      *reinterpret_cast<uint4*>(dst + (4 * w + r) * kLBO) = plane_chunk<NB>(t, x, r);
+  }
+}
+
+// Hands a tile's operand part over: generic writes before the tensor core's reads.
+__device__ __forceinline__ void hand_over(uint64_t* bar, int lane) {
+  tq::fence_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// The three kinds of expander warps.  Each returns false once a wait gave up.
+template <int IB, bool kList>
+__device__ __forceinline__ bool expand_keys(const RowsArgs& a, const CacheSide& side, Smem& sm,
+                                            const Item& it, int first, int lane) {
+  const int off = (first >> 3) * 128 + (lane >> 3) * 128 + (lane & 7) * 16;
+  uint4 next[IB] = {};
+  load_planes<IB>(side.kidx, locate<kList>(a, side.kmap, it, 0, first, lane == 0), side.kslots, lane, next);
+  for (int t = 0; t < it.tiles; ++t) {
+    uint4 c[IB];
+#pragma unroll
+    for (int p = 0; p < IB; ++p) c[p] = next[p];
+    if (t + 1 < it.tiles)
+      load_planes<IB>(side.kidx, locate<kList>(a, side.kmap, it, t + 1, first, lane == 0), side.kslots, lane, next);
+    const int st = t & 1;
+    if (t >= 2 && !warp_wait(&sm.kempty[st], ((t >> 1) - 1) & 1)) return false;
+    put_planes<IB>(a.kt, c, sm.k[st] + off);
+    hand_over(&sm.kfull[st], lane);
+  }
+  return true;
+}
+
+template <bool kList>
+__device__ __forceinline__ bool expand_signs(const RowsArgs& a, const CacheSide& side, Smem& sm,
+                                             const Item& it, int first, int lane) {
+  const int off = (first >> 3) * 128 + (lane >> 3) * 128 + (lane & 7) * 16;
+  struct Raw {
+    uint4 s;
+    float xn, rn, vn;
+    bool ok;
+  };
+  auto load = [&](int t, Raw& o) {
+    const Spot k = locate<kList>(a, side.kmap, it, t, first, false);
+    Spot v = k;
+    if (!side.same_map) v = locate<kList>(a, side.vmap, it, t, first, false);
+    const bool some = k.some && v.some;
+    o.ok = some && k.token0 + lane < it.len;
+    if (!some) return;
+    const long long at = k.row * side.kslots + k.slot + lane;
+    o.s = load_early(reinterpret_cast<const uint4*>(side.ksgn) + at);
+    o.xn = load_early(side.kxn + at);
+    o.rn = load_early(side.krn + at);
+    o.vn = load_early(side.vxn + v.row * side.vslots + v.slot + lane);
+  };
+  Raw next{};
+  load(0, next);
+  for (int t = 0; t < it.tiles; ++t) {
+    const Raw c = next;
+    if (t + 1 < it.tiles) load(t + 1, next);
+    const int st = t & 1, fs = t % kFacSlots;
+    // the factors' slot is free: tile t − 4 was weighed before tile t − 2 was scored (kempty)
+    if (t >= 2 && !warp_wait(&sm.kempty[st], ((t >> 1) - 1) & 1)) return false;
+    const bool some = c.vn >= kTiny;
+    sm.fac[fs][0][first + lane] = c.ok ? c.xn : 0.f;
+    sm.fac[fs][1][first + lane] = !c.ok ? -INFINITY : some ? __log2f(c.vn) : c.vn < kTiny ? -60.f : c.vn;
+    sm.fac[fs][2][first + lane] = !c.ok ? 0.f : some ? __fdividef(1.f, c.vn) : 1.152921504606847e18f;   // 2^60
+    // ρ ≤ 1 or so for codes of any key (‖r‖ is the norm of a quantisation residual); a zero key
+    // has both norms 0
+    const float rho = c.ok && c.xn > 0.f ? __fdividef(c.rn, c.xn) * a.rho_scale : 0.f;
+    const __half2 r2 = __float2half2_rn(rho);
+    const uint32_t neg = *reinterpret_cast<const uint32_t*>(&r2) ^ 0x80008000u;
+    unsigned char* dst = sm.k[st] + 16 * kLBO + off;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t x = word(c.s, w);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint4 o;
+        o.x = (shr(x, 4 * q + 0 - 15) & 0x80008000u) ^ neg;
+        o.y = (shr(x, 4 * q + 1 - 15) & 0x80008000u) ^ neg;
+        o.z = (shr(x, 4 * q + 2 - 15) & 0x80008000u) ^ neg;
+        o.w = (shr(x, 4 * q + 3 - 15) & 0x80008000u) ^ neg;
+        *reinterpret_cast<uint4*>(dst + (4 * w + q) * kLBO) = o;
+      }
+    }
+    hand_over(&sm.kfull[st], lane);
+    if (lane == 0) mbar_arrive(&sm.ffull[fs]);
+  }
+  return true;
+}
+
+template <int VB, bool kList>
+__device__ __forceinline__ bool expand_values(const RowsArgs& a, const CacheSide& side, Smem& sm,
+                                              const Item& it, int first, int lane) {
+  constexpr int kRegs = VB == 4 ? 4 : VB;
+  const int off = (first >> 3) * 128 + (lane >> 3) * 128 + (lane & 7) * 16;
+  uint4 next[kRegs] = {};
+  float next_vn = 0.f;
+  auto load = [&](int t) {
+    const Spot s = locate<kList>(a, side.vmap, it, t, first, lane == 0 && !side.same_map);
+    if (s.some) next_vn = load_early(side.vxn + s.row * side.vslots + s.slot + lane);
+    if constexpr (VB == 4) {
+      if (!s.some) return;
+      const uint4* p = reinterpret_cast<const uint4*>(side.vidx + s.row * ((long long)side.vslots * 64) +
+                                                      (uint32_t)(s.slot + lane) * 64u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) next[i] = load_early(p + i);
+    } else {
+      load_planes<VB>(side.vidx, s, side.vslots, lane, next);
+    }
+  };
+  load(0);
+  for (int t = 0; t < it.tiles; ++t) {
+    uint4 c[kRegs];
+#pragma unroll
+    for (int p = 0; p < kRegs; ++p) c[p] = next[p];
+    // a zero vector adds nothing, whatever its code (a norm that is NaN or past the length has
+    // no weight to meet it)
+    const bool some = next_vn >= kTiny;
+    if (t + 1 < it.tiles) load(t + 1);
+    LevelBytes tb;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      tb.lo[i] = some ? a.vt.lo[i] : 0u;
+      tb.hi[i] = some ? a.vt.hi[i] : 0u;
+    }
+    const int st = t & 1;
+    if (t >= 2 && !warp_wait(&sm.vempty[st], ((t >> 1) - 1) & 1)) return false;
+    unsigned char* dst = sm.v[st] + off;
+    if constexpr (VB == 4) {
+#pragma unroll
+      for (int w = 0; w < 16; ++w) {
+        const uint32_t x = word(c[w / 4], w % 4);
+        *reinterpret_cast<uint4*>(dst + w * kLBO) =
+            levels8<true>(tb, x & 0x77777777u, ((x >> 3) & 0x11111111u) | 0x88888888u);
+      }
+    } else {
+      put_planes<VB>(tb, c, dst);
+    }
+    hand_over(&sm.vfull[st], lane);
+  }
+  return true;
+}
+
 template <int IB, int VB, bool kList>
 __device__ __forceinline__ bool expand(const RowsArgs& a, const CacheSide& side, Smem& sm,
-                                       const Item& it) {
-  const int e = threadIdx.x - kExpThreads, tt = e & 127, half = e >> 7, lane = e & 31;
-  auto get = [&](int t, Codes<IB, VB>& c) {
-    int token;
-    bool there = true;
-    if (kList) {
-      const int at = 2 * (it.t0 + t) + (tt >> 6);
-      const int blk = at < a.max_blocks ? __ldg(it.list + at) : -1;
-      there = blk >= 0 && blk < it.nblk;
-      token = blk * 64 + (tt & 63);
-    } else {
-      token = (it.t0 + t) * kTile + tt;
-    }
-    fetch<IB, VB>(side, a.Hkv, it.b, it.h, token, there && token < it.len, half, c);
-  };
-  const int row_off = (tt >> 3) * 128 + (tt & 7) * 16;
-  bool ok = true;
-  auto wait = [&](uint64_t* bar, unsigned parity) {
-    return ok = __all_sync(0xffffffffu, tq::mbar_wait(bar, parity));
-  };
-  Codes<IB, VB> next;
-  get(0, next);
-  for (int t = 0; t < it.tiles; ++t) {
-    const Codes<IB, VB> c = next;
-    if (t + 1 < it.tiles) get(t + 1, next);
-    const int st = t & 1, fs = t % kFacSlots;
-    if (t >= 2 && !wait(&sm.kempty[st], ((t >> 1) - 1) & 1)) break;
-    if (half == 0) {
-      const bool some = c.vn >= kTiny;
-      sm.fac[fs][0][tt] = c.ok ? c.xn : 0.f;
-      sm.fac[fs][1][tt] = !c.ok ? -INFINITY : some ? log2f(c.vn) : c.vn < kTiny ? -60.f : c.vn;
-      sm.fac[fs][2][tt] = !c.ok ? 0.f : some ? 1.f / c.vn : 1.152921504606847e18f;   // 2^60
-    }
-    expand_key<IB, VB>(a, c, half, sm.k[st] + row_off);
-    tq::fence_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(&sm.ffull[fs]);
-      mbar_arrive(&sm.kfull[st]);
-    }
-    if (t >= 2 && !wait(&sm.vempty[st], ((t >> 1) - 1) & 1)) break;
-    expand_value<IB, VB>(a, c, half, sm.v[st] + row_off);
-    tq::fence_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.vfull[st]);
-  }
-  return ok;
+                                       const Item& it, int warp, int lane) {
+  const int first = 32 * (warp & 3);
+  if (warp < kSignWarp) return expand_keys<IB, kList>(a, side, sm, it, first, lane);
+  if (warp < kValueWarp) return expand_signs<kList>(a, side, sm, it, first, lane);
+  return expand_values<VB, kList>(a, side, sm, it, first, lane);
 }
 
 // Valid length of a sequence: clamped to what the call was sized for, flagged if longer.
@@ -361,15 +451,122 @@ __device__ __forceinline__ int clamp_len(int len, int most) {
   return len < 0 ? 0 : len;
 }
 
+// What a softmax thread ends with.
+struct Stats {
+  float m, l;
+  bool ok;
+};
+
+// The softmax of every tile by 8 warps: thread (lane group wl, half hf) of TMEM lane 32·wl + lane.
+// An item of at most 32 (64) rows holds each row in 4 (2) lane groups, the replicas of a row
+// taking a quarter (half) of a tile's tokens each, so that a thread has kCols = 16 (32) scores
+// instead of 64: with few rows a tile's time is this chain's.  Weights of the tokens that a
+// replica leaves to the others are 0, and its O and l are those of its tokens.
+template <int kCols>
+__device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int wl, int hf, int lane, float f) {
+  constexpr int kReps = 64 / kCols;
+  const int rep = wl / (4 / kReps);
+  const int col0 = (2 * rep + hf) * kCols;      // the thread's first token of a tile
+  const uint32_t lane_base = (uint32_t)(32 * wl) << 16;
+  const int r = 32 * wl + lane;
+  Stats z{-INFINITY, 0.f, true};
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, unsigned parity) { return ok = ok && warp_wait(bar, parity); };
+  for (int t = 0; t < tiles; ++t) {
+    const int buf = t & 1;
+    wait(&sm.ffull[t % kFacSlots], (t / kFacSlots) & 1);
+    wait(&sm.sfull[buf], (t >> 1) & 1);
+    tc_after();
+    const uint32_t dcol = lane_base + kDCol + 128 * buf;
+    float e[kCols];
+    tmem_load<kCols>(dcol + col0, reinterpret_cast<uint32_t*>(e));
+    tq::tmem_wait_ld();
+    const float* fx = sm.fac[t % kFacSlots][0] + col0;
+    float mt = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kCols; i += 4) {
+      const float4 xn = *reinterpret_cast<const float4*>(fx + i);
+      const float4 lv = *reinterpret_cast<const float4*>(fx + kTile + i);
+      e[i] = fmaf(e[i] * f, xn.x, lv.x);
+      e[i + 1] = fmaf(e[i + 1] * f, xn.y, lv.y);
+      e[i + 2] = fmaf(e[i + 2] * f, xn.z, lv.z);
+      e[i + 3] = fmaf(e[i + 3] * f, xn.w, lv.w);
+      mt = fmaxf(mt, fmaxf(fmaxf(e[i], e[i + 1]), fmaxf(e[i + 2], e[i + 3])));
+    }
+    sm.tmax[buf][hf][r] = mt;
+    // both halves have read D: it may be overwritten by the weights.  A wait that gave up ends
+    // both halves' loops here, together (neither then waits for the other)
+    if (!tq::named_sync_and(1 + wl, 64, ok)) {
+      z.ok = false;
+      return z;
+    }
+    mt = fmaxf(mt, sm.tmax[buf][hf ^ 1][r]);
+    const float m_new = mt > z.m + kGrow ? mt : z.m;
+    if (t > 0 && __any_sync(0xffffffffu, m_new != z.m)) {
+      // O (this half of its columns) follows the reference, once O += W(t − 1)·V(t − 1) is
+      // done (vempty).  Its barrier is that of every other tile: the phase before, tile t − 3's,
+      // ended before tile t was scored, so the parity says which tile is meant
+      wait(&sm.vempty[buf ^ 1], ((t - 1) >> 1) & 1);
+      tc_after();
+      const float corr = z.m == -INFINITY ? 0.f : ex2(z.m - m_new);
+#pragma unroll 1
+      for (int c = 0; c < 64; c += 16) {   // 16 columns at a time: e stays in registers
+        uint32_t o[16];
+        const uint32_t at = lane_base + kOCol + 64 * hf + c;
+        tmem_load<16>(at, o);
+        tq::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
+        tmem_store<16>(at, o);
+      }
+      z.l *= corr;
+    }
+    z.m = m_new;
+    const float ref = m_new == -INFINITY ? 0.f : m_new;
+    uint32_t w[kCols / 2];
+#pragma unroll
+    for (int i = 0; i < kCols; i += 4) {
+      const float4 iv = *reinterpret_cast<const float4*>(fx + 2 * kTile + i);
+      const float w0 = ex2(e[i] - ref), w1 = ex2(e[i + 1] - ref);
+      const float w2 = ex2(e[i + 2] - ref), w3 = ex2(e[i + 3] - ref);
+      z.l = fmaf(w0, iv.x, z.l);
+      z.l = fmaf(w1, iv.y, z.l);
+      z.l = fmaf(w2, iv.z, z.l);
+      z.l = fmaf(w3, iv.w, z.l);
+      const __half2 p0 = __floats2half2_rn(w0, w1), p1 = __floats2half2_rn(w2, w3);
+      w[i / 2] = *reinterpret_cast<const uint32_t*>(&p0);
+      w[i / 2 + 1] = *reinterpret_cast<const uint32_t*>(&p1);
+    }
+    tmem_store<kCols / 2>(dcol + col0 / 2, w);
+    if constexpr (kReps > 1) {
+      // the other replicas' tokens: 64 − kCols columns of weights, half of them by each half
+      constexpr int kRest = (64 - kCols) / 2;
+      const uint32_t none[16] = {};
+#pragma unroll
+      for (int c = 0; c < kRest; c += kCols / 2)
+        tmem_store<kCols / 2>(dcol + ((rep * kCols + kCols + hf * kRest + c) & 63), none);
+    }
+    tq::tmem_wait_st();
+    tc_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.pfull[buf]);
+    // tile t + 2 is scored after both halves have arrived here: until then this tile's tmax and
+    // factors may still be read (tile t + 1 may be scored already)
+  }
+  wait(&sm.vempty[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1);
+  z.ok = ok;
+  return z;
+}
+
 template <int IB, int VB>
 __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_constant__ RowsArgs a) {
   extern __shared__ unsigned char smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  static_assert(128 * kRegsIssue + 256 * (kRegsLaunch + kRegsSoftmax) <= kThreads * kRegsLaunch, "register split");
+  static_assert(128 * kRegsIssue + 384 * kRegsExpand + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
 
   // ---- the item: prefix items first (they are the long ones)
   int item = blockIdx.x;
@@ -423,183 +620,127 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
     }
     return;
   }
-  const int active = (rows + 31) / 32;   // softmax warp pairs with a row to work on
+  const int reps = rows <= 32 ? 4 : rows <= 64 ? 2 : 1;   // lane groups that hold a row
 
-  if (warp == 16) tq::tmem_alloc(&sm.tmem, 512);
+  if (warp == kIssueWarp) tq::tmem_alloc(&sm.tmem, 512);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       tq::mbar_init(&sm.kfull[i], 8);
-      tq::mbar_init(&sm.vfull[i], 8);
+      tq::mbar_init(&sm.vfull[i], 4);
       tq::mbar_init(&sm.kempty[i], 1);
       tq::mbar_init(&sm.vempty[i], 1);
       tq::mbar_init(&sm.sfull[i], 1);
-      tq::mbar_init(&sm.pfull[i], 2 * active);
+      tq::mbar_init(&sm.pfull[i], 8);
     }
-    for (int i = 0; i < kFacSlots; ++i) tq::mbar_init(&sm.ffull[i], 8);
-    tq::mbar_init(&sm.qfull, 2 * active);
+    for (int i = 0; i < kFacSlots; ++i) tq::mbar_init(&sm.ffull[i], 4);
+    tq::mbar_init(&sm.qfull, 8);
     tq::mbar_init(&sm.drain, 1);
     tq::mbar_init_fence();
   }
   tc_before();
   __syncthreads();
   tc_after();
-  const uint32_t tmem = sm.tmem;
-  bool ok = true;   // false once a bounded wait gave up: every role then leaves its loop
+  // all 512 columns were asked for, so they begin at address 0: addresses are constants
+  constexpr uint32_t tmem = 0;
+  bool ok = sm.tmem == 0;   // false once a bounded wait gave up: every role then leaves its loop
   auto wait = [&](uint64_t* bar, unsigned parity) {
-    return ok = __all_sync(0xffffffffu, ok && tq::mbar_wait(bar, parity));
+    return ok = ok && warp_wait(bar, parity);
   };
 
   if (warp < 8) {
     // ================================================================ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int wl = warp & 3, hf = warp >> 2;
-    const int r = 32 * wl + lane;
-    if (wl < active) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      const uint32_t lane_base = tmem + ((uint32_t)(32 * wl) << 16);
-      float f = 0.f;
-      {
-        const long long qr = r < rows ? qrow_of(r) : 0;
-        if (r < rows) f = __ldg(a.qf + qr);
+    const int per = kTile / reps;              // rows per replica
+    const int r = (32 * wl + lane) & (per - 1);
+    const uint32_t lane_base = (uint32_t)(32 * wl) << 16;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const long long qr = r < rows ? qrow_of(r) : 0;
+    const float f = r < rows ? __ldg(a.qf + qr) : 0.f;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t q[32];
+    for (int c = 0; c < 2; ++c) {
+      uint32_t q[32];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint4 x = r < rows ? __ldg(a.qop + qr * 32 + 16 * hf + 8 * c + i) : make_uint4(0, 0, 0, 0);
-            q[4 * i] = x.x; q[4 * i + 1] = x.y; q[4 * i + 2] = x.z; q[4 * i + 3] = x.w;
-          }
-          tq::tmem_st_32x32b_x32(lane_base + kQCol + 64 * hf + 32 * c, q);
-        }
-        tq::tmem_wait_st();
-        tc_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.qfull);
+      for (int i = 0; i < 8; ++i) {
+        const uint4 x = r < rows ? __ldg(a.qop + qr * 32 + 16 * hf + 8 * c + i) : make_uint4(0, 0, 0, 0);
+        q[4 * i] = x.x; q[4 * i + 1] = x.y; q[4 * i + 2] = x.z; q[4 * i + 3] = x.w;
       }
-      float m = -INFINITY, l = 0.f;
-      bool alive = true;
-      for (int t = 0; t < tiles; ++t) {
-        const int buf = t & 1;
-        wait(&sm.ffull[t % kFacSlots], (t / kFacSlots) & 1);
-        wait(&sm.sfull[buf], (t >> 1) & 1);
-        tc_after();
-        const uint32_t dcol = lane_base + kDCol + 128 * buf;
-        float e[64];
-        tq::tmem_ld_32x32b_x32(dcol + 64 * hf, reinterpret_cast<uint32_t*>(e));
-        tq::tmem_ld_32x32b_x32(dcol + 64 * hf + 32, reinterpret_cast<uint32_t*>(e + 32));
+      tmem_store<32>(lane_base + kQCol + 64 * hf + 32 * c, q);
+    }
+    tq::tmem_wait_st();
+    tc_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.qfull);
+    const Stats z = reps == 4 ? softmax_tiles<16>(sm, tiles, wl, hf, lane, f)
+                  : reps == 2 ? softmax_tiles<32>(sm, tiles, wl, hf, lane, f)
+                              : softmax_tiles<64>(sm, tiles, wl, hf, lane, f);
+    // ---- the item's record: lanes' parts through shared memory (the operands are done with),
+    // replicas of a row added up with their log-sum-exp weights
+    ok = ok && tq::named_sync_and(5, 256, z.ok);
+    if (ok) {
+      tc_after();
+      float* part = reinterpret_cast<float*>(sm.k[0]);      // [128 lanes][kRecFloats]
+      float* mine = part + (32 * wl + lane) * kRecFloats;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float o[32];
+        tmem_load<32>(lane_base + kOCol + 64 * hf + 32 * c, reinterpret_cast<uint32_t*>(o));
         tq::tmem_wait_ld();
-        const float* fx = sm.fac[t % kFacSlots][0] + 64 * hf;
-        float mt = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float4 xn = *reinterpret_cast<const float4*>(fx + 4 * i);
-          const float4 lv = *reinterpret_cast<const float4*>(fx + kTile + 4 * i);
-          e[4 * i] = fmaf(e[4 * i] * f, xn.x, lv.x);
-          e[4 * i + 1] = fmaf(e[4 * i + 1] * f, xn.y, lv.y);
-          e[4 * i + 2] = fmaf(e[4 * i + 2] * f, xn.z, lv.z);
-          e[4 * i + 3] = fmaf(e[4 * i + 3] * f, xn.w, lv.w);
-          mt = fmaxf(mt, fmaxf(fmaxf(e[4 * i], e[4 * i + 1]), fmaxf(e[4 * i + 2], e[4 * i + 3])));
-        }
-        sm.tmax[buf][hf][r] = mt;
-        // both halves have read D: it may be overwritten by the weights.  A wait that gave up
-        // ends both halves' loops here, together (neither then waits for the other)
-        if (!(alive = tq::named_sync_and(1 + wl, 64, ok))) break;
-        mt = fmaxf(mt, sm.tmax[buf][hf ^ 1][r]);
-        const float m_new = mt > m + kGrow ? mt : m;
-        if (t > 0 && __any_sync(0xffffffffu, m_new != m)) {
-          // O (this half of its columns) follows the reference, once O += W(t − 1)·V(t − 1) is
-          // done (vempty).  Its barrier is that of every other tile: the phase before, tile
-          // t − 3's, ended before tile t was scored, so the parity says which tile is meant
-          wait(&sm.vempty[buf ^ 1], ((t - 1) >> 1) & 1);
-          tc_after();
-          const float corr = m == -INFINITY ? 0.f : ex2(m - m_new);
-#pragma unroll 1
-          for (int c = 0; c < 64; c += 16) {   // 16 columns at a time: e stays in registers
-            uint32_t o[16];
-            const uint32_t at = lane_base + kOCol + 64 * hf + c;
-            tmem_ld_x16(at, o);
-            tq::tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
-            tq::tmem_st_32x32b_x16(at, o);
-          }
-          l *= corr;
-        }
-        m = m_new;
-        const float ref = m == -INFINITY ? 0.f : m;
-        uint32_t w[32];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float4 iv = *reinterpret_cast<const float4*>(fx + 2 * kTile + 4 * i);
-          const float w0 = ex2(e[4 * i] - ref), w1 = ex2(e[4 * i + 1] - ref);
-          const float w2 = ex2(e[4 * i + 2] - ref), w3 = ex2(e[4 * i + 3] - ref);
-          l = fmaf(w0, iv.x, l);
-          l = fmaf(w1, iv.y, l);
-          l = fmaf(w2, iv.z, l);
-          l = fmaf(w3, iv.w, l);
-          const __half2 p0 = __floats2half2_rn(w0, w1), p1 = __floats2half2_rn(w2, w3);
-          w[2 * i] = *reinterpret_cast<const uint32_t*>(&p0);
-          w[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&p1);
-        }
-        tq::tmem_st_32x32b_x32(dcol + 32 * hf, w);
-        tq::tmem_wait_st();
-        tc_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.pfull[buf]);
-        // tile t + 2 is scored after both halves have arrived here: until then this tile's tmax
-        // and factors may still be read (tile t + 1 may be scored already)
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<float4*>(mine + 64 * hf + 32 * c + 4 * i) =
+              make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
       }
-      if (alive) {
-        wait(&sm.vempty[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1);
-        if (hf) sm.lsum[r] = l;
-        alive = tq::named_sync_and(1 + wl, 64, ok);
-      }
-      ok = ok && alive;
-      if (ok) {
-        tc_after();
-        if (!hf) l += sm.lsum[r];
-        float* rec = r < rows
-            ? a.rec + ((long long)rec_split * a.B * a.Hq + qrow_of(r)) * kRecFloats : nullptr;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float o[32];
-          tq::tmem_ld_32x32b_x32(lane_base + kOCol + 64 * hf + 32 * c, reinterpret_cast<uint32_t*>(o));
-          tq::tmem_wait_ld();
-          if (rec) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<float4*>(rec + 64 * hf + 32 * c + 4 * i) =
-                  make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          }
+      mine[128 + 2 * hf] = z.m;       // both halves have the same reference
+      mine[129 + 2 * hf] = z.l;
+      tq::named_sync(5, 256);
+      for (int row = warp; row < rows; row += 8) {
+        float* rec = a.rec + ((long long)rec_split * a.B * a.Hq + qrow_of(row)) * kRecFloats;
+        float m = -INFINITY;
+        for (int k = 0; k < reps; ++k) m = fmaxf(m, part[(k * per + row) * kRecFloats + 128]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+        for (int k = 0; k < reps; ++k) {
+          const float* p = part + (k * per + row) * kRecFloats;
+          const float w = p[128] == -INFINITY ? 0.f : ex2(p[128] - m);
+          const float4 x = *reinterpret_cast<const float4*>(p + 4 * lane);
+          acc.x = fmaf(w, x.x, acc.x);
+          acc.y = fmaf(w, x.y, acc.y);
+          acc.z = fmaf(w, x.z, acc.z);
+          acc.w = fmaf(w, x.w, acc.w);
+          l = fmaf(w, p[129] + p[131], l);
         }
-        if (rec && !hf) {
-          rec[128] = m;
-          rec[129] = l;
-        }
+        *reinterpret_cast<float4*>(rec + 4 * lane) = acc;
+        if (lane == 0) *reinterpret_cast<float2*>(rec + 128) = make_float2(m, l);
       }
     }
-  } else if (warp < 16) {
+  } else if (warp < kIssueWarp) {
     // ================================================================ expanders
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsExpand));
     const Item it{t0, tiles, len, nblk, b, h, list};
-    if (pre) ok = expand<IB, VB, false>(a, a.pre, sm, it);
-    else if (list) ok = expand<IB, VB, true>(a, a.own, sm, it);
-    else ok = expand<IB, VB, false>(a, a.own, sm, it);
+    if (pre) ok = expand<IB, VB, false>(a, a.pre, sm, it, warp, lane);
+    else if (list) ok = expand<IB, VB, true>(a, a.own, sm, it, warp, lane);
+    else ok = expand<IB, VB, false>(a, a.own, sm, it, warp, lane);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     // ================================================================ MMA issuer
-    if (warp == 16) {
+    if (warp == kIssueWarp) {
     constexpr uint32_t kIdescS = tq::idesc_f16(128, 128);
     constexpr uint32_t kIdescO = kIdescS | (1u << 16);   // B (values) is N-major
+    // Operands are uniform values (one base descriptor each, constant steps), so that an issue
+    // is one instruction and the queue of the tensor core does not run dry.
+    const uint64_t kdesc = tq::smem_desc(s32(sm.k[0]), kLBO, 128);
+    const uint64_t vdesc = tq::smem_desc(s32(sm.v[0]), 128, kLBO);
     auto weigh = [&](int t) {   // O += W(t)·V(t)
       const int st = t & 1;
       if (!wait(&sm.vfull[st], (t >> 1) & 1) || !wait(&sm.pfull[st], (t >> 1) & 1)) return;
       tc_after();
-      if (lane == 0) {
-        const uint32_t v = s32(sm.v[st]);
+      if (elect_one()) {
+        const uint64_t v = vdesc + st * (kVBytes >> 4);
+        const uint32_t w = kDCol + 128 * st;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          tq::mma_ts(tmem + kOCol, tmem + kDCol + 128 * st + 8 * ks,
-                     tq::smem_desc(v + ks * 256, 128, kLBO), kIdescO, t > 0 || ks > 0);
+          tq::mma_ts(kOCol, w + 8 * ks, v + ks * (256 >> 4), kIdescO, t > 0 || ks > 0);
         tq::mma_commit(&sm.vempty[st]);
       }
       __syncwarp();
@@ -609,12 +750,12 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
       const int st = t & 1;
       if (!wait(&sm.kfull[st], (t >> 1) & 1)) break;
       tc_after();
-      if (lane == 0) {
-        const uint32_t k = s32(sm.k[st]);
+      if (elect_one()) {
+        const uint64_t k = kdesc + st * (kKBytes >> 4);
+        const uint32_t d = kDCol + 128 * st;
 #pragma unroll
         for (int ks = 0; ks < 16; ++ks)
-          tq::mma_ts(tmem + kDCol + 128 * st, tmem + kQCol + 8 * ks,
-                     tq::smem_desc(k + ks * 2 * kLBO, kLBO, 128), kIdescS, ks > 0);
+          tq::mma_ts(d, kQCol + 8 * ks, k + ks * (2 * kLBO >> 4), kIdescS, ks > 0);
         tq::mma_commit(&sm.sfull[st]);
         tq::mma_commit(&sm.kempty[st]);
       }
@@ -623,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
     }
     if (ok) weigh(tiles - 1);
     // whatever was issued has ended before the tensor memory is given back
-    if (lane == 0) tq::mma_commit(&sm.drain);
+    if (elect_one()) tq::mma_commit(&sm.drain);
     __syncwarp();
     if (!tq::mbar_wait(&sm.drain, 0)) ok = false;
     }
@@ -632,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == 16) tq::tmem_dealloc(tmem, 512);
+  if (warp == kIssueWarp) tq::tmem_dealloc(sm.tmem, 512);
 }
 
 // ---------------------------------------------------------------- row operands
@@ -869,6 +1010,7 @@ tq_status cache_side(const tq_prod_cache& k, const tq_mse_cache& v, int capacity
   s->vslots = tq_row_slots(s->vmap, capacity);
   s->same_map = s->kmap.table == s->vmap.table && s->kmap.max_pages == s->vmap.max_pages &&
                 s->kmap.page_tokens == s->vmap.page_tokens && s->kmap.num_pages == s->vmap.num_pages;
+  if (s->kslots > (1 << 26) || s->vslots > (1 << 26)) return TQ_ERR_UNSUPPORTED;   // 32-bit offsets
   return TQ_OK;
 }
 
