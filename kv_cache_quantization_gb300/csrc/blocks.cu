@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(256) block_bounds_kernel(const BoundsArgs a) {
 // ---------------------------------------------------------------- selection
 struct SelectArgs {
   const void* q;
-  int q_dtype;
+  int q_dtype, q_vec;     // q_vec: rows are 16-byte aligned
   const __nv_bfloat16* bounds;
   tq_rowmap map;
   int capacity, max_len;
@@ -165,7 +165,8 @@ struct SelectArgs {
   int* list;              // [B·Hkv][keep]
 };
 
-constexpr int kPerCta = 64;      // blocks per CTA of the scoring kernel
+constexpr int kPerWarp = 4;      // blocks per warp and per CTA of the scoring kernel
+constexpr int kPerCta = 8 * kPerWarp;
 
 __device__ __forceinline__ float load_elem(const void* base, int dtype, long long i) {
   if (dtype == TQ_F32) return static_cast<const float*>(base)[i];
@@ -186,64 +187,119 @@ __device__ __forceinline__ int blocks_of(const SelectArgs& a, int b) {
   return (min(max(a.seq_lens[b], 0), a.max_len) + kBlock - 1) / kBlock;
 }
 
+// Sums over the 32 lanes of each of N values a lane: N/2 + N/4 + ... shuffles instead of 5·N.
+// Lane l ends with the sum of value l / (32 / N) (N ≤ 32, a power of two) in v[0].
+template <int N>
+__device__ __forceinline__ void lane_sums(float (&v)[N], int lane) {
+#pragma unroll
+  for (int o = 16, n = N; o; o >>= 1) {
+    if (n > 1) {
+      // the upper lanes take the upper half of the values
+      n /= 2;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i)
+        if (i < n) {
+          const float mine = lane & o ? v[i + n] : v[i], other = lane & o ? v[i] : v[i + n];
+          v[i] = mine + __shfl_xor_sync(0xffffffffu, other, o);
+        }
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    }
+  }
+}
+
+// Eight consecutive values of a row of queries.
+__device__ __forceinline__ void load8(const void* base, int dtype, long long at, bool vec, float (&o)[8]) {
+  if (!vec) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = load_elem(base, dtype, at + j);
+  } else if (dtype == TQ_F32) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+    const float4 x = __ldg(p), y = __ldg(p + 1);
+    o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
+    o[4] = y.x; o[5] = y.y; o[6] = y.z; o[7] = y.w;
+  } else {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint16_t u = (uint16_t)(j & 1 ? w[j / 2] >> 16 : w[j / 2] & 0xffffu);
+      o[j] = dtype == TQ_BF16 ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
+    }
+  }
+}
+
 // Scores in 32 bits of the blocks of one (sequence, KV head): the largest over the group's
-// query heads.  A warp takes a block at a time, lanes 0–15 its lower and lanes 16–31 its upper
-// bounds (one 512-byte load), each with its half of the query rows.
+// query heads.  A warp takes four blocks with one 512-byte load each, lanes 0–15 the lower and
+// lanes 16–31 the upper bounds, each with its half of the query rows; all loads (bounds and
+// queries) are issued before any is used.  Bound by their latency for short rows (two dependent
+// loads, about 3 us in all) and by reading the bounds for long ones.
 template <int kG>
 __global__ void __launch_bounds__(256) block_score_kernel(const SelectArgs a) {
   __shared__ float s_err[8];
   const int row = blockIdx.y, b = row / a.Hkv, h = row % a.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  float q[kG][8];
+#pragma unroll
+  for (int g = 0; g < kG; ++g)   // absent heads repeat head 0: the maximum over them is the same
+    load8(a.q, a.q_dtype, ((long long)row * a.G + (g < a.G ? g : 0)) * TQ_D + (lane & 15) * 8, a.q_vec, q[g]);
   const int len = a.seq_lens[b];
   if (len > a.max_len && blockIdx.x == 0 && h == 0 && threadIdx.x == 0)
     atomicOr(&g_tq_flags, TQ_FLAG_LEN_OVERFLOW);
   const int nblk = blocks_of(a, b);
-  const int begin = blockIdx.x * kPerCta, end = min(begin + kPerCta, nblk);
-  if (nblk <= a.keep || begin >= end) return;   // nothing to choose, or nothing here
-  float q[kG][8], most[8];
+  const int begin = blockIdx.x * kPerCta + warp * kPerWarp;
+  if (nblk <= a.keep || (int)blockIdx.x * kPerCta >= nblk) return;   // nothing to choose, or nothing here
+  uint4 x[kPerWarp];
+  bool in[kPerWarp];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) most[j] = 0.f;
+  for (int i = 0; i < kPerWarp; ++i) {
+    const __nv_bfloat16* p = begin + i < nblk ? bounds_at(a, b, h, begin + i) : nullptr;
+    in[i] = p != nullptr;
+    x[i] = p ? __ldg(reinterpret_cast<const uint4*>(p) + lane) : make_uint4(0, 0, 0, 0);
+    if (!p && begin + i < nblk && lane == 0) atomicOr(&g_tq_flags, TQ_FLAG_PAGE);
+  }
+  float most[8];
 #pragma unroll
-  for (int g = 0; g < kG; ++g)
+  for (int j = 0; j < 8; ++j) {
+    most[j] = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      // absent heads repeat head 0: the maximum over them is the same
-      const float v = load_elem(a.q, a.q_dtype, ((long long)row * a.G + (g < a.G ? g : 0)) * TQ_D +
-                                                    (lane & 15) * 8 + j);
+    for (int g = 0; g < kG; ++g) {
+      const float v = q[g][j];
       q[g][j] = (lane < 16 ? v > 0.f : v < 0.f) ? 0.f : v;   // NaN goes to both
       most[j] = fmaxf(most[j], fabsf(q[g][j]));
     }
-  float err = 0.f;
-  for (int blk = begin + warp; blk < end; blk += 8) {
-    const __nv_bfloat16* p = bounds_at(a, b, h, blk);
-    float s = -INFINITY;
-    if (p) {
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(p) + lane);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      float v[8], t[kG], e = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[j] = __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
-        e = fmaf(most[j], fabsf(v[j]), e);
-      }
-      err = e <= err ? err : e;   // NaN stays
-#pragma unroll
-      for (int g = 0; g < kG; ++g) {
-        t[g] = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) t[g] = fmaf(q[g][j], v[j], t[g]);
-      }
-#pragma unroll
-      for (int g = 0; g < kG; ++g) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) t[g] += __shfl_xor_sync(0xffffffffu, t[g], o);
-        s = fmaxf(s, t[g]);
-      }
-    } else if (lane == 0) {
-      atomicOr(&g_tq_flags, TQ_FLAG_PAGE);
-    }
-    if (lane == 0) a.score[(long long)row * a.nb + blk] = s;
   }
+  float err = 0.f, s[kPerWarp * kG];
+#pragma unroll
+  for (int i = 0; i < kPerWarp; ++i) {
+    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    float v[8], e = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+      e = fmaf(most[j], fabsf(v[j]), e);
+    }
+    err = e <= err ? err : e;   // NaN stays
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      float t = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t = fmaf(q[g][j], v[j], t);
+      s[i * kG + g] = t;
+    }
+  }
+  lane_sums<kPerWarp * kG>(s, lane);
+  // lane l holds (block, head) l / (32 / (4·kG)); the largest over the heads (NaN left out)
+  float best = fmaxf(-INFINITY, s[0]);
+#pragma unroll
+  for (int o = 32 / (kPerWarp * kG); o < 32 / kPerWarp; o *= 2)
+    best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+#pragma unroll
+  for (int i = 0; i < kPerWarp; ++i)
+    if (lane == i * (32 / kPerWarp) && begin + i < nblk)
+      a.score[(long long)row * a.nb + begin + i] = in[i] ? best : -INFINITY;
   // Σ over lanes of each lane's largest partial sum: at least every block's Σ|terms|
 #pragma unroll
   for (int o = 16; o; o >>= 1) err += __shfl_xor_sync(0xffffffffu, err, o);
@@ -271,26 +327,31 @@ __device__ __forceinline__ unsigned long long ordered(double x) {
 
 constexpr int kSelThreads = 1024;
 
-// Sum over the CTA of one int per thread (every thread gets it).
-__device__ __forceinline__ int cta_sum(int v, int* scratch) {
-  v = __reduce_add_sync(0xffffffffu, v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  const int w = threadIdx.x & 31;
-  return __reduce_add_sync(0xffffffffu, w < (int)(blockDim.x >> 5) ? scratch[w] : 0);
-}
+// Sums over the CTA, one barrier each: consecutive sums use the two halves of the scratch in
+// turn, so that a thread may write the next one while others read this one.
+struct CtaSum {
+  int (*scratch)[32];
+  int turn;
+  __device__ __forceinline__ int operator()(int v) {
+    v = __reduce_add_sync(0xffffffffu, v);
+    if ((threadIdx.x & 31) == 0) scratch[turn][threadIdx.x >> 5] = v;
+    __syncthreads();
+    const int w = threadIdx.x & 31;
+    v = __reduce_add_sync(0xffffffffu, w < (int)(blockDim.x >> 5) ? scratch[turn][w] : 0);
+    turn ^= 1;
+    return v;
+  }
+};
 
-// The largest t with at least `want` of the n keys ≥ t (want ≥ 1, want ≤ n): bit by bit, one
-// count of the CTA per bit, stopping early at a count that is `want` exactly.
-template <typename K, typename F>
-__device__ __forceinline__ K kth_key(int n, int want, int bits, F key, int* scratch) {
-  K t = 0;
-  for (int bit = bits - 1; bit >= 0; --bit) {
+// The largest t ≥ start with at least `want` of the keys ≥ t (start has at least that many):
+// bit by bit from `bit` down, one count per bit, stopping at a count that is `want` exactly.
+// Bits above are those of start.
+template <typename K, typename Count>
+__device__ __forceinline__ K kth_key(K start, int bit, int want, CtaSum& sum, Count count) {
+  K t = start;
+  for (; bit >= 0; --bit) {
     const K c = t | ((K)1 << bit);
-    int mine = 0;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) mine += key(i) >= c;
-    const int got = cta_sum(mine, scratch);
+    const int got = sum(count(c));
     if (got >= want) t = c;
     if (got == want) break;
   }
@@ -301,94 +362,141 @@ __device__ __forceinline__ K kth_key(int n, int want, int bits, F key, int* scra
 // smallest score among the `want` largest, blocks above v + 2E are kept and blocks below v − 2E
 // are not, whatever the rounding.  Those between are scored again in 64 bits (the products are
 // exact there) and ranked, ties to the lowest number: the selection does not depend on the
-// order of any sum.
+// order of any sum.  The ordered scores stay in registers, kItems a thread (kItems = 0: read
+// again from the workspace, for rows of more than 16 · 1024 candidates).  Bound by the latency
+// of the counts, one per bit until the kept ones are told apart.
+template <int kItems>
 __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const SelectArgs a) {
-  extern __shared__ uint32_t s_dyn[];     // keep bits, then per-word offsets
-  __shared__ int s_red[32];
+  extern __shared__ uint32_t s_dyn[];     // keep bits
+  __shared__ int s_red[2][32];
+  __shared__ uint32_t s_low[32], s_high[32], s_err[32], s_kth[32];
   const int row = blockIdx.x, b = row / a.Hkv, h = row % a.Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarps = blockDim.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int nblk = blocks_of(a, b);
   int* list = a.list + (long long)row * a.keep;
   if (nblk <= a.keep) {
     for (int i = tid; i < a.keep; i += blockDim.x) list[i] = i < nblk ? i : -1;
     return;
   }
+  CtaSum sum{s_red, 0};
   const int words = (nblk + 31) / 32;
   uint32_t* bits = s_dyn;
-  const float* score = a.score + (long long)row * a.nb;
   const int lo = a.first, n = nblk - a.first - a.last;      // candidates lo .. lo + n − 1
-  const int want = a.keep - a.first - a.last;
-  for (int i = tid; i < words; i += blockDim.x) bits[i] = 0;
-  float err = 0.f;
+  const float* score = a.score + (long long)row * a.nb + lo;
+  const int want = a.keep - a.first - a.last;               // < n
+  // visits (candidate, ordered score) of this thread
+  uint32_t keys[kItems > 0 ? kItems : 1];
+  if (kItems > 0) {
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const int i = tid + k * (int)blockDim.x;
+      keys[k] = i < n ? ordered(score[i]) : 0u;     // (0 is below every number's)
+    }
+  }
+  auto each = [&](auto&& f) {
+    if (kItems > 0) {
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        const int i = tid + k * (int)blockDim.x;
+        if (i < n) f(i, keys[k]);
+      }
+    } else {
+      for (int i = tid; i < n; i += blockDim.x) f(i, ordered(score[i]));
+    }
+  };
+  for (int i = tid; i < words; i += blockDim.x) {
+    // the forced blocks' bits of this word
+    uint32_t m = 0;
+    const int w0 = 32 * i;
+    for (int k = 0; k < 32; ++k)
+      if (w0 + k < nblk && (w0 + k < a.first || w0 + k >= nblk - a.last)) m |= 1u << k;
+    bits[i] = m;
+  }
+  uint32_t low = ~0u, high = 0u, worst = 0u;
+  each([&](int, uint32_t k) {
+    low = min(low, k);
+    high = max(high, k);
+  });
   for (int i = tid; i < (nblk + kPerCta - 1) / kPerCta; i += blockDim.x) {
     const float e = a.err[(long long)row * a.chunks + i];
-    err = e <= err ? err : e;
+    worst = max(worst, e != e ? ~0u : __float_as_uint(e));     // NaN above all
   }
-  // the largest bound of the row, NaN above all
-  const uint32_t worst = __reduce_max_sync(0xffffffffu, err != err ? ~0u : __float_as_uint(err));
-  if (lane == 0) s_red[warp] = (int)worst;
+  low = __reduce_min_sync(0xffffffffu, low);
+  high = __reduce_max_sync(0xffffffffu, high);
+  worst = __reduce_max_sync(0xffffffffu, worst);
+  if (lane == 0) {
+    s_low[warp] = low;
+    s_high[warp] = high;
+    s_err[warp] = worst;
+  }
   __syncthreads();
-  const uint32_t wall = __reduce_max_sync(0xffffffffu, lane < nwarps ? (uint32_t)s_red[lane] : 0u);
+  low = __reduce_min_sync(0xffffffffu, lane < nwarps ? s_low[lane] : ~0u);
+  high = __reduce_max_sync(0xffffffffu, lane < nwarps ? s_high[lane] : 0u);
+  worst = __reduce_max_sync(0xffffffffu, lane < nwarps ? s_err[lane] : 0u);
   // eight multiply-adds and five additions per lane and shuffle, half a step of 32 bits each:
   // 13·2^-24·Σ|terms|; 2^-20 leaves room for the rounding of the bound itself
-  const float E = wall == ~0u ? INFINITY : __uint_as_float(wall) * 9.5367431640625e-7f;
-  for (int i = tid; i < a.first; i += blockDim.x) atomicOr(&bits[i >> 5], 1u << (i & 31));
-  for (int i = nblk - a.last + tid; i < nblk; i += blockDim.x) atomicOr(&bits[i >> 5], 1u << (i & 31));
+  const float E = worst == ~0u ? INFINITY : __uint_as_float(worst) * 9.5367431640625e-7f;
   if (want > 0) {
-    auto key = [&](int i) { return ordered(score[lo + i]); };
-    const uint32_t t = kth_key<uint32_t>(n, want, 32, key, s_red);
+    // all keys agree above the highest bit in which low and high differ
+    const int top = low == high ? -1 : 31 - __clz((int)(low ^ high));
+    const uint32_t start = top < 0 ? low : high & ~((2u << top) - 1u);
+    const uint32_t t = kth_key<uint32_t>(start, top, want, sum, [&](uint32_t c) {
+      int mine = 0;
+      each([&](int, uint32_t k) { mine += k >= c; });
+      return mine;
+    });
     // v: the smallest key ≥ t
     uint32_t v = ~0u;
-    for (int i = tid; i < n; i += blockDim.x) {
-      const uint32_t k = key(i);
+    each([&](int, uint32_t k) {
       if (k >= t) v = min(v, k);
-    }
+    });
     v = __reduce_min_sync(0xffffffffu, v);
+    if (lane == 0) s_kth[warp] = v;
     __syncthreads();
-    if (lane == 0) s_red[warp] = (int)v;
-    __syncthreads();
-    v = __reduce_min_sync(0xffffffffu, lane < nwarps ? (uint32_t)s_red[lane] : ~0u);
+    v = __reduce_min_sync(0xffffffffu, lane < nwarps ? s_kth[lane] : ~0u);
     const float vf = unordered(v);
     const float up = vf + 2.f * E, down = vf - 2.f * E;
     // kept whatever the rounding; in doubt (with an infinite E every block is)
     int sure = 0, open = 0;
-    for (int i = tid; i < n; i += blockDim.x) {
-      const float s = score[lo + i];
+    each([&](int i, uint32_t k) {
+      const float s = unordered(k);
       const bool in = s > up, out = s < down;
       sure += in;
       open += !in && !out;
       if (in) atomicOr(&bits[(lo + i) >> 5], 1u << ((lo + i) & 31));
-    }
-    sure = cta_sum(sure, s_red);
-    open = cta_sum(open, s_red);
+    });
+    sure = sum(sure);
+    open = sum(open);
     const int need = want - sure;
     int* doubt = a.doubt + (long long)row * a.nb;
     unsigned long long* exact = a.exact + (long long)row * a.nb;
     if (open <= need) {
-      for (int i = tid; i < n; i += blockDim.x) {
-        const float s = score[lo + i];
+      each([&](int i, uint32_t k) {
+        const float s = unordered(k);
         if (!(s > up) && !(s < down)) atomicOr(&bits[(lo + i) >> 5], 1u << ((lo + i) & 31));
-      }
+      });
     } else {
-      // the blocks in doubt, in ascending order, each warp of 32 candidates at a time
+      // the blocks in doubt, in ascending order
       int base = 0;
       for (int i0 = 0; i0 < n; i0 += blockDim.x) {
         const int i = i0 + tid;
-        const float s = i < n ? score[lo + i] : 0.f;
+        const float s = i < n ? score[i] : 0.f;
         const bool d = i < n && !(s > up) && !(s < down);
         const uint32_t vote = __ballot_sync(0xffffffffu, d);
         __syncthreads();
-        if (lane == 0) s_red[warp] = __popc(vote);
+        if (lane == 0) s_red[0][warp] = __popc(vote);
         __syncthreads();
-        const int c = lane < nwarps ? s_red[lane] : 0;
+        const int c = lane < nwarps ? s_red[0][lane] : 0;
         const int before = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
         if (d) doubt[base + before + __popc(vote & ((1u << lane) - 1))] = lo + i;
         base += __reduce_add_sync(0xffffffffu, c);
       }
       __syncthreads();
       // (a row of zero queries has nothing to score: every term is 0)
-      for (int i = tid; wall == 0u && i < open; i += blockDim.x) exact[i] = ordered(0.0);
-      for (int i = warp; wall != 0u && i < open; i += nwarps) {
+      for (int i = tid; worst == 0u && i < open; i += blockDim.x) exact[i] = ordered(0.0);
+      for (int i = warp; worst != 0u && i < open; i += nwarps) {
         const __nv_bfloat16* p = bounds_at(a, b, h, doubt[i]);
         double best = -INFINITY;
         for (int g = 0; p && g < a.G; ++g) {
@@ -407,22 +515,26 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const SelectA
         if (lane == 0) exact[i] = ordered(best);
       }
       __syncthreads();
-      auto key64 = [&](int i) { return exact[i]; };
-      const unsigned long long t64 = kth_key<unsigned long long>(open, need, 64, key64, s_red);
-      // above t64, and of those at it (or from it on, where the count was exact) the first
+      const unsigned long long t64 =
+          kth_key<unsigned long long>(0ull, 63, need, sum, [&](unsigned long long c) {
+            int mine = 0;
+            for (int i = tid; i < open; i += blockDim.x) mine += exact[i] >= c;
+            return mine;
+          });
       int above = 0;
       for (int i = tid; i < open; i += blockDim.x) above += exact[i] > t64;
-      above = cta_sum(above, s_red);
-      int left = need - above, at = 0;    // places for keys equal to t64, in ascending order
+      above = sum(above);
+      const int left = need - above;    // places for keys equal to t64, in ascending order
+      int at = 0;
       for (int i0 = 0; i0 < open; i0 += blockDim.x) {
         const int i = i0 + tid;
         const unsigned long long k = i < open ? exact[i] : 0ull;
         const bool eq = i < open && k == t64;
         const uint32_t vote = __ballot_sync(0xffffffffu, eq);
         __syncthreads();
-        if (lane == 0) s_red[warp] = __popc(vote);
+        if (lane == 0) s_red[0][warp] = __popc(vote);
         __syncthreads();
-        const int c = lane < nwarps ? s_red[lane] : 0;
+        const int c = lane < nwarps ? s_red[0][lane] : 0;
         const int before = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
         const bool in = i < open && (k > t64 || (eq && at + before + __popc(vote & ((1u << lane) - 1)) < left));
         if (in) atomicOr(&bits[doubt[i] >> 5], 1u << (doubt[i] & 31));
@@ -443,9 +555,9 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const SelectA
       const int x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
-    if (lane == 31) s_red[warp] = incl;
+    if (lane == 31) s_red[0][warp] = incl;
     __syncthreads();
-    const int ws = lane < nwarps ? s_red[lane] : 0;
+    const int ws = lane < nwarps ? s_red[0][lane] : 0;
     int at = base + __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0) + incl - c;
     base += __reduce_add_sync(0xffffffffu, ws);
     while (m) {
@@ -461,6 +573,43 @@ template <typename T>
 void launch_bounds_t(const BoundsArgs& a, bool vec, unsigned grid, cudaStream_t stream) {
   if (vec) block_bounds_kernel<T, true><<<grid, 256, 0, stream>>>(a);
   else block_bounds_kernel<T, false><<<grid, 256, 0, stream>>>(a);
+}
+
+cudaLaunchConfig_t config(dim3 grid, unsigned block, size_t smem, cudaStream_t stream,
+                          cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(block);
+  c.dynamicSmemBytes = smem;
+  c.stream = stream;
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = attr;
+  c.numAttrs = 1;
+  return c;
+}
+
+tq_status launch_score(const SelectArgs& a, int G, dim3 grid, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = config(grid, 256, 0, stream, attr);
+  return tq_cuda_status(cudaLaunchKernelEx(&cfg, G <= 1 ? block_score_kernel<1>
+                                                 : G <= 2 ? block_score_kernel<2>
+                                                 : G <= 4 ? block_score_kernel<4>
+                                                          : block_score_kernel<8>, a));
+}
+
+tq_status launch_select(const SelectArgs& a, int rows, int nb, cudaStream_t stream) {
+  // about four candidates a thread, 16 where that is not enough threads
+  const int threads = std::min(kSelThreads, std::max(128, ((nb + 3) / 4 + 31) / 32 * 32));
+  auto kern = nb <= 4 * threads ? block_select_kernel<4>
+            : nb <= 16 * threads ? block_select_kernel<16> : block_select_kernel<0>;
+  const size_t smem = (size_t)(nb + 31) / 32 * sizeof(uint32_t);
+  if (smem > 40 * 1024 &&
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return TQ_ERR_CUDA;
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = config(dim3(rows), threads, smem, stream, attr);
+  return tq_cuda_status(cudaLaunchKernelEx(&cfg, kern, a));
 }
 
 struct SelPlan {
@@ -550,7 +699,7 @@ extern "C" tq_status tq_block_select(const tq_attn_desc* desc, const void* q, tq
   if ((st = tq_rowmap_of(blocks.pages, desc->capacity, &a.map)) != TQ_OK) return st;
   if (desc->batch == 0) return TQ_OK;
   char* ws = static_cast<char*>(workspace);
-  a.q = q; a.q_dtype = desc->q_dtype;
+  a.q = q; a.q_dtype = desc->q_dtype; a.q_vec = aligned16(q);
   a.bounds = reinterpret_cast<const __nv_bfloat16*>(blocks.bounds);
   a.capacity = desc->capacity; a.max_len = desc->max_seq_len;
   a.seq_lens = seq_lens;
@@ -564,25 +713,6 @@ extern "C" tq_status tq_block_select(const tq_attn_desc* desc, const void* q, tq
   a.list = list;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   const int rows = desc->batch * desc->kv_heads;
-  const dim3 grid(p.chunks, rows);
-  if (p.G <= 1) block_score_kernel<1><<<grid, 256, 0, stream>>>(a);
-  else if (p.G <= 2) block_score_kernel<2><<<grid, 256, 0, stream>>>(a);
-  else if (p.G <= 4) block_score_kernel<4><<<grid, 256, 0, stream>>>(a);
-  else block_score_kernel<8><<<grid, 256, 0, stream>>>(a);
-  if ((st = tq_cuda_status(cudaGetLastError())) != TQ_OK) return st;
-  // about four blocks a thread
-  const int want = (p.nb + 3) / 4;
-  const int threads = std::min(kSelThreads, std::max(128, (want + 31) / 32 * 32));
-  const size_t smem = (size_t)(p.nb + 31) / 32 * sizeof(uint32_t);
-  static bool configured[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return TQ_ERR_CUDA;
-  if (!configured[dev]) {
-    if (cudaFuncSetAttribute(block_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             200 * 1024) != cudaSuccess)
-      return TQ_ERR_CUDA;
-    configured[dev] = true;
-  }
-  block_select_kernel<<<rows, threads, smem, stream>>>(a);
-  return tq_cuda_status(cudaGetLastError());
+  if ((st = launch_score(a, p.G, dim3(p.chunks, rows), stream)) != TQ_OK) return st;
+  return launch_select(a, rows, p.nb, stream);
 }

@@ -641,13 +641,12 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
   __syncthreads();
   tc_after();
   // all 512 columns were asked for, so they begin at address 0: addresses are constants
-  constexpr uint32_t tmem = 0;
   bool ok = sm.tmem == 0;   // false once a bounded wait gave up: every role then leaves its loop
   auto wait = [&](uint64_t* bar, unsigned parity) {
     return ok = ok && warp_wait(bar, parity);
   };
 
-  if (warp < 8) {
+  if (warp < kKeyWarp) {
     // ================================================================ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int wl = warp & 3, hf = warp >> 2;
@@ -841,64 +840,87 @@ rows_prep_kernel(const void* q, int q_dtype, int nrows, const float* __restrict_
 
 // ---------------------------------------------------------------- merge
 // Rows' records added up with their log-sum-exp weights, then out = Πᵀ·acc / l.  kRows rows per
-// CTA share the reads of Π; 512 threads: 128 columns × 4 quarters (of the records, then of k).
+// CTA of 16 warps: a warp per (row, share of its records), eight 512-byte reads in flight; then
+// 128 columns × 4 quarters of k, the rows sharing the reads of Π.  Bound by the latency of three
+// dependent steps (statistics, records, Π) and, for many rows, by reading the records from L2.
 constexpr int kMergeThreads = 512;
+constexpr int kMaxRecs = 512;           // records of a row (make_plan keeps to it)
 template <int kRows>
 __global__ void __launch_bounds__(kMergeThreads)
 rows_merge_kernel(const float* rec, int nrec, int nrows, const float* __restrict__ pi, int nibbles,
                   float unscale, void* out, int out_dtype) {
-  __shared__ float acc[4][kRows][TQ_D];
+  constexpr int kShares = 16 / kRows;
+  __shared__ float acc[16][TQ_D];
   __shared__ float sum[kRows][TQ_D];
-  __shared__ float ref[kRows], total[kRows];
-  const int tid = threadIdx.x, j = tid & 127, kq = tid >> 7, row0 = blockIdx.x * kRows;
+  __shared__ float weight[kRows][kMaxRecs];
+  __shared__ float total[kRows];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int j = tid & 127, kq = tid >> 7, row0 = blockIdx.x * kRows;
   float w[32];   // Π does not depend on the launch before
 #pragma unroll
   for (int k = 0; k < 32; ++k) w[k] = __ldg(pi + (32 * kq + k) * TQ_D + j);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long stride = (long long)nrows * kRecFloats;
-  if (tid < 32 * kRows) {
-    const int r = tid >> 5, lane = tid & 31;
-    if (row0 + r < nrows) {
-      const float* p = rec + (long long)(row0 + r) * kRecFloats + 128;
-      float m = -INFINITY;
-      for (int s = lane; s < nrec; s += 32)
-        if (p[s * stride + 1] != 0.f) m = fmaxf(m, p[s * stride]);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      float l = 0.f;
-      for (int s = lane; s < nrec; s += 32) {
-        const float ls = p[s * stride + 1];
-        if (ls != 0.f) l += ls * ex2(p[s * stride] - m);
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      if (lane == 0) {
-        ref[r] = m;
-        total[r] = l;
-      }
+  if (warp < kRows) {
+    const int row = min(row0 + warp, nrows - 1);
+    const float* p = rec + (long long)row * kRecFloats + 128;
+    float m = -INFINITY;
+    for (int s = lane; s < nrec; s += 32) {
+      const float2 ml = *reinterpret_cast<const float2*>(p + s * stride);
+      // an empty record weighs nothing; a NaN sum (a NaN query) makes the row NaN
+      weight[warp][s] = ml.y != ml.y ? ml.y : ml.y != 0.f ? ml.x : -INFINITY;
+      if (ml.y != 0.f) m = fmaxf(m, ml.x);
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f;
+    for (int s = lane; s < nrec; s += 32) {
+      const float ls = p[s * stride + 1], ms = weight[warp][s];
+      const float ws = ms == -INFINITY ? 0.f : ex2(ms - m);
+      weight[warp][s] = ws;
+      if (ws != 0.f) l = fmaf(ls, ws, l);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) total[warp] = l;
   }
   __syncthreads();
-  // the position that column j is read at (the value operand's order)
+  {
+    const int r = warp / kShares, share = warp % kShares;
+    const float* p = rec + (long long)min(row0 + r, nrows - 1) * kRecFloats + 4 * lane;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = share; i0 < nrec; i0 += 8 * kShares) {
+      float4 x[8];
+      float ws[8];
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    float s = 0.f;
-    if (row0 + r < nrows) {
-      const float* p = rec + (long long)(row0 + r) * kRecFloats;
-      for (int i = kq; i < nrec; i += 4) {
-        const float ls = p[i * stride + 129];
-        if (ls != 0.f) s = fmaf(p[i * stride + j], ex2(p[i * stride + 128] - ref[r]), s);
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + k * kShares;
+        ws[k] = i < nrec ? weight[r][i] : 0.f;
+        x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (ws[k] != 0.f) x[k] = *reinterpret_cast<const float4*>(p + i * stride);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        s.x = fmaf(x[k].x, ws[k], s.x);
+        s.y = fmaf(x[k].y, ws[k], s.y);
+        s.z = fmaf(x[k].z, ws[k], s.z);
+        s.w = fmaf(x[k].w, ws[k], s.w);
       }
     }
-    acc[kq][r][j] = s;
+    *reinterpret_cast<float4*>(&acc[warp][4 * lane]) = s;
   }
   __syncthreads();
   for (int i = tid; i < kRows * TQ_D; i += kMergeThreads) {
     const int r = i >> 7, c = i & 127;
-    sum[r][nibbles ? c : plane_coord(c)] =
-        (acc[0][r][c] + acc[1][r][c]) + (acc[2][r][c] + acc[3][r][c]);
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < kShares; ++k) s += acc[r * kShares + k][c];
+    // the value operand's order of coordinates
+    sum[r][nibbles ? c : plane_coord(c)] = s;
   }
   __syncthreads();
+  float (*prod)[kRows][TQ_D] = reinterpret_cast<float (*)[kRows][TQ_D]>(acc);   // 4 quarters
+  float part[kRows];
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     float s = 0.f;
@@ -910,14 +932,16 @@ rows_merge_kernel(const float* rec, int nrec, int nrows, const float* __restrict
       s = fmaf(w[k + 2], x.z, s);
       s = fmaf(w[k + 3], x.w, s);
     }
-    acc[kq][r][j] = s;
+    part[r] = s;
   }
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) prod[kq][r][j] = part[r];
   __syncthreads();
   for (int i = tid; i < kRows * TQ_D; i += kMergeThreads) {
     const int r = i >> 7, c = i & 127;
     if (row0 + r >= nrows) continue;
     const float l = total[r];
-    const float s = (acc[0][r][c] + acc[1][r][c]) + (acc[2][r][c] + acc[3][r][c]);
+    const float s = (prod[0][r][c] + prod[1][r][c]) + (prod[2][r][c] + prod[3][r][c]);
     const float o = l == 0.f ? 0.f : s * unscale / l;
     const long long at = (long long)(row0 + r) * TQ_D + c;
     if (out_dtype == TQ_BF16) static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(o);
@@ -933,10 +957,56 @@ struct Plan {
   size_t qf_off, rec_off, bytes;
 };
 
-// Splits that make the estimated time least: an item costs its tiles and about kFixed tiles of
-// start and end; items that fit one wave take as long as the longest, more of them as long as
-// an even share of the SMs and half an item.
-constexpr int kFixed = 4;
+// Time of a grid of n1 items of c1 tiles each and then n2 items of c2, taken in order by `sms` SMs
+// that each work on one (in tiles).
+double makespan(long long n1, double c1, long long n2, double c2, long long sms) {
+  const long long rest = n1 % sms;            // items of the last, partial wave of the first kind
+  const double start = (double)(n1 / sms) * c1;
+  const double until = rest ? start + c1 : start;
+  // second-kind items that the other SMs take meanwhile, then all of them
+  const long long beside = rest ? (sms - rest) * (long long)(c1 / c2) : 0;
+  if (n2 <= beside) return until;
+  return until + (double)((n2 - beside + sms - 1) / sms) * c2;
+}
+
+// Splits that make the estimated time least (find_splits).  An item costs its tiles and about three tiles of
+// start and end (measured: 8,600 cycles, where a tile takes 3,000 to 4,000).
+constexpr double kFixed = 3.0;
+// The arguments that the splits follow from, and what they came to: a call looks its splits up
+// (the search takes some microseconds).
+struct Splits {
+  long long pu, pre, ou, own, sms;
+  int sp, so;
+};
+
+void find_splits(Splits* x) {
+  double best = 0;
+  const long long pre_tiles = x->pre, own_tiles = x->own;
+  // tiles per item of either kind; both grow by steps of an eighth
+  for (long long lp = 1;; lp += std::max<long long>(1, lp / 8)) {
+    lp = std::min(lp, std::max<long long>(pre_tiles, 1));
+    const long long sp = pre_tiles > 0 ? (pre_tiles + lp - 1) / lp : 0;
+    for (long long lo = 1;; lo += std::max<long long>(1, lo / 8)) {
+      lo = std::min(lo, std::max<long long>(own_tiles, 1));
+      const long long so = std::max<long long>((own_tiles + lo - 1) / lo, 1);
+      const bool last = lo >= own_tiles && lp >= pre_tiles;
+      if (sp + so <= kMaxRecs || last) {
+        const double cp = sp ? (double)((pre_tiles + sp - 1) / sp) + kFixed : 0;
+        const double co = (double)((own_tiles + so - 1) / so) + kFixed;
+        // more records cost the merge: about a tile's time for 64 of them
+        const double t = makespan(x->pu * sp, cp, x->ou * so, co, x->sms) + (double)(sp + so) / 64;
+        if (!x->so || t < best) {
+          best = t;
+          x->sp = (int)sp;
+          x->so = (int)so;
+        }
+      }
+      if (lo >= own_tiles) break;
+    }
+    if (lp >= pre_tiles) break;
+  }
+}
+
 tq_status make_plan(const tq_attn_desc* d, long long pre_tiles, long long own_tiles, Plan* p) {
   if (!d) return TQ_ERR_INVALID_ARG;
   if (d->head_dim != TQ_HEAD_DIM) return TQ_ERR_UNSUPPORTED;
@@ -955,29 +1025,18 @@ tq_status make_plan(const tq_attn_desc* d, long long pre_tiles, long long own_ti
   const int n = tq_num_sms();
   const long long sms = n > 0 ? n : 152;
   const long long pu = (long long)p->row_tiles * d->kv_heads, ou = (long long)d->batch * d->kv_heads;
-  double best = 0;
-  p->pre_splits = p->own_splits = 1;
-  bool first = true;
-  const long long longest = std::max<long long>(std::max(pre_tiles, own_tiles), 1);
-  for (long long L = 1;; L += std::max<long long>(1, L / 8)) {
-    L = std::min(L, longest);
-    const long long sp = std::max<long long>((pre_tiles + L - 1) / L, pre_tiles > 0 ? 1 : 0);
-    const long long so = std::max<long long>((own_tiles + L - 1) / L, 1);
-    if (sp + so <= 512 || L == longest) {
-      const long long items = pu * sp + ou * so;
-      const double lp = sp ? (double)((pre_tiles + sp - 1) / sp) : 0, lo = (double)((own_tiles + so - 1) / so);
-      const double most = std::max(lp, lo) + kFixed;
-      const double work = (double)pu * pre_tiles + (double)ou * own_tiles + (double)items * kFixed;
-      const double est = items <= sms ? most : std::max(most, work / sms + 0.5 * most);
-      if (first || est < best) {
-        best = est;
-        first = false;
-        p->pre_splits = (int)sp;
-        p->own_splits = (int)so;
-      }
-    }
-    if (L >= longest) break;
+  thread_local Splits known[8];
+  thread_local int next = 0;
+  Splits want{pu, pre_tiles, ou, own_tiles, sms, 0, 0};
+  for (const Splits& k : known)
+    if (k.so && k.pu == pu && k.pre == pre_tiles && k.ou == ou && k.own == own_tiles && k.sms == sms) want = k;
+  if (!want.so) {
+    find_splits(&want);
+    known[next] = want;
+    next = (next + 1) % 8;
   }
+  p->pre_splits = want.sp;
+  p->own_splits = want.so;
   if (pu * p->pre_splits + ou * p->own_splits > 0x7fffffffLL) return TQ_ERR_UNSUPPORTED;
   p->qf_off = (size_t)p->rows * 512;
   p->rec_off = (p->qf_off + (size_t)p->rows * sizeof(float) + 255) / 256 * 256;
@@ -1061,17 +1120,17 @@ tq_status launch_k(const RowsArgs& a, int vbits, unsigned items, cudaStream_t st
   return TQ_ERR_UNSUPPORTED;
 }
 
-// Rows per CTA of the two kernels around: the fewest (1, 2, 4, 8) that keep about one CTA per SM.
-int rows_per_cta(int rows) {
+// Rows per CTA of the two kernels around: the fewest (1, 2, 4, most) that keep about one CTA per SM.
+int rows_per_cta(int rows, int most) {
   const int sms = std::max(tq_num_sms(), 1);
-  for (int r = 1; r < 8; r *= 2)
+  for (int r = 1; r < most; r *= 2)
     if ((rows + r - 1) / r <= sms) return r;
-  return 8;
+  return most;
 }
 
 tq_status launch_prep(const void* q, int q_dtype, int rows, const tq_codec* kc, float factor,
                       void* qop, float* qf, cudaStream_t stream) {
-  const int rp = rows_per_cta(rows);
+  const int rp = rows_per_cta(rows, 8);
   auto kern = rp == 1 ? rows_prep_kernel<1> : rp == 2 ? rows_prep_kernel<2>
             : rp == 4 ? rows_prep_kernel<4> : rows_prep_kernel<8>;
   cudaLaunchAttribute attr[1];
@@ -1083,9 +1142,8 @@ tq_status launch_prep(const void* q, int q_dtype, int rows, const tq_codec* kc, 
 
 tq_status launch_merge(const float* rec, int nrec, int rows, const tq_codec* vc, void* out,
                        int out_dtype, cudaStream_t stream) {
-  const int rp = rows_per_cta(rows);
-  auto kern = rp == 1 ? rows_merge_kernel<1> : rp == 2 ? rows_merge_kernel<2>
-            : rp == 4 ? rows_merge_kernel<4> : rows_merge_kernel<8>;
+  const int rp = rows_per_cta(rows, 4);
+  auto kern = rp == 1 ? rows_merge_kernel<1> : rp == 2 ? rows_merge_kernel<2> : rows_merge_kernel<4>;
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = config((rows + rp - 1) / rp, kMergeThreads, 0, stream, attr);
   return tq_cuda_status(cudaLaunchKernelEx(&cfg, kern, rec, nrec, rows, (const float*)vc->d_pi,
