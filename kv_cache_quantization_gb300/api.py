@@ -350,12 +350,21 @@ class PrefillPlan:
 
 # ------------------------------------------------------------------ long contexts
 
-def _on_device(*tensors):
-    """The library works on the current device: tensors of another one are refused."""
-    d = torch.cuda.current_device()
+# These calls run once per layer and step and mostly in less time than a careful wrapper takes, so
+# their checks read each property once and the library is called with plain integers.
+
+def _device(*tensors):
+    """The current device, which the library works on: tensors of another one are refused."""
+    d = torch._C._cuda_getDevice()
     for t in tensors:
-        if t is not None and t.get_device() != d:
+        if t.get_device() != d:
             raise ValueError(f"expected tensors on the current device cuda:{d}, got one on {t.device}")
+    return d
+
+
+def _on(stream, device):
+    """Handle of the stream: the device's current one by default."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def _expect(t: torch.Tensor, shape, dtype, name):
@@ -364,17 +373,22 @@ def _expect(t: torch.Tensor, shape, dtype, name):
                          f"got {t.dtype} {list(t.shape)}")
 
 
-def _expect_caches(k: "ProdCache", v: "MSECache", rows, heads, capacity, kc, vc, name):
-    """Shapes of a pair of caches (or pools) for `rows` sequences of `capacity` slots."""
-    for c, what in ((k, "key"), (v, "value")):
-        norms = c.xnorm
-        if c.capacity != capacity or norms.shape[1] != heads:
-            raise ValueError(f"{name}: {what} cache of {norms.shape[1]} heads and {c.capacity} slots, "
-                             f"expected {heads} and {capacity}")
-        if c.pages is None and norms.shape[0] < rows or \
-                c.pages is not None and (c.pages.block_table.shape[0] < rows or
-                                         norms.shape[0] < c.pages.num_pages):
-            raise ValueError(f"{name}: {what} cache has too few sequences or pages")
+def _fits(shape, pages, rows, heads, slots):
+    """Whether arrays of leading dimensions `shape` hold `rows` sequences of `slots` slots."""
+    if shape[1] != heads:
+        return False
+    if pages is None:
+        return shape[0] >= rows and shape[2] == slots
+    return (shape[0] >= pages.num_pages and shape[2] == pages.page_tokens and
+            pages.capacity == slots and pages.block_table.shape[0] >= rows)
+
+
+def _expect_caches(k: "ProdCache", v: "MSECache", rows, heads, slots, kc, vc, name):
+    """Shapes of a pair of caches (or pools) for `rows` sequences of `slots` slots."""
+    if not (_fits(k.xnorm.shape, k.pages, rows, heads, slots) and
+            _fits(v.xnorm.shape, v.pages, rows, heads, slots)):
+        raise ValueError(f"{name}: expected {rows} sequences or a block table for them, {heads} heads and "
+                         f"{slots} slots, got keys {list(k.xnorm.shape)} and values {list(v.xnorm.shape)}")
     if k.idx.shape[2] != kc.index_bits or v.bits != vc.bits:
         raise ValueError(f"{name}: the caches hold codes of other widths than the codecs'")
 
@@ -407,27 +421,35 @@ class BlockBounds:
     def c(self):
         return B.tq_block_cache(self.bounds.data_ptr(), _pages_ptr(self.pages))
 
-    def expect(self, rows, heads):
-        s = self.bounds.shape
-        blocks = self.bounds.shape[2] if self.pages is None \
-            else self.pages.page_tokens // B.TQ_BLOCK_TOKENS
-        _expect(self.bounds, (s[0], heads, blocks, 2, HEAD_DIM), torch.bfloat16, "bounds")
-        if s[0] < (rows if self.pages is None else self.pages.num_pages) or \
-                self.pages is not None and self.pages.block_table.shape[0] < rows:
-            raise ValueError("bounds have too few sequences or pages")
+    def expect(self, rows, heads, slots):
+        """Refuses bounds that are not those of `rows` sequences of `slots` slots."""
+        t, p = self.bounds, self.pages
+        n = slots if p is None else p.page_tokens
+        s = t.shape
+        if s != (s[0], heads, n // B.TQ_BLOCK_TOKENS, 2, HEAD_DIM) or t.dtype != torch.bfloat16 or \
+                not t.is_contiguous() or s[0] < (rows if p is None else p.num_pages) or \
+                p is not None and (p.capacity != slots or p.block_table.shape[0] < rows):
+            raise ValueError(f"bounds: expected {rows} sequences or a block table for them, {heads} heads "
+                             f"and {slots} slots, got {t.dtype} {list(s)}")
 
 
 def block_bounds(x: torch.Tensor, blocks: BlockBounds, pos=None, count=None, stream=None):
     """Folds keys x [batch, heads, tokens, 128] into their blocks' bounds, at the cache positions
     pos[b].. (0) and count[b] tokens each (all): the arguments of quantize_prod."""
     bsz, h, t, sb, sh, st = _x_args(x)
-    _on_device(x, blocks.bounds, pos, count)
-    blocks.expect(bsz, h)
-    for n, v in (("pos", pos), ("count", count)):
+    slots = blocks.capacity
+    blocks.expect(bsz, h, slots)
+    d = _device(x, blocks.bounds)
+    for v in (pos, count):
         if v is not None:
-            _expect(v, (bsz,), torch.int32, n)
-    B.check(B.tq_block_bounds(x, tq_dtype(x.dtype), bsz, h, t, sb, sh, st, pos, count, blocks.c(),
-                              blocks.capacity, _stream(stream)), "tq_block_bounds")
+            _expect(v, (bsz,), torch.int32, "pos and count")
+            _device(v)
+    st = B.load().tq_block_bounds(x.data_ptr(), tq_dtype(x.dtype), bsz, h, t, sb, sh, st,
+                                  None if pos is None else pos.data_ptr(),
+                                  None if count is None else count.data_ptr(), blocks.c(), slots,
+                                  _on(stream, d))
+    if st:
+        B.check(st, "tq_block_bounds")
 
 
 class SparsePlan:
@@ -447,7 +469,9 @@ class SparsePlan:
         if 0 in sizes or first_blocks < 0 or last_blocks < 0 or \
                 first_blocks + last_blocks > max_blocks:
             raise ValueError("invalid sparse-attention configuration")
-        self.workspace = torch.empty(max(sizes), dtype=torch.uint8, device=device)
+        self.nbytes = max(sizes)
+        self.workspace = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        self.rows, self.list_shape = (batch,), (batch, kv_heads, max_blocks)
         self.max_blocks, self.first_blocks, self.last_blocks = max_blocks, first_blocks, last_blocks
         self.batch, self.kv_heads, self.capacity = batch, kv_heads, _cap(capacity)
         self.q_dtype, self.out_dtype = q_dtype, out_dtype
@@ -457,37 +481,39 @@ class SparsePlan:
         return torch.empty(self.shape, dtype=self.out_dtype, device=device)
 
     def new_list(self, device="cuda"):
-        return torch.empty(self.batch, self.kv_heads, self.max_blocks, dtype=torch.int32,
-                           device=device)
+        return torch.empty(self.list_shape, dtype=torch.int32, device=device)
 
     def select(self, q, blocks: BlockBounds, seq_lens, out, stream=None):
         """The blocks of each (sequence, KV head) that q [batch, q_heads, 128] attends, ascending,
         −1 behind them, into out [batch, kv_heads, max_blocks] int32."""
-        _on_device(q, blocks.bounds, seq_lens, out, self.workspace)
+        d = _device(q, blocks.bounds, seq_lens, out, self.workspace)
         _expect(q, self.shape, self.q_dtype, "q")
-        _expect(seq_lens, (self.batch,), torch.int32, "seq_lens")
-        _expect(out, (self.batch, self.kv_heads, self.max_blocks), torch.int32, "out")
-        blocks.expect(self.batch, self.kv_heads)
-        if blocks.capacity != self.capacity:
-            raise ValueError(f"bounds of {blocks.capacity} slots, expected {self.capacity}")
-        B.check(B.tq_block_select(self.desc, q, blocks.c(), seq_lens, self.first_blocks,
-                                  self.last_blocks, self.max_blocks, out, self.workspace,
-                                  self.workspace.numel(), _stream(stream)), "tq_block_select")
+        _expect(seq_lens, self.rows, torch.int32, "seq_lens")
+        _expect(out, self.list_shape, torch.int32, "out")
+        blocks.expect(self.batch, self.kv_heads, self.capacity)
+        st = B.load().tq_block_select(self.desc, q.data_ptr(), blocks.c(), seq_lens.data_ptr(),
+                                      self.first_blocks, self.last_blocks, self.max_blocks,
+                                      out.data_ptr(), self.workspace.data_ptr(), self.nbytes,
+                                      _on(stream, d))
+        if st:
+            B.check(st, "tq_block_select")
         return out
 
     def run(self, kc: Codec, vc: Codec, q, k: ProdCache, v: MSECache, seq_lens, block_list, out,
             stream=None):
         """Attention of q over the listed blocks of the cache, into out [batch, q_heads, 128]."""
-        _on_device(q, k.idx, v.idx, seq_lens, block_list, out, self.workspace)
+        d = _device(q, k.idx, v.idx, seq_lens, block_list, out, self.workspace)
         _expect(q, self.shape, self.q_dtype, "q")
-        _expect(seq_lens, (self.batch,), torch.int32, "seq_lens")
-        _expect(block_list, (self.batch, self.kv_heads, self.max_blocks), torch.int32, "block_list")
+        _expect(seq_lens, self.rows, torch.int32, "seq_lens")
+        _expect(block_list, self.list_shape, torch.int32, "block_list")
         _expect(out, self.shape, self.out_dtype, "out")
         _expect_caches(k, v, self.batch, self.kv_heads, self.capacity, kc, vc, "cache")
-        B.check(B.tq_sparse_attention(self.desc, kc.handle, vc.handle, q, k.c(), v.c(), seq_lens,
-                                      block_list, self.max_blocks, out, self.workspace,
-                                      self.workspace.numel(), _stream(stream)),
-                "tq_sparse_attention")
+        st = B.load().tq_sparse_attention(self.desc, kc.handle, vc.handle, q.data_ptr(), k.c(), v.c(),
+                                          seq_lens.data_ptr(), block_list.data_ptr(),
+                                          self.max_blocks, out.data_ptr(),
+                                          self.workspace.data_ptr(), self.nbytes, _on(stream, d))
+        if st:
+            B.check(st, "tq_sparse_attention")
         return out
 
     def step(self, kc: Codec, vc: Codec, q, k_new, v_new, k: ProdCache, v: MSECache,
@@ -514,7 +540,9 @@ class PrefixPlan:
         nbytes = B.tq_prefix_workspace_bytes(self.desc, prefix_max_len)
         if nbytes == 0 or prefix_max_len > _cap(prefix_capacity):
             raise ValueError("invalid prefix-attention configuration")
+        self.nbytes = nbytes
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.rows = (batch,)
         self.batch, self.kv_heads, self.capacity = batch, kv_heads, _cap(capacity)
         self.prefix_capacity, self.prefix_max_len = _cap(prefix_capacity), prefix_max_len
         self.q_dtype, self.out_dtype = q_dtype, out_dtype
@@ -527,19 +555,21 @@ class PrefixPlan:
             k: ProdCache, v: MSECache, seq_lens, out, stream=None):
         """Attention of q [batch, q_heads, 128] over the prefix's prefix_len (int32 [1]) tokens and
         each sequence's own seq_lens[b] tokens."""
-        _on_device(q, prefix_k.idx, prefix_v.idx, prefix_len, k.idx, v.idx, seq_lens, out,
-                   self.workspace)
+        d = _device(q, prefix_k.idx, prefix_v.idx, prefix_len, k.idx, v.idx, seq_lens, out,
+                    self.workspace)
         _expect(q, self.shape, self.q_dtype, "q")
         _expect(prefix_len, (1,), torch.int32, "prefix_len")
-        _expect(seq_lens, (self.batch,), torch.int32, "seq_lens")
+        _expect(seq_lens, self.rows, torch.int32, "seq_lens")
         _expect(out, self.shape, self.out_dtype, "out")
         _expect_caches(prefix_k, prefix_v, 1, self.kv_heads, self.prefix_capacity, kc, vc, "prefix")
         _expect_caches(k, v, self.batch, self.kv_heads, self.capacity, kc, vc, "cache")
-        B.check(B.tq_prefix_attention(self.desc, kc.handle, vc.handle, q, prefix_k.c(),
-                                      prefix_v.c(), self.prefix_capacity, self.prefix_max_len,
-                                      prefix_len, k.c(), v.c(), seq_lens, out, self.workspace,
-                                      self.workspace.numel(), _stream(stream)),
-                "tq_prefix_attention")
+        st = B.load().tq_prefix_attention(self.desc, kc.handle, vc.handle, q.data_ptr(),
+                                          prefix_k.c(), prefix_v.c(), self.prefix_capacity,
+                                          self.prefix_max_len, prefix_len.data_ptr(), k.c(), v.c(),
+                                          seq_lens.data_ptr(), out.data_ptr(),
+                                          self.workspace.data_ptr(), self.nbytes, _on(stream, d))
+        if st:
+            B.check(st, "tq_prefix_attention")
         return out
 
 

@@ -12,6 +12,7 @@
 
 #include <algorithm>
 
+#include "tc_ptx.h"
 #include "tq_internal.h"
 
 TQ_DEFINE_FLAGS(tq_take_flags_blocks)
@@ -149,14 +150,14 @@ __global__ void __launch_bounds__(256) block_bounds_kernel(const BoundsArgs a) {
 // ---------------------------------------------------------------- selection
 struct SelectArgs {
   const void* q;
-  int q_dtype, q_vec;     // q_vec: rows are 16-byte aligned
+  int q_dtype;
   const __nv_bfloat16* bounds;
   tq_rowmap map;
   int capacity, max_len;
   const int* seq_lens;
   int Hkv, G;
   int nb;                 // blocks of max_len tokens (row stride of the workspace arrays)
-  int chunks;             // CTAs per row of the scoring kernel
+  int rounds, chunks;     // rounds of kRound blocks per CTA of the scoring kernel, CTAs per row
   int first, last, keep;
   float* score;           // [B·Hkv][nb]
   float* err;             // [B·Hkv][chunks] bounds of Σ|terms| of a chunk's blocks
@@ -165,8 +166,8 @@ struct SelectArgs {
   int* list;              // [B·Hkv][keep]
 };
 
-constexpr int kPerWarp = 4;      // blocks per warp and per CTA of the scoring kernel
-constexpr int kPerCta = 8 * kPerWarp;
+constexpr int kPerWarp = 4;      // blocks per warp and round of the scoring kernel
+constexpr int kRound = 8 * kPerWarp;
 
 __device__ __forceinline__ float load_elem(const void* base, int dtype, long long i) {
   if (dtype == TQ_F32) return static_cast<const float*>(base)[i];
@@ -189,8 +190,8 @@ __device__ __forceinline__ int blocks_of(const SelectArgs& a, int b) {
 
 // Sums over the 32 lanes of each of N values a lane: N/2 + N/4 + ... shuffles instead of 5·N.
 // Lane l ends with the sum of value l / (32 / N) (N ≤ 32, a power of two) in v[0].
-template <int N>
-__device__ __forceinline__ void lane_sums(float (&v)[N], int lane) {
+template <int N, typename T>
+__device__ __forceinline__ void lane_sums(T (&v)[N], int lane) {
 #pragma unroll
   for (int o = 16, n = N; o; o >>= 1) {
     if (n > 1) {
@@ -199,7 +200,7 @@ __device__ __forceinline__ void lane_sums(float (&v)[N], int lane) {
 #pragma unroll
       for (int i = 0; i < N / 2; ++i)
         if (i < n) {
-          const float mine = lane & o ? v[i + n] : v[i], other = lane & o ? v[i] : v[i + n];
+          const T mine = lane & o ? v[i + n] : v[i], other = lane & o ? v[i] : v[i + n];
           v[i] = mine + __shfl_xor_sync(0xffffffffu, other, o);
         }
     } else {
@@ -208,98 +209,110 @@ __device__ __forceinline__ void lane_sums(float (&v)[N], int lane) {
   }
 }
 
-// Eight consecutive values of a row of queries.
-__device__ __forceinline__ void load8(const void* base, int dtype, long long at, bool vec, float (&o)[8]) {
-  if (!vec) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = load_elem(base, dtype, at + j);
-  } else if (dtype == TQ_F32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-    const float4 x = __ldg(p), y = __ldg(p + 1);
-    o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
-    o[4] = y.x; o[5] = y.y; o[6] = y.z; o[7] = y.w;
-  } else {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint16_t u = (uint16_t)(j & 1 ? w[j / 2] >> 16 : w[j / 2] & 0xffffu);
-      o[j] = dtype == TQ_BF16 ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
-    }
-  }
-}
-
 // Scores in 32 bits of the blocks of one (sequence, KV head): the largest over the group's
-// query heads.  A warp takes four blocks with one 512-byte load each, lanes 0–15 the lower and
-// lanes 16–31 the upper bounds, each with its half of the query rows; all loads (bounds and
-// queries) are issued before any is used.  Bound by their latency for short rows (two dependent
-// loads, about 3 us in all) and by reading the bounds for long ones.
-template <int kG>
+// query heads.  A warp takes four blocks with one 512-byte load each (the next four in flight),
+// lanes 0–15 the lower and lanes 16–31 the upper bounds, against the negative and the positive
+// parts of the query rows in shared memory, four heads at a time (16 sums share their
+// shuffles).  The loop over heads is kept rolled: most calls are short, and then fetching the
+// instructions costs more than issuing them (unrolled over eight heads this kernel took 8.5 us
+// for 4 × 512 blocks).  Bound by the latency of two dependent loads for short rows, by issuing
+// about 12 instructions per block and head for long ones.
 __global__ void __launch_bounds__(256) block_score_kernel(const SelectArgs a) {
+  __shared__ float4 s_q[TQ_MAX_GROUP + 1][2][32];   // [head][first or second four][lane]; last: max |.|
   __shared__ float s_err[8];
   const int row = blockIdx.y, b = row / a.Hkv, h = row % a.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  float q[kG][8];
-#pragma unroll
-  for (int g = 0; g < kG; ++g)   // absent heads repeat head 0: the maximum over them is the same
-    load8(a.q, a.q_dtype, ((long long)row * a.G + (g < a.G ? g : 0)) * TQ_D + (lane & 15) * 8, a.q_vec, q[g]);
   const int len = a.seq_lens[b];
+  const int heads = (a.G + 3) / 4 * 4;          // absent heads repeat head 0: the maximum is the same
+  for (int i = threadIdx.x; i < heads * TQ_D; i += 256) {
+    const int g = i / TQ_D, c = i % TQ_D;
+    const float v = load_elem(a.q, a.q_dtype, ((long long)row * a.G + (g < a.G ? g : 0)) * TQ_D + c);
+    float* at = reinterpret_cast<float*>(&s_q[g][(c >> 2) & 1][c >> 3]) + (c & 3);
+    at[0] = v > 0.f ? 0.f : v;         // lanes 0–15 (NaN goes to both)
+    at[16 * 4] = v < 0.f ? 0.f : v;    // lanes 16–31
+  }
   if (len > a.max_len && blockIdx.x == 0 && h == 0 && threadIdx.x == 0)
     atomicOr(&g_tq_flags, TQ_FLAG_LEN_OVERFLOW);
-  const int nblk = blocks_of(a, b);
-  const int begin = blockIdx.x * kPerCta + warp * kPerWarp;
-  if (nblk <= a.keep || (int)blockIdx.x * kPerCta >= nblk) return;   // nothing to choose, or nothing here
-  uint4 x[kPerWarp];
-  bool in[kPerWarp];
+  const int nblk = (min(max(len, 0), a.max_len) + kBlock - 1) / kBlock;
+  const int first = blockIdx.x * a.rounds * kRound, end = min(first + a.rounds * kRound, nblk);
+  if (nblk <= a.keep || first >= end) return;   // nothing to choose, or nothing here
+  auto fetch = [&](int begin, uint4 (&x)[kPerWarp], uint32_t& in) {
+    in = 0;
 #pragma unroll
-  for (int i = 0; i < kPerWarp; ++i) {
-    const __nv_bfloat16* p = begin + i < nblk ? bounds_at(a, b, h, begin + i) : nullptr;
-    in[i] = p != nullptr;
-    x[i] = p ? __ldg(reinterpret_cast<const uint4*>(p) + lane) : make_uint4(0, 0, 0, 0);
-    if (!p && begin + i < nblk && lane == 0) atomicOr(&g_tq_flags, TQ_FLAG_PAGE);
-  }
-  float most[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    most[j] = 0.f;
-#pragma unroll
-    for (int g = 0; g < kG; ++g) {
-      const float v = q[g][j];
-      q[g][j] = (lane < 16 ? v > 0.f : v < 0.f) ? 0.f : v;   // NaN goes to both
-      most[j] = fmaxf(most[j], fabsf(q[g][j]));
+    for (int i = 0; i < kPerWarp; ++i) {
+      const __nv_bfloat16* p = begin + i < end ? bounds_at(a, b, h, begin + i) : nullptr;
+      x[i] = p ? __ldg(reinterpret_cast<const uint4*>(p) + lane) : make_uint4(0, 0, 0, 0);
+      if (p) in |= 1u << i;
+      else if (begin + i < end && lane == 0) atomicOr(&g_tq_flags, TQ_FLAG_PAGE);
     }
+  };
+  uint4 next[kPerWarp];
+  uint32_t next_in;
+  int begin = first + warp * kPerWarp;
+  fetch(begin, next, next_in);
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * TQ_D; i += 256) {
+    float m = 0.f;
+    for (int g = 0; g < a.G; ++g) m = fmaxf(m, fabsf(reinterpret_cast<const float*>(s_q[g])[i]));
+    reinterpret_cast<float*>(s_q[TQ_MAX_GROUP])[i] = m;
   }
-  float err = 0.f, s[kPerWarp * kG];
+  __syncthreads();
+  float err = 0.f;
+  for (; begin < end; begin += kRound) {
+    tq::f32x2 v[kPerWarp][4];
+    const uint32_t in = next_in;
 #pragma unroll
-  for (int i = 0; i < kPerWarp; ++i) {
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    float v[8], e = 0.f;
+    for (int i = 0; i < kPerWarp; ++i) {
+      const uint32_t w[4] = {next[i].x, next[i].y, next[i].z, next[i].w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] = __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
-      e = fmaf(most[j], fabsf(v[j]), e);
+      for (int j = 0; j < 4; ++j)
+        v[i][j] = tq::pack2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
     }
-    err = e <= err ? err : e;   // NaN stays
+    if (begin + kRound < end) fetch(begin + kRound, next, next_in);
+    {
+      const float4 m0 = s_q[TQ_MAX_GROUP][0][lane], m1 = s_q[TQ_MAX_GROUP][1][lane];
+      const float m[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
 #pragma unroll
-    for (int g = 0; g < kG; ++g) {
-      float t = 0.f;
+      for (int i = 0; i < kPerWarp; ++i) {
+        float e = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) t = fmaf(q[g][j], v[j], t);
-      s[i * kG + g] = t;
+        for (int j = 0; j < 4; ++j) {
+          const float2 x = tq::unpack2(v[i][j]);
+          e = fmaf(m[2 * j], fabsf(x.x), e);
+          e = fmaf(m[2 * j + 1], fabsf(x.y), e);
+        }
+        err = e <= err ? err : e;   // NaN stays
+      }
     }
+    float best = -INFINITY;
+#pragma unroll 1
+    for (int g = 0; g < heads; g += 4) {
+      float t[4 * kPerWarp];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const ulonglong2 q0 = *reinterpret_cast<const ulonglong2*>(&s_q[g + k][0][lane]);
+        const ulonglong2 q1 = *reinterpret_cast<const ulonglong2*>(&s_q[g + k][1][lane]);
+#pragma unroll
+        for (int i = 0; i < kPerWarp; ++i) {
+          tq::f32x2 s = tq::mul2(q0.x, v[i][0]);
+          s = tq::fma2(q0.y, v[i][1], s);
+          s = tq::fma2(q1.x, v[i][2], s);
+          s = tq::fma2(q1.y, v[i][3], s);
+          const float2 p = tq::unpack2(s);
+          t[4 * i + k] = p.x + p.y;
+        }
+      }
+      lane_sums(t, lane);           // lane l: block l / 8, head g + l / 2 % 4
+      best = fmaxf(best, t[0]);     // (a NaN head is left out)
+    }
+    best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 2));
+    best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 4));
+    const int i = lane / (32 / kPerWarp);
+    if (lane % (32 / kPerWarp) == 0 && begin + i < end)
+      a.score[(long long)row * a.nb + begin + i] = (in >> i) & 1u ? best : -INFINITY;
   }
-  lane_sums<kPerWarp * kG>(s, lane);
-  // lane l holds (block, head) l / (32 / (4·kG)); the largest over the heads (NaN left out)
-  float best = fmaxf(-INFINITY, s[0]);
-#pragma unroll
-  for (int o = 32 / (kPerWarp * kG); o < 32 / kPerWarp; o *= 2)
-    best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-#pragma unroll
-  for (int i = 0; i < kPerWarp; ++i)
-    if (lane == i * (32 / kPerWarp) && begin + i < nblk)
-      a.score[(long long)row * a.nb + begin + i] = in[i] ? best : -INFINITY;
   // Σ over lanes of each lane's largest partial sum: at least every block's Σ|terms|
 #pragma unroll
   for (int o = 16; o; o >>= 1) err += __shfl_xor_sync(0xffffffffu, err, o);
@@ -407,19 +420,17 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const SelectA
     }
   };
   for (int i = tid; i < words; i += blockDim.x) {
-    // the forced blocks' bits of this word
-    uint32_t m = 0;
-    const int w0 = 32 * i;
-    for (int k = 0; k < 32; ++k)
-      if (w0 + k < nblk && (w0 + k < a.first || w0 + k >= nblk - a.last)) m |= 1u << k;
-    bits[i] = m;
+    // the forced blocks of this word: below first, and from tail on
+    const int f = a.first - 32 * i, tail = nblk - a.last - 32 * i, past = nblk - 32 * i;
+    auto below = [](int k) { return k <= 0 ? 0u : k >= 32 ? ~0u : (1u << k) - 1u; };
+    bits[i] = below(f) | (below(past) & ~below(tail));
   }
   uint32_t low = ~0u, high = 0u, worst = 0u;
   each([&](int, uint32_t k) {
     low = min(low, k);
     high = max(high, k);
   });
-  for (int i = tid; i < (nblk + kPerCta - 1) / kPerCta; i += blockDim.x) {
+  for (int i = tid; i < (nblk + a.rounds * kRound - 1) / (a.rounds * kRound); i += blockDim.x) {
     const float e = a.err[(long long)row * a.chunks + i];
     worst = max(worst, e != e ? ~0u : __float_as_uint(e));     // NaN above all
   }
@@ -435,8 +446,9 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const SelectA
   low = __reduce_min_sync(0xffffffffu, lane < nwarps ? s_low[lane] : ~0u);
   high = __reduce_max_sync(0xffffffffu, lane < nwarps ? s_high[lane] : 0u);
   worst = __reduce_max_sync(0xffffffffu, lane < nwarps ? s_err[lane] : 0u);
-  // eight multiply-adds and five additions per lane and shuffle, half a step of 32 bits each:
-  // 13·2^-24·Σ|terms|; 2^-20 leaves room for the rounding of the bound itself
+  // four multiply-adds and six additions on a term's way into the sum, half a step of 32 bits
+  // each, and the product's own: 11·2^-24·Σ|terms|; 2^-20 leaves room for the rounding of the
+  // bound itself
   const float E = worst == ~0u ? INFINITY : __uint_as_float(worst) * 9.5367431640625e-7f;
   if (want > 0) {
     // all keys agree above the highest bit in which low and high differ
@@ -497,24 +509,50 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const SelectA
       // (a row of zero queries has nothing to score: every term is 0)
       for (int i = tid; worst == 0u && i < open; i += blockDim.x) exact[i] = ordered(0.0);
       for (int i = warp; worst != 0u && i < open; i += nwarps) {
+        // lane l: channels 4l .. 4l + 3 of every head, all loads first
         const __nv_bfloat16* p = bounds_at(a, b, h, doubt[i]);
         double best = -INFINITY;
-        for (int g = 0; p && g < a.G; ++g) {
-          double s = 0.0;
+        if (p) {
+          double l[4], u[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int c = 4 * lane + j;
-            const double x = load_elem(a.q, a.q_dtype, ((long long)row * a.G + g) * TQ_D + c);
-            const double l = __bfloat162float(p[c]), u = __bfloat162float(p[TQ_D + c]);
-            s += x < 0.0 ? x * l : x * u;
+            l[j] = __bfloat162float(p[4 * lane + j]);
+            u[j] = __bfloat162float(p[TQ_D + 4 * lane + j]);
           }
+#pragma unroll 1
+          for (int g0 = 0; g0 < a.G; g0 += 4) {     // four heads at a time (absent: head 0 again)
+            double s[4];
 #pragma unroll
-          for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          best = fmax(best, s);   // a NaN head is left out
+            for (int k = 0; k < 4; ++k) {
+              const long long at = ((long long)row * a.G + (g0 + k < a.G ? g0 + k : 0)) * TQ_D + 4 * lane;
+              s[k] = 0.0;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float x = load_elem(a.q, a.q_dtype, at + j);
+                s[k] += (double)x * (x < 0.f ? l[j] : u[j]);
+              }
+            }
+            lane_sums(s, lane);
+            best = fmax(best, s[0]);      // a NaN head is left out
+          }
+          best = fmax(best, __shfl_xor_sync(0xffffffffu, best, 16));
+          best = fmax(best, __shfl_xor_sync(0xffffffffu, best, 8));
         }
         if (lane == 0) exact[i] = ordered(best);
       }
       __syncthreads();
+      if (open <= 32) {
+        // few: each lane ranks its block against the others
+        if (warp == 0) {
+          const unsigned long long k = lane < open ? exact[lane] : 0ull;
+          int ahead = 0;
+          for (int i = 0; i < open; ++i) {
+            const unsigned long long o = __shfl_sync(0xffffffffu, k, i);
+            ahead += o > k || (o == k && i < lane);
+          }
+          if (lane < open && ahead < need) atomicOr(&bits[doubt[lane] >> 5], 1u << (doubt[lane] & 31));
+        }
+      } else {
       const unsigned long long t64 =
           kth_key<unsigned long long>(0ull, 63, need, sum, [&](unsigned long long c) {
             int mine = 0;
@@ -539,6 +577,7 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const SelectA
         const bool in = i < open && (k > t64 || (eq && at + before + __popc(vote & ((1u << lane) - 1)) < left));
         if (in) atomicOr(&bits[doubt[i] >> 5], 1u << (doubt[i] & 31));
         at += __reduce_add_sync(0xffffffffu, c);
+      }
       }
     }
   }
@@ -589,13 +628,10 @@ cudaLaunchConfig_t config(dim3 grid, unsigned block, size_t smem, cudaStream_t s
   return c;
 }
 
-tq_status launch_score(const SelectArgs& a, int G, dim3 grid, cudaStream_t stream) {
+tq_status launch_score(const SelectArgs& a, dim3 grid, cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = config(grid, 256, 0, stream, attr);
-  return tq_cuda_status(cudaLaunchKernelEx(&cfg, G <= 1 ? block_score_kernel<1>
-                                                 : G <= 2 ? block_score_kernel<2>
-                                                 : G <= 4 ? block_score_kernel<4>
-                                                          : block_score_kernel<8>, a));
+  return tq_cuda_status(cudaLaunchKernelEx(&cfg, block_score_kernel, a));
 }
 
 tq_status launch_select(const SelectArgs& a, int rows, int nb, cudaStream_t stream) {
@@ -613,7 +649,7 @@ tq_status launch_select(const SelectArgs& a, int rows, int nb, cudaStream_t stre
 }
 
 struct SelPlan {
-  int G, nb, chunks;
+  int G, nb, rounds, chunks;
   size_t err_off, exact_off, doubt_off, bytes;
 };
 
@@ -630,8 +666,12 @@ tq_status select_plan(const tq_attn_desc* d, SelPlan* p) {
   if ((long long)d->batch * d->kv_heads > 65535 || d->max_seq_len > (1 << 26)) return TQ_ERR_UNSUPPORTED;
   p->G = d->q_heads / d->kv_heads;
   p->nb = std::max((d->max_seq_len + kBlock - 1) / kBlock, 1);
-  p->chunks = (p->nb + kPerCta - 1) / kPerCta;
   const size_t rows = (size_t)d->batch * d->kv_heads;
+  // rounds per CTA: about three CTAs per SM (what fits at once); one round where there are fewer
+  const long long all = (long long)rows * ((p->nb + kRound - 1) / kRound);
+  const long long fit = 3LL * std::max(tq_num_sms(), 1);
+  p->rounds = (int)std::max<long long>(1, (all + fit - 1) / fit);
+  p->chunks = (p->nb + p->rounds * kRound - 1) / (p->rounds * kRound);
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   p->err_off = up(rows * p->nb * sizeof(float));
   p->exact_off = p->err_off + up(rows * p->chunks * sizeof(float));
@@ -699,12 +739,12 @@ extern "C" tq_status tq_block_select(const tq_attn_desc* desc, const void* q, tq
   if ((st = tq_rowmap_of(blocks.pages, desc->capacity, &a.map)) != TQ_OK) return st;
   if (desc->batch == 0) return TQ_OK;
   char* ws = static_cast<char*>(workspace);
-  a.q = q; a.q_dtype = desc->q_dtype; a.q_vec = aligned16(q);
+  a.q = q; a.q_dtype = desc->q_dtype;
   a.bounds = reinterpret_cast<const __nv_bfloat16*>(blocks.bounds);
   a.capacity = desc->capacity; a.max_len = desc->max_seq_len;
   a.seq_lens = seq_lens;
   a.Hkv = desc->kv_heads; a.G = p.G;
-  a.nb = p.nb; a.chunks = p.chunks;
+  a.nb = p.nb; a.rounds = p.rounds; a.chunks = p.chunks;
   a.first = first_blocks; a.last = last_blocks; a.keep = max_blocks;
   a.score = reinterpret_cast<float*>(ws);
   a.err = reinterpret_cast<float*>(ws + p.err_off);
@@ -713,6 +753,6 @@ extern "C" tq_status tq_block_select(const tq_attn_desc* desc, const void* q, tq
   a.list = list;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   const int rows = desc->batch * desc->kv_heads;
-  if ((st = launch_score(a, p.G, dim3(p.chunks, rows), stream)) != TQ_OK) return st;
+  if ((st = launch_score(a, dim3(p.chunks, rows), stream)) != TQ_OK) return st;
   return launch_select(a, rows, p.nb, stream);
 }

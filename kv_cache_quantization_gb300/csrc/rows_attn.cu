@@ -217,7 +217,8 @@ struct Item {
 
 // Where the 32 tokens of a warp lie in a cache's arrays: all in one 64-token block, so the row
 // (and the page) is the warp's.  Slots past the sequence's length but in its last block are in
-// the cache: they are read, and masked where it matters.
+// the cache: they are read, and masked where it matters.  A cursor walks an item's tiles; in a
+// run of tokens it only adds 128 and looks the table up where a page ends.
 struct Spot {
   bool some;      // at least the first token is attended
   int token0;
@@ -225,27 +226,63 @@ struct Spot {
   int slot;
 };
 
-// first: the warp's first token in a tile of 128.
 template <bool kList>
-__device__ __forceinline__ Spot locate(const RowsArgs& a, const tq_rowmap& map, const Item& it,
-                                       int t, int first, bool flag) {
-  Spot s;
-  s.row = 0;
-  s.slot = 0;
-  if (kList) {
-    const int at = 2 * (it.t0 + t) + (first >> 6);
-    const int blk = at < a.max_blocks ? __ldg(it.list + at) : -1;
-    s.token0 = blk >= 0 && blk < it.nblk ? blk * 64 + (first & 63) : -1;
-  } else {
-    s.token0 = (it.t0 + t) * kTile + first;
+struct Cursor {
+  const RowsArgs& a;
+  const tq_rowmap& map;
+  const Item& it;
+  int first;          // the warp's first token in a tile
+  bool flag;          // this thread reports bad pages
+  int t, token0, page, slot, row;
+
+  __device__ __forceinline__ Cursor(const RowsArgs& a_, const tq_rowmap& m, const Item& i, int f, bool fl)
+      : a(a_), map(m), it(i), first(f), flag(fl), t(0), page(0), row(0) {
+    if (!kList) {
+      token0 = slot = it.t0 * kTile + first;
+      if (map.table) {
+        page = token0 / map.page_tokens;
+        slot = token0 - page * map.page_tokens;
+        row = -1;
+      }
+    }
   }
-  s.some = s.token0 >= 0 && s.token0 < it.len;
-  if (s.some) {
-    s.some = tq_map_slot(map, a.Hkv, it.b, it.h, s.token0, s.row, s.slot);
+  __device__ __forceinline__ Spot next() {
+    Spot s{false, -1, 0, 0};
+    if (kList) {
+      const int at = 2 * (it.t0 + t++) + (first >> 6);
+      const int blk = at < a.max_blocks ? __ldg(it.list + at) : -1;
+      if (blk >= 0 && blk < it.nblk) s.token0 = blk * 64 + (first & 63);
+      s.some = s.token0 >= 0 && s.token0 < it.len;
+      if (s.some) s.some = tq_map_slot(map, a.Hkv, it.b, it.h, s.token0, s.row, s.slot);
+      else return s;
+    } else {
+      s.token0 = token0;
+      s.some = token0 < it.len;
+      token0 += kTile;
+      if (!s.some) return s;
+      if (!map.table) {
+        s.row = (long long)it.b * a.Hkv + it.h;
+        s.slot = slot;
+      } else {
+        while (slot >= map.page_tokens) {
+          slot -= map.page_tokens;
+          ++page;
+          row = -1;
+        }
+        if (row < 0) {
+          row = __ldg(map.table + (long long)it.b * map.max_pages + page);
+          if (row < 0 || row >= map.num_pages) row = map.num_pages;   // bad until the page ends
+        }
+        s.some = row < map.num_pages;
+        s.row = (long long)row * a.Hkv + it.h;
+        s.slot = slot;
+      }
+      slot += kTile;
+    }
     if (!s.some && flag) atomicOr(&g_tq_flags, TQ_FLAG_PAGE);
+    return s;
   }
-  return s;
-}
+};
 
 // Loads of the next tile's codes: volatile, so that they are issued here and not where the values
 // are used, a tile later (the compiler may sink a plain read-only load that far).
@@ -306,13 +343,13 @@ __device__ __forceinline__ bool expand_keys(const RowsArgs& a, const CacheSide& 
                                             const Item& it, int first, int lane) {
   const int off = (first >> 3) * 128 + (lane >> 3) * 128 + (lane & 7) * 16;
   uint4 next[IB] = {};
-  load_planes<IB>(side.kidx, locate<kList>(a, side.kmap, it, 0, first, lane == 0), side.kslots, lane, next);
+  Cursor<kList> cur(a, side.kmap, it, first, lane == 0);
+  load_planes<IB>(side.kidx, cur.next(), side.kslots, lane, next);
   for (int t = 0; t < it.tiles; ++t) {
     uint4 c[IB];
 #pragma unroll
     for (int p = 0; p < IB; ++p) c[p] = next[p];
-    if (t + 1 < it.tiles)
-      load_planes<IB>(side.kidx, locate<kList>(a, side.kmap, it, t + 1, first, lane == 0), side.kslots, lane, next);
+    if (t + 1 < it.tiles) load_planes<IB>(side.kidx, cur.next(), side.kslots, lane, next);
     const int st = t & 1;
     if (t >= 2 && !warp_wait(&sm.kempty[st], ((t >> 1) - 1) & 1)) return false;
     put_planes<IB>(a.kt, c, sm.k[st] + off);
@@ -330,10 +367,11 @@ __device__ __forceinline__ bool expand_signs(const RowsArgs& a, const CacheSide&
     float xn, rn, vn;
     bool ok;
   };
-  auto load = [&](int t, Raw& o) {
-    const Spot k = locate<kList>(a, side.kmap, it, t, first, false);
+  Cursor<kList> kcur(a, side.kmap, it, first, false), vcur(a, side.vmap, it, first, false);
+  auto load = [&](Raw& o) {
+    const Spot k = kcur.next();
     Spot v = k;
-    if (!side.same_map) v = locate<kList>(a, side.vmap, it, t, first, false);
+    if (!side.same_map) v = vcur.next();
     const bool some = k.some && v.some;
     o.ok = some && k.token0 + lane < it.len;
     if (!some) return;
@@ -344,10 +382,10 @@ __device__ __forceinline__ bool expand_signs(const RowsArgs& a, const CacheSide&
     o.vn = load_early(side.vxn + v.row * side.vslots + v.slot + lane);
   };
   Raw next{};
-  load(0, next);
+  load(next);
   for (int t = 0; t < it.tiles; ++t) {
     const Raw c = next;
-    if (t + 1 < it.tiles) load(t + 1, next);
+    if (t + 1 < it.tiles) load(next);
     const int st = t & 1, fs = t % kFacSlots;
     // the factors' slot is free: tile t − 4 was weighed before tile t − 2 was scored (kempty)
     if (t >= 2 && !warp_wait(&sm.kempty[st], ((t >> 1) - 1) & 1)) return false;
@@ -387,8 +425,9 @@ __device__ __forceinline__ bool expand_values(const RowsArgs& a, const CacheSide
   const int off = (first >> 3) * 128 + (lane >> 3) * 128 + (lane & 7) * 16;
   uint4 next[kRegs] = {};
   float next_vn = 0.f;
-  auto load = [&](int t) {
-    const Spot s = locate<kList>(a, side.vmap, it, t, first, lane == 0 && !side.same_map);
+  Cursor<kList> cur(a, side.vmap, it, first, lane == 0 && !side.same_map);
+  auto load = [&]() {
+    const Spot s = cur.next();
     if (s.some) next_vn = load_early(side.vxn + s.row * side.vslots + s.slot + lane);
     if constexpr (VB == 4) {
       if (!s.some) return;
@@ -400,7 +439,7 @@ __device__ __forceinline__ bool expand_values(const RowsArgs& a, const CacheSide
       load_planes<VB>(side.vidx, s, side.vslots, lane, next);
     }
   };
-  load(0);
+  load();
   for (int t = 0; t < it.tiles; ++t) {
     uint4 c[kRegs];
 #pragma unroll
@@ -408,7 +447,7 @@ __device__ __forceinline__ bool expand_values(const RowsArgs& a, const CacheSide
     // a zero vector adds nothing, whatever its code (a norm that is NaN or past the length has
     // no weight to meet it)
     const bool some = next_vn >= kTiny;
-    if (t + 1 < it.tiles) load(t + 1);
+    if (t + 1 < it.tiles) load();
     LevelBytes tb;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -465,6 +504,9 @@ struct Stats {
 template <int kCols>
 __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int wl, int hf, int lane, float f) {
   constexpr int kReps = 64 / kCols;
+  // two operations per instruction where the warps' issue slots bound the tile (3% faster with
+  // 112 rows; with 16 scores a thread the packing costs more: 8% slower with 32 rows)
+  constexpr bool kPairs = kCols == 64;
   const int rep = wl / (4 / kReps);
   const int col0 = (2 * rep + hf) * kCols;      // the thread's first token of a tile
   const uint32_t lane_base = (uint32_t)(32 * wl) << 16;
@@ -482,15 +524,24 @@ __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int wl, int 
     tmem_load<kCols>(dcol + col0, reinterpret_cast<uint32_t*>(e));
     tq::tmem_wait_ld();
     const float* fx = sm.fac[t % kFacSlots][0] + col0;
+    const tq::f32x2 f2 = tq::pack2(f, f);
     float mt = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kCols; i += 4) {
       const float4 xn = *reinterpret_cast<const float4*>(fx + i);
       const float4 lv = *reinterpret_cast<const float4*>(fx + kTile + i);
-      e[i] = fmaf(e[i] * f, xn.x, lv.x);
-      e[i + 1] = fmaf(e[i + 1] * f, xn.y, lv.y);
-      e[i + 2] = fmaf(e[i + 2] * f, xn.z, lv.z);
-      e[i + 3] = fmaf(e[i + 3] * f, xn.w, lv.w);
+      if constexpr (kPairs) {
+        const float2 x = tq::unpack2(tq::fma2(tq::mul2(tq::pack2(e[i], e[i + 1]), f2),
+                                              tq::pack2(xn.x, xn.y), tq::pack2(lv.x, lv.y)));
+        const float2 y = tq::unpack2(tq::fma2(tq::mul2(tq::pack2(e[i + 2], e[i + 3]), f2),
+                                              tq::pack2(xn.z, xn.w), tq::pack2(lv.z, lv.w)));
+        e[i] = x.x; e[i + 1] = x.y; e[i + 2] = y.x; e[i + 3] = y.y;
+      } else {
+        e[i] = fmaf(e[i] * f, xn.x, lv.x);
+        e[i + 1] = fmaf(e[i + 1] * f, xn.y, lv.y);
+        e[i + 2] = fmaf(e[i + 2] * f, xn.z, lv.z);
+        e[i + 3] = fmaf(e[i + 3] * f, xn.w, lv.w);
+      }
       mt = fmaxf(mt, fmaxf(fmaxf(e[i], e[i + 1]), fmaxf(e[i + 2], e[i + 3])));
     }
     sm.tmax[buf][hf][r] = mt;
@@ -523,19 +574,34 @@ __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int wl, int 
     }
     z.m = m_new;
     const float ref = m_new == -INFINITY ? 0.f : m_new;
+    const tq::f32x2 ref2 = tq::pack2(-ref, -ref);
     uint32_t w[kCols / 2];
+    tq::f32x2 l2 = tq::pack2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < kCols; i += 4) {
       const float4 iv = *reinterpret_cast<const float4*>(fx + 2 * kTile + i);
-      const float w0 = ex2(e[i] - ref), w1 = ex2(e[i + 1] - ref);
-      const float w2 = ex2(e[i + 2] - ref), w3 = ex2(e[i + 3] - ref);
-      z.l = fmaf(w0, iv.x, z.l);
-      z.l = fmaf(w1, iv.y, z.l);
-      z.l = fmaf(w2, iv.z, z.l);
-      z.l = fmaf(w3, iv.w, z.l);
+      float w0, w1, w2, w3;
+      if constexpr (kPairs) {
+        const float2 x = tq::unpack2(tq::add2(tq::pack2(e[i], e[i + 1]), ref2));
+        const float2 y = tq::unpack2(tq::add2(tq::pack2(e[i + 2], e[i + 3]), ref2));
+        w0 = ex2(x.x), w1 = ex2(x.y), w2 = ex2(y.x), w3 = ex2(y.y);
+        l2 = tq::fma2(tq::pack2(w0, w1), tq::pack2(iv.x, iv.y), l2);
+        l2 = tq::fma2(tq::pack2(w2, w3), tq::pack2(iv.z, iv.w), l2);
+      } else {
+        w0 = ex2(e[i] - ref), w1 = ex2(e[i + 1] - ref);
+        w2 = ex2(e[i + 2] - ref), w3 = ex2(e[i + 3] - ref);
+        z.l = fmaf(w0, iv.x, z.l);
+        z.l = fmaf(w1, iv.y, z.l);
+        z.l = fmaf(w2, iv.z, z.l);
+        z.l = fmaf(w3, iv.w, z.l);
+      }
       const __half2 p0 = __floats2half2_rn(w0, w1), p1 = __floats2half2_rn(w2, w3);
       w[i / 2] = *reinterpret_cast<const uint32_t*>(&p0);
       w[i / 2 + 1] = *reinterpret_cast<const uint32_t*>(&p1);
+    }
+    if constexpr (kPairs) {
+      const float2 lp = tq::unpack2(l2);
+      z.l += lp.x + lp.y;
     }
     tmem_store<kCols / 2>(dcol + col0 / 2, w);
     if constexpr (kReps > 1) {
