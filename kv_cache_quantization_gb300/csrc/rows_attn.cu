@@ -316,17 +316,25 @@ __device__ __forceinline__ void load_planes(const uint8_t* base, const Spot& s, 
     o[p] = load_early(reinterpret_cast<const uint4*>(row + ((uint32_t)(p * slots + s.slot + lane) * 16u)));
 }
 
-// Level chunks 0–15 of a token from its NB planes.
+// Level chunks 0–15 of a token from its NB planes (c is used up).  The loop over words is kept
+// rolled, as the other expanders' are: the roles' code has to fit the instruction caches of an SM
+// side by side.
 template <int NB>
-__device__ __forceinline__ void put_planes(const LevelBytes& t, const uint4 (&c)[NB], unsigned char* dst) {
-#pragma unroll
+__device__ __forceinline__ void put_planes(const LevelBytes& t, uint4 (&c)[NB], unsigned char* dst) {
+#pragma unroll 1
   for (int w = 0; w < 4; ++w) {
     uint32_t x[NB];
 #pragma unroll
-    for (int p = 0; p < NB; ++p) x[p] = word(c[p], w);
+    for (int p = 0; p < NB; ++p) {
+      x[p] = c[p].x;
+      c[p].x = c[p].y;
+      c[p].y = c[p].z;
+      c[p].z = c[p].w;
+    }
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      *reinterpret_cast<uint4*>(dst + (4 * w + r) * kLBO) = plane_chunk<NB>(t, x, r);
+      *reinterpret_cast<uint4*>(dst + r * kLBO) = plane_chunk<NB>(t, x, r);
+    dst += 4 * kLBO;
   }
 }
 
@@ -399,9 +407,13 @@ __device__ __forceinline__ bool expand_signs(const RowsArgs& a, const CacheSide&
     const __half2 r2 = __float2half2_rn(rho);
     const uint32_t neg = *reinterpret_cast<const uint32_t*>(&r2) ^ 0x80008000u;
     unsigned char* dst = sm.k[st] + 16 * kLBO + off;
-#pragma unroll
+    uint4 sg = c.s;
+#pragma unroll 1
     for (int w = 0; w < 4; ++w) {
-      const uint32_t x = word(c.s, w);
+      const uint32_t x = sg.x;
+      sg.x = sg.y;
+      sg.y = sg.z;
+      sg.z = sg.w;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint4 o;
@@ -409,8 +421,9 @@ __device__ __forceinline__ bool expand_signs(const RowsArgs& a, const CacheSide&
         o.y = (shr(x, 4 * q + 1 - 15) & 0x80008000u) ^ neg;
         o.z = (shr(x, 4 * q + 2 - 15) & 0x80008000u) ^ neg;
         o.w = (shr(x, 4 * q + 3 - 15) & 0x80008000u) ^ neg;
-        *reinterpret_cast<uint4*>(dst + (4 * w + q) * kLBO) = o;
+        *reinterpret_cast<uint4*>(dst + q * kLBO) = o;
       }
+      dst += 4 * kLBO;
     }
     hand_over(&sm.kfull[st], lane);
     if (lane == 0) mbar_arrive(&sm.ffull[fs]);
@@ -458,11 +471,17 @@ __device__ __forceinline__ bool expand_values(const RowsArgs& a, const CacheSide
     if (t >= 2 && !warp_wait(&sm.vempty[st], ((t >> 1) - 1) & 1)) return false;
     unsigned char* dst = sm.v[st] + off;
     if constexpr (VB == 4) {
+#pragma unroll 1
+      for (int w = 0; w < 4; ++w) {
 #pragma unroll
-      for (int w = 0; w < 16; ++w) {
-        const uint32_t x = word(c[w / 4], w % 4);
-        *reinterpret_cast<uint4*>(dst + w * kLBO) =
-            levels8<true>(tb, x & 0x77777777u, ((x >> 3) & 0x11111111u) | 0x88888888u);
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t x = word(c[0], k);
+          *reinterpret_cast<uint4*>(dst + k * kLBO) =
+              levels8<true>(tb, x & 0x77777777u, ((x >> 3) & 0x11111111u) | 0x88888888u);
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) c[k] = c[k + 1];
+        dst += 4 * kLBO;
       }
     } else {
       put_planes<VB>(tb, c, dst);
