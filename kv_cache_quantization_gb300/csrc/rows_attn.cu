@@ -48,9 +48,9 @@ constexpr int kTile = 128;              // tokens per tile, and query rows per i
 // 8 softmax warps, 3 × 4 expander warps, and a warpgroup that holds the issuer warp alone
 constexpr int kKeyWarp = 8, kSignWarp = 12, kValueWarp = 16, kIssueWarp = 20;
 constexpr int kThreads = 768;
-// Registers per thread: 80 at launch (61,440 of the block); the softmax warps take what the
-// others give up: 256·104 + 384·72 + 128·56 = 61,440.
-constexpr int kRegsLaunch = 80, kRegsSoftmax = 104, kRegsExpand = 72, kRegsIssue = 56;
+// Registers per thread: 80 at launch (61,440 of the block), which the softmax warps keep; the
+// expanders take what the last warpgroup gives up: 256·80 + 384·88 + 128·56 = 61,440.
+constexpr int kRegsLaunch = 80, kRegsExpand = 88, kRegsIssue = 56;
 constexpr int kRecFloats = 132;         // acc[128], m, l, padding
 constexpr int kLBO = 2048;              // bytes between 8-position chunks of an operand image
 constexpr int kKBytes = 32 * kLBO;      // key operand: 128 tokens × 256 positions, fp16
@@ -133,13 +133,10 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// N consecutive TMEM columns of the thread's lane, for N = 8, 16, 32 or 64.
+// N consecutive TMEM columns of the thread's lane.
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t at, uint32_t* r) {
-  if constexpr (N == 64) {
-    tq::tmem_ld_32x32b_x32(at, r);
-    tq::tmem_ld_32x32b_x32(at + 32, r + 32);
-  } else if constexpr (N == 32) {
+  if constexpr (N == 32) {
     tq::tmem_ld_32x32b_x32(at, r);
   } else {
     static_assert(N == 16, "columns");
@@ -516,20 +513,22 @@ struct Stats {
 };
 
 // The softmax of every tile by 8 warps: thread (lane group wl, half hf) of TMEM lane 32·wl + lane.
-// An item of at most 32 (64) rows holds each row in 4 (2) lane groups, the replicas of a row
-// taking a quarter (half) of a tile's tokens each, so that a thread has kCols = 16 (32) scores
+// An item of at most 32 (64) rows holds each row in 4 (2) lane groups, the `reps` replicas of a
+// row taking a quarter (half) of a tile's tokens each, so that a thread has 16 (32) scores
 // instead of 64: with few rows a tile's time is this chain's.  Weights of the tokens that a
 // replica leaves to the others are 0, and its O and l are those of its tokens.
-template <int kCols>
-__device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int wl, int hf, int lane, float f) {
-  constexpr int kReps = 64 / kCols;
-  // two operations per instruction where the warps' issue slots bound the tile (3% faster with
-  // 112 rows; with 16 scores a thread the packing costs more: 8% slower with 32 rows)
-  constexpr bool kPairs = kCols == 64;
-  const int rep = wl / (4 / kReps);
-  const int col0 = (2 * rep + hf) * kCols;      // the thread's first token of a tile
+//
+// Both passes over a thread's scores go 16 at a time in a rolled loop, with the scores in TMEM
+// between them: the roles' code has to fit the instruction caches of an SM side by side
+// (unrolled, this loop alone took a third of the time of 112 rows).  The weights of a group of
+// 16 tokens are stored over the first half of its scores, which no other thread reads.
+__device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int reps, int wl, int hf, int lane,
+                                               float f) {
+  const int rep = wl / (4 / reps), groups = 4 / reps;       // groups of 16 tokens per thread
+  const int group0 = (2 * rep + hf) * groups;
   const uint32_t lane_base = (uint32_t)(32 * wl) << 16;
   const int r = 32 * wl + lane;
+  const tq::f32x2 f2 = tq::pack2(f, f);
   Stats z{-INFINITY, 0.f, true};
   bool ok = true;
   auto wait = [&](uint64_t* bar, unsigned parity) { return ok = ok && warp_wait(bar, parity); };
@@ -538,34 +537,32 @@ __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int wl, int 
     wait(&sm.ffull[t % kFacSlots], (t / kFacSlots) & 1);
     wait(&sm.sfull[buf], (t >> 1) & 1);
     tc_after();
-    const uint32_t dcol = lane_base + kDCol + 128 * buf;
-    float e[kCols];
-    tmem_load<kCols>(dcol + col0, reinterpret_cast<uint32_t*>(e));
-    tq::tmem_wait_ld();
-    const float* fx = sm.fac[t % kFacSlots][0] + col0;
-    const tq::f32x2 f2 = tq::pack2(f, f);
+    const uint32_t dcol = lane_base + kDCol + 128 * buf + 16 * group0;
+    const float* fx = sm.fac[t % kFacSlots][0] + 16 * group0;
     float mt = -INFINITY;
+    uint32_t d[16];      // the last group's scores stay here, the others go back to TMEM
+#pragma unroll 1
+    for (int c = 0;; c += 16) {
+      tmem_load<16>(dcol + c, d);
+      tq::tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < kCols; i += 4) {
-      const float4 xn = *reinterpret_cast<const float4*>(fx + i);
-      const float4 lv = *reinterpret_cast<const float4*>(fx + kTile + i);
-      if constexpr (kPairs) {
-        const float2 x = tq::unpack2(tq::fma2(tq::mul2(tq::pack2(e[i], e[i + 1]), f2),
+      for (int i = 0; i < 16; i += 4) {
+        const float4 xn = *reinterpret_cast<const float4*>(fx + c + i);
+        const float4 lv = *reinterpret_cast<const float4*>(fx + kTile + c + i);
+        float* e = reinterpret_cast<float*>(d) + i;
+        const float2 x = tq::unpack2(tq::fma2(tq::mul2(tq::pack2(e[0], e[1]), f2),
                                               tq::pack2(xn.x, xn.y), tq::pack2(lv.x, lv.y)));
-        const float2 y = tq::unpack2(tq::fma2(tq::mul2(tq::pack2(e[i + 2], e[i + 3]), f2),
+        const float2 y = tq::unpack2(tq::fma2(tq::mul2(tq::pack2(e[2], e[3]), f2),
                                               tq::pack2(xn.z, xn.w), tq::pack2(lv.z, lv.w)));
-        e[i] = x.x; e[i + 1] = x.y; e[i + 2] = y.x; e[i + 3] = y.y;
-      } else {
-        e[i] = fmaf(e[i] * f, xn.x, lv.x);
-        e[i + 1] = fmaf(e[i + 1] * f, xn.y, lv.y);
-        e[i + 2] = fmaf(e[i + 2] * f, xn.z, lv.z);
-        e[i + 3] = fmaf(e[i + 3] * f, xn.w, lv.w);
+        e[0] = x.x; e[1] = x.y; e[2] = y.x; e[3] = y.y;
+        mt = fmaxf(mt, fmaxf(fmaxf(x.x, x.y), fmaxf(y.x, y.y)));
       }
-      mt = fmaxf(mt, fmaxf(fmaxf(e[i], e[i + 1]), fmaxf(e[i + 2], e[i + 3])));
+      if (c + 16 >= 16 * groups) break;
+      tmem_store<16>(dcol + c, d);
     }
     sm.tmax[buf][hf][r] = mt;
-    // both halves have read D: it may be overwritten by the weights.  A wait that gave up ends
-    // both halves' loops here, together (neither then waits for the other)
+    // A wait that gave up ends both halves' loops here, together (neither then waits for the
+    // other)
     if (!tq::named_sync_and(1 + wl, 64, ok)) {
       z.ok = false;
       return z;
@@ -580,7 +577,7 @@ __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int wl, int 
       tc_after();
       const float corr = z.m == -INFINITY ? 0.f : ex2(z.m - m_new);
 #pragma unroll 1
-      for (int c = 0; c < 64; c += 16) {   // 16 columns at a time: e stays in registers
+      for (int c = 0; c < 64; c += 16) {
         uint32_t o[16];
         const uint32_t at = lane_base + kOCol + 64 * hf + c;
         tmem_load<16>(at, o);
@@ -594,42 +591,37 @@ __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int wl, int 
     z.m = m_new;
     const float ref = m_new == -INFINITY ? 0.f : m_new;
     const tq::f32x2 ref2 = tq::pack2(-ref, -ref);
-    uint32_t w[kCols / 2];
     tq::f32x2 l2 = tq::pack2(0.f, 0.f);
+    if (groups > 1) tq::tmem_wait_st();
+#pragma unroll 1
+    for (int c = 16 * groups - 16;; c -= 16) {
+      uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < kCols; i += 4) {
-      const float4 iv = *reinterpret_cast<const float4*>(fx + 2 * kTile + i);
-      float w0, w1, w2, w3;
-      if constexpr (kPairs) {
-        const float2 x = tq::unpack2(tq::add2(tq::pack2(e[i], e[i + 1]), ref2));
-        const float2 y = tq::unpack2(tq::add2(tq::pack2(e[i + 2], e[i + 3]), ref2));
-        w0 = ex2(x.x), w1 = ex2(x.y), w2 = ex2(y.x), w3 = ex2(y.y);
+      for (int i = 0; i < 16; i += 4) {
+        const float4 iv = *reinterpret_cast<const float4*>(fx + 2 * kTile + c + i);
+        const float* e = reinterpret_cast<const float*>(d) + i;
+        const float2 x = tq::unpack2(tq::add2(tq::pack2(e[0], e[1]), ref2));
+        const float2 y = tq::unpack2(tq::add2(tq::pack2(e[2], e[3]), ref2));
+        const float w0 = ex2(x.x), w1 = ex2(x.y), w2 = ex2(y.x), w3 = ex2(y.y);
         l2 = tq::fma2(tq::pack2(w0, w1), tq::pack2(iv.x, iv.y), l2);
         l2 = tq::fma2(tq::pack2(w2, w3), tq::pack2(iv.z, iv.w), l2);
-      } else {
-        w0 = ex2(e[i] - ref), w1 = ex2(e[i + 1] - ref);
-        w2 = ex2(e[i + 2] - ref), w3 = ex2(e[i + 3] - ref);
-        z.l = fmaf(w0, iv.x, z.l);
-        z.l = fmaf(w1, iv.y, z.l);
-        z.l = fmaf(w2, iv.z, z.l);
-        z.l = fmaf(w3, iv.w, z.l);
+        const __half2 p0 = __floats2half2_rn(w0, w1), p1 = __floats2half2_rn(w2, w3);
+        w[i / 2] = *reinterpret_cast<const uint32_t*>(&p0);
+        w[i / 2 + 1] = *reinterpret_cast<const uint32_t*>(&p1);
       }
-      const __half2 p0 = __floats2half2_rn(w0, w1), p1 = __floats2half2_rn(w2, w3);
-      w[i / 2] = *reinterpret_cast<const uint32_t*>(&p0);
-      w[i / 2 + 1] = *reinterpret_cast<const uint32_t*>(&p1);
+      tmem_store<8>(dcol + c, w);
+      if (c == 0) break;
+      tmem_load<16>(dcol + c - 16, d);
+      tq::tmem_wait_ld();
     }
-    if constexpr (kPairs) {
-      const float2 lp = tq::unpack2(l2);
-      z.l += lp.x + lp.y;
-    }
-    tmem_store<kCols / 2>(dcol + col0 / 2, w);
-    if constexpr (kReps > 1) {
-      // the other replicas' tokens: 64 − kCols columns of weights, half of them by each half
-      constexpr int kRest = (64 - kCols) / 2;
-      const uint32_t none[16] = {};
-#pragma unroll
-      for (int c = 0; c < kRest; c += kCols / 2)
-        tmem_store<kCols / 2>(dcol + ((rep * kCols + kCols + hf * kRest + c) & 63), none);
+    const float2 lp = tq::unpack2(l2);
+    z.l += lp.x + lp.y;
+    if (reps > 1) {
+      // the other replicas' groups, every other one by each half
+      const uint32_t none[8] = {};
+#pragma unroll 1
+      for (int g = hf; g < 8; g += 2)
+        if (g / (2 * groups) != rep) tmem_store<8>(lane_base + kDCol + 128 * buf + 16 * g, none);
     }
     tq::tmem_wait_st();
     tc_before();
@@ -651,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  static_assert(128 * kRegsIssue + 384 * kRegsExpand + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
+  static_assert(128 * kRegsIssue + 384 * kRegsExpand + 256 * kRegsLaunch <= kThreads * kRegsLaunch, "register split");
 
   // ---- the item: prefix items first (they are the long ones)
   int item = blockIdx.x;
@@ -733,7 +725,6 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
 
   if (warp < kKeyWarp) {
     // ================================================================ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int wl = warp & 3, hf = warp >> 2;
     const int per = kTile / reps;              // rows per replica
     const int r = (32 * wl + lane) & (per - 1);
@@ -755,9 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
     tc_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.qfull);
-    const Stats z = reps == 4 ? softmax_tiles<16>(sm, tiles, wl, hf, lane, f)
-                  : reps == 2 ? softmax_tiles<32>(sm, tiles, wl, hf, lane, f)
-                              : softmax_tiles<64>(sm, tiles, wl, hf, lane, f);
+    const Stats z = softmax_tiles(sm, tiles, reps, wl, hf, lane, f);
     // ---- the item's record: lanes' parts through shared memory (the operands are done with),
     // replicas of a row added up with their log-sum-exp weights
     ok = ok && tq::named_sync_and(5, 256, z.ok);
@@ -800,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
     }
   } else if (warp < kIssueWarp) {
     // ================================================================ expanders
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsExpand));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsExpand));
     const Item it{t0, tiles, len, nblk, b, h, list};
     if (pre) ok = expand<IB, VB, false>(a, a.pre, sm, it, warp, lane);
     else if (list) ok = expand<IB, VB, true>(a, a.own, sm, it, warp, lane);
@@ -824,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
         const uint32_t w = kDCol + 128 * st;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          tq::mma_ts(kOCol, w + 8 * ks, v + ks * (256 >> 4), kIdescO, t > 0 || ks > 0);
+          tq::mma_ts(kOCol, w + 16 * ks, v + ks * (256 >> 4), kIdescO, t > 0 || ks > 0);
         tq::mma_commit(&sm.vempty[st]);
       }
       __syncwarp();
