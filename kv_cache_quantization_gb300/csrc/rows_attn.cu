@@ -1043,13 +1043,16 @@ double makespan(long long n1, double c1, long long n2, double c2, long long sms)
   return until + (double)((n2 - beside + sms - 1) / sms) * c2;
 }
 
-// Splits that make the estimated time least (find_splits).  An item costs its tiles and about three tiles of
-// start and end (measured: 8,600 cycles, where a tile takes 3,000 to 4,000).
-constexpr double kFixed = 3.0;
+// Splits that make the estimated time least (find_splits).  An item costs its tiles, those of few
+// rows less (measured: 3,000 cycles with 32 rows, 4,000 with 112), and about two tiles of start
+// and end.  Against 3 tiles and one cost: 62.3 for 66.4 us (prefix of 32768, 32 sequences) and 176
+// for 191 us (65536, 64 sequences); 5 tiles: 70.1 and 176 us; others the same.
+constexpr double kFixed = 2.0, kFewRows = 0.75;
 // The arguments that the splits follow from, and what they came to: a call looks its splits up
 // (the search takes some microseconds).
 struct Splits {
   long long pu, pre, ou, own, sms;
+  bool few;          // at most 64 query rows in an item of the prefix
   int sp, so;
 };
 
@@ -1065,8 +1068,8 @@ void find_splits(Splits* x) {
       const long long so = std::max<long long>((own_tiles + lo - 1) / lo, 1);
       const bool last = lo >= own_tiles && lp >= pre_tiles;
       if (sp + so <= kMaxRecs || last) {
-        const double cp = sp ? (double)((pre_tiles + sp - 1) / sp) + kFixed : 0;
-        const double co = (double)((own_tiles + so - 1) / so) + kFixed;
+        const double cp = sp ? (x->few ? kFewRows : 1.0) * (double)((pre_tiles + sp - 1) / sp) + kFixed : 0;
+        const double co = kFewRows * (double)((own_tiles + so - 1) / so) + kFixed;
         // more records cost the merge: about a tile's time for 64 of them
         const double t = makespan(x->pu * sp, cp, x->ou * so, co, x->sms) + (double)(sp + so) / 64;
         if (!x->so || t < best) {
@@ -1101,9 +1104,9 @@ tq_status make_plan(const tq_attn_desc* d, long long pre_tiles, long long own_ti
   const long long pu = (long long)p->row_tiles * d->kv_heads, ou = (long long)d->batch * d->kv_heads;
   thread_local Splits known[8];
   thread_local int next = 0;
-  Splits want{pu, pre_tiles, ou, own_tiles, sms, 0, 0};
+  Splits want{pu, pre_tiles, ou, own_tiles, sms, (long long)d->batch * p->G <= kTile / 2, 0, 0};
   for (const Splits& k : known)
-    if (k.so && k.pu == pu && k.pre == pre_tiles && k.ou == ou && k.own == own_tiles && k.sms == sms) want = k;
+    if (k.so && k.few == want.few && k.pu == pu && k.pre == pre_tiles && k.ou == ou && k.own == own_tiles && k.sms == sms) want = k;
   if (!want.so) {
     find_splits(&want);
     known[next] = want;

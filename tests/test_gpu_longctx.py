@@ -452,3 +452,213 @@ def test_block_select_length_over_the_plan():
     more = plan.select(q, blocks, i32([64 * 30, 64 * 31]), plan.new_list())
     assert flags() == B.TQ_FLAG_LEN_OVERFLOW
     assert torch.equal(got, more)
+
+
+# ------------------------------------------------------------------ used together, and otherwise
+
+def test_sparse_step_loop():
+    """A prefill's codes and bounds, then decode steps of SparsePlan.step (append, bounds, select,
+    attend) on ragged sequences: lists and rows against the definitions on the cache as it is."""
+    kc, vc = codec("k", 3), codec("v", 4)
+    batch, kv, group, cap, keep = 3, 2, 4, 2048, 6
+    k, v = api.ProdCache.empty(batch, kv, cap, 3), api.MSECache.empty(batch, kv, cap, 4)
+    blocks = api.BlockBounds.empty(batch, kv, cap)
+    x = torch.randn(batch, kv, 1500, D, generator=gen(1), device="cuda").bfloat16()
+    y = torch.randn(batch, kv, 1500, D, generator=gen(2), device="cuda").bfloat16()
+    lens = [1500, 703, 62]
+    pos, now = i32(lens), i32([n + 1 for n in lens])
+    api.quantize_prod(kc, x, k, count=pos)
+    api.quantize_mse(vc, y, v, count=pos)
+    api.block_bounds(x, blocks, count=pos)
+    keys = [x[b, :, :n] for b, n in enumerate(lens)]
+    plan = api.SparsePlan(batch, kv * group, kv, cap, cap, keep, 1, 1, out_dtype=torch.float16)
+    out, lst = plan.new_out(), plan.new_list()
+    for step in range(4):
+        kn, vn = (torch.randn(batch, kv, D, generator=gen(10 + 2 * step + i), device="cuda").bfloat16()
+                  for i in (0, 1))
+        q = queries(batch, kv * group, torch.bfloat16, 50 + step)
+        plan.step(kc, vc, q, kn, vn, k, v, blocks, pos, now, lst, out)
+        lens = [n + 1 for n in lens]
+        keys = [torch.cat([t, kn[b, :, None]], 1) for b, t in enumerate(keys)]
+        for b, n in enumerate(lens):
+            nb = -(-n // 64)
+            padded = torch.nn.functional.pad(keys[b].float(), (0, 0, 0, nb * 64 - n), value=math.nan)
+            t = padded.unflatten(1, (nb, 64))
+            lo = torch.where(t.isnan(), math.inf, t).amin(2).bfloat16()
+            hi = torch.where(t.isnan(), -math.inf, t).amax(2).bfloat16()
+            assert torch.equal(blocks.bounds[b, :, :nb], torch.stack([lo, hi], 2))
+        check_select(q, blocks, lens, keep, 1, 1, group, kv, lst)
+        check_sparse(kc, vc, q, k, v, lst, lens, out, group)
+        pos += 1
+        now += 1
+    assert flags() == 0
+
+
+def test_all_blocks_listed_equal_the_dense_decode():
+    """A list of every block attends what tq_decode_attention attends (fp32 output, its own
+    kernel): both are near the definition, so they are near each other."""
+    kc, vc = codec("k", 4), codec("v", 2)
+    lens = [1000, 64, 1]
+    k, v = caches(3, 2, 1024, 4, 2, 1, None, lens)
+    q = queries(3, 10, torch.float16, 2)
+    plan = api.SparsePlan(3, 10, 2, 1024, 1024, 16, 0, 0, torch.float16, torch.float16)
+    lst = torch.arange(16, dtype=torch.int32, device="cuda").expand(3, 2, -1).contiguous()
+    got = plan.run(kc, vc, q, k, v, i32(lens), lst, plan.new_out())
+    dec = api.DecodePlan(3, 10, 2, 1024, 1024, torch.float16, torch.float32)
+    want = dec.run(kc, vc, q, k, v, i32(lens), dec.new_out())
+    off = (got.double() - want.double()).norm(dim=-1) / want.double().norm(dim=-1)
+    assert float(off.max()) < 4e-3
+
+
+def test_nan_queries_stay_in_their_rows():
+    kc, vc = codec("k", 3), codec("v", 2)
+    lens = [100, 200]
+    k, v = caches(2, 1, 256, 3, 2, 1, None, lens)
+    pk, pv = caches(1, 1, 192, 3, 2, 2)
+    q = queries(2, 4, torch.float32, 3)
+    plan = api.PrefixPlan(2, 4, 1, 256, 256, 192, 192, torch.float32, torch.float16)
+    clean = plan.run(kc, vc, q, pk, pv, i32([150]), k, v, i32(lens), plan.new_out())
+    q[1, 2, 7] = math.nan
+    got = plan.run(kc, vc, q, pk, pv, i32([150]), k, v, i32(lens), plan.new_out())
+    assert got[1, 2].isnan().all()
+    got[1, 2] = clean[1, 2]
+    assert torch.equal(got, clean)
+
+
+def capture(fn, stream):
+    g = torch.cuda.CUDAGraph()
+    fn()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=stream):
+        fn()
+    return g
+
+
+def test_graphs_and_streams():
+    """All four operators captured into one graph on a side stream and replayed on new inputs; the
+    same calls on another stream than the current one; repeated calls give the same bits."""
+    kc, vc = codec("k", 3), codec("v", 4)
+    batch, kv, group, cap, keep = 4, 2, 7, 1024, 5
+    lens = [1024, 800, 64, 3]
+    k, v = caches(batch, kv, cap, 3, 4, 1, None, lens)
+    pk, pv = caches(1, kv, 512, 3, 4, 2)
+    x = torch.randn(batch, kv, cap, D, generator=gen(3), device="cuda").half()
+    blocks = api.BlockBounds.empty(batch, kv, cap)
+    q = queries(batch, kv * group, torch.float16, 4)
+    sp = api.SparsePlan(batch, kv * group, kv, cap, cap, keep, 1, 1, torch.float16, torch.float16)
+    pr = api.PrefixPlan(batch, kv * group, kv, cap, cap, 512, 512, torch.float16, torch.float16)
+    n, pn = i32(lens), i32([500])
+    lst, o1, o2 = sp.new_list(), sp.new_out(), pr.new_out()
+    side = torch.cuda.Stream()
+
+    def all_four(stream=None):
+        api.block_bounds(x, blocks, count=n, stream=stream)
+        sp.select(q, blocks, n, lst, stream=stream)
+        sp.run(kc, vc, q, k, v, n, lst, o1, stream=stream)
+        pr.run(kc, vc, q, pk, pv, pn, k, v, n, o2, stream=stream)
+
+    all_four()
+    torch.cuda.synchronize()
+    first = [t.clone() for t in (blocks.bounds, lst, o1, o2)]
+    side.wait_stream(torch.cuda.current_stream())
+    all_four(stream=side)
+    side.synchronize()
+    for a, b in zip(first, (blocks.bounds, lst, o1, o2)):
+        assert torch.equal(a, b)
+    with torch.cuda.stream(side):
+        g = capture(all_four, side)
+    for seed in (8, 9):
+        q.copy_(queries(batch, kv * group, torch.float16, seed))
+        x.copy_(torch.randn(x.shape, generator=gen(seed), device="cuda"))
+        for t in (blocks.bounds, lst, o1, o2):
+            t.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        check_select(q, blocks, lens, keep, 1, 1, group, kv, lst)
+        check_sparse(kc, vc, q, k, v, lst, lens, o1, group)
+        check_prefix(kc, vc, q, (pk, pv), (k, v), o2, 500, lens, kv, group)
+    assert flags() == 0
+
+
+def test_two_plans_at_once():
+    """Two plans (a workspace each) on two streams, many calls in flight: rows as when alone."""
+    kc, vc = codec("k", 3), codec("v", 2)
+    lens = [640] * 6
+    k, v = caches(6, 2, 640, 3, 2, 1)
+    pk, pv = caches(1, 2, 4096, 3, 2, 2)
+    q = [queries(6, 8, torch.bfloat16, s) for s in (3, 4)]
+    plans = [api.PrefixPlan(6, 8, 2, 640, 640, 4096, 4096) for _ in q]
+    n, pn = i32(lens), i32([4000])
+    alone = [p.run(kc, vc, x, pk, pv, pn, k, v, n, p.new_out()).clone() for p, x in zip(plans, q)]
+    streams = [torch.cuda.Stream() for _ in q]
+    outs = [[p.new_out() for _ in range(20)] for p in plans]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for p, x, s, o in zip(plans, q, streams, outs):
+            p.run(kc, vc, x, pk, pv, pn, k, v, n, o[i], stream=s)
+    torch.cuda.synchronize()
+    for a, o in zip(alone, outs):
+        for t in o:
+            assert torch.equal(a, t)
+
+
+def test_growing_scores_move_the_reference():
+    """Scores that rise along the sequence by far more than 2^8 a tile, and fall: the running
+    reference follows, accumulators are scaled, and what was large first stays."""
+    kc, vc = codec("k", 3), codec("v", 4)
+    n = 1500
+    for order in (1, -1):
+        k, v = caches(1, 1, 1536, 3, 4, 1)
+        ramp = torch.linspace(0.1, 60, 1536, device="cuda")
+        k.xnorm.copy_(ramp if order == 1 else ramp.flip(0))
+        k.rnorm.copy_(0.4 * k.xnorm)
+        pk, pv = caches(1, 1, 1536, 3, 4, 2)
+        pk.xnorm.copy_(ramp if order == 1 else ramp.flip(0))
+        pk.rnorm.copy_(0.4 * pk.xnorm)
+        for rows in (1, 8):
+            q = queries(1, rows, torch.float32, 5, 4.0)
+            plan = api.PrefixPlan(1, rows, 1, 1536, 1536, 1536, 1536, torch.float32, torch.float16)
+            out = plan.run(kc, vc, q, pk, pv, i32([n]), k, v, i32([n]), plan.new_out())
+            check_prefix(kc, vc, q, (pk, pv), (k, v), out, n, [n], 1, rows)
+
+
+@pytest.mark.parametrize("batch,group", [(4, 8), (5, 8), (8, 8), (9, 8), (16, 8), (17, 8)])
+def test_rows_per_item(batch, group):
+    """32, 40, 64, 72, 128 and 136 query rows of a KV head: a row in four lane groups, in two, in
+    one, and in two row tiles."""
+    lens = [(53 * i) % 90 for i in range(batch)]
+    a = run_prefix(3, 2, batch, 1, group, 700, lens, seed=batch)
+    check_prefix(*a[:5], a[6], 700, lens, 1, group)
+
+
+def test_python_layer_refuses_on_the_gpu():
+    kc, vc = codec("k", 3), codec("v", 2)
+    k, v = caches(2, 2, 128, 3, 2, 1)
+    q = queries(2, 4, torch.bfloat16, 1)
+    n = i32([100, 3])
+    plan = api.SparsePlan(2, 4, 2, 128, 128, 2, 0, 0)
+    lst, out = plan.new_list(), plan.new_out()
+    lst.zero_()
+    plan.run(kc, vc, q, k, v, n, lst, out)
+    bad = [(q.float(), k, v, n, lst, out), (q[:1], k, v, n, lst, out), (q, k, v, n.long(), lst, out),
+           (q, k, v, n.cpu(), lst, out), (q, k, v, n, lst[:, :1], out), (q, k, v, n, lst, out.float()),
+           (q.transpose(0, 1).contiguous().transpose(0, 1), k, v, n, lst, out),
+           (q, api.ProdCache.empty(2, 2, 64, 3), v, n, lst, out),
+           (q, api.ProdCache.empty(2, 2, 128, 4), v, n, lst, out),
+           (q, k, api.MSECache.empty(1, 2, 128, 2), n, lst, out)]
+    for args in bad:
+        with pytest.raises(ValueError):
+            plan.run(kc, vc, *args)
+    with pytest.raises(ValueError):      # codecs in each other's place
+        plan.run(vc, kc, q, k, v, n, lst, out)
+    assert B.tq_sparse_attention(plan.desc, vc.handle, kc.handle, q, k.c(), v.c(), n, lst, 2, out,
+                                 plan.workspace, plan.nbytes, None) == B.TQ_ERR_INVALID_ARG
+    x = torch.randn(2, 2, 5, D, device="cuda")
+    blocks = api.BlockBounds.empty(2, 2, 128)
+    for args in ((x[..., :64], blocks), (x, api.BlockBounds.empty(2, 3, 128)), (x, blocks, n.long()),
+                 (x.cpu(), blocks), (x, blocks, i32([1]))):
+        with pytest.raises((ValueError, TypeError)):
+            api.block_bounds(*args)
+    with pytest.raises(TypeError):
+        api.block_bounds(x.double(), blocks)
