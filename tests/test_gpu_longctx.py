@@ -75,6 +75,13 @@ def caches(rows, heads, cap, kbits, vbits, seed, pages=None, used=None):
     return k, v
 
 
+def hide(pages, used):
+    """Table entries past the pages of the first used[b] tokens become -1: nothing may read them."""
+    if pages is not None:
+        for b, n in enumerate(used):
+            pages.block_table[b, -(-n // pages.page_tokens):] = -1
+
+
 def queries(batch, heads, dtype, seed, size=1.0):
     return (size * torch.randn(batch, heads, D, generator=gen(seed), device="cuda")).to(dtype)
 
@@ -99,6 +106,8 @@ def run_prefix(kbits, vbits, batch, kv, group, plen, lens, paged=0, q_dtype=torc
         pp, po = table(1, pcap // paged, paged, seed + 1), table(batch, cap // paged, paged, seed + 2)
     pk, pv = caches(1, kv, pcap, kbits, vbits, seed + 3, pp, [plen])
     k, v = caches(batch, kv, cap, kbits, vbits, seed + 4, po, lens)
+    hide(pp, [plen])
+    hide(po, lens)
     q = queries(batch, kv * group, q_dtype, seed + 5, size)
     plan = api.PrefixPlan(batch, kv * group, kv, cap, max(lens), pcap, plen, q_dtype, out_dtype, scale)
     out = plan.run(kc, vc, q, pk, pv, i32([plen]), k, v, i32(lens), plan.new_out())
@@ -259,6 +268,7 @@ def test_sparse_attention(batch, kv, group, lens, keep, paged, kbits, vbits):
         cap = -(-cap // paged) * paged
         pages = table(batch, cap // paged, paged, 9)
     k, v = caches(batch, kv, cap, kbits, vbits, keep, pages, lens)
+    hide(pages, lens)
     q = queries(batch, kv * group, torch.bfloat16, 1)
     lst = lists_of(lens, kv, keep, 2)
     plan = api.SparsePlan(batch, kv * group, kv, cap, max(lens), keep, 0, 0, out_dtype=torch.float16)
@@ -324,7 +334,12 @@ def test_block_bounds(dtype, batch, heads, tokens, pos, count, paged):
     blocks = blank(batch, heads, cap, pages, 3)
     want = ref.bounds(x, pos or [0] * batch, count or [tokens] * batch, flat_bounds(blocks))
     spare = blocks.bounds.clone()
+    whole = None if pages is None else pages.block_table.clone()
+    hide(pages, [p + n for p, n in zip(pos or [0] * batch, count or [tokens] * batch)])
     api.block_bounds(x, blocks, None if pos is None else i32(pos), None if count is None else i32(count))
+    if pages is not None:
+        torch.cuda.synchronize()
+        pages.block_table.copy_(whole)
     assert torch.equal(flat_bounds(blocks), want)
     if pages is not None:      # pages outside the table are left alone
         free = sorted(set(range(pages.num_pages)) - set(pages.block_table.flatten().tolist()))
@@ -400,6 +415,7 @@ def test_block_select(dtype, batch, kv, group, lens, keep, first, last, paged):
         pages = table(batch, cap // paged, paged, 5)
     blocks = blank(batch, kv, cap, pages, 1)
     blocks.bounds[..., 1, :] += 2
+    hide(pages, lens)
     q = queries(batch, kv * group, dtype, 2)
     _, got = run_select(q, blocks, lens, keep, first, last, group, kv, cap)
     check_select(q, blocks, lens, keep, first, last, group, kv, got)
