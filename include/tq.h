@@ -321,8 +321,9 @@ tq_status tq_decode_attention_asym(const tq_attn_desc* desc, const tq_codec* vc,
  *              seq_lens (longer ones are clamped and flagged).  A sequence with no token at all
  *              gives a zero row.
  *   kc, vc   : key codecs of 2 to 5 bits, value codecs of 1 to 4; created on the current device.
- *   desc->out_dtype is F16 or BF16: the products run on fp16 operands (F32 returns
- *   TQ_ERR_UNSUPPORTED).  Value vectors with norms below 2^-60 count as zero vectors.
+ *   desc->out_dtype is F16 or BF16 (F32 returns TQ_ERR_UNSUPPORTED): the products run on fp16
+ *   operands, and on pairs of them for F16 outputs, so that a row is off by about the rounding of
+ *   its own type.  Value vectors with norms below 2^-60 count as zero vectors.
  *   workspace: ≥ tq_prefix_workspace_bytes(desc, prefix_max_len) bytes, 256-byte aligned, no
  *              initialisation needed; calls that share it must be serialised on one stream.
  *   Other arguments as tq_decode_attention. */

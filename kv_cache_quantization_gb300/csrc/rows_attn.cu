@@ -35,10 +35,12 @@
 // 62 us; 32 blocks of each of 32 sequences 48 us.
 //
 // Roundings to 16 bits: the rotated query and sketch, ρ, the levels (scaled so that fp16 holds
-// them best) and the weights, each off by at most half a step of fp16 (2^-11 relative).  The
-// output's own rounding is 2^-8 in bf16, above all of them together; in fp16 it is 2^-11 and they
-// show: 0.7 to 1.4e-3 of a row's norm against 2e-4.  Twice the matrix products (pairs of fp16)
-// would be needed to hide them.  Scores, maxima, sums and accumulators are 32 bits.
+// them best, to a few 1e-5) and the weights, each off by at most half a step of fp16 (2^-11
+// relative); together 0.7 to 1.4e-3 of a row's norm, below the output's own 2^-8 a value in bf16.
+// fp16 outputs (2^-11 a value) would show them: for those (kFine) query, sketch, ρ and weights are
+// pairs of fp16 numbers (about 2^-21), for 56 instead of 24 matrix instructions a tile, and the
+// second halves of query and sketch take the place of the second D.  Scores, maxima, sums and
+// accumulators are 32 bits.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -69,6 +71,7 @@ constexpr int kLBO = 2048;              // bytes between 8-position chunks of an
 constexpr int kKBytes = 32 * kLBO;      // key operand: 128 tokens × 256 positions, fp16
 constexpr int kVBytes = 16 * kLBO;
 constexpr int kQCol = 0, kDCol = 128, kOCol = 384;   // TMEM columns
+constexpr int kQLowCol = 256;           // (fine: the second halves of y and z, over the second D)
 constexpr int kFacSlots = 4;
 constexpr float kAlpha = 64.f, kBeta = 4.f;   // scales of y and z in the fp16 row operand
 constexpr float kGrow = 8.f;            // the reference follows the maximum when 2^8 above it
@@ -356,9 +359,10 @@ __device__ __forceinline__ void hand_over(uint64_t* bar, int lane) {
 }
 
 // The three kinds of expander warps.  Each returns false once a wait gave up.
-template <int IB, bool kList>
+template <int IB, bool kFine, bool kList>
 __device__ __forceinline__ bool expand_keys(const RowsArgs& a, const CacheSide& side, Smem& sm,
                                             const Item& it, int first, int lane) {
+  constexpr int kBufs = kFine ? 1 : 2;
   const int off = (first >> 3) * 128 + (lane >> 3) * 128 + (lane & 7) * 16;
   uint4 next[IB] = {};
   Cursor<kList> cur(a, side.kmap, it, first, lane == 0);
@@ -368,17 +372,18 @@ __device__ __forceinline__ bool expand_keys(const RowsArgs& a, const CacheSide& 
 #pragma unroll
     for (int p = 0; p < IB; ++p) c[p] = next[p];
     if (t + 1 < it.tiles) load_planes<IB>(side.kidx, cur.next(), side.kslots, lane, next);
-    const int st = t & 1;
-    if (t >= 2 && !warp_wait(&sm.kempty[st], ((t >> 1) - 1) & 1)) return false;
+    const int st = t % kBufs;
+    if (t >= kBufs && !warp_wait(&sm.kempty[st], (t / kBufs - 1) & 1)) return false;
     put_planes<IB>(a.kt, c, sm.k[st] + off);
     hand_over(&sm.kfull[st], lane);
   }
   return true;
 }
 
-template <bool kList>
+template <bool kFine, bool kList>
 __device__ __forceinline__ bool expand_signs(const RowsArgs& a, const CacheSide& side, Smem& sm,
                                              const Item& it, int first, int lane) {
+  constexpr int kBufs = kFine ? 1 : 2;
   const int off = (first >> 3) * 128 + (lane >> 3) * 128 + (lane & 7) * 16;
   struct Raw {
     uint4 s;
@@ -404,9 +409,9 @@ __device__ __forceinline__ bool expand_signs(const RowsArgs& a, const CacheSide&
   for (int t = 0; t < it.tiles; ++t) {
     const Raw c = next;
     if (t + 1 < it.tiles) load(next);
-    const int st = t & 1, fs = t % kFacSlots;
+    const int st = t % kBufs, fs = t % kFacSlots;
     // the factors' slot is free: tile t − 4 was weighed before tile t − 2 was scored (kempty)
-    if (t >= 2 && !warp_wait(&sm.kempty[st], ((t >> 1) - 1) & 1)) return false;
+    if (t >= kBufs && !warp_wait(&sm.kempty[st], (t / kBufs - 1) & 1)) return false;
     const bool some = c.vn >= kTiny;
     sm.fac[fs][0][first + lane] = c.ok ? c.xn : 0.f;
     sm.fac[fs][1][first + lane] = !c.ok ? -INFINITY : some ? __log2f(c.vn) : c.vn < kTiny ? -60.f : c.vn;
@@ -415,11 +420,17 @@ __device__ __forceinline__ bool expand_signs(const RowsArgs& a, const CacheSide&
     // has both norms 0
     const float rho = c.ok && c.xn > 0.f ? __fdividef(c.rn, c.xn) * a.rho_scale : 0.f;
     const __half2 r2 = __float2half2_rn(rho);
-    const uint32_t neg = *reinterpret_cast<const uint32_t*>(&r2) ^ 0x80008000u;
+    uint32_t neg = *reinterpret_cast<const uint32_t*>(&r2) ^ 0x80008000u;
     unsigned char* dst = sm.k[st] + 16 * kLBO + off;
     uint4 sg = c.s;
+    // fine: ρ as two fp16 numbers, the second's 16 chunks behind the first's
 #pragma unroll 1
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < (kFine ? 8 : 4); ++w) {
+      if (kFine && w == 4) {
+        const __half2 l2 = __float2half2_rn(rho - __low2float(r2));
+        neg = *reinterpret_cast<const uint32_t*>(&l2) ^ 0x80008000u;
+        sg = c.s;
+      }
       const uint32_t x = sg.x;
       sg.x = sg.y;
       sg.y = sg.z;
@@ -501,12 +512,12 @@ __device__ __forceinline__ bool expand_values(const RowsArgs& a, const CacheSide
   return true;
 }
 
-template <int IB, int VB, bool kList>
+template <int IB, int VB, bool kFine, bool kList>
 __device__ __forceinline__ bool expand(const RowsArgs& a, const CacheSide& side, Smem& sm,
                                        const Item& it, int warp, int lane) {
   const int first = 32 * (warp & 3);
-  if (warp < kSignWarp) return expand_keys<IB, kList>(a, side, sm, it, first, lane);
-  if (warp < kValueWarp) return expand_signs<kList>(a, side, sm, it, first, lane);
+  if (warp < kSignWarp) return expand_keys<IB, kFine, kList>(a, side, sm, it, first, lane);
+  if (warp < kValueWarp) return expand_signs<kFine, kList>(a, side, sm, it, first, lane);
   return expand_values<VB, kList>(a, side, sm, it, first, lane);
 }
 
@@ -535,6 +546,7 @@ struct Stats {
 // between them: the roles' code has to fit the instruction caches of an SM side by side
 // (unrolled, this loop alone took a third of the time of 112 rows).  The weights of a group of
 // 16 tokens are stored over the first half of its scores, which no other thread reads.
+template <bool kFine>
 __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int reps, int wl, int hf, int lane,
                                                float f) {
   const int rep = wl / (4 / reps), groups = 4 / reps;       // groups of 16 tokens per thread
@@ -546,9 +558,9 @@ __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int reps, in
   bool ok = true;
   auto wait = [&](uint64_t* bar, unsigned parity) { return ok = ok && warp_wait(bar, parity); };
   for (int t = 0; t < tiles; ++t) {
-    const int buf = t & 1;
+    const int buf = kFine ? 0 : t & 1;
     wait(&sm.ffull[t % kFacSlots], (t / kFacSlots) & 1);
-    wait(&sm.sfull[buf], (t >> 1) & 1);
+    wait(&sm.sfull[buf], (kFine ? t : t >> 1) & 1);
     tc_after();
     const uint32_t dcol = lane_base + kDCol + 128 * buf + 16 * group0;
     const float* fx = sm.fac[t % kFacSlots][0] + 16 * group0;
@@ -573,20 +585,20 @@ __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int reps, in
       if (c + 16 >= 16 * groups) break;
       tmem_store<16>(dcol + c, d);
     }
-    sm.tmax[buf][hf][r] = mt;
+    sm.tmax[t & 1][hf][r] = mt;
     // A wait that gave up ends both halves' loops here, together (neither then waits for the
     // other)
     if (!tq::named_sync_and(1 + wl, 64, ok)) {
       z.ok = false;
       return z;
     }
-    mt = fmaxf(mt, sm.tmax[buf][hf ^ 1][r]);
+    mt = fmaxf(mt, sm.tmax[t & 1][hf ^ 1][r]);
     const float m_new = mt > z.m + kGrow ? mt : z.m;
     if (t > 0 && __any_sync(0xffffffffu, m_new != z.m)) {
       // O (this half of its columns) follows the reference, once O += W(t − 1)·V(t − 1) is
       // done (vempty).  Its barrier is that of every other tile: the phase before, tile t − 3's,
       // ended before tile t was scored, so the parity says which tile is meant
-      wait(&sm.vempty[buf ^ 1], ((t - 1) >> 1) & 1);
+      wait(&sm.vempty[(t - 1) & 1], ((t - 1) >> 1) & 1);
       tc_after();
       const float corr = z.m == -INFINITY ? 0.f : ex2(z.m - m_new);
 #pragma unroll 1
@@ -608,7 +620,7 @@ __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int reps, in
     if (groups > 1) tq::tmem_wait_st();
 #pragma unroll 1
     for (int c = 16 * groups - 16;; c -= 16) {
-      uint32_t w[8];
+      uint32_t w[kFine ? 16 : 8];      // fine: then what the rounding left
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
         const float4 iv = *reinterpret_cast<const float4*>(fx + 2 * kTile + c + i);
@@ -621,8 +633,15 @@ __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int reps, in
         const __half2 p0 = __floats2half2_rn(w0, w1), p1 = __floats2half2_rn(w2, w3);
         w[i / 2] = *reinterpret_cast<const uint32_t*>(&p0);
         w[i / 2 + 1] = *reinterpret_cast<const uint32_t*>(&p1);
+        if constexpr (kFine) {
+          const float2 h0 = __half22float2(p0), h1 = __half22float2(p1);
+          const __half2 r0 = __floats2half2_rn(w0 - h0.x, w1 - h0.y);
+          const __half2 r1 = __floats2half2_rn(w2 - h1.x, w3 - h1.y);
+          w[8 + i / 2] = *reinterpret_cast<const uint32_t*>(&r0);
+          w[8 + i / 2 + 1] = *reinterpret_cast<const uint32_t*>(&r1);
+        }
       }
-      tmem_store<8>(dcol + c, w);
+      tmem_store<kFine ? 16 : 8>(dcol + c, w);
       if (c == 0) break;
       tmem_load<16>(dcol + c - 16, d);
       tq::tmem_wait_ld();
@@ -631,10 +650,10 @@ __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int reps, in
     z.l += lp.x + lp.y;
     if (reps > 1) {
       // the other replicas' groups, every other one by each half
-      const uint32_t none[8] = {};
+      const uint32_t none[kFine ? 16 : 8] = {};
 #pragma unroll 1
       for (int g = hf; g < 8; g += 2)
-        if (g / (2 * groups) != rep) tmem_store<8>(lane_base + kDCol + 128 * buf + 16 * g, none);
+        if (g / (2 * groups) != rep) tmem_store<kFine ? 16 : 8>(lane_base + kDCol + 128 * buf + 16 * g, none);
     }
     tq::tmem_wait_st();
     tc_before();
@@ -648,7 +667,7 @@ __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int reps, in
   return z;
 }
 
-template <int IB, int VB>
+template <int IB, int VB, bool kFine>
 __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_constant__ RowsArgs a) {
   extern __shared__ unsigned char smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(
@@ -745,21 +764,23 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long qr = r < rows ? qrow_of(r) : 0;
     const float f = r < rows ? __ldg(a.qf + qr) : 0.f;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    // (fine: the row's second 512 bytes are what the first ones' rounding left)
+#pragma unroll 1
+    for (int c = 0; c < (kFine ? 4 : 2); ++c) {
       uint32_t q[32];
+      const uint4* src = a.qop + qr * (kFine ? 64 : 32) + 32 * (c >> 1) + 16 * hf + 8 * (c & 1);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint4 x = r < rows ? __ldg(a.qop + qr * 32 + 16 * hf + 8 * c + i) : make_uint4(0, 0, 0, 0);
+        const uint4 x = r < rows ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
         q[4 * i] = x.x; q[4 * i + 1] = x.y; q[4 * i + 2] = x.z; q[4 * i + 3] = x.w;
       }
-      tmem_store<32>(lane_base + kQCol + 64 * hf + 32 * c, q);
+      tmem_store<32>(lane_base + (c >> 1 ? kQLowCol : kQCol) + 64 * hf + 32 * (c & 1), q);
     }
     tq::tmem_wait_st();
     tc_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.qfull);
-    const Stats z = softmax_tiles(sm, tiles, reps, wl, hf, lane, f);
+    const Stats z = softmax_tiles<kFine>(sm, tiles, reps, wl, hf, lane, f);
     // ---- the item's record: lanes' parts through shared memory (the operands are done with),
     // replicas of a row added up with their log-sum-exp weights
     ok = ok && tq::named_sync_and(5, 256, z.ok);
@@ -804,9 +825,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
     // ================================================================ expanders
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsExpand));
     const Item it{t0, tiles, len, nblk, b, h, list};
-    if (pre) ok = expand<IB, VB, false>(a, a.pre, sm, it, warp, lane);
-    else if (list) ok = expand<IB, VB, true>(a, a.own, sm, it, warp, lane);
-    else ok = expand<IB, VB, false>(a, a.own, sm, it, warp, lane);
+    if (pre) ok = expand<IB, VB, kFine, false>(a, a.pre, sm, it, warp, lane);
+    else if (list) ok = expand<IB, VB, kFine, true>(a, a.own, sm, it, warp, lane);
+    else ok = expand<IB, VB, kFine, false>(a, a.own, sm, it, warp, lane);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     // ================================================================ MMA issuer
@@ -817,24 +838,30 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
     // is one instruction and the queue of the tensor core does not run dry.
     const uint64_t kdesc = tq::smem_desc(s32(sm.k[0]), kLBO, 128);
     const uint64_t vdesc = tq::smem_desc(s32(sm.v[0]), 128, kLBO);
+    constexpr int kBufs = kFine ? 1 : 2;
     auto weigh = [&](int t) {   // O += W(t)·V(t)
-      const int st = t & 1;
-      if (!wait(&sm.vfull[st], (t >> 1) & 1) || !wait(&sm.pfull[st], (t >> 1) & 1)) return;
+      const int st = t & 1, buf = t % kBufs;
+      if (!wait(&sm.vfull[st], (t >> 1) & 1) || !wait(&sm.pfull[buf], (t / kBufs) & 1)) return;
       tc_after();
       if (elect_one()) {
         const uint64_t v = vdesc + st * (kVBytes >> 4);
-        const uint32_t w = kDCol + 128 * st;
+        const uint32_t w = kDCol + 128 * buf;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
           tq::mma_ts(kOCol, w + 16 * ks, v + ks * (256 >> 4), kIdescO, t > 0 || ks > 0);
+        if (kFine) {
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            tq::mma_ts(kOCol, w + 16 * ks + 8, v + ks * (256 >> 4), kIdescO, 1u);
+        }
         tq::mma_commit(&sm.vempty[st]);
       }
       __syncwarp();
     };
     wait(&sm.qfull, 0);
     for (int t = 0; t < tiles && ok; ++t) {
-      const int st = t & 1;
-      if (!wait(&sm.kfull[st], (t >> 1) & 1)) break;
+      const int st = t % kBufs;
+      if (!wait(&sm.kfull[st], (t / kBufs) & 1)) break;
       tc_after();
       if (elect_one()) {
         const uint64_t k = kdesc + st * (kKBytes >> 4);
@@ -842,13 +869,22 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
 #pragma unroll
         for (int ks = 0; ks < 16; ++ks)
           tq::mma_ts(d, kQCol + 8 * ks, k + ks * (2 * kLBO >> 4), kIdescS, ks > 0);
+        if (kFine) {   // the rests of y and z, and z with the rest of ρ
+#pragma unroll
+          for (int ks = 0; ks < 16; ++ks)
+            tq::mma_ts(d, kQLowCol + 8 * ks, k + ks * (2 * kLBO >> 4), kIdescS, 1u);
+#pragma unroll
+          for (int ks = 8; ks < 16; ++ks)
+            tq::mma_ts(d, kQCol + 8 * ks, k + (ks + 8) * (2 * kLBO >> 4), kIdescS, 1u);
+        }
         tq::mma_commit(&sm.sfull[st]);
         tq::mma_commit(&sm.kempty[st]);
       }
       __syncwarp();
-      if (t > 0) weigh(t - 1);
+      if (kFine) weigh(t);
+      else if (t > 0) weigh(t - 1);
     }
-    if (ok) weigh(tiles - 1);
+    if (!kFine && ok) weigh(tiles - 1);
     // whatever was issued has ended before the tensor memory is given back
     if (elect_one()) tq::mma_commit(&sm.drain);
     __syncwarp();
@@ -868,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
 constexpr int kPrepThreads = 1024;
 template <int kRows>
 __global__ void __launch_bounds__(kPrepThreads)
-rows_prep_kernel(const void* q, int q_dtype, int nrows, const float* __restrict__ piT,
+rows_prep_kernel(const void* q, int q_dtype, int nrows, int fine, const float* __restrict__ piT,
                  const float* __restrict__ sT, float factor, __half* qop, float* qf) {
   __shared__ float qs[kRows][TQ_D];
   __shared__ float part[4][kRows][256];
@@ -920,8 +956,11 @@ rows_prep_kernel(const void* q, int q_dtype, int nrows, const float* __restrict_
     const int r = i >> 8, c = i & 255;
     if (row0 + r >= nrows) continue;
     const float s = (part[0][r][c] + part[1][r][c]) + (part[2][r][c] + part[3][r][c]);
-    qop[(long long)(row0 + r) * 256 + c] =
-        __float2half_rn(s * scale[r] * (c < 128 ? kAlpha : kBeta));
+    const float x = s * scale[r] * (c < 128 ? kAlpha : kBeta);
+    const __half h = __float2half_rn(x);
+    __half* row = qop + (long long)(row0 + r) * (fine ? 512 : 256) + c;
+    row[0] = h;
+    if (fine) row[256] = __float2half_rn(x - __half2float(h));
   }
 }
 
@@ -1041,6 +1080,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 struct Plan {
   int G, rows, row_tiles, pre_splits, own_splits;
+  int fine;        // fp16 outputs: operands as pairs of fp16
   size_t qf_off, rec_off, bytes;
 };
 
@@ -1128,7 +1168,8 @@ tq_status make_plan(const tq_attn_desc* d, long long pre_tiles, long long own_ti
   p->pre_splits = want.sp;
   p->own_splits = want.so;
   if (pu * p->pre_splits + ou * p->own_splits > 0x7fffffffLL) return TQ_ERR_UNSUPPORTED;
-  p->qf_off = (size_t)p->rows * 512;
+  p->fine = d->out_dtype == TQ_F16;
+  p->qf_off = (size_t)p->rows * (p->fine ? 1024 : 512);
   p->rec_off = (p->qf_off + (size_t)p->rows * sizeof(float) + 255) / 256 * 256;
   p->bytes = p->rec_off + (size_t)(p->pre_splits + p->own_splits) * p->rows * kRecFloats * sizeof(float);
   return TQ_OK;
@@ -1177,7 +1218,7 @@ cudaLaunchConfig_t config(unsigned grid, unsigned block, size_t smem, cudaStream
   return c;
 }
 
-template <int IB, int VB>
+template <int IB, int VB, bool kFine>
 tq_status launch_attn(const RowsArgs& a, unsigned items, cudaStream_t stream) {
   constexpr int smem = (int)sizeof(Smem) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");
@@ -1185,29 +1226,34 @@ tq_status launch_attn(const RowsArgs& a, unsigned items, cudaStream_t stream) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return TQ_ERR_CUDA;
   if (!configured[dev]) {
-    if (cudaFuncSetAttribute(rows_attn_kernel<IB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(rows_attn_kernel<IB, VB, kFine>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smem) != cudaSuccess)
       return TQ_ERR_CUDA;
     // the warpgroups' shares add up to what the block is launched with: more would wait forever
     cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, rows_attn_kernel<IB, VB>) != cudaSuccess) return TQ_ERR_CUDA;
+    if (cudaFuncGetAttributes(&fa, rows_attn_kernel<IB, VB, kFine>) != cudaSuccess) return TQ_ERR_CUDA;
     if (fa.numRegs != kRegsLaunch) return TQ_ERR_UNSUPPORTED;
     configured[dev] = true;
   }
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = config(items, kThreads, smem, stream, attr);
-  return tq_cuda_status(cudaLaunchKernelEx(&cfg, rows_attn_kernel<IB, VB>, a));
+  return tq_cuda_status(cudaLaunchKernelEx(&cfg, rows_attn_kernel<IB, VB, kFine>, a));
+}
+
+template <int IB, bool kFine>
+tq_status launch_v(const RowsArgs& a, int vbits, unsigned items, cudaStream_t stream) {
+  switch (vbits) {
+    case 1: return launch_attn<IB, 1, kFine>(a, items, stream);
+    case 2: return launch_attn<IB, 2, kFine>(a, items, stream);
+    case 3: return launch_attn<IB, 3, kFine>(a, items, stream);
+    case 4: return launch_attn<IB, 4, kFine>(a, items, stream);
+  }
+  return TQ_ERR_UNSUPPORTED;
 }
 
 template <int IB>
-tq_status launch_k(const RowsArgs& a, int vbits, unsigned items, cudaStream_t stream) {
-  switch (vbits) {
-    case 1: return launch_attn<IB, 1>(a, items, stream);
-    case 2: return launch_attn<IB, 2>(a, items, stream);
-    case 3: return launch_attn<IB, 3>(a, items, stream);
-    case 4: return launch_attn<IB, 4>(a, items, stream);
-  }
-  return TQ_ERR_UNSUPPORTED;
+tq_status launch_k(const RowsArgs& a, int vbits, bool fine, unsigned items, cudaStream_t stream) {
+  return fine ? launch_v<IB, true>(a, vbits, items, stream) : launch_v<IB, false>(a, vbits, items, stream);
 }
 
 // Rows per CTA of the two kernels around: the fewest (1, 2, 4, most) that keep about one CTA per SM.
@@ -1218,14 +1264,14 @@ int rows_per_cta(int rows, int most) {
   return most;
 }
 
-tq_status launch_prep(const void* q, int q_dtype, int rows, const tq_codec* kc, float factor,
+tq_status launch_prep(const void* q, int q_dtype, int rows, int fine, const tq_codec* kc, float factor,
                       void* qop, float* qf, cudaStream_t stream) {
   const int rp = rows_per_cta(rows, 8);
   auto kern = rp == 1 ? rows_prep_kernel<1> : rp == 2 ? rows_prep_kernel<2>
             : rp == 4 ? rows_prep_kernel<4> : rows_prep_kernel<8>;
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = config((rows + rp - 1) / rp, kPrepThreads, 0, stream, attr);
-  return tq_cuda_status(cudaLaunchKernelEx(&cfg, kern, q, q_dtype, rows, (const float*)kc->d_piT,
+  return tq_cuda_status(cudaLaunchKernelEx(&cfg, kern, q, q_dtype, rows, fine, (const float*)kc->d_piT,
                                            (const float*)kc->d_sT, factor,
                                            static_cast<__half*>(qop), qf));
 }
@@ -1267,16 +1313,16 @@ tq_status run(const tq_attn_desc* d, const Plan& p, const tq_codec* kc, const tq
   a.qf = reinterpret_cast<const float*>(ws + p.qf_off);
   a.rec = reinterpret_cast<float*>(ws + p.rec_off);
   const float factor = scale * 1.4426950408889634f / (kAlpha * kc->lut_scale);
-  st = launch_prep(q, d->q_dtype, p.rows, kc, factor, ws, reinterpret_cast<float*>(ws + p.qf_off),
+  st = launch_prep(q, d->q_dtype, p.rows, p.fine, kc, factor, ws, reinterpret_cast<float*>(ws + p.qf_off),
                    stream);
   if (st != TQ_OK) return st;
   const unsigned items = (unsigned)((long long)p.pre_splits * a.Hkv * p.row_tiles +
                                     (long long)p.own_splits * a.Hkv * a.B);
   switch (kc->ibits) {
-    case 1: st = launch_k<1>(a, vc->ibits, items, stream); break;
-    case 2: st = launch_k<2>(a, vc->ibits, items, stream); break;
-    case 3: st = launch_k<3>(a, vc->ibits, items, stream); break;
-    case 4: st = launch_k<4>(a, vc->ibits, items, stream); break;
+    case 1: st = launch_k<1>(a, vc->ibits, p.fine, items, stream); break;
+    case 2: st = launch_k<2>(a, vc->ibits, p.fine, items, stream); break;
+    case 3: st = launch_k<3>(a, vc->ibits, p.fine, items, stream); break;
+    case 4: st = launch_k<4>(a, vc->ibits, p.fine, items, stream); break;
     default: st = TQ_ERR_UNSUPPORTED;
   }
   if (st != TQ_OK) return st;

@@ -47,15 +47,17 @@ def value_parts(v, vc, b, h, at):
     return torch.tensor(vc.centroids, device=j.device)[j], get(v.xnorm, False).double()
 
 
-def attend(q, parts, kc, vc, scale=None):
+def attend(q, parts, kc, vc, scale=None, pairs=False):
     """Attention of query rows q [g, 128] over tokens given as (c, s, xn, rn, cv, vn); returns the
     rows and the standard deviation of the error (2-norm) that 16-bit operands allow.
 
-    Roundings of the kernel, each uniform and off by at most u = eps(fp16) / 2 = 2^-11 relative
-    (standard deviation u / √3): y_j, z_j and a weight w_t, all independent; ρ_t, one for all of a
-    token's signs; the levels, off by at most ε as scaled (the same for all tokens: taken at ε).
-    A logit error δ_t moves the output by p_t·δ_t·(v_t − out): at most p_t·δ_t·(‖v_t‖ + ‖out‖).
-    Weights below 2^-14 of 2^8 (fp16 subnormals) add an absolute 2^-25 each."""
+    Roundings of the kernel, each uniform and off by at most u = eps(fp16) / 2 = 2^-11 relative, or
+    with pairs of fp16 numbers (fp16 outputs) 2^-21 (standard deviation u / √3): y_j, z_j and a
+    weight w_t, all independent; ρ_t, one for all of a token's signs; the levels, off by at most ε
+    as scaled (the same for all tokens: taken at ε).  32-bit products and sums of a score: 2^-20 of
+    its largest possible value.  A logit error δ_t moves the output by p_t·δ_t·(v_t − out): at
+    most p_t·δ_t·(‖v_t‖ + ‖out‖).  Weights below 2^-14 of 2^8 (fp16 subnormals) add an absolute
+    2^-25 each."""
     c, s, xn, rn, cv, vn = parts
     pi, sk = (torch.tensor(m, device=q.device) for m in (kc.pi, kc.s))
     vpi = torch.tensor(vc.pi, device=q.device)
@@ -68,11 +70,13 @@ def attend(q, parts, kc, vc, scale=None):
     p = torch.softmax(scale * (main + sketch), -1)
     v = vn[:, None] * (cv @ vpi)
     out = p @ v
-    u = 2.0 ** -11 / math.sqrt(3)
+    u = 2.0 ** (-21 if pairs else -11) / math.sqrt(3)
     ek, ev = level_error(kc), level_error(vc)
     var = scale ** 2 * ((u * xn) ** 2 * ((y ** 2) @ (c ** 2).T)
                         + (u * QJL * rn) ** 2 * (z ** 2).sum(-1, keepdim=True)
-                        + (u * sketch) ** 2 + (ek * xn) ** 2 * ((y ** 2) @ (c ** 2).T))
+                        + (u * sketch) ** 2 + (ek * xn) ** 2 * ((y ** 2) @ (c ** 2).T)
+                        + (2.0 ** -20 * (xn * y.norm(dim=-1, keepdim=True) * c.norm(dim=-1)
+                                         + QJL * rn * z.norm(dim=-1, keepdim=True) * math.sqrt(D))) ** 2)
     size = vn + out.norm(dim=-1, keepdim=True)
     err = ((p * size) ** 2 * (var + u ** 2)).sum(-1).sqrt() + ev * out.norm(dim=-1)
     top = (p * vn).amax(-1)

@@ -121,15 +121,17 @@ def check_prefix(kc, vc, q, pre, mine, out, plen, lens, kv, group, scale=None):
         for b, n in enumerate(lens):
             own = parts(*mine, kc, vc, b, h, torch.arange(n, device="cuda"))
             rows = slice(h * group, (h + 1) * group)
-            r, err = ref.attend(q[b, rows], [torch.cat(p) for p in zip(shared, own)], kc, vc, scale)
+            r, err = ref.attend(q[b, rows], [torch.cat(p) for p in zip(shared, own)], kc, vc, scale,
+                                out.dtype == torch.float16)
             worst = max(worst, ref.check_rows(out[b, rows], r, err, f"sequence {b}, KV head {h}"))
     return worst
 
 
+@pytest.mark.parametrize("out_dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("kbits,vbits", [(k, v) for k in (2, 3, 4, 5) for v in (1, 2, 3, 4)])
-def test_prefix_bit_widths(kbits, vbits):
+def test_prefix_bit_widths(kbits, vbits, out_dtype):
     lens = [5, 130]
-    a = run_prefix(kbits, vbits, 2, 1, 3, 200, lens, seed=10 * kbits + vbits)
+    a = run_prefix(kbits, vbits, 2, 1, 3, 200, lens, out_dtype=out_dtype, seed=10 * kbits + vbits)
     check_prefix(*a[:5], a[6], 200, lens, 1, 3)
     assert flags() == 0
 
@@ -144,8 +146,9 @@ def test_prefix_bit_widths(kbits, vbits):
     (5, 1, 8, 20011, [1, 0, 700, 63, 65]),                      # many splits
 ])
 @pytest.mark.parametrize("paged", [0, 64, 192])
-def test_prefix_shapes(batch, kv, group, plen, lens, paged):
-    a = run_prefix(3, 4, batch, kv, group, plen, lens, paged, seed=plen + paged)
+@pytest.mark.parametrize("out_dtype", [torch.float16, torch.bfloat16])
+def test_prefix_shapes(batch, kv, group, plen, lens, paged, out_dtype):
+    a = run_prefix(3, 4, batch, kv, group, plen, lens, paged, out_dtype=out_dtype, seed=plen + paged)
     check_prefix(*a[:5], a[6], plen, lens, kv, group)
     assert flags() == 0
 
@@ -232,7 +235,8 @@ def check_sparse(kc, vc, q, k, v, lists, lens, out, group):
                   if 0 <= i and 64 * i < n]
             at = torch.tensor(np.concatenate(at) if at else [], dtype=torch.long, device="cuda")
             rows = slice(h * group, (h + 1) * group)
-            r, err = ref.attend(q[b, rows], parts(k, v, kc, vc, b, h, at), kc, vc)
+            r, err = ref.attend(q[b, rows], parts(k, v, kc, vc, b, h, at), kc, vc,
+                                pairs=out.dtype == torch.float16)
             ref.check_rows(out[b, rows], r, err, f"sequence {b}, KV head {h}")
 
 
@@ -260,7 +264,8 @@ def lists_of(lens, kv, keep, seed):
     (1, 8, 4, [70001], 300, 0, 3, 2),
     (40, 2, 5, [61 * i for i in range(40)], 9, 128, 4, 1),
 ])
-def test_sparse_attention(batch, kv, group, lens, keep, paged, kbits, vbits):
+@pytest.mark.parametrize("out_dtype", [torch.float16, torch.bfloat16])
+def test_sparse_attention(batch, kv, group, lens, keep, paged, kbits, vbits, out_dtype):
     kc, vc = codec("k", kbits), codec("v", vbits)
     cap = up64(max(lens))
     pages = None
@@ -271,7 +276,7 @@ def test_sparse_attention(batch, kv, group, lens, keep, paged, kbits, vbits):
     hide(pages, lens)
     q = queries(batch, kv * group, torch.bfloat16, 1)
     lst = lists_of(lens, kv, keep, 2)
-    plan = api.SparsePlan(batch, kv * group, kv, cap, max(lens), keep, 0, 0, out_dtype=torch.float16)
+    plan = api.SparsePlan(batch, kv * group, kv, cap, max(lens), keep, 0, 0, out_dtype=out_dtype)
     out = plan.run(kc, vc, q, k, v, i32(lens), lst, plan.new_out())
     check_sparse(kc, vc, q, k, v, lst, lens, out, group)
     assert flags() == 0
@@ -634,17 +639,19 @@ def test_growing_scores_move_the_reference():
         pk.rnorm.copy_(0.4 * pk.xnorm)
         for rows in (1, 8):
             q = queries(1, rows, torch.float32, 5, 4.0)
-            plan = api.PrefixPlan(1, rows, 1, 1536, 1536, 1536, 1536, torch.float32, torch.float16)
-            out = plan.run(kc, vc, q, pk, pv, i32([n]), k, v, i32([n]), plan.new_out())
-            check_prefix(kc, vc, q, (pk, pv), (k, v), out, n, [n], 1, rows)
+            for out_dtype in (torch.float16, torch.bfloat16):
+                plan = api.PrefixPlan(1, rows, 1, 1536, 1536, 1536, 1536, torch.float32, out_dtype)
+                out = plan.run(kc, vc, q, pk, pv, i32([n]), k, v, i32([n]), plan.new_out())
+                check_prefix(kc, vc, q, (pk, pv), (k, v), out, n, [n], 1, rows)
 
 
+@pytest.mark.parametrize("out_dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("batch,group", [(4, 8), (5, 8), (8, 8), (9, 8), (16, 8), (17, 8)])
-def test_rows_per_item(batch, group):
+def test_rows_per_item(batch, group, out_dtype):
     """32, 40, 64, 72, 128 and 136 query rows of a KV head: a row in four lane groups, in two, in
     one, and in two row tiles."""
     lens = [(53 * i) % 90 for i in range(batch)]
-    a = run_prefix(3, 2, batch, 1, group, 700, lens, seed=batch)
+    a = run_prefix(3, 2, batch, 1, group, 700, lens, out_dtype=out_dtype, seed=batch)
     check_prefix(*a[:5], a[6], 700, lens, 1, group)
 
 
