@@ -63,9 +63,14 @@ constexpr int kTile = 128;              // tokens per tile, and query rows per i
 // 8 softmax warps, 3 × 4 expander warps, and a warpgroup that holds the issuer warp alone
 constexpr int kKeyWarp = 8, kSignWarp = 12, kValueWarp = 16, kIssueWarp = 20;
 constexpr int kThreads = 768;
-// Registers per thread: 80 at launch (61,440 of the block), which the softmax warps keep; the
-// expanders take what the last warpgroup gives up: 256·80 + 384·88 + 128·56 = 61,440.
-constexpr int kRegsLaunch = 80, kRegsExpand = 88, kRegsIssue = 56;
+// Registers per thread: 80 at launch, 61,440 of the block, split by what each role spills least
+// with: softmax 80, expanders 88, issuer 56 (256·80 + 384·88 + 128·56 = 61,440), or with pairs of
+// operands 96, 72 and 72 (256·96 + 384·72 + 128·72 = 61,440).
+constexpr int kRegsLaunch = 80;
+template <bool kFine>
+struct Regs {
+  static constexpr int softmax = kFine ? 96 : 80, expand = kFine ? 72 : 88, issue = kFine ? 72 : 56;
+};
 constexpr int kRecFloats = 132;         // acc[128], m, l, padding
 constexpr int kLBO = 2048;              // bytes between 8-position chunks of an operand image
 constexpr int kKBytes = 32 * kLBO;      // key operand: 128 tokens × 256 positions, fp16
@@ -675,7 +680,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  static_assert(128 * kRegsIssue + 384 * kRegsExpand + 256 * kRegsLaunch <= kThreads * kRegsLaunch, "register split");
+  using R = Regs<kFine>;
+  static_assert(256 * R::softmax + 384 * R::expand + 128 * R::issue <= kThreads * kRegsLaunch, "register split");
 
   // ---- the item: prefix items first (they are the long ones)
   int item = blockIdx.x;
@@ -757,6 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
 
   if (warp < kKeyWarp) {
     // ================================================================ softmax
+    if (kFine) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::softmax));
     const int wl = warp & 3, hf = warp >> 2;
     const int per = kTile / reps;              // rows per replica
     const int r = (32 * wl + lane) & (per - 1);
@@ -823,13 +830,14 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
     }
   } else if (warp < kIssueWarp) {
     // ================================================================ expanders
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsExpand));
+    if (kFine) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::expand));
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::expand));
     const Item it{t0, tiles, len, nblk, b, h, list};
     if (pre) ok = expand<IB, VB, kFine, false>(a, a.pre, sm, it, warp, lane);
     else if (list) ok = expand<IB, VB, kFine, true>(a, a.own, sm, it, warp, lane);
     else ok = expand<IB, VB, kFine, false>(a, a.own, sm, it, warp, lane);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::issue));
     // ================================================================ MMA issuer
     if (warp == kIssueWarp) {
     constexpr uint32_t kIdescS = tq::idesc_f16(128, 128);
