@@ -321,6 +321,8 @@ tq_status tq_decode_attention_asym(const tq_attn_desc* desc, const tq_codec* vc,
  *              seq_lens (longer ones are clamped and flagged).  A sequence with no token at all
  *              gives a zero row.
  *   kc, vc   : key codecs of 2 to 5 bits, value codecs of 1 to 4; created on the current device.
+ *   Rows of up to 2^26 slots (a page's, or a flat cache's capacity) and up to 2^24 query rows
+ *   (batch · q_heads); more return TQ_ERR_UNSUPPORTED.
  *   desc->out_dtype is F16 or BF16 (F32 returns TQ_ERR_UNSUPPORTED): the products run on fp16
  *   operands, and on pairs of them for F16 outputs, so that a row is off by about the rounding of
  *   its own type.  Value vectors with norms below 2^-60 count as zero vectors.
@@ -369,7 +371,8 @@ tq_status tq_block_bounds(const void* x, tq_dtype x_dtype, int32_t batch, int32_
  * scores are compared as in 64 bits: the result does not depend on any order of summation.  A
  * query head whose sum is NaN is left out; a block left with none scores −∞.
  *   list     : device int32 [batch][kv_heads][max_blocks], the kept blocks ascending, then −1.
- *   first_blocks + last_blocks ≤ max_blocks.
+ *   first_blocks + last_blocks ≤ max_blocks ≤ 2^24; batch · kv_heads ≤ 65535 and max_seq_len ≤
+ *              2^26, else TQ_ERR_UNSUPPORTED.
  *   desc     : batch, q_heads, kv_heads, capacity, max_seq_len (bounds seq_lens) and q_dtype.
  *   workspace: ≥ tq_block_select_workspace_bytes(desc) bytes, 256-byte aligned, no
  *              initialisation needed; calls that share it must be serialised on one stream. */

@@ -125,6 +125,7 @@ class Pages:
         self.block_table = self.block_table.contiguous()
         self._c = B.tq_pages(self.block_table.data_ptr(), self.block_table.shape[1],
                              self.page_tokens, self.num_pages)
+        self._p = ctypes.pointer(self._c)
 
     @property
     def max_pages(self):
@@ -136,7 +137,7 @@ class Pages:
         return self.max_pages * self.page_tokens
 
     def c(self):
-        return ctypes.pointer(self._c)
+        return self._p
 
 
 def _pages_ptr(pages):
@@ -225,8 +226,7 @@ class MSECache:
 def _x_args(x: torch.Tensor):
     if x.dim() != 4 or x.shape[-1] != HEAD_DIM or x.stride(-1) != 1:
         raise ValueError("x must be [batch, heads, tokens, 128] with contiguous last dim")
-    bsz, h, t, _ = x.shape
-    return bsz, h, t, x.stride(0), x.stride(1), x.stride(2)
+    return *x.shape[:3], *x.stride()[:3]
 
 
 def quantize_prod(codec: Codec, x: torch.Tensor, cache: ProdCache, pos=None, count=None,
@@ -436,18 +436,21 @@ class BlockBounds:
 def block_bounds(x: torch.Tensor, blocks: BlockBounds, pos=None, count=None, stream=None):
     """Folds keys x [batch, heads, tokens, 128] into their blocks' bounds, at the cache positions
     pos[b].. (0) and count[b] tokens each (all): the arguments of quantize_prod."""
-    bsz, h, t, sb, sh, st = _x_args(x)
+    bsz, h, t, sb, sh, stride_t = _x_args(x)
     slots = blocks.capacity
     blocks.expect(bsz, h, slots)
     d = _device(x, blocks.bounds)
-    for v in (pos, count):
-        if v is not None:
-            _expect(v, (bsz,), torch.int32, "pos and count")
-            _device(v)
-    st = B.load().tq_block_bounds(x.data_ptr(), tq_dtype(x.dtype), bsz, h, t, sb, sh, st,
-                                  None if pos is None else pos.data_ptr(),
-                                  None if count is None else count.data_ptr(), blocks.c(), slots,
-                                  _on(stream, d))
+    at = n = None
+    if pos is not None:
+        _expect(pos, (bsz,), torch.int32, "pos")
+        _device(pos)
+        at = pos.data_ptr()
+    if count is not None:
+        _expect(count, (bsz,), torch.int32, "count")
+        _device(count)
+        n = count.data_ptr()
+    st = B.load().tq_block_bounds(x.data_ptr(), tq_dtype(x.dtype), bsz, h, t, sb, sh, stride_t, at, n,
+                                  blocks.c(), slots, _on(stream, d))
     if st:
         B.check(st, "tq_block_bounds")
 

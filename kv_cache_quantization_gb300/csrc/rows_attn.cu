@@ -917,15 +917,15 @@ rows_prep_kernel(const void* q, int q_dtype, int nrows, int fine, const float* _
   __shared__ float qs[kRows][TQ_D];
   __shared__ float part[4][kRows][256];
   __shared__ float scale[kRows];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, row0 = blockIdx.x * kRows;
   const int p = tid & 255, kq = tid >> 8;
   // position p < 128: y at plane_coord(p); else z at sign_coord(p − 128)
   const float* mat = (p < 128 ? piT + plane_coord(p) : sT + sign_coord(p - 128)) + 32 * kq * TQ_D;
-  float w[32];
+  float w[32];   // the codec's matrices do not depend on the launch before
 #pragma unroll
   for (int k = 0; k < 32; ++k) w[k] = __ldg(mat + k * TQ_D);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int i = tid; i < kRows * TQ_D; i += kPrepThreads) {
     const int r = i / TQ_D;
     qs[r][i % TQ_D] = row0 + r < nrows ? load_elem(q, q_dtype, (long long)row0 * TQ_D + i) : 0.f;
@@ -946,7 +946,7 @@ rows_prep_kernel(const void* q, int q_dtype, int nrows, int fine, const float* _
       if (row0 + r < nrows) qf[row0 + r] = ldexpf(factor, e);
     }
   }
-#pragma unroll
+#pragma unroll 1      // (rolled: short kernels wait for their instructions)
   for (int r = 0; r < kRows; ++r) {
     float s = 0.f;
 #pragma unroll
@@ -1054,8 +1054,7 @@ rows_merge_kernel(const float* rec, int nrec, int nrows, const float* __restrict
   }
   __syncthreads();
   float (*prod)[kRows][TQ_D] = reinterpret_cast<float (*)[kRows][TQ_D]>(acc);   // 4 quarters
-  float part[kRows];
-#pragma unroll
+#pragma unroll 1
   for (int r = 0; r < kRows; ++r) {
     float s = 0.f;
 #pragma unroll
@@ -1066,10 +1065,8 @@ rows_merge_kernel(const float* rec, int nrec, int nrows, const float* __restrict
       s = fmaf(w[k + 2], x.z, s);
       s = fmaf(w[k + 3], x.w, s);
     }
-    part[r] = s;
+    prod[kq][r][j] = s;
   }
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) prod[kq][r][j] = part[r];
   __syncthreads();
   for (int i = tid; i < kRows * TQ_D; i += kMergeThreads) {
     const int r = i >> 7, c = i & 127;
