@@ -321,8 +321,8 @@ tq_status tq_decode_attention_asym(const tq_attn_desc* desc, const tq_codec* vc,
  *              seq_lens (longer ones are clamped and flagged).  A sequence with no token at all
  *              gives a zero row.
  *   kc, vc   : key codecs of 2 to 5 bits, value codecs of 1 to 4; created on the current device.
- *   Rows of up to 2^26 slots (a page's, or a flat cache's capacity) and up to 2^24 query rows
- *   (batch · q_heads); more return TQ_ERR_UNSUPPORTED.
+ *   Rows of up to 2^26 slots (a page's, or a flat cache's capacity), up to 2^24 query rows (batch ·
+ *   q_heads) and up to 2^30 tokens a sequence; more return TQ_ERR_UNSUPPORTED.
  *   desc->out_dtype is F16 or BF16 (F32 returns TQ_ERR_UNSUPPORTED): the products run on fp16
  *   operands, and on pairs of them for F16 outputs, so that a row is off by about the rounding of
  *   its own type.  Value vectors with norms below 2^-60 count as zero vectors.

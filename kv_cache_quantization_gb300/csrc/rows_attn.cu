@@ -1154,6 +1154,7 @@ tq_status make_plan(const tq_attn_desc* d, long long pre_tiles, long long own_ti
   if (d->q_dtype != TQ_F32 && d->q_dtype != TQ_F16 && d->q_dtype != TQ_BF16) return TQ_ERR_UNSUPPORTED;
   if (d->out_dtype != TQ_F16 && d->out_dtype != TQ_BF16) return TQ_ERR_UNSUPPORTED;
   if ((long long)d->batch * d->q_heads > (1 << 24)) return TQ_ERR_UNSUPPORTED;
+  if (std::max(pre_tiles, own_tiles) > (1 << 23)) return TQ_ERR_UNSUPPORTED;   // 2^30 tokens: 32-bit token numbers
   p->G = d->q_heads / d->kv_heads;
   p->rows = d->batch * d->q_heads;
   p->row_tiles = (int)(((long long)d->batch * p->G + kTile - 1) / kTile);

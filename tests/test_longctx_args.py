@@ -78,6 +78,17 @@ def test_attention_outputs_are_16_bit():
     assert B.tq_sparse_workspace_bytes(desc(tail=8), 16) == 0      # no FP16 tail here
 
 
+def test_limits_of_size():
+    big = desc(cap=1 << 30, mx=1 << 30)
+    assert B.tq_prefix_workspace_bytes(big, 1 << 20) > 0
+    assert B.tq_prefix_workspace_bytes(desc(cap=(1 << 30) + 64, mx=(1 << 30) + 1), 0) == 0
+    assert B.tq_prefix_workspace_bytes(desc(), (1 << 30) + 1) == 0
+    assert B.tq_prefix_workspace_bytes(desc(batch=1 << 20), 0) == 0       # 28 · 2^20 query rows
+    assert B.tq_block_select_workspace_bytes(desc(batch=1 << 15)) == 0    # 2^17 rows of blocks
+    assert B.tq_block_select_workspace_bytes(big) == 0
+    assert B.tq_sparse_workspace_bytes(desc(), (1 << 24) + 1) == 0
+
+
 def test_workspace_sizes_grow_with_the_call():
     assert 0 < B.tq_sparse_workspace_bytes(desc(batch=1), 16) < B.tq_sparse_workspace_bytes(desc(batch=64), 16)
     assert B.tq_prefix_workspace_bytes(desc(), 0) > 0              # an empty prefix is allowed
