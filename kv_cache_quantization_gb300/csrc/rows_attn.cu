@@ -30,9 +30,10 @@
 // take 1,536.  What bounds a tile is the integer pipe and the issue of the expansion (about 13
 // instructions for eight level coordinates, 8 for eight signs, 40% of the pipe's cycles) beside
 // that of the softmax (about 9 a score), and the instruction caches, which is why the roles' loops
-// are kept rolled.  Measured: a prefix of 262144 tokens for 8 sequences of 32/8 heads 184 us
-// (281 TFLOP/s, 1.07 TB/s), of 65536 for 64 of 28/4 heads 176 us (516 TFLOP/s), of 32768 for 32
-// 62 us; 32 blocks of each of 32 sequences 48 us.
+// are kept rolled.  Measured: a prefix of 262144 tokens for 8 sequences of 32/8 heads 182 us
+// (283 TFLOP/s, 1.08 TB/s), of 65536 for 64 of 28/4 heads 171 us (531 TFLOP/s), of 32768 for 32
+// 60 us; 32 blocks of each of 32 sequences 46 us.  (With 4-bit values the warps of the signs could
+// expand a quarter of them: 167 us for the 64 sequences, 47 us for the blocks; not done.)
 //
 // Roundings to 16 bits: the rotated query and sketch, ρ, the levels (scaled so that fp16 holds
 // them best, to a few 1e-5) and the weights, each off by at most half a step of fp16 (2^-11
