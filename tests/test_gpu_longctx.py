@@ -685,3 +685,37 @@ def test_python_layer_refuses_on_the_gpu():
             api.block_bounds(*args)
     with pytest.raises(TypeError):
         api.block_bounds(x.double(), blocks)
+
+
+def test_offsets_past_32_bits():
+    """A cache whose code arrays are longer than 4 GiB: the last sequence's last head lies behind
+    that, and so do its blocks' bounds behind 2^29 elements."""
+    kc, vc = codec("k", 3), codec("v", 2)
+    batch, kv, cap = 17, 8, 1 << 20
+    k, v = api.ProdCache.empty(batch, kv, cap, 3), api.MSECache.empty(batch, kv, cap, 2)
+    assert k.idx.numel() > 1 << 32
+    g = gen(1)
+    n = cap - 5
+    for t in (k.idx, k.sgn, v.idx):
+        last = t[-1, -1]
+        last.copy_(torch.randint(0, 256, last.shape, generator=g, device="cuda", dtype=torch.uint8))
+    for t in (k.xnorm, k.rnorm, v.xnorm):
+        t[-1, -1] = 6 + 4 * torch.rand(cap, generator=g, device="cuda")
+    lens = [0] * (batch - 1) + [n]
+    q = queries(batch, 4 * kv, torch.bfloat16, 2)
+    blocks = api.BlockBounds.empty(batch, kv, cap)
+    blocks.bounds[-1, -1] = torch.randn(blocks.bounds.shape[2:], generator=g, device="cuda").bfloat16()
+    plan = api.SparsePlan(batch, 4 * kv, kv, cap, cap, 6, 0, 1, out_dtype=torch.float16)
+    lst = plan.select(q, blocks, i32(lens), plan.new_list())
+    want = ref.select(q[-1, -4:], blocks.bounds[-1, -1], -(-n // 64), 6, 0, 1)
+    assert lst[-1, -1].tolist() == want
+    out = plan.run(kc, vc, q, k, v, i32(lens), lst, plan.new_out())
+    at = torch.tensor([t for i in want for t in range(64 * i, min(64 * i + 64, n))], device="cuda")
+    r, err = ref.attend(q[-1, -4:], parts(k, v, kc, vc, batch - 1, kv - 1, at), kc, vc, pairs=True)
+    ref.check_rows(out[-1, -4:], r, err, "last head")
+    assert not out[:-1].any() and flags() == 0
+    x = torch.randn(1, kv, 3, D, generator=g, device="cuda").bfloat16().expand(batch, -1, -1, -1)
+    pos = i32([0] * (batch - 1) + [n])
+    api.block_bounds(x, blocks, pos, i32([0] * (batch - 1) + [3]))
+    old = ref.bounds(x[-1:], [n], [3], blocks.bounds[-1:].clone())
+    assert torch.equal(blocks.bounds[-1:], old)
