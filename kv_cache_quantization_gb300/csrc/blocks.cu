@@ -190,6 +190,9 @@ __device__ __forceinline__ int blocks_of(const SelectArgs& a, int b) {
   return (min(max(a.seq_lens[b], 0), a.max_len) + kBlock - 1) / kBlock;
 }
 
+// The larger of two numbers ≥ 0, NaN if either is one.
+__device__ __forceinline__ float larger_or_nan(float a, float b) { return a != a || b <= a ? a : b; }
+
 // Sums over the 32 lanes of each of N values a lane: N/2 + N/4 + ... shuffles instead of 5·N.
 // Lane l ends with the sum of value l / (32 / N) (N ≤ 32, a power of two) in v[0].
 template <int N, typename T>
@@ -219,6 +222,11 @@ __device__ __forceinline__ void lane_sums(T (&v)[N], int lane) {
 // instructions costs more than issuing them (unrolled over eight heads this kernel took 8.5 us
 // for 4 × 512 blocks).  Bound by the latency of two dependent loads for short rows, by issuing
 // about 12 instructions per block and head for long ones.
+//
+// Beside the scores goes a bound of Σ|terms|, from which the selection takes how far a score may
+// be off.  An infinite bound of a channel times the 0 of queries of the other sign is NaN here, in
+// the score (which is then too low) and in the bound of Σ|terms|, which stays NaN: the selection
+// then trusts no 32-bit score of the row.  The 64-bit scores use one bound a channel, by the sign.
 __global__ void __launch_bounds__(256) block_score_kernel(const SelectArgs a) {
   __shared__ float4 s_q[TQ_MAX_GROUP + 1][2][32];   // [head][first or second four][lane]; last: max |.|
   __shared__ float s_err[8];
@@ -285,7 +293,7 @@ __global__ void __launch_bounds__(256) block_score_kernel(const SelectArgs a) {
           e = fmaf(m[2 * j], fabsf(x.x), e);
           e = fmaf(m[2 * j + 1], fabsf(x.y), e);
         }
-        err = e <= err ? err : e;   // NaN stays
+        err = larger_or_nan(err, e);
       }
     }
     float best = -INFINITY;
@@ -322,7 +330,7 @@ __global__ void __launch_bounds__(256) block_score_kernel(const SelectArgs a) {
   __syncthreads();
   if (threadIdx.x == 0) {
     float e = 0.f;
-    for (int i = 0; i < 8; ++i) e = s_err[i] <= e ? e : s_err[i];
+    for (int i = 0; i < 8; ++i) e = larger_or_nan(e, s_err[i]);
     a.err[(long long)row * a.chunks + blockIdx.x] = e;
   }
 }
