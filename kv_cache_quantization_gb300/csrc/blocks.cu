@@ -458,8 +458,9 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const SelectA
   worst = __reduce_max_sync(0xffffffffu, lane < nwarps ? s_err[lane] : 0u);
   // four multiply-adds and six additions on a term's way into the sum, half a step of 32 bits
   // each, and the product's own: 11·2^-24·Σ|terms|; 2^-20 leaves room for the rounding of the
-  // bound itself
-  const float E = worst == ~0u ? INFINITY : __uint_as_float(worst) * 9.5367431640625e-7f;
+  // bound itself.  Where products are subnormal or vanish, 256 of them are off by at most 2^-150
+  // each, in the score and in the bound: 2^-140 covers both
+  const float E = worst == ~0u ? INFINITY : fmaf(__uint_as_float(worst), 0x1p-20f, 0x1p-140f);
   if (want > 0) {
     // all keys agree above the highest bit in which low and high differ
     const int top = low == high ? -1 : 31 - __clz((int)(low ^ high));
@@ -516,9 +517,16 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const SelectA
         base += __reduce_add_sync(0xffffffffu, c);
       }
       __syncthreads();
-      // (a row of zero queries has nothing to score: every term is 0)
-      for (int i = tid; worst == 0u && i < open; i += blockDim.x) exact[i] = ordered(0.0);
-      for (int i = warp; worst != 0u && i < open; i += nwarps) {
+      // a row of zero queries has nothing to score: every term is 0 (Σ|terms| alone may be 0
+      // because its products vanish in 32 bits)
+      int some = worst != 0u;
+      if (worst == 0u) {
+        for (int i = tid; i < a.G * TQ_D; i += blockDim.x)
+          some |= !(load_elem(a.q, a.q_dtype, (long long)row * a.G * TQ_D + i) == 0.f);
+        some = __syncthreads_or(some);
+      }
+      for (int i = tid; !some && i < open; i += blockDim.x) exact[i] = ordered(0.0);
+      for (int i = warp; some && i < open; i += nwarps) {
         // lane l: channels 4l .. 4l + 3 of every head, all loads first
         const __nv_bfloat16* p = bounds_at(a, b, h, doubt[i]);
         double best = -INFINITY;
