@@ -673,6 +673,8 @@ __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int reps, in
   return z;
 }
 
+// Lengths, lists, block tables and codes are read before this kernel's wait: it starts only when all
+// of rows_prep_kernel is past its own wait, so whatever ran before that has ended and been flushed.
 template <int IB, int VB, bool kFine>
 __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_constant__ RowsArgs a) {
   extern __shared__ unsigned char smem_raw[];
@@ -771,7 +773,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
     const uint32_t lane_base = (uint32_t)(32 * wl) << 16;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long qr = r < rows ? qrow_of(r) : 0;
-    const float f = r < rows ? __ldg(a.qf + qr) : 0.f;
+    // (plain loads: the kernel before writes the operands while this one runs, so they must not go
+    // through the read-only path, which the wait does not order)
+    const float f = r < rows ? a.qf[qr] : 0.f;
     // (fine: the row's second 512 bytes are what the first ones' rounding left)
 #pragma unroll 1
     for (int c = 0; c < (kFine ? 4 : 2); ++c) {
@@ -779,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
       const uint4* src = a.qop + qr * (kFine ? 64 : 32) + 32 * (c >> 1) + 16 * hf + 8 * (c & 1);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint4 x = r < rows ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+        const uint4 x = r < rows ? src[i] : make_uint4(0, 0, 0, 0);
         q[4 * i] = x.x; q[4 * i + 1] = x.y; q[4 * i + 2] = x.z; q[4 * i + 3] = x.w;
       }
       tmem_store<32>(lane_base + (c >> 1 ? kQLowCol : kQCol) + 64 * hf + 32 * (c & 1), q);
@@ -926,6 +930,7 @@ rows_prep_kernel(const void* q, int q_dtype, int nrows, int fine, const float* _
 #pragma unroll
   for (int k = 0; k < 32; ++k) w[k] = __ldg(mat + k * TQ_D);
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // not before the wait: rows_attn_kernel reads lengths and codes before it waits for this one
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int i = tid; i < kRows * TQ_D; i += kPrepThreads) {
     const int r = i / TQ_D;
