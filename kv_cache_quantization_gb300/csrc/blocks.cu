@@ -249,14 +249,19 @@ __global__ void __launch_bounds__(256) block_score_kernel(const SelectArgs a) {
   const int first = blockIdx.x * a.rounds * kRound, end = min(first + a.rounds * kRound, nblk);
   if (nblk <= a.keep || first >= end) return;   // nothing to choose, or nothing here
   auto fetch = [&](int begin, uint4 (&x)[kPerWarp], uint32_t& in) {
+    // (plain loads, the kernel before may have written tables and bounds; all of one kind first, so
+    // that they are in flight together)
+    const __nv_bfloat16* p[kPerWarp];
     in = 0;
 #pragma unroll
     for (int i = 0; i < kPerWarp; ++i) {
-      const __nv_bfloat16* p = begin + i < end ? bounds_at(a, b, h, begin + i) : nullptr;
-      x[i] = p ? __ldg(reinterpret_cast<const uint4*>(p) + lane) : make_uint4(0, 0, 0, 0);
-      if (p) in |= 1u << i;
-      else if (begin + i < end && lane == 0) atomicOr(&g_tq_flags, TQ_FLAG_PAGE);
+      p[i] = begin + i < end ? bounds_at(a, b, h, begin + i) : nullptr;
+      if (p[i]) in |= 1u << i;
     }
+#pragma unroll
+    for (int i = 0; i < kPerWarp; ++i)
+      x[i] = p[i] ? reinterpret_cast<const uint4*>(p[i])[lane] : make_uint4(0, 0, 0, 0);
+    if (lane == 0 && __popc(in) < min(end - begin, kPerWarp)) atomicOr(&g_tq_flags, TQ_FLAG_PAGE);
   };
   uint4 next[kPerWarp];
   uint32_t next_in;

@@ -60,7 +60,8 @@ __host__ __device__ __forceinline__ int tq_row_slots(const tq_rowmap& m, int cap
 }
 // Row and slot of token t (0 ≤ t < capacity) of sequence b, head h.  False for a paged
 // cache whose table entry lies outside [0, num_pages): the caller skips the token and raises
-// TQ_FLAG_PAGE.
+// TQ_FLAG_PAGE.  (A plain load: the kernel before may have written the table, and a load of the
+// read-only path could be moved above a programmatic wait for it.)
 __device__ __forceinline__ bool tq_map_slot(const tq_rowmap& m, int heads, int b, int h, int t,
                                             long long& row, int& slot) {
   if (!m.table) {
@@ -69,7 +70,7 @@ __device__ __forceinline__ bool tq_map_slot(const tq_rowmap& m, int heads, int b
     return true;
   }
   const int q = t / m.page_tokens;
-  const int pg = __ldg(m.table + (long long)b * m.max_pages + q);
+  const int pg = m.table[(long long)b * m.max_pages + q];
   row = (long long)pg * heads + h;
   slot = t - q * m.page_tokens;
   return pg >= 0 && pg < m.num_pages;

@@ -47,3 +47,16 @@ def test_the_preparation_starts_the_attention_after_its_own_wait():
     it can start only once every CTA of rows_prep_kernel is past its wait for what came before."""
     body = dict(kernels(source("rows_attn.cu")))["rows_prep_kernel"]
     assert 0 < body.index("griddepcontrol.wait") < body.index("griddepcontrol.launch_dependents")
+
+
+@pytest.mark.parametrize("kernel", ["block_score_kernel", "block_select_kernel"])
+def test_bounds_and_tables_are_not_read_through_the_read_only_path(kernel):
+    """The kernel before (tq_block_bounds, a caller's own) may have written bounds, queries, lengths
+    and tables; block_bounds_kernel itself is an ordinary launch."""
+    text = source("blocks.cu")
+    assert "__ldg" not in dict(kernels(text))[kernel]
+    helpers = text[:text.index("block_bounds_kernel")] + text[text.index("struct SelectArgs"):]
+    assert "__ldg" not in helpers and ".nc" not in helpers
+    internal = source("tq_internal.h")
+    begin = internal.index("bool tq_map_slot")
+    assert "__ldg" not in internal[begin:internal.index("return pg >= 0", begin)]
