@@ -34,16 +34,18 @@ struct AppendArgs {
   int nibbles;
 };
 
-// 8 consecutive elements of x (dtype F32, F16 or BF16) from element `off`, as floats.
+// 8 consecutive elements of x (dtype F32, F16 or BF16) from element `off`, as floats.  Plain loads:
+// the kernel before may have written x, and a load of the read-only path could be moved above the
+// programmatic wait for it.
 __device__ __forceinline__ void append_load8(const void* base, int dtype, long long off,
                                              float* out) {
   if (dtype == TQ_F32) {
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + off);
-    float4 a = __ldg(p), b = __ldg(p + 1);
+    float4 a = p[0], b = p[1];
     out[0] = a.x; out[1] = a.y; out[2] = a.z; out[3] = a.w;
     out[4] = b.x; out[5] = b.y; out[6] = b.z; out[7] = b.w;
   } else {
-    uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off));
+    uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

@@ -237,17 +237,25 @@ __device__ __forceinline__ void query_prep_role(const tq_mma_launch& a, int bx) 
   // held before (another descriptor's records, an asymmetric call, a call that gave up on a
   // wait): the split grid takes tickets only after this grid has completed.
   if (bx == 0 && tid == 0) a.counters[bh] = 0;
-  for (int i = tid; act && i < 8 * TQ_D; i += kPrepThreads) {
-    const int h = i >> 7, jq = i & 127;
-    float v = 0.f;
-    if (h < a.G) {
-      const long long e = ((long long)b * a.Hq + kvh * a.G + h) * TQ_D + jq;
-      if (a.q_dtype == TQ_F32) v = __ldg(static_cast<const float*>(a.q) + e);
+  // plain loads (the read-only path is not ordered by the wait), all before the stores, so that
+  // they are in flight together
+  constexpr int kQ = 8 * TQ_D / kPrepThreads;
+  float v[kQ];
+#pragma unroll
+  for (int k = 0; k < kQ; ++k) {
+    const int i = tid + k * kPrepThreads, h = i >> 7;
+    v[k] = 0.f;
+    if (act && h < a.G) {
+      const long long e = ((long long)b * a.Hq + kvh * a.G + h) * TQ_D + (i & 127);
+      if (a.q_dtype == TQ_F32) v[k] = static_cast<const float*>(a.q)[e];
       else if (a.q_dtype == TQ_BF16)
-        v = __uint_as_float((uint32_t)__ldg(static_cast<const unsigned short*>(a.q) + e) << 16);
-      else v = __half2float(__ushort_as_half(__ldg(static_cast<const unsigned short*>(a.q) + e)));
+        v[k] = __uint_as_float((uint32_t)static_cast<const unsigned short*>(a.q)[e] << 16);
+      else v[k] = __half2float(__ushort_as_half(static_cast<const unsigned short*>(a.q)[e]));
     }
-    qf[h][jq] = v;
+  }
+  if (act) {
+#pragma unroll
+    for (int k = 0; k < kQ; ++k) qf[(tid + k * kPrepThreads) >> 7][tid & 127] = v[k];
   }
   if (tid < 8) s_inq[tid] = 0.f;
   __syncthreads();

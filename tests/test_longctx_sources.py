@@ -60,3 +60,14 @@ def test_bounds_and_tables_are_not_read_through_the_read_only_path(kernel):
     internal = source("tq_internal.h")
     begin = internal.index("bool tq_map_slot")
     assert "__ldg" not in internal[begin:internal.index("return pg >= 0", begin)]
+
+
+def test_inputs_of_waiting_kernels_are_not_read_through_the_read_only_path():
+    """Queries of the decode's operand kernel and vectors of the appends, both read after the wait."""
+    text = source("decode_tc.cu")
+    begin = text.index("griddepcontrol.wait")
+    prep = text[begin:text.index("query_prep_tc_kernel", begin)]
+    assert "a.q)" in prep and "__ldg" not in prep
+    text = source("append_small.h")
+    begin = text.index("void append_load8")
+    assert "__ldg" not in text[begin:text.index("__device__", begin)]
