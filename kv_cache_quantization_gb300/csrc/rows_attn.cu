@@ -7,9 +7,12 @@
 //   ‖x‖·( ⟨y, c[i]⟩ + ρ·⟨z, s⟩ ),   ρ = ‖r‖/‖x‖·√(π/2)/d,
 // one product of length 256 of the row [y, z] with the token's operand [c[i], ±ρ].  A value is
 // ‖v‖·Πᵀc[j], so the output row is Πᵀ·Σ_t p_t‖v_t‖c[j_t] / Σ_t p_t.  The weights of the value
-// product are w_t = 2^(e_t − m) with e_t = score + log2‖v_t‖ and m a reference near the running
-// maximum of e (not of the score): they are at most 2^kGrow whatever the norms, so fp16 holds
-// them; the denominator is Σ w_t/‖v_t‖ in 32 bits.
+// product are w_t = 2^(e_t − m + kLift) with e_t = score + log2‖v_t‖ and m a reference near the
+// running maximum of e (not of the score): they are at most 2^(kGrow + kLift) = 2^15 whatever the
+// norms, so fp16 holds them; the denominator is Σ w_t/‖v_t‖ in 32 bits.  kLift uses what fp16 has
+// above: a weight is held to 2^-32 of the largest (without it to 2^-25, and the numerator lost a
+// tail of many small weights that the denominator kept: 65535 of 2^-25.1 behind one of 1 moved a
+// row by 2.1e-3 of its norm).
 //
 // One CTA works on one item: up to 128 query rows × a run of 128-token tiles.
 //   12 expander warps turn the codes of a tile into fp16 operands in shared memory, four for
@@ -81,6 +84,7 @@ constexpr int kQLowCol = 256;           // (fine: the second halves of y and z, 
 constexpr int kFacSlots = 4;
 constexpr float kAlpha = 64.f, kBeta = 4.f;   // scales of y and z in the fp16 row operand
 constexpr float kGrow = 8.f;            // the reference follows the maximum when 2^8 above it
+constexpr float kLift = 7.f;            // weights are taken 2^7 times as large
 constexpr float kTiny = 8.6736174e-19f; // 2^-60: smaller value norms count as zero
 constexpr float kQjl = 1.2533141373155003f / 128.f;   // √(π/2)/d
 
@@ -620,7 +624,7 @@ __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int reps, in
       z.l *= corr;
     }
     z.m = m_new;
-    const float ref = m_new == -INFINITY ? 0.f : m_new;
+    const float ref = m_new == -INFINITY ? 0.f : m_new - kLift;
     const tq::f32x2 ref2 = tq::pack2(-ref, -ref);
     tq::f32x2 l2 = tq::pack2(0.f, 0.f);
     if (groups > 1) tq::tmem_wait_st();

@@ -8,7 +8,8 @@ import torch
 import longctx_ref as ref
 from kv_cache_quantization_gb300 import _binding as B
 from kv_cache_quantization_gb300 import api
-from test_gpu_longctx import blank, check_select, flags, queries, run_select
+from test_gpu_longctx import (D, blank, caches, check_select, codec, flags, i32, parts, queries,
+                              run_select)
 
 pytestmark = pytest.mark.gpu
 
@@ -78,3 +79,62 @@ def test_select_among_zeros(what):
     check_select(q, blocks, [64 * n], 40, 2, 1, 4, 1, got)
     if what != "queries but one":
         assert got[0, 0].tolist() == list(range(39)) + [499]
+
+
+# ------------------------------------------------------------------ attention
+
+def alike(t, b, h):
+    """Every token of (b, h) gets the codes and norms of its first one."""
+    x = t[b, h]
+    if x.dim() == 3:
+        x[:] = x[:, :1].clone()
+    else:
+        x[:] = x[:1].clone()
+
+
+@pytest.mark.parametrize("tail", [23.3, 24.6, 25.1])
+@pytest.mark.parametrize("out_dtype", [torch.float16, torch.bfloat16])
+def test_a_peak_before_a_long_even_tail(out_dtype, tail):
+    """One token of weight 1 and then 65535 equal ones of weight 2^-tail, in one item: the tail's sum
+    counts in full, although fp16 holds numbers around 2^-24 as 0, 2^-24 or 2^-23.
+
+    Off by at most, relative to the values' norm V: the output's rounding; the values' levels; the
+    tail's sum n · 2^-tail times twice the error of its one score (2^-18, or 2^-9 with single fp16
+    operands, of the sum of its terms' sizes: three roundings of 2^-21 or 2^-11, the levels, 32-bit
+    sums); each weight's rounding, 2^-25 of a weight taken 2^7 times as large, in the same direction
+    n times; and 2^-23 of the accumulator for each of 4096 matrix instructions."""
+    n, batch, heads, group = 65536, 16, 152, 8       # 128 rows of each of 152 heads: an item a head
+    kc, vc = codec("k", 3), codec("v", 2)
+    k, v = caches(1, heads, n, 3, 2, 1)
+    q = queries(batch, heads * group, torch.float32, 2)
+    pi, sk = (torch.tensor(m, device="cuda") for m in (kc.pi, kc.s))
+    size = {}
+    for h in (0, heads - 1):
+        for t in (k.idx, k.sgn, k.xnorm, k.rnorm, v.idx, v.xnorm):
+            alike(t, 0, h)
+        # the norms of a key scale its score: token 0's is 0, the others' are -tail·ln 2
+        c, s, xn, rn = ref.key_parts(k, kc, 0, h, torch.arange(1, device="cuda"))
+        rows = q[:, h * group:(h + 1) * group]
+        y, z = rows.double() @ pi.T, rows.double() @ sk.T
+        one = (xn * (y @ c[0]) + ref.QJL * rn * (z @ s[0])) / math.sqrt(D)
+        by = -tail * math.log(2) / one
+        rows *= by[..., None].float()
+        terms = (xn * (y * c[0]).abs().sum(-1) + ref.QJL * rn * z.abs().sum(-1)) / math.sqrt(D)
+        size[h] = float((terms * by.abs()).max())
+        k.xnorm[0, h, 0] = k.rnorm[0, h, 0] = 0.0
+        v.idx[0, h, :, 0] = 255 - v.idx[0, h, :, 1]      # the peak's value is another one
+        v.xnorm[0, h] = 10.0
+    plan = api.PrefixPlan(batch, heads * group, heads, 64, 0, n, n, torch.float32, out_dtype)
+    own = caches(batch, heads, 64, 3, 2, 3)
+    out = plan.run(kc, vc, q, k, v, i32([n]), *own, i32([0] * batch), plan.new_out())
+    pairs = out_dtype == torch.float16
+    for h in size:
+        rows = slice(h * group, (h + 1) * group)
+        r, _ = ref.attend(q[:, rows].reshape(-1, D), parts(k, v, kc, vc, 0, h, torch.arange(n, device="cuda")),
+                          kc, vc, pairs=pairs)
+        off = (out[:, rows].reshape(-1, D).double() - r).norm(dim=-1).max()
+        score = 2.0 ** (-18 if pairs else -9) * size[h]
+        most = 10.0 * (torch.finfo(out_dtype).eps / 2 + ref.level_error(vc) + 2 * n * 2.0 ** -tail * score
+                       + n * 2.0 ** -32 + 4096 * 2.0 ** -23)
+        assert float(off) <= most, (h, float(off), most)
+    assert flags() == 0
