@@ -144,8 +144,36 @@ def _pages_ptr(pages):
     return None if pages is None else pages.c()
 
 
+def _holds(t: torch.Tensor, shape, dtype, device):
+    return t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == device
+
+
+class _Arrays:
+    """What the key and value caches share: their layout, (sequences or pages, heads, slots, index
+    bits, device), found out from all arrays at the first call that asks and again after one was
+    replaced.  (The calls of long contexts ask; an array is not to be resized in place.)"""
+
+    _layout = None
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name != "_layout":
+            object.__setattr__(self, "_layout", None)
+
+    def layout(self):
+        """Refuses arrays that are not codes and norms of one layout (include/tq.h) on one device."""
+        n, d = self.xnorm.shape, self.xnorm.get_device()
+        if len(n) != 3 or not _holds(self.xnorm, n, torch.float32, d) or not self._codes(n, d):
+            got = ", ".join(f"{f} {t.dtype} {list(t.shape)} on {t.device}"
+                            for f, t in vars(self).items() if hasattr(t, "dtype"))
+            raise ValueError(f"expected contiguous uint8 codes and float32 norms of one layout on one device, "
+                             f"got {got}")
+        self._layout = (*n, self._bits(), d)
+        return self._layout
+
+
 @dataclasses.dataclass
-class ProdCache:
+class ProdCache(_Arrays):
     """Packed key cache [batch][heads][capacity] (layout of include/tq.h); with `pages` the
     arrays are a page pool [num_pages][heads][page_tokens] addressed through a block table."""
     idx: torch.Tensor      # uint8 [B, H, b-1, cap, 16]
@@ -171,6 +199,14 @@ class ProdCache:
         c.pages = pages
         return c
 
+    def _bits(self):
+        return self.idx.shape[2]
+
+    def _codes(self, n, d):
+        b = self.idx.shape[2] if len(self.idx.shape) == 5 else 0
+        return (_holds(self.rnorm, n, torch.float32, d) and _holds(self.sgn, (*n, 16), torch.uint8, d) and
+                _holds(self.idx, (n[0], n[1], b, n[2], 16), torch.uint8, d))
+
     @property
     def capacity(self):
         return self.pages.capacity if self.pages is not None else self.sgn.shape[2]
@@ -184,7 +220,7 @@ class ProdCache:
 
 
 @dataclasses.dataclass
-class MSECache:
+class MSECache(_Arrays):
     """Packed value cache [batch][heads][capacity]: bit planes, or nibbles for 4 bits; with
     `pages` a page pool as for ProdCache."""
     idx: torch.Tensor      # uint8 [B, H, bits, cap, 16] or [B, H, cap, 64]
@@ -209,6 +245,12 @@ class MSECache:
             raise ValueError("page_tokens must be a multiple of TQ_CAPACITY_ALIGN")
         c.pages = pages
         return c
+
+    def _bits(self):
+        return self.bits
+
+    def _codes(self, n, d):
+        return _holds(self.idx, (*n, 64) if self.bits == 4 else (n[0], n[1], self.bits, n[2], 16), torch.uint8, d)
 
     @property
     def capacity(self):
@@ -373,23 +415,25 @@ def _expect(t: torch.Tensor, shape, dtype, name):
                          f"got {t.dtype} {list(t.shape)}")
 
 
-def _fits(shape, pages, rows, heads, slots):
-    """Whether arrays of leading dimensions `shape` hold `rows` sequences of `slots` slots."""
-    if shape[1] != heads:
+def _fits(layout, pages, rows, heads, slots):
+    """Whether arrays of a layout hold `rows` sequences of `slots` slots."""
+    if layout[1] != heads:
         return False
     if pages is None:
-        return shape[0] >= rows and shape[2] == slots
-    return (shape[0] >= pages.num_pages and shape[2] == pages.page_tokens and
-            pages.capacity == slots and pages.block_table.shape[0] >= rows)
+        return layout[0] >= rows and layout[2] == slots
+    return (layout[0] >= pages.num_pages and layout[2] == pages.page_tokens and
+            pages.capacity == slots and pages.block_table.shape[0] >= rows and
+            pages.block_table.get_device() == layout[4])
 
 
 def _expect_caches(k: "ProdCache", v: "MSECache", rows, heads, slots, kc, vc, name):
-    """Shapes of a pair of caches (or pools) for `rows` sequences of `slots` slots."""
-    if not (_fits(k.xnorm.shape, k.pages, rows, heads, slots) and
-            _fits(v.xnorm.shape, v.pages, rows, heads, slots)):
+    """A pair of caches (or pools) for `rows` sequences of `slots` slots: every array of each."""
+    kl, vl = k._layout or k.layout(), v._layout or v.layout()
+    if not (_fits(kl, k.pages, rows, heads, slots) and _fits(vl, v.pages, rows, heads, slots)) or kl[4] != vl[4]:
         raise ValueError(f"{name}: expected {rows} sequences or a block table for them, {heads} heads and "
-                         f"{slots} slots, got keys {list(k.xnorm.shape)} and values {list(v.xnorm.shape)}")
-    if k.idx.shape[2] != kc.index_bits or v.bits != vc.bits:
+                         f"{slots} slots on one device, got keys {list(k.xnorm.shape)} on {k.xnorm.device} and "
+                         f"values {list(v.xnorm.shape)} on {v.xnorm.device}")
+    if kl[3] != kc.index_bits or vl[3] != vc.bits:
         raise ValueError(f"{name}: the caches hold codes of other widths than the codecs'")
 
 
@@ -428,7 +472,8 @@ class BlockBounds:
         s = t.shape
         if s != (s[0], heads, n // B.TQ_BLOCK_TOKENS, 2, HEAD_DIM) or t.dtype != torch.bfloat16 or \
                 not t.is_contiguous() or s[0] < (rows if p is None else p.num_pages) or \
-                p is not None and (p.capacity != slots or p.block_table.shape[0] < rows):
+                p is not None and (p.capacity != slots or p.block_table.shape[0] < rows or
+                                   p.block_table.get_device() != t.get_device()):
             raise ValueError(f"bounds: expected {rows} sequences or a block table for them, {heads} heads "
                              f"and {slots} slots, got {t.dtype} {list(s)}")
 

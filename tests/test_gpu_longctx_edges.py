@@ -138,3 +138,48 @@ def test_a_peak_before_a_long_even_tail(out_dtype, tail):
                        + n * 2.0 ** -32 + 4096 * 2.0 ** -23)
         assert float(off) <= most, (h, float(off), most)
     assert flags() == 0
+
+
+# ------------------------------------------------------------------ refusals
+
+def test_arrays_and_tables_of_the_host_are_refused():
+    """Block tables, norms and signs that lie on the host, or of another capacity: refused before
+    anything is launched, by every call."""
+    kc, vc = codec("k", 3), codec("v", 2)
+    there = api.Pages(torch.arange(4, dtype=torch.int32, device="cuda").view(2, 2), 64, 4)
+    host = api.Pages(torch.arange(4, dtype=torch.int32).view(2, 2), 64, 4)
+    k, v = caches(2, 2, 128, 3, 2, 1)
+    pk, pv = caches(2, 2, 128, 3, 2, 1, there)
+    q, n = queries(2, 4, torch.bfloat16, 1), i32([100, 3])
+    sp, pr = api.SparsePlan(2, 4, 2, 128, 128, 1, 0, 0), api.PrefixPlan(2, 4, 2, 128, 128, 128, 128)
+    lst, out = sp.new_list(), sp.new_out()
+    lst.zero_()
+
+    def sparse(a, b):
+        sp.run(kc, vc, q, a, b, n, lst, out)
+
+    def prefix(a, b):
+        pr.run(kc, vc, q, a, b, i32([50]), k, v, n, out)
+
+    for run in (sparse, prefix):
+        run(k, v)
+        run(pk, pv)
+        bad = [(api.ProdCache(pk.idx, pk.sgn, pk.xnorm, pk.rnorm, host), pv),
+               (pk, api.MSECache(pv.idx, pv.xnorm, 2, host)),
+               (api.ProdCache(k.idx, k.sgn, k.xnorm, k.rnorm.cpu()), v),
+               (api.ProdCache(k.idx, k.sgn[:, :, :64].contiguous(), k.xnorm, k.rnorm), v),
+               (k, api.MSECache(v.idx, v.xnorm.cpu(), 2)),
+               (k, api.MSECache(v.idx.int(), v.xnorm, 2))]
+        for a, b in bad:
+            with pytest.raises(ValueError):
+                run(a, b)
+    blocks = api.BlockBounds.empty_paged(there, 2)
+    sp.select(q, blocks, n, lst)
+    api.block_bounds(torch.zeros(2, 2, 3, D, device="cuda"), blocks)
+    blocks.pages = host
+    with pytest.raises(ValueError):
+        sp.select(q, blocks, n, lst)
+    with pytest.raises(ValueError):
+        api.block_bounds(torch.zeros(2, 2, 3, D, device="cuda"), blocks)
+    torch.cuda.synchronize()
+    assert flags() == 0
