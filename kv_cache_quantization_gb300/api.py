@@ -531,48 +531,75 @@ class SparsePlan:
     def new_list(self, device="cuda"):
         return torch.empty(self.list_shape, dtype=torch.int32, device=device)
 
-    def select(self, q, blocks: BlockBounds, seq_lens, out, stream=None):
-        """The blocks of each (sequence, KV head) that q [batch, q_heads, 128] attends, ascending,
-        −1 behind them, into out [batch, kv_heads, max_blocks] int32."""
-        d = _device(q, blocks.bounds, seq_lens, out, self.workspace)
+    def _check_select(self, q, blocks, seq_lens, out):
         _expect(q, self.shape, self.q_dtype, "q")
         _expect(seq_lens, self.rows, torch.int32, "seq_lens")
         _expect(out, self.list_shape, torch.int32, "out")
         blocks.expect(self.batch, self.kv_heads, self.capacity)
+
+    def _select(self, q, blocks, seq_lens, out, stream):
         st = B.load().tq_block_select(self.desc, q.data_ptr(), blocks.c(), seq_lens.data_ptr(),
                                       self.first_blocks, self.last_blocks, self.max_blocks,
-                                      out.data_ptr(), self.workspace.data_ptr(), self.nbytes,
-                                      _on(stream, d))
+                                      out.data_ptr(), self.workspace.data_ptr(), self.nbytes, stream)
         if st:
             B.check(st, "tq_block_select")
+        return out
+
+    def select(self, q, blocks: BlockBounds, seq_lens, out, stream=None):
+        """The blocks of each (sequence, KV head) that q [batch, q_heads, 128] attends, ascending,
+        −1 behind them, into out [batch, kv_heads, max_blocks] int32."""
+        d = _device(q, blocks.bounds, seq_lens, out, self.workspace)
+        self._check_select(q, blocks, seq_lens, out)
+        return self._select(q, blocks, seq_lens, out, _on(stream, d))
+
+    def _check_run(self, kc, vc, q, k, v, seq_lens, block_list, out):
+        _expect(q, self.shape, self.q_dtype, "q")
+        _expect(seq_lens, self.rows, torch.int32, "seq_lens")
+        _expect(block_list, self.list_shape, torch.int32, "block_list")
+        _expect(out, self.shape, self.out_dtype, "out")
+        _expect_caches(k, v, self.batch, self.kv_heads, self.capacity, kc, vc, "cache")
+
+    def _run(self, kc, vc, q, k, v, seq_lens, block_list, out, stream):
+        st = B.load().tq_sparse_attention(self.desc, kc.handle, vc.handle, q.data_ptr(), k.c(), v.c(),
+                                          seq_lens.data_ptr(), block_list.data_ptr(),
+                                          self.max_blocks, out.data_ptr(),
+                                          self.workspace.data_ptr(), self.nbytes, stream)
+        if st:
+            B.check(st, "tq_sparse_attention")
         return out
 
     def run(self, kc: Codec, vc: Codec, q, k: ProdCache, v: MSECache, seq_lens, block_list, out,
             stream=None):
         """Attention of q over the listed blocks of the cache, into out [batch, q_heads, 128]."""
         d = _device(q, k.idx, v.idx, seq_lens, block_list, out, self.workspace)
-        _expect(q, self.shape, self.q_dtype, "q")
-        _expect(seq_lens, self.rows, torch.int32, "seq_lens")
-        _expect(block_list, self.list_shape, torch.int32, "block_list")
-        _expect(out, self.shape, self.out_dtype, "out")
-        _expect_caches(k, v, self.batch, self.kv_heads, self.capacity, kc, vc, "cache")
-        st = B.load().tq_sparse_attention(self.desc, kc.handle, vc.handle, q.data_ptr(), k.c(), v.c(),
-                                          seq_lens.data_ptr(), block_list.data_ptr(),
-                                          self.max_blocks, out.data_ptr(),
-                                          self.workspace.data_ptr(), self.nbytes, _on(stream, d))
-        if st:
-            B.check(st, "tq_sparse_attention")
-        return out
+        self._check_run(kc, vc, q, k, v, seq_lens, block_list, out)
+        return self._run(kc, vc, q, k, v, seq_lens, block_list, out, _on(stream, d))
 
     def step(self, kc: Codec, vc: Codec, q, k_new, v_new, k: ProdCache, v: MSECache,
              blocks: BlockBounds, pos, seq_lens, block_list, out, stream=None):
         """One decode step: appends k_new, v_new [batch, kv_heads, 128] at pos[b] (codes and
-        bounds), selects blocks and attends them.  seq_lens holds pos + 1."""
-        quantize_prod(kc, k_new.unsqueeze(2), k, pos=pos, stream=stream)
-        quantize_mse(vc, v_new.unsqueeze(2), v, pos=pos, stream=stream)
-        block_bounds(k_new.unsqueeze(2), blocks, pos=pos, stream=stream)
-        self.select(q, blocks, seq_lens, block_list, stream=stream)
-        return self.run(kc, vc, q, k, v, seq_lens, block_list, out, stream=stream)
+        bounds), selects blocks and attends them.  seq_lens holds pos + 1.  All arguments are
+        checked before anything is written."""
+        d = _device(q, k_new, v_new, k.idx, v.idx, blocks.bounds, pos, seq_lens, block_list, out, self.workspace)
+        for x, name in ((k_new, "k_new"), (v_new, "v_new")):
+            if x.shape != (self.batch, self.kv_heads, HEAD_DIM) or x.dtype not in _DT:
+                raise ValueError(f"{name} must be [{self.batch}, {self.kv_heads}, {HEAD_DIM}] of float32, "
+                                 f"float16 or bfloat16, got {x.dtype} {list(x.shape)}")
+            size = x.element_size()
+            if x.stride(2) != 1 or (x.data_ptr() | x.stride(0) * size | x.stride(1) * size) % 16:
+                raise ValueError(f"{name} must have contiguous vectors that begin at multiples of 16 bytes")
+        if kc.kind != B.TQ_PROD or vc.kind != B.TQ_MSE:
+            raise ValueError("expected a codec of keys (TQ_PROD) and one of values (TQ_MSE)")
+        _expect(pos, self.rows, torch.int32, "pos")
+        self._check_select(q, blocks, seq_lens, block_list)
+        self._check_run(kc, vc, q, k, v, seq_lens, block_list, out)
+        stream = _on(stream, d)
+        k_new, v_new = k_new.unsqueeze(2), v_new.unsqueeze(2)
+        quantize_prod(kc, k_new, k, pos=pos, stream=stream)
+        quantize_mse(vc, v_new, v, pos=pos, stream=stream)
+        block_bounds(k_new, blocks, pos=pos, stream=stream)
+        self._select(q, blocks, seq_lens, block_list, stream)
+        return self._run(kc, vc, q, k, v, seq_lens, block_list, out, stream)
 
 
 class PrefixPlan:

@@ -183,3 +183,41 @@ def test_arrays_and_tables_of_the_host_are_refused():
         api.block_bounds(torch.zeros(2, 2, 3, D, device="cuda"), blocks)
     torch.cuda.synchronize()
     assert flags() == 0
+
+
+def test_a_refused_step_writes_nothing():
+    """Every argument of SparsePlan.step is checked before the appends: a refused step leaves codes,
+    norms and bounds as they are."""
+    kc, vc = codec("k", 3), codec("v", 2)
+    k, v = caches(2, 2, 128, 3, 2, 1)
+    blocks = blank(2, 2, 128, None, 2)
+    plan = api.SparsePlan(2, 4, 2, 128, 128, 1, 0, 0, out_dtype=torch.float16)
+    g = torch.randn(2, 2, D, device="cuda").half()
+    good = dict(kc=kc, vc=vc, q=queries(2, 4, torch.bfloat16, 1), k_new=g, v_new=g.clone(), k=k, v=v,
+                blocks=blocks, pos=i32([70, 3]), seq_lens=i32([71, 4]), block_list=plan.new_list(),
+                out=plan.new_out())
+    arrays = (k.idx, k.sgn, k.xnorm, k.rnorm, v.idx, v.xnorm, blocks.bounds)
+    before = [t.clone() for t in arrays]
+    odd = torch.zeros(2 * 2 * D + 8, device="cuda").half()
+    bad = dict(kc=[vc, codec("k", 4)], vc=[kc, codec("v", 4)], q=[good["q"].half(), good["q"][:1]],
+               k_new=[g[:1], g.double(), torch.cat([g, g]), odd[1:1 + 2 * 2 * D].view(2, 2, D), g.cpu()],
+               v_new=[g[:, :1], g.long(), g.transpose(1, 2).contiguous().transpose(1, 2), g[..., :64]],
+               k=[caches(2, 2, 64, 3, 2, 1)[0]], v=[caches(1, 2, 128, 3, 2, 1)[1]],
+               blocks=[blank(2, 2, 64, None, 2)], pos=[i32([70, 3]).long(), i32([1]), i32([1, 2]).cpu()],
+               seq_lens=[i32([71]), i32([71, 4]).float()], block_list=[plan.new_list()[:1]],
+               out=[plan.new_out().float()])
+    for name, values in bad.items():
+        for x in values:
+            with pytest.raises(ValueError):
+                plan.step(**{**good, name: x})
+    torch.cuda.synchronize()
+    for t, b in zip(arrays, before):
+        assert torch.equal(t, b)
+    plan.step(**good)
+    assert flags() == 0 and not torch.equal(k.sgn, before[1])
+    strided = torch.randn(2, 2, 2 * D, device="cuda").half()[..., :D]      # rows of a wider tensor
+    plan.step(**{**good, "k_new": strided, "v_new": strided})
+    one = [t.clone() for t in arrays]
+    plan.step(**{**good, "k_new": strided.contiguous(), "v_new": strided.contiguous()})
+    for t, b in zip(arrays, one):
+        assert torch.equal(t, b)
