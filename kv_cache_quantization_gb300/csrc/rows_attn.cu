@@ -1116,39 +1116,62 @@ double makespan(long long n1, double c1, long long n2, double c2, long long sms)
 // and end.  Against 3 tiles and one cost: 62.3 for 66.4 us (prefix of 32768, 32 sequences) and 176
 // for 191 us (65536, 64 sequences); 5 tiles: 70.1 and 176 us; others the same.
 constexpr double kFixed = 2.0, kFewRows = 0.75;
-// The arguments that the splits follow from, and what they came to: a call looks its splits up
-// (the search takes some microseconds).
+// The arguments that the splits follow from, and what they came to.
 struct Splits {
   long long pu, pre, ou, own, sms;
   bool few;          // at most 64 query rows in an item of the prefix
   int sp, so;
 };
 
-void find_splits(Splits* x) {
-  double best = 0;
-  const long long pre_tiles = x->pre, own_tiles = x->own;
-  // tiles per item of either kind; both grow by steps of an eighth
-  for (long long lp = 1;; lp += std::max<long long>(1, lp / 8)) {
-    lp = std::min(lp, std::max<long long>(pre_tiles, 1));
-    const long long sp = pre_tiles > 0 ? (pre_tiles + lp - 1) / lp : 0;
-    for (long long lo = 1;; lo += std::max<long long>(1, lo / 8)) {
-      lo = std::min(lo, std::max<long long>(own_tiles, 1));
-      const long long so = std::max<long long>((own_tiles + lo - 1) / lo, 1);
-      const bool last = lo >= own_tiles && lp >= pre_tiles;
-      if (sp + so <= kMaxRecs || last) {
-        const double cp = sp ? (x->few ? kFewRows : 1.0) * (double)((pre_tiles + sp - 1) / sp) + kFixed : 0;
-        const double co = kFewRows * (double)((own_tiles + so - 1) / so) + kFixed;
-        // more records cost the merge: about a tile's time for 64 of them
-        const double t = makespan(x->pu * sp, cp, x->ou * so, co, x->sms) + (double)(sp + so) / 64;
-        if (!x->so || t < best) {
-          best = t;
-          x->sp = (int)sp;
-          x->so = (int)so;
-        }
-      }
-      if (lo >= own_tiles) break;
+// The numbers of items that `tiles` are split into, ascending: tiles per item grow by steps of an
+// eighth.
+constexpr int kMaxWays = 192;
+int split_ways(long long tiles, int* ways) {
+  int n = 0, begin = kMaxWays;
+  for (long long l = 1;; l += std::max<long long>(1, l / 8)) {
+    const long long s = (tiles + l - 1) / l;
+    if (l >= tiles || s <= kMaxRecs) {
+      const int w = l >= tiles ? 1 : (int)s;
+      if (begin == kMaxWays || ways[begin] != w) ways[--begin] = w;
     }
-    if (lp >= pre_tiles) break;
+    if (l >= tiles) break;
+  }
+  for (; begin < kMaxWays; ++begin) ways[n++] = ways[begin];
+  return n;
+}
+
+// The search of all pairs, without those that a lower bound of the time rules out (every SM busy all
+// the time): 0.1 to 0.4 us of host time a call, 4 us for 65536 and 8192 tiles (all pairs: ten times
+// that).
+void find_splits(Splits* x) {
+  int pw[kMaxWays] = {0}, ow[kMaxWays];
+  const int np = x->pre > 0 ? split_ways(x->pre, pw) : 1;
+  const int no = split_ways(std::max<long long>(x->own, 1), ow);
+  const double tile = x->few ? kFewRows : 1.0, sms = (double)x->sms;
+  double best = 0;
+  for (int i = 0; i < np; ++i) {
+    const long long sp = pw[i];
+    const double cp = sp ? tile * (double)((x->pre + sp - 1) / sp) + kFixed : 0;
+    const double pre_least = (double)x->pu * (tile * (double)x->pre + kFixed * (double)sp);
+    for (int j = 0; j < no; ++j) {
+      const long long so = ow[j];
+      if (sp + so > kMaxRecs) break;
+      // more records cost the merge: about a tile's time for 64 of them
+      const double merge = (double)(sp + so) / 64;
+      const double own_least = (double)x->ou * (kFewRows * (double)x->own + kFixed * (double)so);
+      if (x->so && (pre_least + own_least) * (1 - 1e-9) > (best - merge) * sms) {
+        if (!j) return;      // more items take longer still
+        break;
+      }
+      const double co = kFewRows * (double)((x->own + so - 1) / so) + kFixed;
+      if (x->so && std::max(cp, co) + merge > best) continue;
+      const double t = makespan(x->pu * sp, cp, x->ou * so, co, x->sms) + merge;
+      if (!x->so || t <= best) {      // (equal times: more items)
+        best = t;
+        x->sp = (int)sp;
+        x->so = (int)so;
+      }
+    }
   }
 }
 
@@ -1171,16 +1194,8 @@ tq_status make_plan(const tq_attn_desc* d, long long pre_tiles, long long own_ti
   const int n = tq_num_sms();
   const long long sms = n > 0 ? n : 152;
   const long long pu = (long long)p->row_tiles * d->kv_heads, ou = (long long)d->batch * d->kv_heads;
-  thread_local Splits known[8];
-  thread_local int next = 0;
   Splits want{pu, pre_tiles, ou, own_tiles, sms, (long long)d->batch * p->G <= kTile / 2, 0, 0};
-  for (const Splits& k : known)
-    if (k.so && k.few == want.few && k.pu == pu && k.pre == pre_tiles && k.ou == ou && k.own == own_tiles && k.sms == sms) want = k;
-  if (!want.so) {
-    find_splits(&want);
-    known[next] = want;
-    next = (next + 1) % 8;
-  }
+  find_splits(&want);
   p->pre_splits = want.sp;
   p->own_splits = want.so;
   if (pu * p->pre_splits + ou * p->own_splits > 0x7fffffffLL) return TQ_ERR_UNSUPPORTED;
