@@ -1,5 +1,6 @@
 """Operators of long contexts at values and layouts where they can go wrong: infinite and tiny
-values in a selection, against the definitions in 64 bits (longctx_ref.py)."""
+values in a selection, long even tails, block tables of their own for keys and values, bad pages,
+refusals; against the definitions in 64 bits (longctx_ref.py)."""
 import math
 
 import pytest
@@ -8,8 +9,8 @@ import torch
 import longctx_ref as ref
 from kv_cache_quantization_gb300 import _binding as B
 from kv_cache_quantization_gb300 import api
-from test_gpu_longctx import (D, blank, caches, check_select, codec, flags, i32, parts, queries,
-                              run_select)
+from test_gpu_longctx import (D, blank, caches, check_prefix, check_select, check_sparse, codec, flags,
+                              flat_bounds, hide, i32, lists_of, parts, queries, run_select, table)
 
 pytestmark = pytest.mark.gpu
 
@@ -221,3 +222,136 @@ def test_a_refused_step_writes_nothing():
     plan.step(**{**good, "k_new": strided.contiguous(), "v_new": strided.contiguous()})
     for t, b in zip(arrays, one):
         assert torch.equal(t, b)
+
+
+# ------------------------------------------------------------------ pages
+
+def two_tables(rows, heads, cap, kbits, vbits, kpage, vpage, seed, used):
+    """Keys and values with block tables (0: flat) and page sizes of their own."""
+    def pages(page, s):
+        return table(rows, cap // page, page, s) if page else None
+
+    k = caches(rows, heads, cap, kbits, vbits, seed, pages(kpage, seed + 1), used)[0]
+    v = caches(rows, heads, cap, kbits, vbits, seed + 2, pages(vpage, seed + 3), used)[1]
+    for c in (k, v):
+        hide(c.pages, used)
+    return k, v
+
+
+@pytest.mark.parametrize("kpage,vpage", [(64, 192), (192, 64), (0, 64), (384, 0), (64, 64)])
+@pytest.mark.parametrize("out_dtype", [torch.float16, torch.bfloat16])
+def test_keys_and_values_behind_tables_of_their_own(kpage, vpage, out_dtype):
+    kc, vc = codec("k", 3), codec("v", 4)
+    batch, kv, group, cap = 3, 2, 5, 1152
+    lens, plen = [1000, 65, 0], 700
+    k, v = two_tables(batch, kv, cap, 3, 4, kpage, vpage, 1, lens)
+    pk, pv = two_tables(1, kv, 768, 3, 4, kpage, vpage, 9, [plen])
+    q = queries(batch, kv * group, torch.bfloat16, 2)
+    pr = api.PrefixPlan(batch, kv * group, kv, cap, cap, 768, 768, out_dtype=out_dtype)
+    out = pr.run(kc, vc, q, pk, pv, i32([plen]), k, v, i32(lens), pr.new_out())
+    check_prefix(kc, vc, q, (pk, pv), (k, v), out, plen, lens, kv, group)
+    sp = api.SparsePlan(batch, kv * group, kv, cap, cap, 7, 0, 0, out_dtype=out_dtype)
+    lst = lists_of(lens, kv, 7, 3)
+    out = sp.run(kc, vc, q, k, v, i32(lens), lst, sp.new_out())
+    check_sparse(kc, vc, q, k, v, lst, lens, out, group)
+    assert flags() == 0
+
+
+@pytest.mark.parametrize("value", [-1, 0, 1 << 30])
+@pytest.mark.parametrize("which", ["keys", "values", "both", "same table"])
+@pytest.mark.parametrize("page", [64, 192])
+def test_attention_leaves_bad_pages_out(page, which, value):
+    """Entries of the block tables that are no page, in the middle and at the end of the prefix and
+    of a sequence: their tokens are left out of numerator and denominator, and the flag is raised."""
+    kc, vc = codec("k", 4), codec("v", 2)
+    batch, kv, group, cap = 2, 2, 4, 1152
+    lens, plen = [1100, 300], 1000
+    if which == "same table":
+        k, v = caches(batch, kv, cap, 4, 2, 1, table(batch, cap // page, page, 2), lens)
+        pk, pv = caches(1, kv, cap, 4, 2, 7, table(1, cap // page, page, 8), [plen])
+        hide(k.pages, lens)
+        hide(pk.pages, [plen])
+    else:
+        k, v = two_tables(batch, kv, cap, 4, 2, page, page, 1, lens)
+        pk, pv = two_tables(1, kv, cap, 4, 2, page, page, 7, [plen])
+    q = queries(batch, kv * group, torch.bfloat16, 2)
+    n, pn = i32(lens), i32([plen])
+    pr = api.PrefixPlan(batch, kv * group, kv, cap, cap, cap, cap, out_dtype=torch.float16)
+    sp = api.SparsePlan(batch, kv * group, kv, cap, cap, 9, 0, 0, out_dtype=torch.float16)
+    lst = lists_of(lens, kv, 9, 3)
+    lst[0, :, 3] = 192 // 64           # a block of page 1 (192) or 3 (64)
+    bad = [1, (1000 - 1) // page]
+    if page == 64:
+        bad.append(3)
+    gone = (k, pk) if which == "keys" else (v, pv) if which == "values" else (k, v, pk, pv)
+    seen = list({id(c.pages): c.pages for c in gone}.values())
+    good = [p.block_table.clone() for p in seen]
+    for p in seen:
+        p.block_table[0, bad] = value if value < 0 else p.num_pages + value if value < 1000 else value
+    o1 = pr.run(kc, vc, q, pk, pv, pn, k, v, n, pr.new_out())
+    assert flags() == B.TQ_FLAG_PAGE
+    o2 = sp.run(kc, vc, q, k, v, n, lst, sp.new_out())
+    assert flags() == B.TQ_FLAG_PAGE
+    for p, t in zip(seen, good):
+        p.block_table.copy_(t)
+
+    def there(at, b):
+        keep = torch.ones_like(at, dtype=torch.bool)
+        for i in bad if b == 0 else []:
+            keep &= at // page != i
+        return at[keep]
+
+    for h in range(kv):
+        rows = slice(h * group, (h + 1) * group)
+        shared = parts(pk, pv, kc, vc, 0, h, there(torch.arange(plen, device="cuda"), 0))
+        for b, m in enumerate(lens):
+            own = parts(k, v, kc, vc, b, h, there(torch.arange(m, device="cuda"), b))
+            r, err = ref.attend(q[b, rows], [torch.cat(t) for t in zip(shared, own)], kc, vc, pairs=True)
+            ref.check_rows(o1[b, rows], r, err, f"prefix, sequence {b}, KV head {h}")
+            at = [torch.arange(64 * i, min(64 * i + 64, m), device="cuda") for i in lst[b, h].tolist()
+                  if 0 <= i and 64 * i < m]
+            at = there(torch.cat(at), b) if at else torch.zeros(0, dtype=torch.long, device="cuda")
+            r, err = ref.attend(q[b, rows], parts(k, v, kc, vc, b, h, at), kc, vc, pairs=True)
+            ref.check_rows(o2[b, rows], r, err, f"list, sequence {b}, KV head {h}")
+
+
+@pytest.mark.parametrize("value", [-1, 0, 1 << 30])
+@pytest.mark.parametrize("page", [64, 256])
+def test_bounds_and_selection_pass_bad_pages_over(page, value):
+    """tq_block_bounds leaves such a page's blocks out and writes the others; tq_block_select scores
+    them -inf, so they come last (also among each other, where only they are left)."""
+    batch, kv, group, tokens = 2, 2, 3, 64 * 40 - 5
+    cap = 64 * 40
+    pages = table(batch, cap // page, page, 5)
+    blocks = blank(batch, kv, cap, pages, 1)
+    old = blocks.bounds.clone()
+    x = 3 * torch.randn(batch, kv, tokens, D, generator=torch.Generator("cuda").manual_seed(3), device="cuda")
+    good = pages.block_table.clone()
+    bad = [1, 2, 5]
+    pages.block_table[0, bad] = value if value < 0 else pages.num_pages + value if value < 1000 else value
+    api.block_bounds(x, blocks)
+    assert flags() == B.TQ_FLAG_PAGE
+    broken = pages.block_table.clone()
+    pages.block_table.copy_(good)
+    want = ref.bounds(x, [0, 0], [tokens] * 2, torch.zeros_like(flat_bounds(blocks)))
+    got, was = flat_bounds(blocks), flat_bounds(api.BlockBounds(old, pages))
+    out = torch.zeros(batch, 40, dtype=torch.bool, device="cuda")
+    for i in bad:
+        out[0, i * page // 64:(i + 1) * page // 64] = True
+    for b in range(batch):
+        assert torch.equal(got[b][:, out[b]], was[b][:, out[b]])
+        assert torch.equal(got[b][:, ~out[b]], want[b][:, ~out[b]])
+    q = queries(batch, kv * group, torch.bfloat16, 2)
+    gone = int(out[0].sum())
+    for keep in (7, 40 - gone, 40 - gone + 2, 39):
+        pages.block_table.copy_(broken)
+        plan, lst = run_select(q, blocks, [tokens] * 2, keep, 1, 2, group, kv, cap)
+        assert flags() == (B.TQ_FLAG_PAGE if keep < 40 else 0)
+        pages.block_table.copy_(good)
+        flat = flat_bounds(blocks).clone()
+        for b in range(batch):
+            for h in range(kv):
+                t = flat[b, h].clone()
+                t[out[b], 0], t[out[b], 1] = math.inf, -math.inf      # (scores -inf)
+                w = ref.select(q[b, h * group:(h + 1) * group], t, 40, keep, 1, 2)
+                assert lst[b, h].tolist() == w, (keep, b, h)
