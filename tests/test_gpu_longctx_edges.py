@@ -355,3 +355,67 @@ def test_bounds_and_selection_pass_bad_pages_over(page, value):
                 t[out[b], 0], t[out[b], 1] = math.inf, -math.inf      # (scores -inf)
                 w = ref.select(q[b, h * group:(h + 1) * group], t, 40, keep, 1, 2)
                 assert lst[b, h].tolist() == w, (keep, b, h)
+
+
+# ------------------------------------------------------------------ a captured step
+
+@pytest.mark.parametrize("kbits,vbits,page", [(3, 4, 0), (5, 2, 128)])
+def test_a_captured_step_replayed(kbits, vbits, page):
+    """SparsePlan.step captured once with its counters, replayed on new inputs across block and page
+    borders: caches, bounds, lists and rows are those of the same steps called eagerly."""
+    kc, vc = codec("k", kbits), codec("v", vbits)
+    batch, kv, group, cap, keep = 3, 2, 4, 1024, 5
+    lens = [1000, 125, 0]
+
+    def state():
+        p = table(batch, cap // page, page, 4) if page else None
+        k, v = caches(batch, kv, cap, kbits, vbits, 1, p)
+        blocks = blank(batch, kv, cap, p, 2)
+        blocks.bounds[..., 1, :] += 3
+        plan = api.SparsePlan(batch, kv * group, kv, cap, cap, keep, 1, 1, out_dtype=torch.float16)
+        return dict(plan=plan, k=k, v=v, blocks=blocks, pos=i32(lens), n=i32([x + 1 for x in lens]),
+                    q=torch.zeros(batch, kv * group, D, device="cuda").bfloat16(),
+                    kn=torch.zeros(batch, kv, D, device="cuda").half(),
+                    vn=torch.zeros(batch, kv, D, device="cuda").half(), lst=plan.new_list(), out=plan.new_out())
+
+    def step(s):
+        s["plan"].step(kc, vc, s["q"], s["kn"], s["vn"], s["k"], s["v"], s["blocks"], s["pos"], s["n"], s["lst"],
+                       s["out"])
+        s["pos"] += 1
+        s["n"] += 1
+
+    def feed(s, seed):
+        g = torch.Generator("cuda").manual_seed(seed)
+        for f in ("q", "kn", "vn"):
+            s[f].copy_(torch.randn(s[f].shape, generator=g, device="cuda"))
+
+    a, b = state(), state()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    step(b)                    # (warmed, then as it was)
+    fresh = state()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        step(b)
+    for f in ("pos", "n"):
+        b[f].copy_(fresh[f])
+    for x, y in ((b["k"], fresh["k"]), (b["v"], fresh["v"])):
+        for f in ("idx", "sgn", "xnorm", "rnorm"):
+            if hasattr(x, f):
+                getattr(x, f).copy_(getattr(y, f))
+    b["blocks"].bounds.copy_(fresh["blocks"].bounds)
+    for i in range(8):
+        feed(a, i)
+        feed(b, i)
+        step(a)
+        graph.replay()
+        torch.cuda.synchronize()
+        for f in ("pos", "n", "lst", "out"):
+            assert torch.equal(a[f], b[f]), (i, f)
+    for f in ("idx", "sgn", "xnorm", "rnorm"):
+        assert torch.equal(getattr(a["k"], f), getattr(b["k"], f)), f
+    assert torch.equal(a["v"].idx, b["v"].idx) and torch.equal(a["blocks"].bounds, b["blocks"].bounds)
+    now = [x + 8 for x in lens]
+    check_select(b["q"], b["blocks"], now, keep, 1, 1, group, kv, b["lst"])
+    check_sparse(kc, vc, b["q"], b["k"], b["v"], b["lst"], now, b["out"], group)
+    assert flags() == 0
