@@ -142,7 +142,9 @@ typedef struct {
    * change until the work has run).  Taken by tq_quantize_prod / tq_quantize_mse and by
    * tq_decode_attention, its no-alloc form, tq_decode_step and tq_prefill_attention where
    * they decode on the tensor cores (keys of 2 to 4 bits; 5-bit keys return
-   * TQ_ERR_UNSUPPORTED); the other calls take flat caches only (TQ_ERR_UNSUPPORTED). */
+   * TQ_ERR_UNSUPPORTED), and by tq_prefix_attention and tq_sparse_attention (every width; the
+   * two caches of a call may have tables and page sizes of their own); the other calls take flat
+   * caches only (TQ_ERR_UNSUPPORTED). */
   const tq_pages* pages;
 } tq_prod_cache;
 
@@ -325,7 +327,12 @@ tq_status tq_decode_attention_asym(const tq_attn_desc* desc, const tq_codec* vc,
  *   q_heads) and up to 2^30 tokens a sequence; more return TQ_ERR_UNSUPPORTED.
  *   desc->out_dtype is F16 or BF16 (F32 returns TQ_ERR_UNSUPPORTED): the products run on fp16
  *   operands, and on pairs of them for F16 outputs, so that a row is off by about the rounding of
- *   its own type.  Value vectors with norms below 2^-60 count as zero vectors.
+ *   its own type (F16 with 5-bit keys: 1.5 times that).  Softmax weights are held to 2^-32 of a row's
+ *   largest, value vectors with norms below 2^-60 count as zero vectors.
+ *   desc->max_seq_len and prefix_max_len bound the lengths, and the work is split by them, not by the
+ *   lengths: bounds far above the lengths cost time (bounds equal to the lengths: 59 us for a prefix
+ *   of 32768 and 32 sequences of up to 512 tokens; max_seq_len = 4096: 82 us, 16384: 126 us).
+ *   Tokens on a page outside the pool are left out, and TQ_FLAG_PAGE is raised.
  *   workspace: ≥ tq_prefix_workspace_bytes(desc, prefix_max_len) bytes, 256-byte aligned, no
  *              initialisation needed; calls that share it must be serialised on one stream.
  *   Other arguments as tq_decode_attention. */
@@ -356,20 +363,24 @@ typedef struct {
  * tq_quantize_prod (the same call for a prefill, a chunk or a decode step's tokens).  A token in
  * the first slot of a block begins its bounds anew; other tokens widen what is there, so a
  * block's bounds are those of the tokens written since its first slot.  Keys that bf16 does not
- * hold are rounded outward (the bounds stay bounds); NaN values are left out.  Blocks without a
- * token of the call are left as they are.  x needs the alignment of its type only. */
+ * hold are rounded outward (the bounds stay bounds); NaN values are left out (a channel of nothing
+ * else has the bounds +∞ and −∞).  Blocks without a token of the call are left as they are, and so
+ * are blocks on a page outside the pool (TQ_FLAG_PAGE) and all blocks of a sequence whose position
+ * is negative (TQ_FLAG_POS_OVERFLOW).  x needs the alignment of its type only. */
 tq_status tq_block_bounds(const void* x, tq_dtype x_dtype, int32_t batch, int32_t heads,
                           int32_t tokens, int64_t stride_b, int64_t stride_h, int64_t stride_t,
                           const int32_t* pos, const int32_t* count, tq_block_cache blocks,
                           int32_t capacity, tq_stream_t stream);
 
 /* Selects the blocks that each (sequence, KV head) attends.  The score of a block is the largest,
- * over the query heads g of the KV head's group, of Σ_j max(q_gj·lo_j, q_gj·hi_j); the last
- * block's bounds may cover only its first tokens.  Of the n = ⌈seq_lens[b]/64⌉ blocks of a
- * sequence all are kept if n ≤ max_blocks; else the first first_blocks, the last last_blocks and,
- * of those between, the ones with the largest scores, equal scores by the lower number.  The
- * scores are compared as in 64 bits: the result does not depend on any order of summation.  A
- * query head whose sum is NaN is left out; a block left with none scores −∞.
+ * over the query heads g of the KV head's group, of Σ_j max(q_gj·lo_j, q_gj·hi_j), that is of
+ * Σ_j q_gj·(lo_j where q_gj < 0, else hi_j); the last block's bounds may cover only its first
+ * tokens.  Of the n = ⌈seq_lens[b]/64⌉ blocks of a sequence all are kept if n ≤ max_blocks; else
+ * the first first_blocks, the last last_blocks and, of those between, the ones with the largest
+ * scores, equal scores by the lower number.  The scores are compared as summed in 64 bits, in one
+ * fixed order (the products are exact there).  A query head whose sum is NaN is left out; a block
+ * left with none scores −∞, as does one on a page outside the pool (TQ_FLAG_PAGE).  Where a row has
+ * an infinite or NaN bound or query, all its blocks are scored in 64 bits, which takes longer.
  *   list     : device int32 [batch][kv_heads][max_blocks], the kept blocks ascending, then −1.
  *   first_blocks + last_blocks ≤ max_blocks ≤ 2^24; batch · kv_heads ≤ 65535 and max_seq_len ≤
  *              2^26, else TQ_ERR_UNSUPPORTED.

@@ -389,10 +389,10 @@ __device__ __forceinline__ K kth_key(K start, int bit, int want, CtaSum& sum, Co
 // One CTA per (sequence, KV head).  The 32-bit scores are off by at most E each; with v the
 // smallest score among the `want` largest, blocks above v + 2E are kept and blocks below v − 2E
 // are not, whatever the rounding.  Those between are scored again in 64 bits (the products are
-// exact there) and ranked, ties to the lowest number: the selection does not depend on the
-// order of any sum.  The ordered scores stay in registers, kItems a thread (kItems = 0: read
-// again from the workspace, for rows of more than 16 · 1024 candidates).  Bound by the latency
-// of the counts, one per bit until the kept ones are told apart.
+// exact there, the sums have one fixed order) and ranked, ties to the lowest number: the selection
+// does not depend on how 32-bit sums round.  The ordered scores stay in registers, kItems a thread
+// (kItems = 0: read again from the workspace, for rows of more than 16 · 1024 candidates).  Bound
+// by the latency of the counts, one per bit until the kept ones are told apart.
 template <int kItems>
 __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const SelectArgs a) {
   extern __shared__ uint32_t s_dyn[];     // keep bits
@@ -692,7 +692,8 @@ tq_status select_plan(const tq_attn_desc* d, SelPlan* p) {
   const size_t rows = (size_t)d->batch * d->kv_heads;
   // rounds per CTA: about three CTAs per SM; one round where there are fewer.  (Two per SM, what
   // fits at once, took 15.3 for 18.0 us on 8 × 4096 blocks and 19.3 for 16.1 us on 128 ragged rows
-  // of 64 to 256, where smaller CTAs even the rows out.)
+  // of 64 to 256, where smaller CTAs even the rows out: calls in a row, in one run; runs of one
+  // version differ by up to 2 us, 17.8 to 20.1 and 14.9 to 18.5 us.)
   const long long all = (long long)rows * ((p->nb + kRound - 1) / kRound);
   const long long fit = 3LL * std::max(tq_num_sms(), 1);
   p->rounds = (int)std::max<long long>(1, (all + fit - 1) / fit);

@@ -30,21 +30,25 @@
 // Why the rows are the M dimension: the expansion of a token, which is most of the work, is then
 // shared by up to 128 rows, and a row's softmax is one thread's.  Few rows waste MMA rows, not
 // time: with 32 rows a tile takes about 3,000 cycles, with 112 about 4,000, where the MMAs alone
-// take 1,536.  What bounds a tile is the integer pipe and the issue of the expansion (about 13
-// instructions for eight level coordinates, 8 for eight signs, 40% of the pipe's cycles) beside
-// that of the softmax (about 9 a score), and the instruction caches, which is why the roles' loops
-// are kept rolled.  Measured: a prefix of 262144 tokens for 8 sequences of 32/8 heads 182 us
-// (283 TFLOP/s, 1.08 TB/s), of 65536 for 64 of 28/4 heads 171 us (531 TFLOP/s), of 32768 for 32
-// 60 us; 32 blocks of each of 32 sequences 46 us.  (With 4-bit values the warps of the signs could
-// expand a quarter of them: 167 us for the 64 sequences, 47 us for the blocks; not done.)
+// take 1,536.  No unit is near its peak: with 32 rows issue is at 58%, the integer pipe at 52, the
+// tensor pipe at 50 and shared memory at 52%, with 112 rows at 50, 40, 27 and less; the first stall
+// is a wait for memory or TMEM (long scoreboard).  So a tile's time is the chain of hand-overs from
+// expansion (about 13 instructions for eight level coordinates, 8 for eight signs) to product to
+// softmax (about 9 a score, through TMEM and back), with units that are half busy.  Instruction
+// fetch shows wherever code is long, which is why the roles' loops are kept rolled.  Measured: a
+// prefix of 262144 tokens for 8 sequences of 32/8 heads 184 us (281 TFLOP/s, 1.07 TB/s), of 65536
+// for 64 of 28/4 heads 171 us (531 TFLOP/s), of 32768 for 32 60 us; 32 blocks of each of 32
+// sequences 46 us.  (With 4-bit values the warps of the signs could expand a quarter of them: 167 us
+// for the 64 sequences, 47 us for the blocks; not done.)
 //
 // Roundings to 16 bits: the rotated query and sketch, ρ, the levels (scaled so that fp16 holds
-// them best, to a few 1e-5) and the weights, each off by at most half a step of fp16 (2^-11
-// relative); together 0.7 to 1.4e-3 of a row's norm, below the output's own 2^-8 a value in bf16.
-// fp16 outputs (2^-11 a value) would show them: for those (kFine) query, sketch, ρ and weights are
-// pairs of fp16 numbers (about 2^-21), for 56 instead of 24 matrix instructions a tile, and the
-// second halves of query and sketch take the place of the second D.  Scores, maxima, sums and
-// accumulators are 32 bits.
+// them best, to 8e-5 with 16 levels, 2e-5 with 8 and 2e-6 with 4) and the weights, each off by at
+// most half a step of fp16 (2^-11 relative); together 0.7 to 1.4e-3 of a row's norm, below the
+// output's own 2^-8 a value in bf16.  fp16 outputs (2^-11 a value) would show them: for those (kFine)
+// query, sketch, ρ and weights are pairs of fp16 numbers (about 2^-21; the levels stay single), for
+// 56 instead of 24 matrix instructions a tile, and the second halves of query and sketch take the
+// place of the second D: 97 us for the 32 sequences, 395 for the 8, 289 for the 64, 69 for the
+// blocks.  Scores, maxima, sums and accumulators are 32 bits.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
