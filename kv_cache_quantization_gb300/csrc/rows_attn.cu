@@ -7,10 +7,10 @@
 //   ‖x‖·( ⟨y, c[i]⟩ + ρ·⟨z, s⟩ ),   ρ = ‖r‖/‖x‖·√(π/2)/d,
 // one product of length 256 of the row [y, z] with the token's operand [c[i], ±ρ].  A value is
 // ‖v‖·Πᵀc[j], so the output row is Πᵀ·Σ_t p_t‖v_t‖c[j_t] / Σ_t p_t.  The weights of the value
-// product are w_t = 2^(e_t − m + kLift) with e_t = score + log2‖v_t‖ and m a reference near the
-// running maximum of e (not of the score): they are at most 2^(kGrow + kLift) = 2^15 whatever the
-// norms, so fp16 holds them; the denominator is Σ w_t/‖v_t‖ in 32 bits.  kLift uses what fp16 has
-// above: a weight is held to 2^-32 of the largest (without it to 2^-25, and the numerator lost a
+// product are w_t = 2^(e_t − m) with e_t = score + log2‖v_t‖ and m a reference kLift below the
+// running maximum of e (not of the score) or up to kGrow lower: they are at most 2^(kGrow + kLift) =
+// 2^15 whatever the norms, so fp16 holds them; the denominator is Σ w_t/‖v_t‖ in 32 bits.  kLift
+// uses what fp16 has above: a weight is held to 2^-32 of the largest (without it to 2^-25, and the numerator lost a
 // tail of many small weights that the denominator kept: 65535 of 2^-25.1 behind one of 1 moved a
 // row by 2.1e-3 of its norm).
 //
@@ -87,8 +87,8 @@ constexpr int kQCol = 0, kDCol = 128, kOCol = 384;   // TMEM columns
 constexpr int kQLowCol = 256;           // (fine: the second halves of y and z, over the second D)
 constexpr int kFacSlots = 4;
 constexpr float kAlpha = 64.f, kBeta = 4.f;   // scales of y and z in the fp16 row operand
-constexpr float kGrow = 8.f;            // the reference follows the maximum when 2^8 above it
-constexpr float kLift = 7.f;            // weights are taken 2^7 times as large
+constexpr float kLift = 7.f;            // the reference is taken 2^7 below the maximum
+constexpr float kGrow = 8.f;            // and follows it when it has grown by 2^8
 constexpr float kTiny = 8.6736174e-19f; // 2^-60: smaller value norms count as zero
 constexpr float kQjl = 1.2533141373155003f / 128.f;   // √(π/2)/d
 
@@ -607,7 +607,9 @@ __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int reps, in
       return z;
     }
     mt = fmaxf(mt, sm.tmax[t & 1][hf ^ 1][r]);
-    const float m_new = mt > z.m + kGrow ? mt : z.m;
+    // the reference, kLift below the maximum it was taken from (differences of near numbers are
+    // exact, so that a weight stays below 2^(kLift + kGrow) however large the scores are)
+    const float m_new = mt - z.m > kGrow + kLift ? mt - kLift : z.m;
     if (t > 0 && __any_sync(0xffffffffu, m_new != z.m)) {
       // O (this half of its columns) follows the reference, once O += W(t − 1)·V(t − 1) is
       // done (vempty).  Its barrier is that of every other tile: the phase before, tile t − 3's,
@@ -628,7 +630,7 @@ __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int reps, in
       z.l *= corr;
     }
     z.m = m_new;
-    const float ref = m_new == -INFINITY ? 0.f : m_new - kLift;
+    const float ref = m_new == -INFINITY ? 0.f : m_new;
     const tq::f32x2 ref2 = tq::pack2(-ref, -ref);
     tq::f32x2 l2 = tq::pack2(0.f, 0.f);
     if (groups > 1) tq::tmem_wait_st();

@@ -141,6 +141,40 @@ def test_a_peak_before_a_long_even_tail(out_dtype, tail):
     assert flags() == 0
 
 
+@pytest.mark.parametrize("out_dtype", [torch.float16, torch.bfloat16])
+def test_scores_so_large_that_32_bits_hold_them_to_units(out_dtype):
+    """Base-2 scores of 2^20 to 2^30 whose maximum grows by 0 to 5 steps of 32 bits in the second
+    tile: such scores are known to some units only, so the weights of the two tokens that share the
+    maximum are anything, but the row is finite and lies between their values."""
+    batch, n = 304, 256            # (two items an SM, so that an item has both tiles)
+    kc, vc = codec("k", 3), codec("v", 2)
+    k, v = caches(batch, 1, n, 3, 2, 1)
+    k.xnorm.zero_()
+    k.rnorm.zero_()
+    v.xnorm.fill_(1.0)
+    top = (37, 37 + 128)           # the same lane of either tile
+    b = torch.arange(batch, device="cuda")
+    q = torch.empty(batch, 1, D, device="cuda")
+    c = ref.key_parts(k, kc, 0, 0, torch.tensor([37], device="cuda"))[0][0]
+    for t in (k.idx, k.sgn):
+        for i in top:
+            t[:, :, ..., i, :] = t[:1, :, ..., 37, :]
+    v.xnorm[:, 0, top[0]] = v.xnorm[:, 0, top[1]] = 8.0
+    k.xnorm[:, 0, top[0]] = 1.0
+    k.xnorm[:, 0, top[1]] = 1.0 + 2.0 ** -23 * (b % 6)
+    one = (c @ c) / math.sqrt(D) / math.log(2)             # base-2 score of q = Π^T c
+    want = 2.0 ** (20 + 10 * b.double() / batch)
+    q[:, 0] = ((want / one)[:, None] * (c @ torch.tensor(kc.pi, device="cuda"))).float()
+    lens = i32([n] * batch)
+    plan = api.PrefixPlan(batch, 1, 1, n, n, 64, 0, torch.float32, out_dtype)
+    out = plan.run(kc, vc, q, *caches(1, 1, 64, 3, 2, 3), i32([0]), k, v, lens, plan.new_out())
+    assert out.isfinite().all(), (~out.isfinite()).any(-1).any(-1).nonzero().flatten().tolist()[:20]
+    cv = torch.stack([ref.value_parts(v, vc, i, 0, torch.tensor(top, device="cuda"))[0] for i in range(batch)])
+    most = 8.0 * cv.norm(dim=-1).amax(-1)
+    assert bool((out[:, 0].double().norm(dim=-1) <= most * (1 + 2.0 ** -7)).all())
+    assert flags() == 0
+
+
 # ------------------------------------------------------------------ refusals
 
 def test_arrays_and_tables_of_the_host_are_refused():
