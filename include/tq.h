@@ -380,7 +380,8 @@ tq_status tq_block_bounds(const void* x, tq_dtype x_dtype, int32_t batch, int32_
  * scores, equal scores by the lower number.  The scores are compared as summed in 64 bits, in one
  * fixed order (the products are exact there).  A query head whose sum is NaN is left out; a block
  * left with none scores −∞, as does one on a page outside the pool (TQ_FLAG_PAGE).  Where a row has
- * an infinite or NaN bound or query, all its blocks are scored in 64 bits, which takes longer.
+ * an infinite or NaN bound, or an infinite query, all its blocks are scored in 64 bits, which takes
+ * longer.
  *   list     : device int32 [batch][kv_heads][max_blocks], the kept blocks ascending, then −1.
  *   first_blocks + last_blocks ≤ max_blocks ≤ 2^24; batch · kv_heads ≤ 65535 and max_seq_len ≤
  *              2^26, else TQ_ERR_UNSUPPORTED.
