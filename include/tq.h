@@ -183,6 +183,54 @@ tq_status tq_quantize_mse(const tq_codec* vc, const void* x, tq_dtype x_dtype, i
                           int64_t stride_t, const int32_t* pos, const int32_t* count,
                           tq_mse_cache cache, int32_t capacity, tq_stream_t stream);
 
+/* ------------------------------------------------------------------ rotary positions */
+
+/* Rotary positions of queries and keys, applied before they are coded or attended: pair i of a
+ * vector at position p is turned by the angle p·f_i, in radians, and scaled by `magnitude`.  The
+ * pairs are coordinates (2i, 2i + 1) (interleaved) or (i, i + rotary_dim/2); coordinates from
+ * rotary_dim on are copied. */
+typedef struct {
+  int32_t rotary_dim;      /* even, 2..128 */
+  int32_t interleaved;
+  float magnitude;
+  uint64_t turns[TQ_HEAD_DIM / 2];   /* f_i / 2π as fractions of 2^64, whole turns dropped */
+} tq_rotary;
+
+/* f_i = base^(−2i / rotary_dim), i < rotary_dim / 2 (host, caller-owned), made slower for contexts
+ * longer than those a model knows: with original_len = 0 all are divided by `factor` (1: none);
+ * else a frequency that makes n = original_len·f_i/2π turns over the original length becomes
+ * s·f_i + (1 − s)·f_i/factor with s = (n − low_turns)/(high_turns − low_turns), at least 0 and at
+ * most 1.  Pure host code. */
+tq_status tq_rotary_frequencies(int32_t rotary_dim, double base, double factor,
+                                int32_t original_len, double low_turns, double high_turns,
+                                double* frequencies);
+
+/* Fills in `r` from frequencies (|f_i| ≤ 1e6 radians a position; those above or other ones of the
+ * caller's own).  Pure host code. */
+tq_status tq_rotary_init(tq_rotary* r, int32_t rotary_dim, int32_t interleaved,
+                         const double* frequencies, double magnitude);
+
+/* Vectors of one kind (the query heads, or the key heads): vector (b, h, t) starts at
+ * x + b*x_stride_b + h*x_stride_h + t*x_stride_t (elements, ≥ 0), its 128 coordinates are
+ * contiguous, and it is written at the same place of y, which is x itself with the same strides, or
+ * memory apart from every input of the call. */
+typedef struct {
+  const void* x;
+  void* y;
+  int32_t heads;
+  int64_t x_stride_b, x_stride_h, x_stride_t, y_stride_b, y_stride_h, y_stride_t;
+} tq_rotary_io;
+
+/* Turns q and k (either may be NULL or have no heads) of `dtype` (F32, F16 or BF16) in one launch.
+ *   positions : device int32 [batch][tokens], rows pos_stride_b apart (0: one row for all); any
+ *               number, negative ones turn backwards.
+ * Angles are right to 2^-32 turns at any position; products and sums are 32 bits, rounded once.
+ * Vectors at multiples of 16 bytes and a rotary_dim that is a multiple of 16 take 16-byte accesses;
+ * others work and are slower. */
+tq_status tq_rotary_apply(const tq_rotary* r, tq_dtype dtype, int32_t batch, int32_t tokens,
+                          const int32_t* positions, int64_t pos_stride_b, const tq_rotary_io* q,
+                          const tq_rotary_io* k, tq_stream_t stream);
+
 /* ------------------------------------------------------------------ scores */
 
 /* Raw estimator ⟨q, k⟩ ≈ ‖x‖·⟨Π q, c[idx]⟩ + ‖r‖·√(π/2)/d·⟨S q, 2·sign − 1⟩ for every
@@ -344,6 +392,29 @@ tq_status tq_prefix_attention(const tq_attn_desc* desc, const tq_codec* kc, cons
                               const int32_t* seq_lens, void* out, void* workspace,
                               size_t workspace_bytes, tq_stream_t stream);
 
+/* ------------------------------------------------------------------ drafted tokens */
+
+#define TQ_TREE_NODES 64        /* maximum drafted tokens of a sequence */
+
+/* Attention of n_nodes drafted tokens per sequence over the compressed cache, e.g. a tree of tokens
+ * that a smaller model proposes and one pass verifies: node i of sequence b attends the history's
+ * seq_lens[b] tokens and those drafted tokens j whose bit j is set in its mask (its ancestors and
+ * itself; any mask is allowed), in one softmax of the estimator scores ([QJL] §五, §六).  The
+ * drafted keys and values were appended behind the history: node j is token seq_lens[b] + j.
+ *   q, out   : device [batch][n_nodes][q_heads][128] of desc->q_dtype / desc->out_dtype.
+ *   tree     : device uint64 [batch][n_nodes], rows tree_stride_b elements apart (0: one tree for
+ *              all sequences); bits n_nodes and above are not read.
+ *   desc->max_seq_len bounds seq_lens[b] + n_nodes (longer histories are clamped and flagged).
+ *   A node that attends no token at all gives a zero row.
+ *   Other arguments, types, precision and limits as tq_prefix_attention (every key and value width,
+ *   flat and paged caches; n_nodes · batch · q_heads ≤ 2^24); n_nodes ≤ TQ_TREE_NODES.  Workspace ≥
+ *   tq_tree_workspace_bytes(desc, n_nodes) bytes.  tq_keep_tokens keeps the accepted nodes. */
+size_t tq_tree_workspace_bytes(const tq_attn_desc* desc, int32_t n_nodes);
+tq_status tq_tree_attention(const tq_attn_desc* desc, int32_t n_nodes, const tq_codec* kc,
+                            const tq_codec* vc, const void* q, tq_prod_cache k, tq_mse_cache v,
+                            const int32_t* seq_lens, const uint64_t* tree, int64_t tree_stride_b,
+                            void* out, void* workspace, size_t workspace_bytes, tq_stream_t stream);
+
 /* ------------------------------------------------------------------ block-sparse attention */
 
 /* A long cache can be read in part: the keys of every block of TQ_BLOCK_TOKENS tokens have
@@ -405,6 +476,40 @@ tq_status tq_sparse_attention(const tq_attn_desc* desc, const tq_codec* kc, cons
                               const int32_t* seq_lens, const int32_t* list, int32_t max_blocks,
                               void* out, void* workspace, size_t workspace_bytes,
                               tq_stream_t stream);
+
+/* ------------------------------------------------------------------ moving codes */
+
+#define TQ_MAX_PAIRS 65536      /* maximum pages copied in a call */
+
+/* Copies whole pages of a pool: page src[i] to page dst[i] in every array given, i < n.  A fork of a
+ * sequence gets pages of its own this way (its block table's other entries may name the same pages
+ * as the original's), and a pool is put in order.
+ *   k, v, blocks : host, each may be NULL (not all); arrays with num_pages in place of batch and
+ *              page_tokens in place of capacity (a flat cache: its sequences are the pages; their
+ *              `pages` members are not read).
+ *   src, dst : device int32[n].  A pair with a −1 is passed over.  A pair is left out, and
+ *              TQ_FLAG_PAGE raised, if a page lies outside [0, num_pages) or its destination is also
+ *              another pair's source or destination.
+ * n ≤ TQ_MAX_PAIRS and heads · page_tokens ≤ 2^26, else TQ_ERR_UNSUPPORTED. */
+tq_status tq_copy_pages(const tq_prod_cache* k, int32_t key_bits, const tq_mse_cache* v,
+                        int32_t value_bits, const tq_block_cache* blocks, int32_t heads,
+                        int32_t num_pages, int32_t page_tokens, const int32_t* src,
+                        const int32_t* dst, int32_t n, tq_stream_t stream);
+
+/* Keeps tokens of those behind a sequence: for each entry j = keep[b][i] ≥ 0 the codes of token
+ * pos[b] + j become those of token pos[b] + i, in all heads of both caches, as if all were read
+ * before any is written (entries may be in any order and repeat).  After drafted tokens were
+ * verified, the accepted path moves to the front of them this way and the sequence's length grows by
+ * its number of tokens.
+ *   pos      : device int32[batch].
+ *   keep     : device int32 [batch][max_keep]; negative entries leave their slot as it is.
+ * Tokens at or beyond the capacity (TQ_FLAG_POS_OVERFLOW) or on a page outside the pool
+ * (TQ_FLAG_PAGE) are left out.  A page that is written may not be another sequence's of the same
+ * call.  Block bounds are not moved: fold kept keys in with tq_block_bounds once they are kept.
+ * max_keep ≤ TQ_TREE_NODES, else TQ_ERR_UNSUPPORTED. */
+tq_status tq_keep_tokens(tq_prod_cache k, int32_t key_bits, tq_mse_cache v, int32_t value_bits,
+                         int32_t batch, int32_t heads, int32_t capacity, const int32_t* pos,
+                         const int32_t* keep, int32_t max_keep, tq_stream_t stream);
 
 /* ------------------------------------------------------------------ store with an FP16 tail */
 

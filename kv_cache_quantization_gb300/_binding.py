@@ -20,6 +20,8 @@ TQ_HEAD_DIM = 128
 TQ_MAX_GROUP = 8
 TQ_CAPACITY_ALIGN = 64
 TQ_BLOCK_TOKENS = 64
+TQ_TREE_NODES = 64
+TQ_MAX_PAIRS = 65536
 TQ_FLAG_POS_OVERFLOW, TQ_FLAG_LEN_OVERFLOW, TQ_FLAG_TIMEOUT, TQ_FLAG_PAGE = 1, 2, 4, 8
 
 _vp = ctypes.c_void_p
@@ -43,6 +45,17 @@ class tq_mse_cache(ctypes.Structure):
 
 class tq_block_cache(ctypes.Structure):
     _fields_ = [("bounds", _vp), ("pages", ctypes.POINTER(tq_pages))]
+
+
+class tq_rotary(ctypes.Structure):
+    _fields_ = [("rotary_dim", _i32), ("interleaved", _i32), ("magnitude", ctypes.c_float),
+                ("turns", ctypes.c_uint64 * (TQ_HEAD_DIM // 2))]
+
+
+class tq_rotary_io(ctypes.Structure):
+    _fields_ = [("x", _vp), ("y", _vp), ("heads", _i32), ("x_stride_b", _i64), ("x_stride_h", _i64),
+                ("x_stride_t", _i64), ("y_stride_b", _i64), ("y_stride_h", _i64),
+                ("y_stride_t", _i64)]
 
 
 class tq_attn_desc(ctypes.Structure):
@@ -108,6 +121,23 @@ SIGNATURES = {
                                            tq_prod_cache, tq_mse_cache, _vp, _vp, _i32, _vp, _vp,
                                            ctypes.c_size_t, _vp]),
     "tq_check_bounded_wait": (ctypes.c_int, [ctypes.c_uint32, _vp]),
+    "tq_rotary_frequencies": (ctypes.c_int, [_i32, ctypes.c_double, ctypes.c_double, _i32,
+                                             ctypes.c_double, ctypes.c_double, _vp]),
+    "tq_rotary_init": (ctypes.c_int, [ctypes.POINTER(tq_rotary), _i32, _i32, _vp,
+                                      ctypes.c_double]),
+    "tq_rotary_apply": (ctypes.c_int, [ctypes.POINTER(tq_rotary), ctypes.c_int, _i32, _i32, _vp, _i64,
+                                       ctypes.POINTER(tq_rotary_io), ctypes.POINTER(tq_rotary_io),
+                                       _vp]),
+    "tq_tree_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(tq_attn_desc), _i32]),
+    "tq_tree_attention": (ctypes.c_int, [ctypes.POINTER(tq_attn_desc), _i32, _vp, _vp, _vp,
+                                         tq_prod_cache, tq_mse_cache, _vp, _vp, _i64, _vp, _vp,
+                                         ctypes.c_size_t, _vp]),
+    "tq_copy_pages": (ctypes.c_int, [ctypes.POINTER(tq_prod_cache), _i32,
+                                     ctypes.POINTER(tq_mse_cache), _i32,
+                                     ctypes.POINTER(tq_block_cache), _i32, _i32, _i32, _vp, _vp,
+                                     _i32, _vp]),
+    "tq_keep_tokens": (ctypes.c_int, [tq_prod_cache, _i32, tq_mse_cache, _i32, _i32, _i32, _i32, _vp,
+                                      _vp, _i32, _vp]),
 }
 
 _lib = None
@@ -291,6 +321,46 @@ def tq_sparse_attention(desc: tq_attn_desc, kc, vc, q, k: tq_prod_cache, v: tq_m
     return load().tq_sparse_attention(ctypes.byref(desc), kc, vc, ptr(q), k, v, ptr(seq_lens),
                                       ptr(block_list), max_blocks, ptr(out), ptr(workspace),
                                       workspace_bytes, ptr(stream))
+
+
+def tq_rotary_frequencies(rotary_dim, base, factor, original_len, low_turns, high_turns,
+                          frequencies) -> int:
+    return load().tq_rotary_frequencies(rotary_dim, base, factor, original_len, low_turns, high_turns,
+                                        ptr(frequencies))
+
+
+def tq_rotary_init(r: tq_rotary, rotary_dim, interleaved, frequencies, magnitude) -> int:
+    return load().tq_rotary_init(ctypes.byref(r), rotary_dim, interleaved, ptr(frequencies), magnitude)
+
+
+def tq_rotary_apply(r: tq_rotary, dtype, batch, tokens, positions, pos_stride_b, q, k, stream) -> int:
+    """q, k: tq_rotary_io or None."""
+    return load().tq_rotary_apply(ctypes.byref(r), dtype, batch, tokens, ptr(positions), pos_stride_b,
+                                  q, k, ptr(stream))
+
+
+def tq_tree_workspace_bytes(desc: tq_attn_desc, n_nodes: int) -> int:
+    return load().tq_tree_workspace_bytes(ctypes.byref(desc), n_nodes)
+
+
+def tq_tree_attention(desc: tq_attn_desc, n_nodes, kc, vc, q, k: tq_prod_cache, v: tq_mse_cache,
+                      seq_lens, tree, tree_stride_b, out, workspace, workspace_bytes, stream) -> int:
+    return load().tq_tree_attention(ctypes.byref(desc), n_nodes, kc, vc, ptr(q), k, v, ptr(seq_lens),
+                                    ptr(tree), tree_stride_b, ptr(out), ptr(workspace),
+                                    workspace_bytes, ptr(stream))
+
+
+def tq_copy_pages(k, key_bits, v, value_bits, blocks, heads, num_pages, page_tokens, src, dst, n,
+                  stream) -> int:
+    """k, v, blocks: tq_prod_cache, tq_mse_cache, tq_block_cache or None."""
+    return load().tq_copy_pages(k, key_bits, v, value_bits, blocks, heads, num_pages, page_tokens,
+                                ptr(src), ptr(dst), n, ptr(stream))
+
+
+def tq_keep_tokens(k: tq_prod_cache, key_bits, v: tq_mse_cache, value_bits, batch, heads, capacity, pos,
+                   keep, max_keep, stream) -> int:
+    return load().tq_keep_tokens(k, key_bits, v, value_bits, batch, heads, capacity, ptr(pos),
+                                 ptr(keep), max_keep, ptr(stream))
 
 
 def tq_check_bounded_wait(limit_us: int, stream) -> int:

@@ -648,6 +648,172 @@ class PrefixPlan:
         return out
 
 
+# ------------------------------------------------------------------ rotary positions
+
+def _span(t: torch.Tensor):
+    """First byte and the one behind the last that a tensor without negative strides reaches."""
+    n = sum((d - 1) * s for d, s in zip(t.shape, t.stride())) + 1
+    return t.data_ptr(), t.data_ptr() + n * t.element_size()
+
+
+class Rotary:
+    """Rotary positions (include/tq.h, tq_rotary): angles position · f_i on pairs of the first
+    rotary_dim coordinates, neighbouring ones (interleaved) or halves.  Frequencies are
+    base^(−2i/rotary_dim), divided by `factor` for longer contexts, all of them or, with
+    original_len, by parts (tq_rotary_frequencies); or an array of rotary_dim / 2 of the caller's."""
+
+    def __init__(self, rotary_dim=HEAD_DIM, base=10000.0, interleaved=False, factor=1.0, original_len=0,
+                 low_turns=1.0, high_turns=32.0, magnitude=1.0, frequencies=None):
+        if frequencies is None:
+            frequencies = np.zeros(HEAD_DIM // 2, dtype=np.float64)
+            B.check(B.tq_rotary_frequencies(rotary_dim, base, factor, original_len, low_turns, high_turns,
+                                            frequencies.ctypes.data), "tq_rotary_frequencies")
+            frequencies = frequencies[:rotary_dim // 2]
+        self.frequencies = np.ascontiguousarray(frequencies, dtype=np.float64)
+        if self.frequencies.shape != (rotary_dim // 2,):
+            raise ValueError(f"expected {rotary_dim // 2} frequencies, got {list(self.frequencies.shape)}")
+        self.rotary_dim, self.interleaved, self.magnitude = rotary_dim, bool(interleaved), float(magnitude)
+        self._c = B.tq_rotary()
+        B.check(B.tq_rotary_init(self._c, rotary_dim, int(self.interleaved), self.frequencies,
+                                 self.magnitude), "tq_rotary_init")
+
+    @staticmethod
+    def _io(x, y, name, batch, tokens, dtype):
+        sx, sy = x.stride(), y.stride()
+        shape = x.shape
+        if len(shape) != 4 or shape[0] != batch or shape[2] != tokens or shape[3] != HEAD_DIM or x.dtype != dtype or \
+                y.shape != shape or y.dtype != dtype or sx[3] != 1 or sy[3] != 1:
+            raise ValueError(f"{name} must be [{batch}, heads, {tokens}, {HEAD_DIM}] of {dtype} with contiguous "
+                             f"last dim, and its output the same, got {x.dtype} {list(shape)} and {y.dtype} "
+                             f"{list(y.shape)}")
+        if y is not x and (x.data_ptr() != y.data_ptr() or sx != sy):
+            (a, b), (c, d) = _span(x), _span(y)
+            if a < d and c < b:
+                raise ValueError(f"the output of {name} must be {name} itself or memory apart from it")
+        # every vector has a place of its own: dims by stride, none inside another's
+        at = HEAD_DIM
+        for s, n in sorted(zip(sy[:3], shape[:3])):
+            if n > 1:
+                if s < at:
+                    raise ValueError(f"vectors of the output of {name} overlap")
+                at = s * n
+        return B.tq_rotary_io(x.data_ptr(), y.data_ptr(), shape[1], sx[0], sx[1], sx[2], sy[0], sy[1], sy[2])
+
+    def apply(self, q, k, positions, q_out=None, k_out=None, stream=None):
+        """Turns q and k [batch, heads, tokens, 128] (any strides, k may be None) by their positions,
+        int32 [batch, tokens], in one launch; into q_out and k_out, or in place.  Returns both."""
+        q_out = q if q_out is None else q_out
+        batch, tokens = positions.shape
+        if positions.dtype != torch.int32 or (tokens > 1 and positions.stride(1) != 1):
+            raise ValueError("positions must be int32 [batch, tokens] with contiguous rows")
+        io_q = self._io(q, q_out, "q", batch, tokens, q.dtype)
+        io_k = None
+        if k is None:
+            d = _device(q, positions, q_out)
+        else:
+            k_out = k if k_out is None else k_out
+            d = _device(q, k, positions, q_out, k_out)
+            io_k = self._io(k, k_out, "k", batch, tokens, q.dtype)
+        st = B.load().tq_rotary_apply(self._c, tq_dtype(q.dtype), batch, tokens, positions.data_ptr(),
+                                      positions.stride(0), io_q, io_k, _on(stream, d))
+        if st:
+            B.check(st, "tq_rotary_apply")
+        return q_out, k_out
+
+
+# ------------------------------------------------------------------ drafted tokens
+
+class TreePlan:
+    """Attention of drafted tokens over the compressed cache (tq_tree_attention), with its workspace
+    (allocated once, reused; calls of a plan are to be serialised on one stream).  The drafted
+    tokens' keys and values are in the cache behind the history; max_seq_len bounds a history and
+    its drafted tokens."""
+
+    def __init__(self, batch, n_nodes, q_heads, kv_heads, capacity, max_seq_len, q_dtype=torch.bfloat16,
+                 out_dtype=torch.bfloat16, softmax_scale=None, device="cuda"):
+        self.desc = B.tq_attn_desc(batch, q_heads, kv_heads, HEAD_DIM, _cap(capacity),
+                                   max_seq_len, 0, softmax_scale if softmax_scale else 0.0,
+                                   tq_dtype(q_dtype), tq_dtype(out_dtype))
+        self.nbytes = B.tq_tree_workspace_bytes(self.desc, n_nodes)
+        if self.nbytes == 0:
+            raise ValueError("invalid tree-attention configuration")
+        self.workspace = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        self.batch, self.n_nodes, self.kv_heads, self.capacity = batch, n_nodes, kv_heads, _cap(capacity)
+        self.q_dtype, self.out_dtype = q_dtype, out_dtype
+        self.rows, self.shape = (batch,), (batch, n_nodes, q_heads, HEAD_DIM)
+
+    def new_out(self, device="cuda"):
+        return torch.empty(self.shape, dtype=self.out_dtype, device=device)
+
+    def run(self, kc: Codec, vc: Codec, q, k: ProdCache, v: MSECache, seq_lens, tree, out, stream=None):
+        """Attention of q [batch, n_nodes, q_heads, 128] over each sequence's seq_lens[b] tokens and the
+        drafted tokens that tree, int64 [batch, n_nodes] ([1, n_nodes]: one for all sequences), names:
+        bit j of a node's number is drafted token j, token seq_lens[b] + j of the cache."""
+        d = _device(q, k.idx, v.idx, seq_lens, tree, out, self.workspace)
+        _expect(q, self.shape, self.q_dtype, "q")
+        _expect(seq_lens, self.rows, torch.int32, "seq_lens")
+        shared = tree.shape[0] == 1
+        _expect(tree, (1 if shared else self.batch, self.n_nodes), torch.int64, "tree")
+        _expect(out, self.shape, self.out_dtype, "out")
+        _expect_caches(k, v, self.batch, self.kv_heads, self.capacity, kc, vc, "cache")
+        st = B.load().tq_tree_attention(self.desc, self.n_nodes, kc.handle, vc.handle, q.data_ptr(), k.c(), v.c(),
+                                        seq_lens.data_ptr(), tree.data_ptr(), 0 if shared else self.n_nodes,
+                                        out.data_ptr(), self.workspace.data_ptr(), self.nbytes, _on(stream, d))
+        if st:
+            B.check(st, "tq_tree_attention")
+        return out
+
+
+def keep_tokens(k: ProdCache, v: MSECache, pos, keep, stream=None):
+    """Keeps tokens of those behind pos[b] (int32 [batch]): for each entry j ≥ 0 of keep, int32 [batch,
+    at most 64], the codes of token pos[b] + j become those of token pos[b] + i, i the entry's index
+    (include/tq.h, tq_keep_tokens)."""
+    (batch,) = pos.shape
+    kl, vl, slots = k._layout or k.layout(), v._layout or v.layout(), k.capacity
+    if not (_fits(kl, k.pages, batch, kl[1], slots) and _fits(vl, v.pages, batch, kl[1], slots)) or kl[4] != vl[4]:
+        raise ValueError(f"expected caches of {batch} sequences or block tables for them, of the same heads and "
+                         f"slots on one device, got keys {list(k.xnorm.shape)} and values {list(v.xnorm.shape)}")
+    _expect(pos, (batch,), torch.int32, "pos")
+    if keep.dim() != 2:
+        raise ValueError("keep must be int32 [batch, tokens]")
+    _expect(keep, (batch, keep.shape[1]), torch.int32, "keep")
+    d = _device(k.idx, pos, keep)
+    st = B.load().tq_keep_tokens(k.c(), kl[3] + 1, v.c(), vl[3], batch, kl[1], slots, pos.data_ptr(),
+                                 keep.data_ptr(), keep.shape[1], _on(stream, d))
+    if st:
+        B.check(st, "tq_keep_tokens")
+
+
+def copy_pages(src, dst, k: Optional[ProdCache] = None, v: Optional[MSECache] = None,
+               blocks: Optional[BlockBounds] = None, stream=None):
+    """Copies page src[i] to page dst[i] (int32 [n], −1: passed over) of a pool in every array given: its
+    keys, values and block bounds (include/tq.h, tq_copy_pages).  Of a flat cache the sequences are
+    the pages."""
+    kl = k and (k._layout or k.layout())
+    vl = v and (v._layout or v.layout())
+    shapes = {x[:3] + x[4:] for x in (kl, vl) if x}
+    if blocks is not None:
+        s, t = blocks.bounds.shape, blocks.bounds
+        if len(s) != 5 or s[3:] != (2, HEAD_DIM) or t.dtype != torch.bfloat16 or not t.is_contiguous():
+            raise ValueError(f"bounds must be contiguous bfloat16 [pages, heads, blocks, 2, 128], got {t.dtype} {list(s)}")
+        shapes.add((s[0], s[1], s[2] * B.TQ_BLOCK_TOKENS, t.get_device()))
+    if len(shapes) != 1:
+        raise ValueError("expected keys, values or bounds of pools of one shape on one device, got "
+                         + (", ".join(str(list(x[:3])) for x in sorted(shapes)) or "none"))
+    ((pages, heads, slots, where),) = shapes
+    n = len(src)
+    _expect(src, (n,), torch.int32, "src")
+    _expect(dst, (n,), torch.int32, "dst")
+    d = _device(src, dst)
+    if where != d:
+        raise ValueError(f"expected a pool on the current device cuda:{d}")
+    st = B.load().tq_copy_pages(k and k.c(), kl[3] + 1 if k else 0, v and v.c(), vl[3] if v else 0,
+                                blocks and blocks.c(), heads, pages, slots, src.data_ptr(), dst.data_ptr(), n,
+                                _on(stream, d))
+    if st:
+        B.check(st, "tq_copy_pages")
+
+
 class TailStore:
     """A cache in the asymmetric layout: a compressed part (FP16 keys, MSE-coded values) and an
     FP16 tail of the most recent tokens that compacts into the compressed part when it fills

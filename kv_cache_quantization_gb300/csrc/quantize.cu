@@ -503,13 +503,19 @@ tq_status tq_launch_append_kv(const tq::AppendKV& a, int batch, cudaStream_t str
 extern "C" tq_status tq_device_status(uint32_t* flags) {
   if (!flags) return TQ_ERR_INVALID_ARG;
   if (cudaDeviceSynchronize() != cudaSuccess) return TQ_ERR_CUDA;
-  const unsigned int a = tq_take_flags_quantize(), b = tq_take_flags_attention();
-  const unsigned int d = tq_take_flags_quantize_tc(), e = tq_take_flags_decode_tc();
-  const unsigned int f = tq_take_flags_decode_asym(), g = tq_take_flags_store();
-  const unsigned int h = tq_take_flags_rows(), i = tq_take_flags_blocks();
-  if (a == ~0u || b == ~0u || d == ~0u || e == ~0u || f == ~0u || g == ~0u || h == ~0u || i == ~0u)
-    return TQ_ERR_CUDA;
-  *flags = a | b | d | e | f | g | h | i;
+  unsigned int (*const words[])() = {
+      tq_take_flags_quantize, tq_take_flags_attention, tq_take_flags_quantize_tc, tq_take_flags_decode_tc,
+      tq_take_flags_decode_asym, tq_take_flags_store, tq_take_flags_rows, tq_take_flags_blocks,
+      tq_take_flags_moves, tq_take_flags_tree};
+  uint32_t all = 0;
+  bool bad = false;
+  for (auto take : words) {
+    const unsigned int w = take();
+    bad = bad || w == ~0u;
+    all |= w;
+  }
+  if (bad) return TQ_ERR_CUDA;
+  *flags = all;
   if (*flags & TQ_FLAG_TIMEOUT) return TQ_ERR_TIMEOUT;
   return *flags ? TQ_ERR_DEVICE_STATUS : TQ_OK;
 }

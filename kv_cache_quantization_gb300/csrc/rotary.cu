@@ -1,0 +1,291 @@
+// Rotary positions of queries and keys, before they are attended or coded (tq_rotary_apply).
+//
+// Mathematics.  Pair i of a vector at position p turns by θ = p·f_i and is scaled by m:
+//   y_a = m·(a·cos θ − b·sin θ),   y_b = m·(a·sin θ + b·cos θ).
+// f_i/2π is held as a fraction of 2^64 (turns per position), so that p·f_i is one 64-bit
+// multiplication whose overflow drops whole turns: the angle is as good at position 2^31 as at 1
+// (2^-33 turns).  The nearest quarter turn is taken out in integers; what is left, at most an
+// eighth of a turn, is exact in 32 bits to 2^-27 radians or so.  Products and sums are 32 bits,
+// rounded once to the output's type.
+//
+// Bound by reading and writing the vectors.  A warp takes four heads of a token at a time, eight
+// lanes a vector and 16 coordinates (8 pairs) a lane, and keeps its lanes' sines and cosines while
+// it goes through the token's heads.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "tq_internal.h"
+
+namespace {
+
+struct Side {
+  const char* x;
+  char* y;
+  long long xb, xh, xt, yb, yh, yt;   // strides in bytes
+};
+
+struct RotaryArgs {
+  tq_rotary r;
+  Side q, k;
+  int q_heads, heads;       // heads: of both
+  int tokens;
+  long long rows;           // batch · tokens
+  const int* positions;
+  long long pos_b;
+  int ways;                 // warps that share a token's heads
+};
+
+template <typename T>
+__device__ __forceinline__ float to_float(T x);
+template <>
+__device__ __forceinline__ float to_float(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+template <>
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_float(float x);
+template <>
+__device__ __forceinline__ float from_float(float x) { return x; }
+template <>
+__device__ __forceinline__ __half from_float(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float(float x) { return __float2bfloat16_rn(x); }
+
+// cos and sin (times m) of pair i at a position.
+__device__ __forceinline__ void angle(const tq_rotary& r, int i, int position, float& c, float& s) {
+  const uint64_t turns = (uint64_t)(int64_t)position * r.turns[i];
+  const uint32_t u = (uint32_t)(turns >> 32);
+  const uint32_t quarter = (u + (1u << 29)) >> 30;
+  float s0, c0;
+  sincospif((float)(int32_t)(u - (quarter << 30)) * 0x1p-31f, &s0, &c0);   // half turns, |·| ≤ 1/4
+  const float a = quarter & 1 ? s0 : c0, b = quarter & 1 ? c0 : s0;
+  c = (quarter + 1) & 2 ? -a : a;
+  s = quarter & 2 ? -b : b;
+  c *= r.magnitude;
+  s *= r.magnitude;
+}
+
+__device__ __forceinline__ void turn(float a, float b, float c, float s, float& ya, float& yb) {
+  ya = fmaf(a, c, -b * s);
+  yb = fmaf(a, s, b * c);
+}
+
+// kPer = 16 bytes of T.  Lane l of a vector's eight holds pairs 8l..8l + 7 of the turned
+// coordinates: neighbouring ones are the 16 coordinates from 16l, halves are 8 from 8l and the 8
+// that lie rotary_dim/2 behind; lanes past the turned coordinates copy 16 of the others.
+template <typename T, bool kInterleaved>
+__global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ RotaryArgs a) {
+  constexpr int kPer = 16 / (int)sizeof(T), kVecs = 8 / kPer;      // 16-byte loads of 8 coordinates
+  constexpr int kFlight = sizeof(T) == 4 ? 2 : 4;                  // heads in flight a lane
+  const int lane = threadIdx.x & 31, unit = lane & 7;
+  const long long warp = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const long long row = warp / a.ways;
+  if (row >= a.rows) return;
+  const int h0 = (int)(warp % a.ways) * 4 + (lane >> 3), step = a.ways * 4;
+  const int b = (int)(row / a.tokens), t = (int)(row % a.tokens);
+  const int units = a.r.rotary_dim / 16;
+  const bool turned = unit < units;
+  const int first = turned && !kInterleaved ? 8 * unit : 16 * unit;
+  const int second = turned && !kInterleaved ? a.r.rotary_dim / 2 + 8 * unit : 16 * unit + 8;
+  const int position = a.positions[b * a.pos_b + t];
+  float c[8], s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    c[i] = 1.f;
+    s[i] = 0.f;
+    if (turned) angle(a.r, 8 * unit + i, position, c[i], s[i]);
+  }
+  for (int h = h0; h < a.heads; h += kFlight * step) {
+    uint4 v[kFlight][2][kVecs];
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      const int hf = h + f * step;
+      if (hf >= a.heads) break;
+      const bool key = hf >= a.q_heads;
+      const Side& x = key ? a.k : a.q;
+      if (!turned && x.x == x.y) continue;      // in place: nothing to copy
+      const char* p = x.x + b * x.xb + (hf - (key ? a.q_heads : 0)) * x.xh + t * x.xt;
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        v[f][0][i] = reinterpret_cast<const uint4*>(p + first * sizeof(T))[i];
+        v[f][1][i] = reinterpret_cast<const uint4*>(p + second * sizeof(T))[i];
+      }
+    }
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      const int hf = h + f * step;
+      if (hf >= a.heads) break;
+      const bool key = hf >= a.q_heads;
+      const Side& x = key ? a.k : a.q;
+      if (!turned && x.x == x.y) continue;
+      char* p = x.y + b * x.yb + (hf - (key ? a.q_heads : 0)) * x.yh + t * x.yt;
+      if (turned) {
+        T* e[2] = {reinterpret_cast<T*>(v[f][0]), reinterpret_cast<T*>(v[f][1])};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          T* ea = kInterleaved ? &e[i >> 2][2 * (i & 3)] : &e[0][i];
+          T* eb = kInterleaved ? ea + 1 : &e[1][i];
+          float ya, yb;
+          turn(to_float<T>(*ea), to_float<T>(*eb), c[i], s[i], ya, yb);
+          *ea = from_float<T>(ya);
+          *eb = from_float<T>(yb);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        reinterpret_cast<uint4*>(p + first * sizeof(T))[i] = v[f][0][i];
+        reinterpret_cast<uint4*>(p + second * sizeof(T))[i] = v[f][1][i];
+      }
+    }
+  }
+}
+
+// Any even rotary_dim, any strides: two lanes' worth of pairs a warp, one pair (or two coordinates
+// that are copied) a lane at a time.
+template <typename T>
+__global__ void __launch_bounds__(256) rotary_any_kernel(const __grid_constant__ RotaryArgs a) {
+  const int lane = threadIdx.x & 31;
+  const long long warp = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const long long row = warp / a.ways;
+  if (row >= a.rows) return;
+  const int b = (int)(row / a.tokens), t = (int)(row % a.tokens);
+  const int position = a.positions[b * a.pos_b + t], half = a.r.rotary_dim / 2;
+#pragma unroll 1
+  for (int i = lane; i < TQ_D / 2; i += 32) {
+    const bool turned = i < half;
+    float c = 1.f, s = 0.f;
+    if (turned) angle(a.r, i, position, c, s);
+    const int first = turned && !a.r.interleaved ? i : 2 * i;
+    const int second = turned && !a.r.interleaved ? i + half : 2 * i + 1;
+    for (int h = (int)(warp % a.ways); h < a.heads; h += a.ways) {
+      const bool key = h >= a.q_heads;
+      const Side& x = key ? a.k : a.q;
+      const int hh = h - (key ? a.q_heads : 0);
+      const T* p = reinterpret_cast<const T*>(x.x + b * x.xb + hh * x.xh + t * x.xt);
+      T* y = reinterpret_cast<T*>(x.y + b * x.yb + hh * x.yh + t * x.yt);
+      T va = p[first], vb = p[second];
+      if (turned) {
+        float ya, yb;
+        turn(to_float<T>(va), to_float<T>(vb), c, s, ya, yb);
+        va = from_float<T>(ya);
+        vb = from_float<T>(yb);
+      }
+      y[first] = va;
+      y[second] = vb;
+    }
+  }
+}
+
+// One side of a call in bytes; false for a bad one.
+bool side_of(const tq_rotary_io* io, int elem, Side* s, bool* vec) {
+  *s = Side{};
+  if (!io || io->heads == 0) return true;
+  if (io->heads < 0 || !io->x || !io->y) return false;
+  const int64_t strides[6] = {io->x_stride_b, io->x_stride_h, io->x_stride_t,
+                              io->y_stride_b, io->y_stride_h, io->y_stride_t};
+  uintptr_t low = reinterpret_cast<uintptr_t>(io->x) | reinterpret_cast<uintptr_t>(io->y);
+  if (low % elem) return false;
+  for (int64_t x : strides) {
+    if (x < 0) return false;
+    low |= (uintptr_t)(x * elem);
+  }
+  if (io->x == io->y && (strides[0] != strides[3] || strides[1] != strides[4] || strides[2] != strides[5]))
+    return false;
+  *vec = *vec && low % 16 == 0;
+  *s = Side{static_cast<const char*>(io->x), static_cast<char*>(io->y), strides[0] * elem, strides[1] * elem,
+            strides[2] * elem, strides[3] * elem, strides[4] * elem, strides[5] * elem};
+  return true;
+}
+
+template <typename T>
+void launch(const RotaryArgs& a, bool vec, unsigned grid, cudaStream_t stream) {
+  if (!vec) rotary_any_kernel<T><<<grid, 256, 0, stream>>>(a);
+  else if (a.r.interleaved) rotary_kernel<T, true><<<grid, 256, 0, stream>>>(a);
+  else rotary_kernel<T, false><<<grid, 256, 0, stream>>>(a);
+}
+
+}  // namespace
+
+extern "C" tq_status tq_rotary_frequencies(int32_t rotary_dim, double base, double factor,
+                                           int32_t original_len, double low_turns,
+                                           double high_turns, double* frequencies) {
+  if (rotary_dim < 2 || rotary_dim > TQ_HEAD_DIM || rotary_dim % 2 || !frequencies) return TQ_ERR_INVALID_ARG;
+  if (!(base > 0) || !std::isfinite(base) || !(factor > 0) || !std::isfinite(factor) || original_len < 0)
+    return TQ_ERR_INVALID_ARG;
+  if (original_len && (!(low_turns >= 0) || !(high_turns > low_turns) || !std::isfinite(high_turns)))
+    return TQ_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586477;
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    const double f = std::pow(base, -2.0 * i / rotary_dim);
+    double share = 0;            // of the frequency that stays
+    if (original_len) {
+      const double turns = original_len * f / two_pi;
+      share = std::min(1.0, std::max(0.0, (turns - low_turns) / (high_turns - low_turns)));
+    }
+    frequencies[i] = share * f + (1 - share) * (f / factor);
+  }
+  return TQ_OK;
+}
+
+extern "C" tq_status tq_rotary_init(tq_rotary* r, int32_t rotary_dim, int32_t interleaved,
+                                    const double* frequencies, double magnitude) {
+  if (!r || !frequencies || rotary_dim < 2 || rotary_dim > TQ_HEAD_DIM || rotary_dim % 2)
+    return TQ_ERR_INVALID_ARG;
+  if (!std::isfinite(magnitude) || !std::isfinite((float)magnitude)) return TQ_ERR_INVALID_ARG;
+  for (int i = 0; i < rotary_dim / 2; ++i)
+    if (!std::isfinite(frequencies[i]) || std::fabs(frequencies[i]) > 1e6) return TQ_ERR_INVALID_ARG;
+  *r = tq_rotary{};
+  r->rotary_dim = rotary_dim;
+  r->interleaved = interleaved != 0;
+  r->magnitude = (float)magnitude;
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    // f/2π as the exact product with 1/2π in two parts (106 bits), whole turns dropped
+    const double f = std::fabs(frequencies[i]), hi = f * 0x1.45f306dc9c883p-3;
+    const double lo = std::fma(f, 0x1.45f306dc9c883p-3, -hi) + f * -0x1.6b01ec5417056p-57;
+    const double frac = hi - std::floor(hi);
+    const uint64_t turns = (uint64_t)std::ldexp(frac, 64) + (uint64_t)(int64_t)std::ldexp(lo, 64);
+    r->turns[i] = frequencies[i] < 0 ? 0 - turns : turns;
+  }
+  return TQ_OK;
+}
+
+extern "C" tq_status tq_rotary_apply(const tq_rotary* r, tq_dtype dtype, int32_t batch,
+                                     int32_t tokens, const int32_t* positions,
+                                     int64_t pos_stride_b, const tq_rotary_io* q,
+                                     const tq_rotary_io* k, tq_stream_t stream_) {
+  if (!r || r->rotary_dim < 2 || r->rotary_dim > TQ_HEAD_DIM || r->rotary_dim % 2) return TQ_ERR_INVALID_ARG;
+  if (dtype != TQ_F32 && dtype != TQ_F16 && dtype != TQ_BF16) return TQ_ERR_UNSUPPORTED;
+  if (batch < 0 || tokens < 0 || pos_stride_b < 0) return TQ_ERR_INVALID_ARG;
+  if (!batch || !tokens) return TQ_OK;
+  if (!positions || reinterpret_cast<uintptr_t>(positions) % 4) return TQ_ERR_INVALID_ARG;
+  RotaryArgs a{};
+  bool vec = r->rotary_dim % 16 == 0;
+  const int elem = dtype == TQ_F32 ? 4 : 2;
+  if (!side_of(q, elem, &a.q, &vec) || !side_of(k, elem, &a.k, &vec)) return TQ_ERR_INVALID_ARG;
+  const long long qh = q ? q->heads : 0, heads = qh + (k ? k->heads : 0);
+  if (heads > (1 << 20)) return TQ_ERR_UNSUPPORTED;
+  a.rows = (long long)batch * tokens;
+  if (heads == 0) return TQ_OK;
+  a.r = *r;
+  a.q_heads = (int)qh;
+  a.heads = (int)heads;
+  a.tokens = tokens;
+  a.positions = positions;
+  a.pos_b = pos_stride_b;
+  // Warps a token: one while the tokens alone fill the GPU (each computes its angles once for all
+  // heads), more where they do not, up to one for each four heads (one, where lanes take pairs).
+  const int most = (int)(vec ? (heads + 3) / 4 : heads);
+  const long long want = (long long)std::max(tq_num_sms(), 1) * 32;
+  a.ways = (int)std::min<long long>(most, std::max<long long>(1, (want + a.rows - 1) / a.rows));
+  const long long grid = (a.rows * a.ways + 7) / 8;
+  if (grid > 0x7fffffffLL) return TQ_ERR_UNSUPPORTED;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (dtype == TQ_F32) launch<float>(a, vec, (unsigned)grid, stream);
+  else if (dtype == TQ_F16) launch<__half>(a, vec, (unsigned)grid, stream);
+  else launch<__nv_bfloat16>(a, vec, (unsigned)grid, stream);
+  return tq_cuda_status(cudaGetLastError());
+}

@@ -1,6 +1,7 @@
 // Decode attention of many query rows over one token stream of the compressed cache: over a
-// prefix that a whole batch shares (tq_prefix_attention) and over the blocks that a selection
-// kept of each sequence (tq_sparse_attention).
+// prefix that a whole batch shares (tq_prefix_attention), over the blocks that a selection
+// kept of each sequence (tq_sparse_attention), and of the tokens drafted behind a sequence over its
+// history and each other (tq_tree_attention, which rows_tree.cu compiles from this file).
 //
 // Mathematics.  With y = Π q, z = S q and a token's code (i, s, ‖x‖, ‖r‖), the estimator of
 // ⟨q, k⟩ (QJL deep-dive §五) is
@@ -58,7 +59,11 @@
 #include "tc_ptx.h"
 #include "tq_internal.h"
 
+#ifdef TQ_ROWS_TREE
+TQ_DEFINE_FLAGS(tq_take_flags_tree)
+#else
 TQ_DEFINE_FLAGS(tq_take_flags_rows)
+#endif
 
 namespace {
 
@@ -67,6 +72,11 @@ using tq::s32;
 using tq::tc_after;
 using tq::tc_before;
 
+#ifdef TQ_ROWS_TREE
+constexpr bool kTree = true;
+#else
+constexpr bool kTree = false;
+#endif
 constexpr int kTile = 128;              // tokens per tile, and query rows per item
 // 8 softmax warps, 3 × 4 expander warps, and a warpgroup that holds the issuer warp alone
 constexpr int kKeyWarp = 8, kSignWarp = 12, kValueWarp = 16, kIssueWarp = 20;
@@ -123,6 +133,13 @@ struct RowsArgs {
   const uint4* qop;         // [B·Hq][256] fp16 row operands
   const float* qf;          // [B·Hq] factor of the products
   float* rec;               // [pre_splits + own_splits][B·Hq][kRecFloats]
+#ifdef TQ_ROWS_TREE
+  // Trees: rows are [B][nodes][Hq]; every item is of one sequence, row_tiles items a (sequence, KV
+  // head) and split, own_splits splits.
+  const unsigned long long* tree;   // [B][nodes], rows tree_b apart: drafted tokens that a node attends
+  long long tree_b;
+  int nodes;
+#endif
 };
 
 struct alignas(1024) Smem {
@@ -544,6 +561,21 @@ __device__ __forceinline__ int clamp_len(int len, int most) {
   return len < 0 ? 0 : len;
 }
 
+// Which drafted tokens a row attends (trees): token t is the item's token j0 + t of them, the ones
+// before them (the history) are all attended, and those past the length have no weight anyway.
+struct RowMask {
+  unsigned long long seen;
+  int j0;
+
+  // Bit i: whether the row attends token t + i, i < 16.
+  __device__ __forceinline__ uint32_t at(int t) const {
+    const int j = j0 + t;
+    if (j <= -16) return 0xffffu;
+    if (j < 0) return (uint32_t)(seen << -j) | ((1u << -j) - 1u);
+    return j < TQ_TREE_NODES ? (uint32_t)(seen >> j) : 0u;
+  }
+};
+
 // What a softmax thread ends with.
 struct Stats {
   float m, l;
@@ -562,7 +594,7 @@ struct Stats {
 // 16 tokens are stored over the first half of its scores, which no other thread reads.
 template <bool kFine>
 __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int reps, int wl, int hf, int lane,
-                                               float f) {
+                                               float f, const RowMask& mask) {
   const int rep = wl / (4 / reps), groups = 4 / reps;       // groups of 16 tokens per thread
   const int group0 = (2 * rep + hf) * groups;
   const uint32_t lane_base = (uint32_t)(32 * wl) << 16;
@@ -583,6 +615,10 @@ __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int reps, in
 #pragma unroll 1
     for (int c = 0;; c += 16) {
       tmem_load<16>(dcol + c, d);
+      // (uniform: the tile's groups of 16 tokens are the same for all rows of an item)
+      const int token = t * kTile + 16 * group0 + c;
+      const bool drafted = kTree && mask.j0 + token > -16;
+      const uint32_t seen = kTree && drafted ? mask.at(token) : 0u;
       tq::tmem_wait_ld();
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
@@ -594,7 +630,13 @@ __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int reps, in
         const float2 y = tq::unpack2(tq::fma2(tq::mul2(tq::pack2(e[2], e[3]), f2),
                                               tq::pack2(xn.z, xn.w), tq::pack2(lv.z, lv.w)));
         e[0] = x.x; e[1] = x.y; e[2] = y.x; e[3] = y.y;
-        mt = fmaxf(mt, fmaxf(fmaxf(x.x, x.y), fmaxf(y.x, y.y)));
+        if (kTree && drafted) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (!(seen >> (i + k) & 1u)) e[k] = -INFINITY;
+        }
+        mt = kTree ? fmaxf(mt, fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])))
+                   : fmaxf(mt, fmaxf(fmaxf(x.x, x.y), fmaxf(y.x, y.y)));
       }
       if (c + 16 >= 16 * groups) break;
       tmem_store<16>(dcol + c, d);
@@ -698,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
 
   // ---- the item: prefix items first (they are the long ones)
   int item = blockIdx.x;
-  const int npre = a.pre_splits * a.Hkv * a.row_tiles;
+  const int npre = kTree ? 0 : a.pre_splits * a.Hkv * a.row_tiles;
   const bool pre = item < npre;
   int split, h, b = 0, rt = 0;
   if (pre) {
@@ -707,12 +749,23 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
     split = item / (a.row_tiles * a.Hkv);
   } else {
     item -= npre;
+    if (kTree) {
+      rt = item % a.row_tiles;
+      item /= a.row_tiles;
+    }
     h = item % a.Hkv;
     b = item / a.Hkv % a.B;
     split = item / (a.Hkv * a.B);
   }
+#ifdef TQ_ROWS_TREE
+  const int rows = min(kTile, a.nodes * a.G - rt * kTile);
+  const int hist = clamp_len(a.seq_lens[b], a.max_len - a.nodes), len = hist + a.nodes;
+  const long long nrows = (long long)a.B * a.nodes * a.Hq;
+#else
   const int rows = pre ? min(kTile, a.B * a.G - rt * kTile) : a.G;
   const int len = pre ? clamp_len(*a.pre_len, a.max_pre) : clamp_len(a.seq_lens[b], a.max_len);
+  const long long nrows = (long long)a.B * a.Hq;
+#endif
   const int splits = pre ? a.pre_splits : a.own_splits;
   const int* list = a.list ? a.list + ((long long)b * a.Hkv + h) * a.max_blocks : nullptr;
   const int nblk = (len + 63) / 64;
@@ -735,6 +788,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
   }
   const int rec_split = pre ? split : a.pre_splits + split;
   auto qrow_of = [&](int r) -> long long {   // query row (b·Hq + head) of item row r
+#ifdef TQ_ROWS_TREE
+    const int nr = rt * kTile + r;
+    return ((long long)b * a.nodes + nr / a.G) * a.Hq + h * a.G + nr % a.G;
+#endif
     if (!pre) return (long long)b * a.Hq + h * a.G + r;
     const int rr = rt * kTile + r;
     return (long long)(rr / a.G) * a.Hq + h * a.G + rr % a.G;
@@ -742,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
   if (tiles <= 0) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (tid < rows) {
-      float* rec = a.rec + ((long long)rec_split * a.B * a.Hq + qrow_of(tid)) * kRecFloats;
+      float* rec = a.rec + (rec_split * nrows + qrow_of(tid)) * kRecFloats;
       rec[128] = -INFINITY;
       rec[129] = 0.f;
     }
@@ -802,7 +859,12 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
     tc_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.qfull);
-    const Stats z = softmax_tiles<kFine>(sm, tiles, reps, wl, hf, lane, f);
+    RowMask mask{0, 0};
+#ifdef TQ_ROWS_TREE
+    mask.j0 = t0 * kTile - hist;
+    if (r < rows) mask.seen = a.tree[b * a.tree_b + (rt * kTile + r) / a.G];
+#endif
+    const Stats z = softmax_tiles<kFine>(sm, tiles, reps, wl, hf, lane, f, mask);
     // ---- the item's record: lanes' parts through shared memory (the operands are done with),
     // replicas of a row added up with their log-sum-exp weights
     ok = ok && tq::named_sync_and(5, 256, z.ok);
@@ -824,7 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
       mine[129 + 2 * hf] = z.l;
       tq::named_sync(5, 256);
       for (int row = warp; row < rows; row += 8) {
-        float* rec = a.rec + ((long long)rec_split * a.B * a.Hq + qrow_of(row)) * kRecFloats;
+        float* rec = a.rec + (rec_split * nrows + qrow_of(row)) * kRecFloats;
         float m = -INFINITY;
         for (int k = 0; k < reps; ++k) m = fmaxf(m, part[(k * per + row) * kRecFloats + 128]);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1181,7 +1243,7 @@ void find_splits(Splits* x) {
   }
 }
 
-tq_status make_plan(const tq_attn_desc* d, long long pre_tiles, long long own_tiles, Plan* p) {
+tq_status check_desc(const tq_attn_desc* d, long long pre_tiles, long long own_tiles) {
   if (!d) return TQ_ERR_INVALID_ARG;
   if (d->head_dim != TQ_HEAD_DIM) return TQ_ERR_UNSUPPORTED;
   if (d->batch < 0 || d->q_heads <= 0 || d->kv_heads <= 0) return TQ_ERR_INVALID_ARG;
@@ -1194,6 +1256,20 @@ tq_status make_plan(const tq_attn_desc* d, long long pre_tiles, long long own_ti
   if (d->out_dtype != TQ_F16 && d->out_dtype != TQ_BF16) return TQ_ERR_UNSUPPORTED;
   if ((long long)d->batch * d->q_heads > (1 << 24)) return TQ_ERR_UNSUPPORTED;
   if (std::max(pre_tiles, own_tiles) > (1 << 23)) return TQ_ERR_UNSUPPORTED;   // 2^30 tokens: 32-bit token numbers
+  return TQ_OK;
+}
+
+// Where things lie in the workspace.
+void lay_out(const tq_attn_desc* d, Plan* p) {
+  p->fine = d->out_dtype == TQ_F16;
+  p->qf_off = (size_t)p->rows * (p->fine ? 1024 : 512);
+  p->rec_off = (p->qf_off + (size_t)p->rows * sizeof(float) + 255) / 256 * 256;
+  p->bytes = p->rec_off + (size_t)(p->pre_splits + p->own_splits) * p->rows * kRecFloats * sizeof(float);
+}
+
+tq_status make_plan(const tq_attn_desc* d, long long pre_tiles, long long own_tiles, Plan* p) {
+  const tq_status st = check_desc(d, pre_tiles, own_tiles);
+  if (st != TQ_OK) return st;
   p->G = d->q_heads / d->kv_heads;
   p->rows = d->batch * d->q_heads;
   p->row_tiles = (int)(((long long)d->batch * p->G + kTile - 1) / kTile);
@@ -1205,10 +1281,7 @@ tq_status make_plan(const tq_attn_desc* d, long long pre_tiles, long long own_ti
   p->pre_splits = want.sp;
   p->own_splits = want.so;
   if (pu * p->pre_splits + ou * p->own_splits > 0x7fffffffLL) return TQ_ERR_UNSUPPORTED;
-  p->fine = d->out_dtype == TQ_F16;
-  p->qf_off = (size_t)p->rows * (p->fine ? 1024 : 512);
-  p->rec_off = (p->qf_off + (size_t)p->rows * sizeof(float) + 255) / 256 * 256;
-  p->bytes = p->rec_off + (size_t)(p->pre_splits + p->own_splits) * p->rows * kRecFloats * sizeof(float);
+  lay_out(d, p);
   return TQ_OK;
 }
 
@@ -1354,7 +1427,7 @@ tq_status run(const tq_attn_desc* d, const Plan& p, const tq_codec* kc, const tq
                    stream);
   if (st != TQ_OK) return st;
   const unsigned items = (unsigned)((long long)p.pre_splits * a.Hkv * p.row_tiles +
-                                    (long long)p.own_splits * a.Hkv * a.B);
+                                    (long long)p.own_splits * a.Hkv * a.B * (kTree ? p.row_tiles : 1));
   switch (kc->ibits) {
     case 1: st = launch_k<1>(a, vc->ibits, p.fine, items, stream); break;
     case 2: st = launch_k<2>(a, vc->ibits, p.fine, items, stream); break;
@@ -1367,6 +1440,57 @@ tq_status run(const tq_attn_desc* d, const Plan& p, const tq_codec* kc, const tq
 }
 
 long long tiles_of(long long tokens) { return (tokens + kTile - 1) / kTile; }
+
+#ifdef TQ_ROWS_TREE
+
+// Splits as a prefix has them: row_tiles items of up to 128 rows for each (sequence, KV head).
+tq_status plan_tree(const tq_attn_desc* d, int nodes, Plan* p) {
+  if (!d || nodes <= 0) return TQ_ERR_INVALID_ARG;
+  const long long tiles = tiles_of(d->max_seq_len);
+  const tq_status st = check_desc(d, 0, tiles);
+  if (st != TQ_OK) return st;
+  if (nodes > TQ_TREE_NODES || (long long)d->batch * d->q_heads * nodes > (1 << 24)) return TQ_ERR_UNSUPPORTED;
+  if (d->max_seq_len < nodes) return TQ_ERR_INVALID_ARG;
+  p->G = d->q_heads / d->kv_heads;
+  p->rows = d->batch * d->q_heads * nodes;
+  p->row_tiles = (nodes * p->G + kTile - 1) / kTile;
+  const int n = tq_num_sms();
+  const long long units = (long long)d->batch * d->kv_heads * p->row_tiles;
+  Splits want{units, tiles, 0, 0, n > 0 ? n : 152, nodes * p->G <= kTile / 2, 0, 0};
+  find_splits(&want);
+  p->pre_splits = 0;
+  p->own_splits = want.sp;
+  if (units * p->own_splits > 0x7fffffffLL) return TQ_ERR_UNSUPPORTED;
+  lay_out(d, p);
+  return TQ_OK;
+}
+
+}  // namespace
+
+extern "C" size_t tq_tree_workspace_bytes(const tq_attn_desc* desc, int32_t n_nodes) {
+  Plan p;
+  return plan_tree(desc, n_nodes, &p) == TQ_OK ? p.bytes : 0;
+}
+
+extern "C" tq_status tq_tree_attention(const tq_attn_desc* desc, int32_t n_nodes, const tq_codec* kc,
+                                       const tq_codec* vc, const void* q, tq_prod_cache k,
+                                       tq_mse_cache v, const int32_t* seq_lens, const uint64_t* tree,
+                                       int64_t tree_stride_b, void* out, void* workspace,
+                                       size_t workspace_bytes, tq_stream_t stream) {
+  Plan p;
+  tq_status st = plan_tree(desc, n_nodes, &p);
+  if (st != TQ_OK) return st;
+  RowsArgs a{};
+  if (!tree || reinterpret_cast<uintptr_t>(tree) % 8 || tree_stride_b < 0) return TQ_ERR_INVALID_ARG;
+  if ((st = cache_side(k, v, desc->capacity, &a.own)) != TQ_OK) return st;
+  a.seq_lens = seq_lens;
+  a.tree = reinterpret_cast<const unsigned long long*>(tree);
+  a.tree_b = tree_stride_b;
+  a.nodes = n_nodes;
+  return run(desc, p, kc, vc, q, a, out, workspace, workspace_bytes, stream);
+}
+
+#else
 
 tq_status plan_sparse(const tq_attn_desc* d, int max_blocks, Plan* p) {
   if (max_blocks <= 0 || max_blocks > (1 << 24)) return TQ_ERR_INVALID_ARG;
@@ -1430,3 +1554,5 @@ extern "C" tq_status tq_prefix_attention(const tq_attn_desc* desc, const tq_code
   a.max_pre = prefix_max_len;
   return run(desc, p, kc, vc, q, a, out, workspace, workspace_bytes, stream);
 }
+
+#endif
