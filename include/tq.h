@@ -231,6 +231,47 @@ tq_status tq_rotary_apply(const tq_rotary* r, tq_dtype dtype, int32_t batch, int
                           const int32_t* positions, int64_t pos_stride_b, const tq_rotary_io* q,
                           const tq_rotary_io* k, tq_stream_t stream);
 
+/* ------------------------------------------------------------------ prompts on exact keys */
+
+typedef struct {
+  int32_t batch;          /* sequences */
+  int32_t q_heads;        /* Hq */
+  int32_t kv_heads;       /* Hkv; Hq % Hkv == 0 and Hq / Hkv ≤ TQ_MAX_GROUP */
+  int32_t head_dim;       /* must be 128 */
+  int32_t total_q;        /* rows of q and out */
+  int32_t total_k;        /* rows of k and v */
+  int32_t max_k_len;      /* keys of the longest sequence, or about that many: splits the work */
+  int32_t causal;
+  float softmax_scale;    /* ≤ 0 selects 1/√head_dim */
+  tq_dtype dtype;         /* of q, k, v and out: F16 or BF16 */
+} tq_prompt_desc;
+
+/* Attention of packed sequences over their exact keys and values, e.g. whole prompts before their keys
+ * and values are coded, chunks behind an uncoded history, or single new tokens:
+ *   out_i = Σ_j softmax_j(softmax_scale·⟨q_i, k_j⟩)·v_j,
+ * over all keys of query i's sequence or, where causal, keys j ≤ i + nk − nq of a sequence with nq
+ * queries and nk keys (the last query attends all of them).  A query without a key gives a zero row.
+ *   q, k, v  : device, vectors of 128 contiguous coordinates; vector (token t, head h) starts at
+ *              t*stride_t + h*stride_h (elements, multiples of 8 and ≥ 128; views of one fused
+ *              projection are fine), 16-byte aligned.  Query head h reads KV head h / G.
+ *   q_starts, k_starts : device int32[batch + 1], ascending: sequence b's queries are rows
+ *              q_starts[b] .. q_starts[b + 1] − 1 of q, its keys those of k and v (the same array for
+ *              whole prompts).  Rows of no sequence are neither read into anything nor written.
+ *              Entries outside [0, total] are clamped and TQ_FLAG_LEN_OVERFLOW is raised.
+ *   out      : device [total_q][q_heads][128], contiguous.
+ *   workspace: ≥ tq_prompt_workspace_bytes(desc) bytes, 256-byte aligned, no initialisation needed;
+ *              calls that share it must be serialised on one stream.
+ * Scores, sums and accumulators are 32 bits; softmax weights are rounded to the inputs' type and held
+ * to 2^-32 of a row's largest.  Infinite or NaN keys and values show in the rows that attend them only.
+ * total_q, total_k ≤ 2^28 and batch ≤ 2^20, else TQ_ERR_UNSUPPORTED. */
+size_t tq_prompt_workspace_bytes(const tq_prompt_desc* desc);
+tq_status tq_prompt_attention(const tq_prompt_desc* desc, const void* q, int64_t q_stride_t,
+                              int64_t q_stride_h, const void* k, int64_t k_stride_t,
+                              int64_t k_stride_h, const void* v, int64_t v_stride_t,
+                              int64_t v_stride_h, const int32_t* q_starts, const int32_t* k_starts,
+                              void* out, void* workspace, size_t workspace_bytes,
+                              tq_stream_t stream);
+
 /* ------------------------------------------------------------------ scores */
 
 /* Raw estimator ⟨q, k⟩ ≈ ‖x‖·⟨Π q, c[idx]⟩ + ‖r‖·√(π/2)/d·⟨S q, 2·sign − 1⟩ for every

@@ -65,6 +65,12 @@ class tq_attn_desc(ctypes.Structure):
                 ("out_dtype", ctypes.c_int)]
 
 
+class tq_prompt_desc(ctypes.Structure):
+    _fields_ = [("batch", _i32), ("q_heads", _i32), ("kv_heads", _i32), ("head_dim", _i32),
+                ("total_q", _i32), ("total_k", _i32), ("max_k_len", _i32), ("causal", _i32),
+                ("softmax_scale", ctypes.c_float), ("dtype", ctypes.c_int)]
+
+
 # name -> (restype, argtypes), mirroring include/tq.h
 SIGNATURES = {
     "tq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -128,6 +134,10 @@ SIGNATURES = {
     "tq_rotary_apply": (ctypes.c_int, [ctypes.POINTER(tq_rotary), ctypes.c_int, _i32, _i32, _vp, _i64,
                                        ctypes.POINTER(tq_rotary_io), ctypes.POINTER(tq_rotary_io),
                                        _vp]),
+    "tq_prompt_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(tq_prompt_desc)]),
+    "tq_prompt_attention": (ctypes.c_int, [ctypes.POINTER(tq_prompt_desc), _vp, _i64, _i64, _vp, _i64,
+                                           _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp,
+                                           ctypes.c_size_t, _vp]),
     "tq_tree_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(tq_attn_desc), _i32]),
     "tq_tree_attention": (ctypes.c_int, [ctypes.POINTER(tq_attn_desc), _i32, _vp, _vp, _vp,
                                          tq_prod_cache, tq_mse_cache, _vp, _vp, _i64, _vp, _vp,
@@ -337,6 +347,19 @@ def tq_rotary_apply(r: tq_rotary, dtype, batch, tokens, positions, pos_stride_b,
     """q, k: tq_rotary_io or None."""
     return load().tq_rotary_apply(ctypes.byref(r), dtype, batch, tokens, ptr(positions), pos_stride_b,
                                   q, k, ptr(stream))
+
+
+def tq_prompt_workspace_bytes(desc: tq_prompt_desc) -> int:
+    return load().tq_prompt_workspace_bytes(ctypes.byref(desc))
+
+
+def tq_prompt_attention(desc: tq_prompt_desc, q, q_stride_t, q_stride_h, k, k_stride_t, k_stride_h, v,
+                        v_stride_t, v_stride_h, q_starts, k_starts, out, workspace, workspace_bytes,
+                        stream) -> int:
+    return load().tq_prompt_attention(ctypes.byref(desc), ptr(q), q_stride_t, q_stride_h, ptr(k),
+                                      k_stride_t, k_stride_h, ptr(v), v_stride_t, v_stride_h,
+                                      ptr(q_starts), ptr(k_starts), ptr(out), ptr(workspace),
+                                      workspace_bytes, ptr(stream))
 
 
 def tq_tree_workspace_bytes(desc: tq_attn_desc, n_nodes: int) -> int:

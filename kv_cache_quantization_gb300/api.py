@@ -721,6 +721,49 @@ class Rotary:
         return q_out, k_out
 
 
+# ------------------------------------------------------------------ prompts on exact keys
+
+class PromptPlan:
+    """Attention of packed sequences over their exact keys and values (tq_prompt_attention), with its
+    workspace (allocated once, reused; calls of a plan are to be serialised on one stream).  total_q
+    and total_k are the rows of q and of k and v, which may hold more than the sequences; max_k_len is
+    about the keys of the longest sequence and splits the work."""
+
+    def __init__(self, batch, q_heads, kv_heads, total_q, total_k, max_k_len, causal=True, dtype=torch.bfloat16,
+                 softmax_scale=None, device="cuda"):
+        self.desc = B.tq_prompt_desc(batch, q_heads, kv_heads, HEAD_DIM, total_q, total_k, max_k_len, int(bool(causal)),
+                                     softmax_scale if softmax_scale else 0.0, tq_dtype(dtype))
+        self.nbytes = B.tq_prompt_workspace_bytes(self.desc)
+        if self.nbytes == 0:
+            raise ValueError("invalid prompt-attention configuration")
+        self.workspace = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        self.dtype, self.shape, self.k_shape = dtype, (total_q, q_heads, HEAD_DIM), (total_k, kv_heads, HEAD_DIM)
+        self.starts = (batch + 1,)
+
+    def new_out(self, device="cuda"):
+        return torch.empty(self.shape, dtype=self.dtype, device=device)
+
+    def run(self, q, k, v, q_starts, k_starts, out, stream=None):
+        """Attention of q [total_q, q_heads, 128] over k and v [total_k, kv_heads, 128] (views with any
+        strides of multiples of 8 elements), into out [total_q, q_heads, 128]; q_starts and k_starts,
+        int32 [batch + 1], are where each sequence's rows begin (the same for whole prompts)."""
+        d = _device(q, k, v, q_starts, k_starts, out, self.workspace)
+        sq, sk, sv = q.stride(), k.stride(), v.stride()
+        for t, s, shape, name in ((q, sq, self.shape, "q"), (k, sk, self.k_shape, "k"), (v, sv, self.k_shape, "v")):
+            if t.shape != shape or t.dtype != self.dtype or s[2] != 1:
+                raise ValueError(f"{name} must be {self.dtype} {list(shape)} with contiguous last dim, "
+                                 f"got {t.dtype} {list(t.shape)}")
+        _expect(q_starts, self.starts, torch.int32, "q_starts")
+        _expect(k_starts, self.starts, torch.int32, "k_starts")
+        _expect(out, self.shape, self.dtype, "out")
+        st = B.load().tq_prompt_attention(self.desc, q.data_ptr(), sq[0], sq[1], k.data_ptr(), sk[0], sk[1], v.data_ptr(),
+                                          sv[0], sv[1], q_starts.data_ptr(), k_starts.data_ptr(), out.data_ptr(),
+                                          self.workspace.data_ptr(), self.nbytes, _on(stream, d))
+        if st:
+            B.check(st, "tq_prompt_attention")
+        return out
+
+
 # ------------------------------------------------------------------ drafted tokens
 
 class TreePlan:

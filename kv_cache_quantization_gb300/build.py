@@ -18,7 +18,8 @@ LIB = os.path.join(LIBDIR, "libtq.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["host.cpp", "quantize.cu", "quantize_tc.cu", "attention.cu", "scores.cu",
            "decode_tc.cu", "decode_asym.cu", "decode_noalloc.cu", "store.cu", "quality.cu",
-           "rows_attn.cu", "rows_tree.cu", "blocks.cu", "rotary.cu", "moves.cu"]
+           "rows_attn.cu", "rows_tree.cu", "blocks.cu", "rotary.cu", "moves.cu",
+           "prompt.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,754 @@
+// Attention of packed prompts over exact keys and values (tq_prompt_attention), before they are coded.
+//
+// Mathematics.  Query i of a sequence with nq queries and nk keys attends keys j < lim(i), nk or
+// i + nk − nq + 1 where causal:  out_i = Σ_j w_j v_j / Σ_j w_j,  w_j = 2^(scale·log2(e)·q_i·k_j − ref),
+// in one pass over the keys with a running reference ref per row.  The reference follows the running
+// maximum only when that has grown by 2^8, so the accumulator is hardly ever scaled; weights are at
+// most 2^8 in bf16, and at most 2^15 in fp16, whose reference lies 2^7 below the maximum so that a
+// long tail of small weights stays above what fp16 holds (2^-32 of the largest).
+//
+// A CTA has two streams of 128 query rows × tiles of 128 keys.  The rows are `tokens` tokens × the
+// query heads of one KV head (a group of 7: 18 tokens, 126 rows), so that a tile of keys is read
+// once for the group and the causal border crosses few tiles.  With more rows than one stream holds,
+// the streams are two blocks of rows over the same keys; otherwise they are the same rows over
+// alternating tiles of keys, added up at the end.
+//   1 loader thread   TMA tiles of K and V (32 KB each, 128-byte swizzle) into a ring of 5
+//   1 issuer warp     S = Q·Kᵀ (128 × 128 × 128), O += P·V (P in TMEM over the scores it came from):
+//                     PV of job u, then QK of job u + 2, so that one stream's softmax runs beside
+//                     the other one's products
+//   8 softmax warps   a thread per row and stream: 128 scores in registers, maximum, powers,
+//                     weights back to TMEM
+//   2 guard warps     tiles of V that some row does not attend in full: rows past the sequence are
+//                     zeroed, and infinite or NaN values past the first row's border are taken out
+//                     (a weight of 0 would not hide them); rows that do attend those get them back
+//                     at the end
+// Where the rows are too few to fill the GPU the keys are split over CTAs, whose records (ref, Σw, O)
+// prompt_merge_kernel joins.
+//
+// Roundings: P to the inputs' type (half a step of it relative to each weight, as V itself is held),
+// the output once.  Scores, references, sums and accumulators are 32 bits.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "tc_ptx.h"
+#include "tq_internal.h"
+
+TQ_DEFINE_FLAGS(tq_take_flags_prompt)
+
+namespace {
+
+using tq::mbar_arrive;
+using tq::s32;
+using tq::tc_after;
+using tq::tc_before;
+
+constexpr int kTile = 128;              // query rows of a stream, keys of a tile
+constexpr int kStages = 5;
+constexpr int kTileBytes = kTile * TQ_D * 2, kHalfBytes = kTileBytes / 2;   // halves: 64 channels
+constexpr int kThreads = 384;
+// Registers: 168 at launch (384 threads), 256 × 216 + 128 × 72 = 384 × 168 after the split.
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 216, kRegsOther = 72;
+static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsLaunch, "register split");
+constexpr int kLoadWarp = 8, kIssueWarp = 9, kGuardWarp = 10;
+constexpr int kRecFloats = 132;         // O[128], ref, Σw, padding
+constexpr float kGrow = 8.f;
+constexpr int kMaxGuarded = 4;          // tiles that the borders of a CTA's rows can cross: at most 3
+constexpr int kSCol = 0, kOCol = 256;   // TMEM columns: scores (weights over them) and O of both streams
+
+struct PromptArgs {
+  const int* q_starts;
+  const int* k_starts;
+  int batch, total_q, total_k;
+  int G, Hq, causal;
+  int tokens;               // of a stream's rows
+  int per_cta;              // tokens of a CTA: `tokens` or twice that
+  int tiles, splits;        // CTAs along the queries, along the keys
+  float scale;              // softmax_scale · log2(e)
+  void* out;                // [total_q][Hq][128]
+  float* rec;               // [splits][total_q · Hq][kRecFloats]
+  const uint16_t* v;        // for values that the guard took out
+  long long v_t, v_h;
+};
+
+struct alignas(1024) Smem {
+  unsigned char q[2][kTileBytes];
+  unsigned char kv[kStages][kTileBytes];
+  uint64_t full[kStages], empty[kStages];
+  uint64_t gfull[kMaxGuarded];    // V of a guarded tile has arrived (`full`: it may be used)
+  uint64_t qfull, gdone, sfull[2], pfull[2], odone[2], drain;
+  uint32_t tmem;
+  int poison;               // the guard took values out
+};
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity) {
+  return __all_sync(0xffffffffu, tq::mbar_wait(bar, parity));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// One box of a tensor map: 64 channels of (heads, tokens) from (channel, head, token).
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int channel, int head, int token,
+                                         uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(s32(dst)), "l"(map), "r"(channel), "r"(head), "r"(token), "r"(s32(bar))
+      : "memory");
+}
+// Shared-memory matrix descriptor with 128-byte swizzle.
+__device__ __forceinline__ uint64_t swizzled_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return tq::smem_desc(saddr, lbo, sbo) | (2ull << 61);
+}
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  if constexpr (kBf16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+template <bool kBf16>
+__device__ __forceinline__ float widen(uint16_t u) {
+  if constexpr (kBf16) return __uint_as_float((uint32_t)u << 16);
+  return __half2float(__ushort_as_half(u));
+}
+// The 16-bit exponent field that infinities and NaN have.
+template <bool kBf16>
+__device__ __forceinline__ bool finite16(uint32_t u) {
+  constexpr uint32_t m = kBf16 ? 0x7f80u : 0x7c00u;
+  return (u & m) != m;
+}
+
+// What a CTA works on.
+struct Work {
+  int h;                    // KV head
+  int q0, k0, nq, nk;       // the sequence's first query and key, its numbers of them
+  int tok0, ntok;           // its tokens here
+  int split;
+  int j0, n;                // tiles of keys: first, number (of the stream with most)
+  int n0;                   // tiles of stream 0
+  bool pair;                // streams are two blocks of rows
+  int free_to;              // keys before this one are attended by every row here
+
+  __device__ __forceinline__ int limit(const PromptArgs& a, int token) const {
+    return a.causal ? min(max(token + nk - nq + 1, 0), nk) : nk;
+  }
+};
+
+// Tiles [first, first + count) of a stream, every `step`-th of the CTA's.
+struct Stream {
+  int count, step, tile0, tok0;
+};
+__device__ __forceinline__ Stream stream_of(const PromptArgs& a, const Work& w, int s) {
+  if (w.pair) return Stream{s ? w.n : w.n0, 1, w.j0, w.tok0 + s * a.tokens};
+  return Stream{s ? w.n / 2 : (w.n + 1) / 2, 2, w.j0 + s, w.tok0};
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void put_row(const PromptArgs& a, long long row, const float (&o)[32], float inv, int c) {
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * TQ_D + 32 * c);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    dst[i] = make_uint4(pack<kBf16>(o[8 * i] * inv, o[8 * i + 1] * inv), pack<kBf16>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                        pack<kBf16>(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack<kBf16>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+}
+
+// The softmax of one stream's tiles: a thread per row.
+template <bool kBf16>
+__device__ __forceinline__ bool softmax_stream(const PromptArgs& a, Smem& sm, const Work& w, int s, int warp4, int lane,
+                                               float& ref, float& sum) {
+  constexpr float kLift = kBf16 ? 0.f : 7.f;
+  const Stream st = stream_of(a, w, s);
+  const int r = 32 * warp4 + lane, token = st.tok0 + r / a.G;
+  const int lim = token < w.tok0 + w.ntok && r < a.tokens * a.G ? w.limit(a, token) : 0;
+  const uint32_t lanes = (uint32_t)(32 * warp4) << 16;
+  const uint32_t scol = lanes + kSCol + 128 * s, ocol = lanes + kOCol + 128 * s;
+  const tq::f32x2 scale2 = tq::pack2(a.scale, a.scale);
+  bool ok = true;
+  ref = -INFINITY;          // in the units of the exponent
+  sum = 0.f;
+  for (int i = 0; i < st.count; ++i) {
+    const int at = (st.tile0 + i * st.step) * kTile;
+    ok = ok && warp_wait(&sm.sfull[s], i & 1);
+    if (!ok) break;
+    tc_after();
+    float x[128];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tq::tmem_ld_32x32b_x32(scol + 32 * c, reinterpret_cast<uint32_t*>(x) + 32 * c);
+    tq::tmem_wait_ld();
+    if (at + kTile > w.free_to) {
+#pragma unroll
+      for (int c = 0; c < 128; ++c)
+        if (at + c >= lim) x[c] = -INFINITY;
+    }
+    float m[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+    for (int c = 4; c < 124; c += 8)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m[k] = max3(m[k], x[c + k], x[c + 4 + k]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = fmaxf(m[k], x[124 + k]);
+    const float top = max3(m[0], m[1], fmaxf(m[2], m[3])) * a.scale;
+    const float next = top - ref > kGrow + kLift ? top - kLift : ref;
+    if (i > 0 && __any_sync(0xffffffffu, next != ref)) {
+      ok = ok && warp_wait(&sm.odone[s], (i - 1) & 1);
+      if (!ok) break;
+      tc_after();
+      const float corr = ref == -INFINITY ? 0.f : ex2(ref - next);
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t o[32];
+        tq::tmem_ld_32x32b_x32(ocol + c, o);
+        tq::tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
+        tq::tmem_st_32x32b_x32(ocol + c, o);
+      }
+      sum *= corr;
+    }
+    ref = next;
+    const float off = ref == -INFINITY ? 0.f : -ref;
+    const tq::f32x2 off2 = tq::pack2(off, off);
+    tq::f32x2 l0 = tq::pack2(0.f, 0.f), l1 = l0;
+#pragma unroll
+    for (int c = 0; c < 128; c += 64) {
+      uint32_t p[32];
+#pragma unroll
+      for (int k = 0; k < 64; k += 4) {
+        const float2 u = tq::unpack2(tq::fma2(tq::pack2(x[c + k], x[c + k + 1]), scale2, off2));
+        const float2 v = tq::unpack2(tq::fma2(tq::pack2(x[c + k + 2], x[c + k + 3]), scale2, off2));
+        const float w0 = ex2(u.x), w1 = ex2(u.y), w2 = ex2(v.x), w3 = ex2(v.y);
+        l0 = tq::add2(l0, tq::pack2(w0, w1));
+        l1 = tq::add2(l1, tq::pack2(w2, w3));
+        p[k / 2] = pack<kBf16>(w0, w1);
+        p[k / 2 + 1] = pack<kBf16>(w2, w3);
+      }
+      tq::tmem_st_32x32b_x32(scol + c / 2, p);
+    }
+    tq::tmem_wait_st();
+    tc_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.pfull[s]);
+    const float2 l = tq::unpack2(tq::add2(l0, l1));
+    sum += l.x + l.y;
+  }
+  if (st.count > 0) ok = ok && warp_wait(&sm.odone[s], (st.count - 1) & 1);
+  return ok;
+}
+
+// Values that the guard took out, given back to a row that attends them: O and so the row become
+// what they are (infinite or NaN).  Rare and slow.
+template <bool kBf16>
+__device__ __noinline__ void give_back(const PromptArgs& a, const Work& w, int lim, int c, float* o) {
+  const int first = max(w.free_to, w.j0 * kTile), last = min(lim, (w.j0 + w.n) * kTile);
+  for (int j = first; j < last; ++j) {
+    const uint16_t* v = a.v + (long long)(w.k0 + j) * a.v_t + w.h * a.v_h + 32 * c;
+    for (int k = 0; k < 32; ++k)
+      if (!finite16<kBf16>(v[k])) o[k] += widen<kBf16>(v[k]);
+  }
+}
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+              const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PromptArgs a) {
+  extern __shared__ unsigned char smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+
+  // ---- the CTA's work.  Sequence b's CTAs are numbered from ⌊q_starts[b] / per_cta⌋ + b on, which
+  // leaves each enough numbers; the last tokens of a sequence, which attend most, come first
+  Work w;
+  w.split = blockIdx.x % a.splits;
+  const int rest = blockIdx.x / a.splits;
+  w.h = rest / a.tiles;
+  const int number = a.tiles - 1 - rest % a.tiles;
+  auto start = [&](const int* p, int b, int most) { return min(max(p[b], 0), most); };
+  if (blockIdx.x == 0) {
+    bool bad = false;
+    for (int i = tid; i < a.batch; i += kThreads) {
+      const int qa = a.q_starts[i], qb = a.q_starts[i + 1], ka = a.k_starts[i], kb = a.k_starts[i + 1];
+      bad |= qa < 0 || qb < qa || qb > a.total_q || ka < 0 || kb < ka || kb > a.total_k;
+    }
+    if (bad) atomicOr(&g_tq_flags, TQ_FLAG_LEN_OVERFLOW);
+  }
+  int b = -1;
+  for (int i = 0; i < a.batch; i += kThreads)
+    b += __syncthreads_count(i + tid < a.batch && start(a.q_starts, i + tid, a.total_q) / a.per_cta + i + tid <= number);
+  if (b < 0) return;        // before the first sequence
+  w.q0 = start(a.q_starts, b, a.total_q);
+  w.k0 = start(a.k_starts, b, a.total_k);
+  w.nq = max(start(a.q_starts, b + 1, a.total_q) - w.q0, 0);
+  w.nk = max(start(a.k_starts, b + 1, a.total_k) - w.k0, 0);
+  w.tok0 = (number - w.q0 / a.per_cta - b) * a.per_cta;
+  w.ntok = min(a.per_cta, w.nq - w.tok0);
+  if (w.ntok <= 0 || w.tok0 < 0) return;      // (below 0: starts that do not ascend)
+  w.pair = w.ntok > a.tokens;
+  w.free_to = w.limit(a, w.tok0);
+  const int total = (w.limit(a, w.tok0 + w.ntok - 1) + kTile - 1) / kTile;
+  w.j0 = (int)((long long)total * w.split / a.splits);
+  w.n = (int)((long long)total * (w.split + 1) / a.splits) - w.j0;
+  // (pairs: stream 0's tokens come first and attend fewer tiles)
+  w.n0 = w.pair ? min(max((w.limit(a, w.tok0 + a.tokens - 1) + kTile - 1) / kTile - w.j0, 0), w.n) : w.n;
+  // tiles that some row does not attend in full: the last `guarded` ones
+  const int guarded = min(w.n, max(0, w.j0 + w.n - w.free_to / kTile));
+
+  if (warp == kIssueWarp) tq::tmem_alloc(&sm.tmem, 512);
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      tq::mbar_init(&sm.full[i], 1);
+      tq::mbar_init(&sm.empty[i], 1);
+    }
+    tq::mbar_init(&sm.qfull, 1);
+    tq::mbar_init(&sm.gdone, 1);
+    for (int i = 0; i < kMaxGuarded; ++i) tq::mbar_init(&sm.gfull[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      tq::mbar_init(&sm.sfull[i], 1);
+      tq::mbar_init(&sm.pfull[i], 4);
+      tq::mbar_init(&sm.odone[i], 1);
+    }
+    tq::mbar_init(&sm.drain, 1);
+    sm.poison = 0;
+    tq::mbar_init_fence();
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  bool ok = sm.tmem == 0;   // all 512 columns: they begin at address 0
+  // Jobs u = 0, 1, ...: stream u & 1, tile u / 2 of both (pairs) or u.  The ring holds, in the order
+  // of the jobs' products, K of jobs 0 and 1, then for each job its V and K of job u + 2; a pair's
+  // second job shares the first one's tiles.
+  const int jobs = w.pair ? 2 * w.n : w.n;
+  auto tile_of = [&](int u) { return w.pair ? u >> 1 : u; };
+
+  if (warp < 8) {
+    // ================================================================ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int s = warp >> 2, warp4 = warp & 3, r = 32 * warp4 + lane;
+    float ref, sum;
+    ok = softmax_stream<kBf16>(a, sm, w, s, warp4, lane, ref, sum) && ok;
+    if (guarded) ok = ok && warp_wait(&sm.gdone, 0);
+    ok = tq::named_sync_and(1, 256, ok);
+    if (ok) {
+      tc_after();
+      const bool poison = guarded && *reinterpret_cast<volatile int*>(&sm.poison);
+      const Stream st = stream_of(a, w, s);
+      const int token = st.tok0 + r / a.G;
+      const bool there = r < a.tokens * a.G && token < w.tok0 + w.ntok;
+      const int lim = there ? w.limit(a, token) : 0;
+      const long long row = (long long)(w.q0 + token) * a.Hq + w.h * a.G + r % a.G;
+      const uint32_t ocol = ((uint32_t)(32 * warp4) << 16) + kOCol + 128 * s;
+      float* rec = a.rec + ((long long)w.split * a.total_q * a.Hq + row) * kRecFloats;
+      float* part = reinterpret_cast<float*>(sm.kv[0]) + r * kRecFloats;      // (the ring is done with)
+      float mine = 1.f, other = 0.f;       // factors of the two streams' parts of a row
+      if (!w.pair) {
+        if (s == 1) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float o[32];
+            if (st.count > 0) {
+              tq::tmem_ld_32x32b_x32(ocol + 32 * c, reinterpret_cast<uint32_t*>(o));
+              tq::tmem_wait_ld();
+            }
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<float4*>(part + 32 * c + k) =
+                  st.count > 0 ? make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          *reinterpret_cast<float2*>(part + 128) = make_float2(ref, sum);
+        }
+        tq::named_sync(1, 256);
+        if (s == 0) {
+          const float2 rs = *reinterpret_cast<const float2*>(part + 128);
+          const float both = fmaxf(ref, rs.x);
+          mine = ref == -INFINITY ? 0.f : ex2(ref - both);
+          other = rs.x == -INFINITY ? 0.f : ex2(rs.x - both);
+          sum = sum * mine + rs.y * other;     // (a NaN sum stays)
+          ref = both;
+        }
+      }
+      if (w.pair || s == 0) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float o[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0.f;
+          if (st.count > 0) {
+            tq::tmem_ld_32x32b_x32(ocol + 32 * c, reinterpret_cast<uint32_t*>(o));
+            tq::tmem_wait_ld();
+          }
+          if (!w.pair) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(part + 32 * c + k);
+              o[k] = fmaf(o[k], mine, x.x * other);
+              o[k + 1] = fmaf(o[k + 1], mine, x.y * other);
+              o[k + 2] = fmaf(o[k + 2], mine, x.z * other);
+              o[k + 3] = fmaf(o[k + 3], mine, x.w * other);
+            }
+          }
+          if (poison && there) {
+            float p[32];
+            for (int k = 0; k < 32; ++k) p[k] = o[k];
+            give_back<kBf16>(a, w, lim, c, p);
+            for (int k = 0; k < 32; ++k) o[k] = p[k];
+          }
+          if (there) {
+            if (a.splits > 1) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 4)
+                *reinterpret_cast<float4*>(rec + 32 * c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            } else {
+              put_row<kBf16>(a, row, o, inv, c);
+            }
+          }
+        }
+        if (there && a.splits > 1) *reinterpret_cast<float2*>(rec + 128) = make_float2(ref, sum);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == kLoadWarp) {
+      // ============================================================== loader
+      if (lane == 0 && w.n > 0) {
+        int at = 0;
+        auto load = [&](const CUtensorMap* map, int tile, int guard) {
+          const int st = at % kStages;
+          if (at >= kStages && !(ok = ok && tq::mbar_wait(&sm.empty[st], (at / kStages - 1) & 1))) return;
+          uint64_t* bar = guard >= 0 ? &sm.gfull[guard] : &sm.full[st];
+          tq::mbar_expect_tx(bar, kTileBytes);
+          for (int c = 0; c < 2; ++c)
+            tma_load(sm.kv[st] + c * kHalfBytes, map, 64 * c, w.h, w.k0 + (w.j0 + tile) * kTile, bar);
+          ++at;
+        };
+        const int blocks = w.pair ? 2 : 1, bytes = a.tokens * a.G * 128;
+        tq::mbar_expect_tx(&sm.qfull, blocks * 2 * bytes);
+        for (int s = 0; s < blocks; ++s)
+          for (int c = 0; c < 2; ++c)
+            tma_load(sm.q[s] + c * kHalfBytes, &qmap, 64 * c, w.h * a.G, w.q0 + w.tok0 + s * a.tokens, &sm.qfull);
+        const int ahead = w.pair ? 1 : 2;          // tiles of K before the first V
+        for (int t = 0; t < min(ahead, w.n) && ok; ++t) load(&kmap, t, -1);
+        for (int t = 0; t < w.n && ok; ++t) {
+          load(&vmap, t, t - (w.n - guarded));
+          if (t + ahead < w.n && ok) load(&kmap, t + ahead, -1);
+        }
+        // copies in flight end before the block does, whatever happened
+        // (a guarded tile's `full` follows its copy)
+        ok = tq::mbar_wait(&sm.qfull, 0) && ok;
+        for (int i = max(0, at - kStages); i < at; ++i) ok = tq::mbar_wait(&sm.full[i % kStages], (i / kStages) & 1) && ok;
+      }
+    } else if (warp == kIssueWarp) {
+      // ============================================================== issuer
+      constexpr uint32_t kType = kBf16 ? (1u << 7) | (1u << 10) : 0u;
+      constexpr uint32_t kIdescS = tq::idesc_f16(128, 128) | kType;
+      constexpr uint32_t kIdescO = kIdescS | (1u << 16);       // B (values) is N-major
+      const uint64_t qdesc = swizzled_desc(s32(sm.q[0]), 16, 1024);
+      const uint64_t kdesc = swizzled_desc(s32(sm.kv[0]), 16, 1024);
+      const uint64_t vdesc = swizzled_desc(s32(sm.kv[0]), kHalfBytes, 1024);
+      int at = 0, kst = 0, vst = 0;                // ring position, stages in use
+      auto wait = [&](uint64_t* bar, unsigned parity) { return ok = ok && warp_wait(bar, parity); };
+      auto next = [&](int& st) {                   // the ring's next tile
+        st = at % kStages;
+        if (!wait(&sm.full[st], (at / kStages) & 1)) return;
+        ++at;
+      };
+      auto live = [&](int u) { return u < jobs && (!w.pair || (u & 1) || tile_of(u) < w.n0); };
+      auto score = [&](int u) {
+        if (u >= jobs) return;
+        const int s = u & 1;
+        if (!w.pair || !s) next(kst);
+        if (!ok) return;
+        tc_after();
+        if (elect_one()) {
+          if (live(u)) {
+            const uint64_t q = qdesc + (w.pair && s ? kTileBytes >> 4 : 0), k = kdesc + kst * (kTileBytes >> 4);
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+              const int step = (ks >> 2) * (kHalfBytes >> 4) + (ks & 3) * 2;
+              tq::mma_ss(kSCol + 128 * s, q + step, k + step, kIdescS, ks > 0);
+            }
+            tq::mma_commit(&sm.sfull[s]);
+          }
+          if (!w.pair || s) tq::mma_commit(&sm.empty[kst]);
+        }
+        __syncwarp();
+      };
+      auto weigh = [&](int u) {
+        const int s = u & 1, t = tile_of(u);
+        if (!w.pair || !s) next(vst);
+        if (!ok) return;
+        if (live(u)) {
+          const int i = w.pair ? t : t >> 1;
+          if (!wait(&sm.pfull[s], i & 1)) return;
+          tc_after();
+          if (elect_one()) {
+            const uint64_t v = vdesc + vst * (kTileBytes >> 4);
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              tq::mma_ts(kOCol + 128 * s, kSCol + 128 * s + 8 * ks, v + ks * (2048 >> 4), kIdescO, i > 0 || ks > 0);
+            tq::mma_commit(&sm.odone[s]);
+          }
+          __syncwarp();
+        }
+        if (!w.pair || s) {
+          if (elect_one()) tq::mma_commit(&sm.empty[vst]);
+          __syncwarp();
+        }
+      };
+      if (w.n > 0) wait(&sm.qfull, 0);
+      score(0);
+      score(1);
+      for (int u = 0; u < jobs && ok; ++u) {
+        weigh(u);
+        if (ok) score(u + 2);
+      }
+      // whatever was issued has ended before the tensor memory is given back
+      if (elect_one()) tq::mma_commit(&sm.drain);
+      __syncwarp();
+      if (!tq::mbar_wait(&sm.drain, 0)) ok = false;
+    } else {
+      // ============================================================== guard
+      const int id = tid - 32 * kGuardWarp;        // of 64
+      for (int g = 0; g < guarded && ok; ++g) {
+        const int t = w.n - guarded + g;
+        const int at = w.pair ? 2 * t + 1 : min(2 * t + 2, 2 * w.n - 1);     // its V's place in the ring
+        const int st = at % kStages;
+        // (the guarded tiles are the last ones: a limit that grows with the tiles before them)
+        ok = __all_sync(0xffffffffu, tq::mbar_wait(&sm.gfull[g], 0, 20000000ull + 20000ull * w.n));
+        if (!tq::named_sync_and(2, 64, ok)) break;
+        const int key0 = (w.j0 + t) * kTile;
+        bool bad = false;
+        for (int i = id; i < 2 * kTile; i += 64) {           // (row, half of the channels)
+          const int j = i & (kTile - 1);
+          uint4* row = reinterpret_cast<uint4*>(sm.kv[st] + (i >> 7) * kHalfBytes + j * 128);
+          if (key0 + j >= w.nk) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) row[c] = make_uint4(0, 0, 0, 0);
+          } else if (key0 + j >= w.free_to) {
+            uint32_t* word = reinterpret_cast<uint32_t*>(row);
+            for (int c = 0; c < 32; ++c) {
+              uint32_t u = word[(c + id) & 31];
+              const bool lo = finite16<kBf16>(u), hi = finite16<kBf16>(u >> 16);
+              if (lo && hi) continue;
+              bad = true;
+              word[(c + id) & 31] = (lo ? u & 0xffffu : 0u) | (hi ? u & 0xffff0000u : 0u);
+            }
+          }
+        }
+        if (bad) *reinterpret_cast<volatile int*>(&sm.poison) = 1;
+        tq::fence_async_smem();
+        tq::named_sync(2, 64);
+        if (id == 0) {
+          mbar_arrive(&sm.full[st]);
+          if (g == guarded - 1) mbar_arrive(&sm.gdone);
+        }
+      }
+    }
+  }
+  if (!ok && lane == 0) atomicOr(&g_tq_flags, TQ_FLAG_TIMEOUT);
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == kIssueWarp) tq::tmem_dealloc(sm.tmem, 512);
+}
+
+// Records of a row joined with their log-sum-exp weights: a warp per row.
+template <bool kBf16>
+__global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptArgs a) {
+  const long long rows = (long long)a.total_q * a.Hq, row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  // rows of no sequence are left as they are
+  if (row >= rows || row / a.Hq < a.q_starts[0] || row / a.Hq >= a.q_starts[a.batch]) return;
+  const float* rec = a.rec + row * kRecFloats;
+  float m = -INFINITY;
+  for (int s = 0; s < a.splits; ++s) {
+    const float2 ml = *reinterpret_cast<const float2*>(rec + s * rows * kRecFloats + 128);
+    if (ml.y != 0.f) m = fmaxf(m, ml.x);
+  }
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s) {
+    const float* r = rec + s * rows * kRecFloats;
+    const float2 ml = *reinterpret_cast<const float2*>(r + 128);
+    const float4 x = *reinterpret_cast<const float4*>(r + 4 * lane);
+    if (ml.y == 0.f) continue;             // (attends nothing there)
+    const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
+    l = fmaf(ml.y, f, l);
+    o.x = fmaf(x.x, f, o.x);
+    o.y = fmaf(x.y, f, o.y);
+    o.z = fmaf(x.z, f, o.z);
+    o.w = fmaf(x.w, f, o.w);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * TQ_D) + lane;
+  *dst = make_uint2(pack<kBf16>(o.x * inv, o.y * inv), pack<kBf16>(o.z * inv, o.w * inv));
+}
+
+// ---------------------------------------------------------------- host
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+struct Plan {
+  int G, tokens, per_cta, tiles, splits;
+  size_t bytes;
+};
+
+tq_status make_plan(const tq_prompt_desc* d, Plan* p) {
+  if (!d) return TQ_ERR_INVALID_ARG;
+  if (d->head_dim != TQ_HEAD_DIM) return TQ_ERR_UNSUPPORTED;
+  if (d->batch < 0 || d->q_heads <= 0 || d->kv_heads <= 0 || d->q_heads % d->kv_heads) return TQ_ERR_INVALID_ARG;
+  if (d->q_heads / d->kv_heads > TQ_MAX_GROUP) return TQ_ERR_UNSUPPORTED;
+  if (d->total_q < 0 || d->total_k < 0 || d->max_k_len < 0) return TQ_ERR_INVALID_ARG;
+  if (d->dtype != TQ_F16 && d->dtype != TQ_BF16) return TQ_ERR_UNSUPPORTED;
+  if (d->total_q > (1 << 28) || d->total_k > (1 << 28) || d->batch > (1 << 20)) return TQ_ERR_UNSUPPORTED;
+  p->G = d->q_heads / d->kv_heads;
+  p->tokens = kTile / p->G;
+  const int n = tq_num_sms();
+  const long long sms = n > 0 ? n : 152;
+  auto ctas = [&](long long per) { return (d->total_q / per + d->batch) * d->kv_heads; };
+  // Two blocks of rows a CTA where that fills the GPU, else one.
+  p->per_cta = ctas(2 * p->tokens) >= sms ? 2 * p->tokens : p->tokens;
+  p->tiles = (int)(ctas(p->per_cta) / d->kv_heads);
+  const long long units = std::max<long long>(ctas(p->per_cta), 1);
+  // Keys split so that the CTAs fill the GPU once, each with at least four tiles.
+  const long long key_tiles = ((long long)d->max_k_len + kTile - 1) / kTile;
+  p->splits = (int)std::max<long long>(1, std::min<long long>(sms / units, key_tiles / 4));
+  if (units * p->splits > 0x7fffffffLL) return TQ_ERR_UNSUPPORTED;
+  p->bytes = 256;
+  if (p->splits > 1) p->bytes += (size_t)p->splits * d->total_q * d->q_heads * kRecFloats * sizeof(float);
+  return TQ_OK;
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder() {
+  static EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+// Vectors [tokens][heads][128] in boxes of 64 channels × `box_heads` heads × `box_tokens` tokens.
+bool encode(CUtensorMap* map, bool bf16, const void* x, int tokens, int heads, int64_t stride_t, int64_t stride_h,
+            int box_heads, int box_tokens) {
+  EncodeFn fn = encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {TQ_D, (cuuint64_t)heads, (cuuint64_t)std::max(tokens, 1)};
+  // (a dimension of one has no stride of its own)
+  const cuuint64_t strides[2] = {(cuuint64_t)(heads > 1 ? stride_h : TQ_D) * 2, (cuuint64_t)(tokens > 1 ? stride_t : TQ_D) * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens}, one[3] = {1, 1, 1};
+  return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(x), dims,
+            strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Vectors at multiples of 16 bytes, at distances below 2^40 bytes.
+bool good(const void* x, int tokens, int heads, int64_t stride_t, int64_t stride_h) {
+  if (tokens == 0) return true;
+  auto bad = [](int n, int64_t s) { return n > 1 && (s < TQ_D || s % 8 || s >= (1ll << 39)); };
+  return x && aligned16(x) && !bad(tokens, stride_t) && !bad(heads, stride_h);
+}
+
+template <bool kBf16>
+tq_status launch(const CUtensorMap (&maps)[3], const PromptArgs& a, long long grid, cudaStream_t stream) {
+  constexpr int smem = (int)sizeof(Smem) + 1024;
+  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+  static bool configured[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return TQ_ERR_CUDA;
+  if (!configured[dev]) {
+    if (cudaFuncSetAttribute(prompt_kernel<kBf16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      return TQ_ERR_CUDA;
+    // the warpgroups' shares add up to what the block is launched with: more would wait forever
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, prompt_kernel<kBf16>) != cudaSuccess) return TQ_ERR_CUDA;
+    if (fa.numRegs != kRegsLaunch) return TQ_ERR_UNSUPPORTED;
+    configured[dev] = true;
+  }
+  prompt_kernel<kBf16><<<(unsigned)grid, kThreads, smem, stream>>>(maps[0], maps[1], maps[2], a);
+  if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
+  if (a.splits > 1) {
+    const long long rows = (long long)a.total_q * a.Hq;
+    prompt_merge_kernel<kBf16><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(a);
+  }
+  return tq_cuda_status(cudaGetLastError());
+}
+
+}  // namespace
+
+extern "C" size_t tq_prompt_workspace_bytes(const tq_prompt_desc* desc) {
+  Plan p;
+  return make_plan(desc, &p) == TQ_OK ? p.bytes : 0;
+}
+
+extern "C" tq_status tq_prompt_attention(const tq_prompt_desc* d, const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                                         const void* k, int64_t k_stride_t, int64_t k_stride_h, const void* v,
+                                         int64_t v_stride_t, int64_t v_stride_h, const int32_t* q_starts,
+                                         const int32_t* k_starts, void* out, void* workspace, size_t workspace_bytes,
+                                         tq_stream_t stream) {
+  Plan p;
+  tq_status st = make_plan(d, &p);
+  if (st != TQ_OK) return st;
+  if (d->batch == 0 || d->total_q == 0) return TQ_OK;
+  if (!good(q, d->total_q, d->q_heads, q_stride_t, q_stride_h) || !good(k, d->total_k, d->kv_heads, k_stride_t, k_stride_h) ||
+      !good(v, d->total_k, d->kv_heads, v_stride_t, v_stride_h))
+    return TQ_ERR_INVALID_ARG;
+  if (!q_starts || !k_starts || !out || !aligned16(out) || reinterpret_cast<uintptr_t>(q_starts) % 4 ||
+      reinterpret_cast<uintptr_t>(k_starts) % 4)
+    return TQ_ERR_INVALID_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < p.bytes) return TQ_ERR_INVALID_ARG;
+  const bool bf16 = d->dtype == TQ_BF16;
+  CUtensorMap maps[3];
+  // (without keys nothing is loaded; the maps need some address all the same)
+  if (!encode(&maps[0], bf16, q, d->total_q, d->q_heads, q_stride_t, q_stride_h, p.G, p.tokens) ||
+      !encode(&maps[1], bf16, d->total_k ? k : q, d->total_k, d->kv_heads, k_stride_t, k_stride_h, 1, kTile) ||
+      !encode(&maps[2], bf16, d->total_k ? v : q, d->total_k, d->kv_heads, v_stride_t, v_stride_h, 1, kTile))
+    return TQ_ERR_CUDA;
+  PromptArgs a{};
+  a.q_starts = q_starts;
+  a.k_starts = k_starts;
+  a.batch = d->batch;
+  a.total_q = d->total_q;
+  a.total_k = d->total_k;
+  a.G = p.G;
+  a.Hq = d->q_heads;
+  a.causal = d->causal != 0;
+  a.tokens = p.tokens;
+  a.per_cta = p.per_cta;
+  a.tiles = p.tiles;
+  a.splits = p.splits;
+  a.scale = (d->softmax_scale > 0.f ? d->softmax_scale : 1.0f / sqrtf((float)TQ_D)) * 1.4426950408889634f;
+  a.out = out;
+  a.rec = static_cast<float*>(workspace);
+  a.v = static_cast<const uint16_t*>(v);
+  a.v_t = v_stride_t;
+  a.v_h = v_stride_h;
+  const long long grid = (long long)p.tiles * d->kv_heads * p.splits;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return bf16 ? launch<true>(maps, a, grid, s) : launch<false>(maps, a, grid, s);
+}

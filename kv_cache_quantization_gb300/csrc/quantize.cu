@@ -506,7 +506,7 @@ extern "C" tq_status tq_device_status(uint32_t* flags) {
   unsigned int (*const words[])() = {
       tq_take_flags_quantize, tq_take_flags_attention, tq_take_flags_quantize_tc, tq_take_flags_decode_tc,
       tq_take_flags_decode_asym, tq_take_flags_store, tq_take_flags_rows, tq_take_flags_blocks,
-      tq_take_flags_moves, tq_take_flags_tree};
+      tq_take_flags_moves, tq_take_flags_tree, tq_take_flags_prompt};
   uint32_t all = 0;
   bool bad = false;
   for (auto take : words) {

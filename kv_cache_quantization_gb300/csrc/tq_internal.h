@@ -100,6 +100,7 @@ unsigned int tq_take_flags_rows();
 unsigned int tq_take_flags_blocks();
 unsigned int tq_take_flags_moves();
 unsigned int tq_take_flags_tree();
+unsigned int tq_take_flags_prompt();
 
 static inline tq_status tq_cuda_status(cudaError_t e) {
   return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;

@@ -179,3 +179,45 @@ def test_keep_tokens_refuses():
         call(UNSUPPORTED, **kw)
     call(B.TQ_OK, batch=0)
     call(B.TQ_OK, most=0)
+
+
+# ------------------------------------------------------------------ prompts
+
+def prompt(batch=2, hq=28, hkv=4, d=128, tq=1000, tk=2000, longest=900, causal=1, dtype=B.TQ_BF16):
+    return B.tq_prompt_desc(batch, hq, hkv, d, tq, tk, longest, causal, 0.0, dtype)
+
+
+PROMPT_BAD = [
+    (prompt(d=64), UNSUPPORTED), (prompt(batch=-1), INVALID), (prompt(hkv=0), INVALID), (prompt(hkv=5), INVALID), (prompt(hq=0), INVALID),
+    (prompt(hq=36), UNSUPPORTED), (prompt(tq=-1), INVALID), (prompt(tk=-1), INVALID), (prompt(longest=-1), INVALID),
+    (prompt(dtype=B.TQ_F32), UNSUPPORTED), (prompt(dtype=9), UNSUPPORTED), (prompt(tq=(1 << 28) + 1), UNSUPPORTED),
+    (prompt(tk=(1 << 28) + 1), UNSUPPORTED), (prompt(batch=(1 << 20) + 1), UNSUPPORTED)]
+
+
+@pytest.mark.parametrize("d,status", PROMPT_BAD)
+def test_prompt_bad_descriptors(d, status):
+    assert B.tq_prompt_workspace_bytes(d) == 0
+    assert B.tq_prompt_attention(d, OK16, 3584, 128, OK16, 512, 128, OK16, 512, 128, OK16, OK16, OK16, OK256, 1 << 40, None) == status
+
+
+def test_prompt_refuses():
+    def call(status, d=prompt(), q=OK16, qt=3584, qh=128, k=OK16, kt=512, kh=128, v=OK16, vt=512, vh=128, qs=OK16, ks=OK16, out=OK16,
+             ws=OK256, n=1 << 40):
+        assert B.tq_prompt_attention(d, q, qt, qh, k, kt, kh, v, vt, vh, qs, ks, out, ws, n, None) == status
+
+    for kw in (dict(q=0), dict(k=0), dict(v=0), dict(q=OK16 + 8), dict(k=OK16 + 2), dict(v=OK16 + 4), dict(qt=3588), dict(qh=0), dict(kt=-512),
+               dict(kh=132), dict(vt=64), dict(vh=-128), dict(qt=1 << 39), dict(qs=0), dict(ks=0), dict(qs=OK16 + 2), dict(ks=OK16 + 1),
+               dict(out=0), dict(out=OK16 + 8), dict(ws=0), dict(ws=OK256 + 16), dict(n=0)):
+        call(INVALID, **kw)
+    call(B.TQ_OK, d=prompt(batch=0))
+    call(B.TQ_OK, d=prompt(tq=0))
+
+
+def test_prompt_workspaces():
+    """Records for single tokens behind long histories, whose keys are split; none for whole prompts."""
+    small = B.tq_prompt_workspace_bytes(prompt(batch=1, tq=1, tk=65536, longest=65536))
+    assert small > B.tq_prompt_workspace_bytes(prompt(batch=1, tq=65536, tk=65536, longest=65536)) > 0
+    with pytest.raises(ValueError):
+        api.PromptPlan(1, 28, 4, 10, 10, 10, dtype=torch.float32, device="cpu")
+    with pytest.raises(ValueError):
+        api.PromptPlan(1, 27, 4, 10, 10, 10, device="cpu")
