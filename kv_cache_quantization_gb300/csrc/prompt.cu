@@ -13,12 +13,11 @@
 // the streams are two blocks of rows over the same keys; otherwise they are the same rows over
 // alternating tiles of keys, added up at the end.
 //   1 loader thread   TMA tiles of K and V (32 KB each, 128-byte swizzle) into a ring of 5
-//   1 issuer warp     S = Q·Kᵀ (128 × 128 × 128), O += P·V (P in TMEM over the scores it came from):
-//                     PV of job u, then QK of job u + 2, so that one stream's softmax runs beside
-//                     the other one's products
-//   8 softmax warps   a thread per row and stream: 128 scores in registers, maximum, powers,
+//   2 issuer warps    S = Q·Kᵀ (128 × 128 × 128) and O += P·V (P in TMEM over the scores it came from)
+//                     of a stream each, so that one's softmax runs beside the other one's products
+//   16 softmax warps  two threads per row and stream: 64 scores each in registers, maximum, powers,
 //                     weights back to TMEM
-//   2 guard warps     tiles of V that some row does not attend in full: rows past the sequence are
+//   1 guard warp      tiles of V that some row does not attend in full: rows past the sequence are
 //                     zeroed, and infinite or NaN values past the first row's border are taken out
 //                     (a weight of 0 would not hide them); rows that do attend those get them back
 //                     at the end
@@ -49,11 +48,10 @@ using tq::tc_before;
 constexpr int kTile = 128;              // query rows of a stream, keys of a tile
 constexpr int kStages = 5;
 constexpr int kTileBytes = kTile * TQ_D * 2, kHalfBytes = kTileBytes / 2;   // halves: 64 channels
-constexpr int kThreads = 384;
-// Registers: 168 at launch (384 threads), 256 × 216 + 128 × 72 = 384 × 168 after the split.
-constexpr int kRegsLaunch = 168, kRegsSoftmax = 216, kRegsOther = 72;
-static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsLaunch, "register split");
-constexpr int kLoadWarp = 8, kIssueWarp = 9, kGuardWarp = 10;
+constexpr int kThreads = 640;
+constexpr int kLoadWarp = 16, kIssueWarp = 17, kGuardWarp = 19;      // (an issuer per stream)
+// named barriers
+constexpr int kBarSoftmax = 1, kBarTurn = 2, kBarRows = 4;      // + stream; + 4·stream + lane group
 constexpr int kRecFloats = 132;         // O[128], ref, Σw, padding
 constexpr float kGrow = 8.f;
 constexpr int kMaxGuarded = 4;          // tiles that the borders of a CTA's rows can cross: at most 3
@@ -82,6 +80,7 @@ struct alignas(1024) Smem {
   uint64_t qfull, gdone, sfull[2], pfull[2], odone[2], drain;
   uint32_t tmem;
   int poison;               // the guard took values out
+  float top[2][kTile];      // [stream]: maxima that a row's two threads exchange
 };
 
 __device__ __forceinline__ bool elect_one() {
@@ -96,6 +95,16 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// 16 consecutive TMEM columns of the thread's lane.
+__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -129,11 +138,11 @@ __device__ __forceinline__ float widen(uint16_t u) {
   if constexpr (kBf16) return __uint_as_float((uint32_t)u << 16);
   return __half2float(__ushort_as_half(u));
 }
-// The 16-bit exponent field that infinities and NaN have.
+// The top bit of each half of a pair that is infinite or NaN (its exponent is all ones).
 template <bool kBf16>
-__device__ __forceinline__ bool finite16(uint32_t u) {
-  constexpr uint32_t m = kBf16 ? 0x7f80u : 0x7c00u;
-  return (u & m) != m;
+__device__ __forceinline__ uint32_t special2(uint32_t u) {
+  constexpr uint32_t m = kBf16 ? 0x7f807f80u : 0x7c007c00u, one = kBf16 ? 0x00800080u : 0x04000400u;
+  return ((u & m) + one) & 0x80008000u;
 }
 
 // What a CTA works on.
@@ -162,85 +171,113 @@ __device__ __forceinline__ Stream stream_of(const PromptArgs& a, const Work& w, 
 }
 
 template <bool kBf16>
-__device__ __forceinline__ void put_row(const PromptArgs& a, long long row, const float (&o)[32], float inv, int c) {
-  uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * TQ_D + 32 * c);
+__device__ __forceinline__ void put16(const PromptArgs& a, long long row, const float (&o)[16], float inv, int c) {
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * TQ_D + c);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 2; ++i)
     dst[i] = make_uint4(pack<kBf16>(o[8 * i] * inv, o[8 * i + 1] * inv), pack<kBf16>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
                         pack<kBf16>(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack<kBf16>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
 }
 
-// The softmax of one stream's tiles: a thread per row.
+// The softmax of one stream's tiles: a row's two threads take 64 scores of a tile each, 32 at a time,
+// once for the maximum and once for the weights (which lie over the first half of the thread's own
+// scores).  The loops are rolled and the scores stay in TMEM between the passes, because the roles'
+// code has to fit the instruction caches of an SM side by side: with 64 scores in registers and
+// everything unrolled, the maximum of 64 scores took 550 cycles instead of 50.  The two threads agree
+// on the reference, which the products of both halves share, only where one of their warps' rows
+// moves it (one barrier that ORs a predicate tells).
 template <bool kBf16>
-__device__ __forceinline__ bool softmax_stream(const PromptArgs& a, Smem& sm, const Work& w, int s, int warp4, int lane,
+__device__ __forceinline__ bool softmax_stream(const PromptArgs& a, Smem& sm, const Work& w, int s, int hf, int warp4, int lane,
                                                float& ref, float& sum) {
   constexpr float kLift = kBf16 ? 0.f : 7.f;
   const Stream st = stream_of(a, w, s);
-  const int r = 32 * warp4 + lane, token = st.tok0 + r / a.G;
+  const int r = 32 * warp4 + lane, token = st.tok0 + r / a.G, bar = kBarRows + 4 * s + warp4;
   const int lim = token < w.tok0 + w.ntok && r < a.tokens * a.G ? w.limit(a, token) : 0;
   const uint32_t lanes = (uint32_t)(32 * warp4) << 16;
-  const uint32_t scol = lanes + kSCol + 128 * s, ocol = lanes + kOCol + 128 * s;
+  const uint32_t scol = lanes + kSCol + 128 * s + 64 * hf, ocol = lanes + kOCol + 128 * s + 64 * hf;
   const tq::f32x2 scale2 = tq::pack2(a.scale, a.scale);
   bool ok = true;
   ref = -INFINITY;          // in the units of the exponent
   sum = 0.f;
+#pragma unroll 1
   for (int i = 0; i < st.count; ++i) {
     const int at = (st.tile0 + i * st.step) * kTile;
     ok = ok && warp_wait(&sm.sfull[s], i & 1);
-    if (!ok) break;
     tc_after();
-    float x[128];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) tq::tmem_ld_32x32b_x32(scol + 32 * c, reinterpret_cast<uint32_t*>(x) + 32 * c);
-    tq::tmem_wait_ld();
     if (at + kTile > w.free_to) {
-#pragma unroll
-      for (int c = 0; c < 128; ++c)
-        if (at + c >= lim) x[c] = -INFINITY;
-    }
-    float m[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-    for (int c = 4; c < 124; c += 8)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) m[k] = max3(m[k], x[c + k], x[c + 4 + k]);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) m[k] = fmaxf(m[k], x[124 + k]);
-    const float top = max3(m[0], m[1], fmaxf(m[2], m[3])) * a.scale;
-    const float next = top - ref > kGrow + kLift ? top - kLift : ref;
-    if (i > 0 && __any_sync(0xffffffffu, next != ref)) {
-      ok = ok && warp_wait(&sm.odone[s], (i - 1) & 1);
-      if (!ok) break;
-      tc_after();
-      const float corr = ref == -INFINITY ? 0.f : ex2(ref - next);
+      const int n = lim - at - 64 * hf;      // scores that the row attends
 #pragma unroll 1
-      for (int c = 0; c < 128; c += 32) {
-        uint32_t o[32];
-        tq::tmem_ld_32x32b_x32(ocol + c, o);
+      for (int c = 0; c < 64; c += 16) {
+        float x[16];
+        tmem_load16(scol + c, reinterpret_cast<uint32_t*>(x));
         tq::tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
-        tq::tmem_st_32x32b_x32(ocol + c, o);
+        for (int k = 0; k < 16; ++k)
+          if (c + k >= n) x[k] = -INFINITY;
+        tq::tmem_st_32x32b_x16(scol + c, reinterpret_cast<uint32_t*>(x));
       }
-      sum *= corr;
+      tq::tmem_wait_st();
     }
-    ref = next;
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 64; c += 32) {
+      float x[32];
+      tq::tmem_ld_32x32b_x32(scol + c, reinterpret_cast<uint32_t*>(x));
+      tq::tmem_wait_ld();
+      float m[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+      for (int k = 4; k < 28; k += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m[e] = max3(m[e], x[k + e], x[k + 4 + e]);
+      top = fmaxf(top, max3(max3(m[0], m[1], x[28]), max3(m[2], m[3], x[29]), fmaxf(x[30], x[31])));
+    }
+    top *= a.scale;
+    // (a wait that gave up ends both halves' loops here, together)
+    if (tq::named_sync_or(bar, 64, top - ref > kGrow + kLift || !ok)) {
+      if (!tq::named_sync_and(bar, 64, ok)) return false;
+      if (hf == 0) sm.top[s][r] = top;
+      tq::named_sync(bar, 64);
+      if (hf == 1) sm.top[s][r] = top = fmaxf(top, sm.top[s][r]);
+      tq::named_sync(bar, 64);
+      if (hf == 0) top = sm.top[s][r];
+      const float next = top - ref > kGrow + kLift ? top - kLift : ref;
+      if (i > 0) {
+        ok = warp_wait(&sm.odone[s], (i - 1) & 1);
+        tc_after();
+        const float corr = ref == -INFINITY ? 0.f : ex2(ref - next);
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 16) {
+          uint32_t o[16];
+          tmem_load16(ocol + c, o);
+          tq::tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
+          tq::tmem_st_32x32b_x16(ocol + c, o);
+        }
+        sum *= corr;
+      }
+      ref = next;
+    }
     const float off = ref == -INFINITY ? 0.f : -ref;
     const tq::f32x2 off2 = tq::pack2(off, off);
     tq::f32x2 l0 = tq::pack2(0.f, 0.f), l1 = l0;
+#pragma unroll 1
+    for (int c = 0; c < 64; c += 32) {
+      float x[32];
+      uint32_t p[16];
+      tq::tmem_ld_32x32b_x32(scol + c, reinterpret_cast<uint32_t*>(x));
+      tq::tmem_wait_ld();
 #pragma unroll
-    for (int c = 0; c < 128; c += 64) {
-      uint32_t p[32];
-#pragma unroll
-      for (int k = 0; k < 64; k += 4) {
-        const float2 u = tq::unpack2(tq::fma2(tq::pack2(x[c + k], x[c + k + 1]), scale2, off2));
-        const float2 v = tq::unpack2(tq::fma2(tq::pack2(x[c + k + 2], x[c + k + 3]), scale2, off2));
+      for (int k = 0; k < 32; k += 4) {
+        const float2 u = tq::unpack2(tq::fma2(tq::pack2(x[k], x[k + 1]), scale2, off2));
+        const float2 v = tq::unpack2(tq::fma2(tq::pack2(x[k + 2], x[k + 3]), scale2, off2));
         const float w0 = ex2(u.x), w1 = ex2(u.y), w2 = ex2(v.x), w3 = ex2(v.y);
         l0 = tq::add2(l0, tq::pack2(w0, w1));
         l1 = tq::add2(l1, tq::pack2(w2, w3));
         p[k / 2] = pack<kBf16>(w0, w1);
         p[k / 2 + 1] = pack<kBf16>(w2, w3);
       }
-      tq::tmem_st_32x32b_x32(scol + c / 2, p);
+      tq::tmem_st_32x32b_x16(scol + c / 2, p);
     }
     tq::tmem_wait_st();
     tc_before();
@@ -253,16 +290,93 @@ __device__ __forceinline__ bool softmax_stream(const PromptArgs& a, Smem& sm, co
   return ok;
 }
 
-// Values that the guard took out, given back to a row that attends them: O and so the row become
-// what they are (infinite or NaN).  Rare and slow.
+// A channel's values that the guard took out of n keys (v: the first one's, `stride` elements apart),
+// given back to a row that attends them: O and so the row become what they are, infinite or NaN.
+// Rare and slow.
 template <bool kBf16>
-__device__ __noinline__ void give_back(const PromptArgs& a, const Work& w, int lim, int c, float* o) {
-  const int first = max(w.free_to, w.j0 * kTile), last = min(lim, (w.j0 + w.n) * kTile);
-  for (int j = first; j < last; ++j) {
-    const uint16_t* v = a.v + (long long)(w.k0 + j) * a.v_t + w.h * a.v_h + 32 * c;
-    for (int k = 0; k < 32; ++k)
-      if (!finite16<kBf16>(v[k])) o[k] += widen<kBf16>(v[k]);
+__device__ __noinline__ float give_back(const uint16_t* v, long long stride, int n, float o) {
+  for (int j = 0; j < n; ++j)
+    if (special2<kBf16>(v[j * stride])) o += widen<kBf16>(v[j * stride]);
+  return o;
+}
+
+// Where K (value = 0) and V (1) of a tile lie.  Pairs share a ring of kStages stages that holds K and
+// V of tiles 0, 1, ... in turn; alternating streams have a stage each for their K and their V.  Who
+// waits for a stage waits for every use of it, so that a phase's parity says which one is meant.
+struct Place {
+  int stage;
+  unsigned phase;
+};
+__device__ __forceinline__ Place place(const Work& w, int t, int value) {
+  if (w.pair) return Place{(2 * t + value) % kStages, (unsigned)((2 * t + value) / kStages) & 1};
+  return Place{2 * (t & 1) + value, (unsigned)(t >> 1) & 1};
+}
+
+// The products of one stream: S = Q·Kᵀ of its first tile, then O += P·V of each with S of the next.
+//
+// An issuer a stream, because around the products of a tile an issuer has 400 cycles and more of
+// waits and commits, in which the tensor pipe stood still with one issuer for both (without any
+// softmax 1560 TFLOP/s for 8192 × 8192 bf16; 2056 with two).  Pairs issue in turn, a tile's 16
+// products each: left alone, both streams' products run at once and then both softmaxes (4250 cycles
+// a tile of both, 1850 of them waiting for S).  The stream is a constant, so that TMEM addresses are.
+template <bool kBf16, int s>
+__device__ __forceinline__ bool issue_stream(Smem& sm, const Work& w) {
+  constexpr uint32_t kType = kBf16 ? (1u << 7) | (1u << 10) : 0u;
+  constexpr uint32_t kIdescS = tq::idesc_f16(128, 128) | kType;
+  constexpr uint32_t kIdescO = kIdescS | (1u << 16);       // B (values) is N-major
+  const uint64_t q = swizzled_desc(s32(sm.q[0]), 16, 1024) + (s && w.pair ? kTileBytes >> 4 : 0);
+  const uint64_t kdesc = swizzled_desc(s32(sm.kv[0]), 16, 1024);
+  const uint64_t vdesc = swizzled_desc(s32(sm.kv[0]), kHalfBytes, 1024);
+  const int step = w.pair ? 1 : 2, first = w.pair ? 0 : s;
+  const int live = w.pair && !s ? w.n0 : w.n;              // tiles before this one are this stream's too
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, unsigned parity) { ok = ok && warp_wait(bar, parity); };
+  if (s == 1 && w.pair) tq::named_arrive(kBarTurn, 64);
+  if (first < w.n) wait(&sm.qfull, 0);
+  // (a wait that gave up stops the issues, not the turns: both issuers take the same number of them)
+  int i = -1;
+  for (int t = first - step; t < w.n; t += step, ++i) {
+    const Place pv = place(w, max(t, 0), 1), pk = place(w, t + step, 0);
+    const bool weigh = i >= 0, score = t + step < w.n;
+    if (weigh) {
+      wait(&sm.full[pv.stage], pv.phase);
+      if (t < live) wait(&sm.pfull[s], i & 1);
+    }
+    if (score) wait(&sm.full[pk.stage], pk.phase);
+    if (w.pair) tq::named_sync(kBarTurn + s, 64);
+    tc_after();
+    if (ok && elect_one()) {
+      if (weigh) {
+        if (t < live) {
+          const uint64_t v = vdesc + pv.stage * (kTileBytes >> 4);
+          tq::mma_ts(kOCol + 128 * s, kSCol + 128 * s, v, kIdescO, i > 0);
+#pragma unroll
+          for (int ks = 1; ks < 8; ++ks)
+            tq::mma_ts(kOCol + 128 * s, kSCol + 128 * s + 8 * ks + (ks >= 4 ? 32 : 0), v + ks * (2048 >> 4), kIdescO, 1u);
+          tq::mma_commit(&sm.odone[s]);
+        }
+        tq::mma_commit(&sm.empty[pv.stage]);
+      }
+      if (score) {
+        if (t + step < live) {
+          const uint64_t k = kdesc + pk.stage * (kTileBytes >> 4);
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks) {
+            const int d = (ks >> 2) * (kHalfBytes >> 4) + (ks & 3) * 2;
+            tq::mma_ss(kSCol + 128 * s, q + d, k + d, kIdescS, ks > 0);
+          }
+          tq::mma_commit(&sm.sfull[s]);
+        }
+        tq::mma_commit(&sm.empty[pk.stage]);
+      }
+    }
+    __syncwarp();
+    if (w.pair && (s == 0 || score)) tq::named_arrive(kBarTurn + (s ^ 1), 64);
   }
+  // whatever was issued has ended before the tensor memory is given back
+  if (elect_one()) tq::mma_commit(&sm.drain);
+  __syncwarp();
+  return tq::mbar_wait(&sm.drain, 0) && ok;
 }
 
 template <bool kBf16>
@@ -314,17 +428,17 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       tq::mbar_init(&sm.full[i], 1);
-      tq::mbar_init(&sm.empty[i], 1);
+      tq::mbar_init(&sm.empty[i], w.pair ? 2 : 1);
     }
     tq::mbar_init(&sm.qfull, 1);
     tq::mbar_init(&sm.gdone, 1);
     for (int i = 0; i < kMaxGuarded; ++i) tq::mbar_init(&sm.gfull[i], 1);
     for (int i = 0; i < 2; ++i) {
       tq::mbar_init(&sm.sfull[i], 1);
-      tq::mbar_init(&sm.pfull[i], 4);
+      tq::mbar_init(&sm.pfull[i], 8);
       tq::mbar_init(&sm.odone[i], 1);
     }
-    tq::mbar_init(&sm.drain, 1);
+    tq::mbar_init(&sm.drain, 2);
     sm.poison = 0;
     tq::mbar_init_fence();
   }
@@ -332,231 +446,162 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
   __syncthreads();
   tc_after();
   bool ok = sm.tmem == 0;   // all 512 columns: they begin at address 0
-  // Jobs u = 0, 1, ...: stream u & 1, tile u / 2 of both (pairs) or u.  The ring holds, in the order
-  // of the jobs' products, K of jobs 0 and 1, then for each job its V and K of job u + 2; a pair's
-  // second job shares the first one's tiles.
-  const int jobs = w.pair ? 2 * w.n : w.n;
-  auto tile_of = [&](int u) { return w.pair ? u >> 1 : u; };
-
-  if (warp < 8) {
+  if (warp < kLoadWarp) {
     // ================================================================ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    const int s = warp >> 2, warp4 = warp & 3, r = 32 * warp4 + lane;
+    const int s = warp >> 3, hf = (warp >> 2) & 1, warp4 = warp & 3, r = 32 * warp4 + lane;
     float ref, sum;
-    ok = softmax_stream<kBf16>(a, sm, w, s, warp4, lane, ref, sum) && ok;
+    ok = softmax_stream<kBf16>(a, sm, w, s, hf, warp4, lane, ref, sum) && ok;
     if (guarded) ok = ok && warp_wait(&sm.gdone, 0);
-    ok = tq::named_sync_and(1, 256, ok);
+    ok = tq::named_sync_and(kBarSoftmax, 512, ok);
     if (ok) {
       tc_after();
       const bool poison = guarded && *reinterpret_cast<volatile int*>(&sm.poison);
       const Stream st = stream_of(a, w, s);
       const int token = st.tok0 + r / a.G;
       const bool there = r < a.tokens * a.G && token < w.tok0 + w.ntok;
-      const int lim = there ? w.limit(a, token) : 0;
       const long long row = (long long)(w.q0 + token) * a.Hq + w.h * a.G + r % a.G;
-      const uint32_t ocol = ((uint32_t)(32 * warp4) << 16) + kOCol + 128 * s;
-      float* rec = a.rec + ((long long)w.split * a.total_q * a.Hq + row) * kRecFloats;
+      const uint32_t ocol = ((uint32_t)(32 * warp4) << 16) + kOCol + 128 * s + 64 * hf;
       float* part = reinterpret_cast<float*>(sm.kv[0]) + r * kRecFloats;      // (the ring is done with)
-      float mine = 1.f, other = 0.f;       // factors of the two streams' parts of a row
-      if (!w.pair) {
-        if (s == 1) {
+      // Σw of a row's halves [stream][half][row]
+      float* sums = reinterpret_cast<float*>(sm.kv[0]) + kTile * kRecFloats;
+      sums[(2 * s + hf) * kTile + r] = sum;
+      if (!w.pair && s == 1) {
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float o[32];
-            if (st.count > 0) {
-              tq::tmem_ld_32x32b_x32(ocol + 32 * c, reinterpret_cast<uint32_t*>(o));
-              tq::tmem_wait_ld();
-            }
-#pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<float4*>(part + 32 * c + k) =
-                  st.count > 0 ? make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < 64; c += 16) {
+          float o[16];
+          if (st.count > 0) {
+            tmem_load16(ocol + c, reinterpret_cast<uint32_t*>(o));
+            tq::tmem_wait_ld();
           }
-          *reinterpret_cast<float2*>(part + 128) = make_float2(ref, sum);
+#pragma unroll
+          for (int k = 0; k < 16; k += 4)
+            *reinterpret_cast<float4*>(part + 64 * hf + c + k) =
+                st.count > 0 ? make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        tq::named_sync(1, 256);
-        if (s == 0) {
-          const float2 rs = *reinterpret_cast<const float2*>(part + 128);
-          const float both = fmaxf(ref, rs.x);
-          mine = ref == -INFINITY ? 0.f : ex2(ref - both);
-          other = rs.x == -INFINITY ? 0.f : ex2(rs.x - both);
-          sum = sum * mine + rs.y * other;     // (a NaN sum stays)
-          ref = both;
-        }
+        if (hf == 0) part[128] = ref;
+      }
+      tq::named_sync(kBarSoftmax, 512);
+      sum += sums[(2 * s + (hf ^ 1)) * kTile + r];
+      float mine = 1.f, other = 0.f;       // factors of the two streams' parts of a row
+      if (!w.pair && s == 0) {
+        const float ref1 = part[128], both = fmaxf(ref, ref1);
+        mine = ref == -INFINITY ? 0.f : ex2(ref - both);
+        other = ref1 == -INFINITY ? 0.f : ex2(ref1 - both);
+        sum = sum * mine + (sums[2 * kTile + r] + sums[3 * kTile + r]) * other;     // (a NaN sum stays)
+        ref = both;
       }
       if (w.pair || s == 0) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        float* rec = a.rec + ((long long)w.split * a.total_q * a.Hq + row) * kRecFloats;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          float o[32];
+        for (int c = 64 * hf; c < 64 * hf + 64; c += 16) {
+          float o[16];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0.f;
+          for (int k = 0; k < 16; ++k) o[k] = 0.f;
           if (st.count > 0) {
-            tq::tmem_ld_32x32b_x32(ocol + 32 * c, reinterpret_cast<uint32_t*>(o));
+            tmem_load16(ocol + c - 64 * hf, reinterpret_cast<uint32_t*>(o));
             tq::tmem_wait_ld();
           }
           if (!w.pair) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              const float4 x = *reinterpret_cast<const float4*>(part + 32 * c + k);
+            for (int k = 0; k < 16; k += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(part + c + k);
               o[k] = fmaf(o[k], mine, x.x * other);
               o[k + 1] = fmaf(o[k + 1], mine, x.y * other);
               o[k + 2] = fmaf(o[k + 2], mine, x.z * other);
               o[k + 3] = fmaf(o[k + 3], mine, x.w * other);
             }
           }
-          if (poison && there) {
-            float p[32];
-            for (int k = 0; k < 32; ++k) p[k] = o[k];
-            give_back<kBf16>(a, w, lim, c, p);
-            for (int k = 0; k < 32; ++k) o[k] = p[k];
-          }
-          if (there) {
-            if (a.splits > 1) {
+          if (!there) continue;
+          if (poison) {
+            const int first = max(w.free_to, w.j0 * kTile), n = min(w.limit(a, token), (w.j0 + w.n) * kTile) - first;
+            const uint16_t* v = a.v + (long long)(w.k0 + first) * a.v_t + w.h * a.v_h + c;
 #pragma unroll
-              for (int k = 0; k < 32; k += 4)
-                *reinterpret_cast<float4*>(rec + 32 * c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-            } else {
-              put_row<kBf16>(a, row, o, inv, c);
-            }
+            for (int k = 0; k < 16; ++k) o[k] = give_back<kBf16>(v + k, a.v_t, n, o[k]);
+          }
+          if (a.splits > 1) {
+#pragma unroll
+            for (int k = 0; k < 16; k += 4)
+              *reinterpret_cast<float4*>(rec + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          } else {
+            put16<kBf16>(a, row, o, inv, c);
           }
         }
-        if (there && a.splits > 1) *reinterpret_cast<float2*>(rec + 128) = make_float2(ref, sum);
+        if (there && a.splits > 1 && hf == 0) *reinterpret_cast<float2*>(rec + 128) = make_float2(ref, sum);
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == kLoadWarp) {
       // ============================================================== loader
       if (lane == 0 && w.n > 0) {
-        int at = 0;
-        auto load = [&](const CUtensorMap* map, int tile, int guard) {
-          const int st = at % kStages;
-          if (at >= kStages && !(ok = ok && tq::mbar_wait(&sm.empty[st], (at / kStages - 1) & 1))) return;
+        int uses[kStages] = {};        // of each stage so far
+        auto load = [&](int t, int value) {
+          const int st = place(w, t, value).stage, guard = value ? t - (w.n - guarded) : -1;
+          if (uses[st] && !(ok = ok && tq::mbar_wait(&sm.empty[st], (uses[st] - 1) & 1))) return;
+          ++uses[st];
           uint64_t* bar = guard >= 0 ? &sm.gfull[guard] : &sm.full[st];
           tq::mbar_expect_tx(bar, kTileBytes);
           for (int c = 0; c < 2; ++c)
-            tma_load(sm.kv[st] + c * kHalfBytes, map, 64 * c, w.h, w.k0 + (w.j0 + tile) * kTile, bar);
-          ++at;
+            tma_load(sm.kv[st] + c * kHalfBytes, value ? &vmap : &kmap, 64 * c, w.h, w.k0 + (w.j0 + t) * kTile, bar);
         };
         const int blocks = w.pair ? 2 : 1, bytes = a.tokens * a.G * 128;
         tq::mbar_expect_tx(&sm.qfull, blocks * 2 * bytes);
         for (int s = 0; s < blocks; ++s)
           for (int c = 0; c < 2; ++c)
             tma_load(sm.q[s] + c * kHalfBytes, &qmap, 64 * c, w.h * a.G, w.q0 + w.tok0 + s * a.tokens, &sm.qfull);
-        const int ahead = w.pair ? 1 : 2;          // tiles of K before the first V
-        for (int t = 0; t < min(ahead, w.n) && ok; ++t) load(&kmap, t, -1);
-        for (int t = 0; t < w.n && ok; ++t) {
-          load(&vmap, t, t - (w.n - guarded));
-          if (t + ahead < w.n && ok) load(&kmap, t + ahead, -1);
+        const int step = w.pair ? 1 : 2;
+        for (int t = 0; t < w.n && ok; t += step) {
+          load(t, 0);
+          if (!w.pair && t + 1 < w.n && ok) load(t + 1, 0);
+          if (ok) load(t, 1);
+          if (!w.pair && t + 1 < w.n && ok) load(t + 1, 1);
         }
         // copies in flight end before the block does, whatever happened
         // (a guarded tile's `full` follows its copy)
         ok = tq::mbar_wait(&sm.qfull, 0) && ok;
-        for (int i = max(0, at - kStages); i < at; ++i) ok = tq::mbar_wait(&sm.full[i % kStages], (i / kStages) & 1) && ok;
+        for (int i = 0; i < kStages; ++i)
+          if (uses[i]) ok = tq::mbar_wait(&sm.full[i], (uses[i] - 1) & 1) && ok;
       }
-    } else if (warp == kIssueWarp) {
-      // ============================================================== issuer
-      constexpr uint32_t kType = kBf16 ? (1u << 7) | (1u << 10) : 0u;
-      constexpr uint32_t kIdescS = tq::idesc_f16(128, 128) | kType;
-      constexpr uint32_t kIdescO = kIdescS | (1u << 16);       // B (values) is N-major
-      const uint64_t qdesc = swizzled_desc(s32(sm.q[0]), 16, 1024);
-      const uint64_t kdesc = swizzled_desc(s32(sm.kv[0]), 16, 1024);
-      const uint64_t vdesc = swizzled_desc(s32(sm.kv[0]), kHalfBytes, 1024);
-      int at = 0, kst = 0, vst = 0;                // ring position, stages in use
-      auto wait = [&](uint64_t* bar, unsigned parity) { return ok = ok && warp_wait(bar, parity); };
-      auto next = [&](int& st) {                   // the ring's next tile
-        st = at % kStages;
-        if (!wait(&sm.full[st], (at / kStages) & 1)) return;
-        ++at;
-      };
-      auto live = [&](int u) { return u < jobs && (!w.pair || (u & 1) || tile_of(u) < w.n0); };
-      auto score = [&](int u) {
-        if (u >= jobs) return;
-        const int s = u & 1;
-        if (!w.pair || !s) next(kst);
-        if (!ok) return;
-        tc_after();
-        if (elect_one()) {
-          if (live(u)) {
-            const uint64_t q = qdesc + (w.pair && s ? kTileBytes >> 4 : 0), k = kdesc + kst * (kTileBytes >> 4);
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-              const int step = (ks >> 2) * (kHalfBytes >> 4) + (ks & 3) * 2;
-              tq::mma_ss(kSCol + 128 * s, q + step, k + step, kIdescS, ks > 0);
-            }
-            tq::mma_commit(&sm.sfull[s]);
-          }
-          if (!w.pair || s) tq::mma_commit(&sm.empty[kst]);
-        }
-        __syncwarp();
-      };
-      auto weigh = [&](int u) {
-        const int s = u & 1, t = tile_of(u);
-        if (!w.pair || !s) next(vst);
-        if (!ok) return;
-        if (live(u)) {
-          const int i = w.pair ? t : t >> 1;
-          if (!wait(&sm.pfull[s], i & 1)) return;
-          tc_after();
-          if (elect_one()) {
-            const uint64_t v = vdesc + vst * (kTileBytes >> 4);
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              tq::mma_ts(kOCol + 128 * s, kSCol + 128 * s + 8 * ks, v + ks * (2048 >> 4), kIdescO, i > 0 || ks > 0);
-            tq::mma_commit(&sm.odone[s]);
-          }
-          __syncwarp();
-        }
-        if (!w.pair || s) {
-          if (elect_one()) tq::mma_commit(&sm.empty[vst]);
-          __syncwarp();
-        }
-      };
-      if (w.n > 0) wait(&sm.qfull, 0);
-      score(0);
-      score(1);
-      for (int u = 0; u < jobs && ok; ++u) {
-        weigh(u);
-        if (ok) score(u + 2);
-      }
-      // whatever was issued has ended before the tensor memory is given back
-      if (elect_one()) tq::mma_commit(&sm.drain);
-      __syncwarp();
-      if (!tq::mbar_wait(&sm.drain, 0)) ok = false;
+    } else if (warp < kGuardWarp) {
+      // ============================================================== issuers
+      if (warp == kIssueWarp) ok = issue_stream<kBf16, 0>(sm, w) && ok;
+      else ok = issue_stream<kBf16, 1>(sm, w) && ok;
     } else {
       // ============================================================== guard
-      const int id = tid - 32 * kGuardWarp;        // of 64
       for (int g = 0; g < guarded && ok; ++g) {
         const int t = w.n - guarded + g;
-        const int at = w.pair ? 2 * t + 1 : min(2 * t + 2, 2 * w.n - 1);     // its V's place in the ring
-        const int st = at % kStages;
+        const int st = place(w, t, 1).stage;
         // (the guarded tiles are the last ones: a limit that grows with the tiles before them)
         ok = __all_sync(0xffffffffu, tq::mbar_wait(&sm.gfull[g], 0, 20000000ull + 20000ull * w.n));
-        if (!tq::named_sync_and(2, 64, ok)) break;
+        if (!ok) break;
         const int key0 = (w.j0 + t) * kTile;
-        bool bad = false;
-        for (int i = id; i < 2 * kTile; i += 64) {           // (row, half of the channels)
+        for (int i = lane; i < 2 * kTile; i += 32) {         // (row, half of the channels)
           const int j = i & (kTile - 1);
           uint4* row = reinterpret_cast<uint4*>(sm.kv[st] + (i >> 7) * kHalfBytes + j * 128);
           if (key0 + j >= w.nk) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) row[c] = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < 8; ++c) row[(c + lane) & 7] = make_uint4(0, 0, 0, 0);
           } else if (key0 + j >= w.free_to) {
-            uint32_t* word = reinterpret_cast<uint32_t*>(row);
-            for (int c = 0; c < 32; ++c) {
-              uint32_t u = word[(c + id) & 31];
-              const bool lo = finite16<kBf16>(u), hi = finite16<kBf16>(u >> 16);
-              if (lo && hi) continue;
-              bad = true;
-              word[(c + id) & 31] = (lo ? u & 0xffffu : 0u) | (hi ? u & 0xffff0000u : 0u);
+            uint32_t bad = 0;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const uint4 x = row[(c + lane) & 7];
+              bad |= special2<kBf16>(x.x) | special2<kBf16>(x.y) | special2<kBf16>(x.z) | special2<kBf16>(x.w);
+            }
+            if (bad) {
+              uint32_t* word = reinterpret_cast<uint32_t*>(row);
+#pragma unroll 1
+              for (int c = 0; c < 32; ++c) {
+                const uint32_t x = special2<kBf16>(word[c]);
+                word[c] &= ~((x >> 15) * 0xffffu);
+              }
+              *reinterpret_cast<volatile int*>(&sm.poison) = 1;
             }
           }
         }
-        if (bad) *reinterpret_cast<volatile int*>(&sm.poison) = 1;
         tq::fence_async_smem();
-        tq::named_sync(2, 64);
-        if (id == 0) {
+        __syncwarp();
+        if (lane == 0) {
           mbar_arrive(&sm.full[st]);
           if (g == guarded - 1) mbar_arrive(&sm.gdone);
         }
@@ -684,10 +729,6 @@ tq_status launch(const CUtensorMap (&maps)[3], const PromptArgs& a, long long gr
   if (!configured[dev]) {
     if (cudaFuncSetAttribute(prompt_kernel<kBf16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
       return TQ_ERR_CUDA;
-    // the warpgroups' shares add up to what the block is launched with: more would wait forever
-    cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, prompt_kernel<kBf16>) != cudaSuccess) return TQ_ERR_CUDA;
-    if (fa.numRegs != kRegsLaunch) return TQ_ERR_UNSUPPORTED;
     configured[dev] = true;
   }
   prompt_kernel<kBf16><<<(unsigned)grid, kThreads, smem, stream>>>(maps[0], maps[1], maps[2], a);
