@@ -338,17 +338,16 @@ __device__ __forceinline__ bool issue_stream(Smem& sm, const Work& w) {
   for (int t = first - step; t < w.n; t += step, ++i) {
     const Place pv = place(w, max(t, 0), 1), pk = place(w, t + step, 0);
     const bool weigh = i >= 0, score = t + step < w.n;
-    if (weigh) {
-      wait(&sm.full[pv.stage], pv.phase);
-      if (t < live) wait(&sm.pfull[s], i & 1);
-    }
+    const uint64_t v = vdesc + pv.stage * (kTileBytes >> 4), k = kdesc + pk.stage * (kTileBytes >> 4);
+    // (the weights come last: the rest is there before them)
+    if (weigh) wait(&sm.full[pv.stage], pv.phase);
     if (score) wait(&sm.full[pk.stage], pk.phase);
     if (w.pair) tq::named_sync(kBarTurn + s, 64);
+    if (weigh && t < live) wait(&sm.pfull[s], i & 1);
     tc_after();
     if (ok && elect_one()) {
       if (weigh) {
         if (t < live) {
-          const uint64_t v = vdesc + pv.stage * (kTileBytes >> 4);
           tq::mma_ts(kOCol + 128 * s, kSCol + 128 * s, v, kIdescO, i > 0);
 #pragma unroll
           for (int ks = 1; ks < 8; ++ks)
@@ -359,7 +358,6 @@ __device__ __forceinline__ bool issue_stream(Smem& sm, const Work& w) {
       }
       if (score) {
         if (t + step < live) {
-          const uint64_t k = kdesc + pk.stage * (kTileBytes >> 4);
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks) {
             const int d = (ks >> 2) * (kHalfBytes >> 4) + (ks & 3) * 2;
