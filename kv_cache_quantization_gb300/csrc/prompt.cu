@@ -15,8 +15,7 @@
 //   1 loader thread   TMA tiles of K and V (32 KB each, 128-byte swizzle) into a ring of 5
 //   2 issuer warps    S = Q·Kᵀ (128 × 128 × 128) and O += P·V (P in TMEM over the scores it came from)
 //                     of a stream each, so that one's softmax runs beside the other one's products
-//   16 softmax warps  two threads per row and stream: 64 scores each in registers, maximum, powers,
-//                     weights back to TMEM
+//   8 softmax warps   a thread per row and stream: scores to weights, back to TMEM
 //   1 guard warp      tiles of V that some row does not attend in full: rows past the sequence are
 //                     zeroed, and infinite or NaN values past the first row's border are taken out
 //                     (a weight of 0 would not hide them); rows that do attend those get them back
@@ -48,12 +47,11 @@ using tq::tc_before;
 constexpr int kTile = 128;              // query rows of a stream, keys of a tile
 constexpr int kStages = 5;
 constexpr int kTileBytes = kTile * TQ_D * 2, kHalfBytes = kTileBytes / 2;   // halves: 64 channels
-constexpr int kThreads = 640;
-constexpr int kLoadWarp = 16, kIssueWarp = 17, kGuardWarp = 19;      // (an issuer per stream)
+constexpr int kThreads = 384;
+constexpr int kLoadWarp = 8, kIssueWarp = 9, kGuardWarp = 11;      // (an issuer per stream)
 // named barriers
-constexpr int kBarSoftmax = 1, kBarTurn = 2, kBarRows = 4;      // + stream; + 4·stream + lane group
+constexpr int kBarSoftmax = 1, kBarTurn = 2;      // + stream
 constexpr int kRecFloats = 132;         // O[128], ref, Σw, padding
-constexpr float kGrow = 8.f;
 constexpr int kMaxGuarded = 4;          // tiles that the borders of a CTA's rows can cross: at most 3
 constexpr int kSCol = 0, kOCol = 256;   // TMEM columns: scores (weights over them) and O of both streams
 
@@ -77,10 +75,9 @@ struct alignas(1024) Smem {
   unsigned char kv[kStages][kTileBytes];
   uint64_t full[kStages], empty[kStages];
   uint64_t gfull[kMaxGuarded];    // V of a guarded tile has arrived (`full`: it may be used)
-  uint64_t qfull, gdone, sfull[2], pfull[2], odone[2], drain;
+  uint64_t qfull, gdone, sfull[2], pfull[2][2], odone[2][2], drain;     // [stream][part of a tile]
   uint32_t tmem;
   int poison;               // the guard took values out
-  float top[2][kTile];      // [stream]: maxima that a row's two threads exchange
 };
 
 __device__ __forceinline__ bool elect_one() {
@@ -145,6 +142,27 @@ __device__ __forceinline__ uint32_t special2(uint32_t u) {
   return ((u & m) + one) & 0x80008000u;
 }
 
+// Weights of 64 scores with a reference, packed; returns their sum.  Without a reference: of any
+// size (the caller takes them again).
+template <bool kBf16>
+__device__ __forceinline__ float weights(const float (&x)[64], tq::f32x2 scale2, float ref, uint32_t (&p)[32]) {
+  const float off = ref == -INFINITY ? 0.f : -ref;
+  const tq::f32x2 off2 = tq::pack2(off, off);
+  tq::f32x2 l0 = tq::pack2(0.f, 0.f), l1 = l0;
+#pragma unroll
+  for (int k = 0; k < 64; k += 4) {
+    const float2 u = tq::unpack2(tq::fma2(tq::pack2(x[k], x[k + 1]), scale2, off2));
+    const float2 v = tq::unpack2(tq::fma2(tq::pack2(x[k + 2], x[k + 3]), scale2, off2));
+    const float w0 = ex2(u.x), w1 = ex2(u.y), w2 = ex2(v.x), w3 = ex2(v.y);
+    l0 = tq::add2(l0, tq::pack2(w0, w1));
+    l1 = tq::add2(l1, tq::pack2(w2, w3));
+    p[k / 2] = pack<kBf16>(w0, w1);
+    p[k / 2 + 1] = pack<kBf16>(w2, w3);
+  }
+  const float2 l = tq::unpack2(tq::add2(l0, l1));
+  return l.x + l.y;
+}
+
 // What a CTA works on.
 struct Work {
   int h;                    // KV head
@@ -179,35 +197,37 @@ __device__ __forceinline__ void put16(const PromptArgs& a, long long row, const 
                         pack<kBf16>(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack<kBf16>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
 }
 
-// The softmax of one stream's tiles: a row's two threads take 64 scores of a tile each, 32 at a time,
-// once for the maximum and once for the weights (which lie over the first half of the thread's own
-// scores).  The loops are rolled and the scores stay in TMEM between the passes, because the roles'
-// code has to fit the instruction caches of an SM side by side: with 64 scores in registers and
-// everything unrolled, the maximum of 64 scores took 550 cycles instead of 50.  The two threads agree
-// on the reference, which the products of both halves share, only where one of their warps' rows
-// moves it (one barrier that ORs a predicate tells).
+// The softmax of one stream's tiles: a thread per row, 64 scores at a time.
+//
+// Weights are taken with the reference as it is, and their sum tells whether that was right: a sum of
+// at most 2^8 (fp16: 2^15) has no weight above.  Only where a row's sum is larger, or where a row
+// has no reference yet, is the maximum looked for, the reference moved there and O scaled.  So there
+// is no pass for the maximum in the chain from S to P (350 of 3000 cycles a tile).  Weights are handed
+// over 64 at a time, so that their products begin while the other 64 are made.
 template <bool kBf16>
-__device__ __forceinline__ bool softmax_stream(const PromptArgs& a, Smem& sm, const Work& w, int s, int hf, int warp4, int lane,
+__device__ __forceinline__ bool softmax_stream(const PromptArgs& a, Smem& sm, const Work& w, int s, int warp4, int lane,
                                                float& ref, float& sum) {
-  constexpr float kLift = kBf16 ? 0.f : 7.f;
+  constexpr float kLift = kBf16 ? 0.f : 7.f, kMost = kBf16 ? 256.f : 32768.f;   // 2^8 above the reference's maximum
   const Stream st = stream_of(a, w, s);
-  const int r = 32 * warp4 + lane, token = st.tok0 + r / a.G, bar = kBarRows + 4 * s + warp4;
-  const int lim = token < w.tok0 + w.ntok && r < a.tokens * a.G ? w.limit(a, token) : 0;
+  const int r = 32 * warp4 + lane, token = st.tok0 + r / a.G;
+  const bool there = token < w.tok0 + w.ntok && r < a.tokens * a.G;
+  const int lim = there ? w.limit(a, token) : 0;
   const uint32_t lanes = (uint32_t)(32 * warp4) << 16;
-  const uint32_t scol = lanes + kSCol + 128 * s + 64 * hf, ocol = lanes + kOCol + 128 * s + 64 * hf;
+  const uint32_t scol = lanes + kSCol + 128 * s, ocol = lanes + kOCol + 128 * s;
   const tq::f32x2 scale2 = tq::pack2(a.scale, a.scale);
   bool ok = true;
-  ref = -INFINITY;          // in the units of the exponent
+  ref = there ? -INFINITY : 0.f;      // in the units of the exponent (rows that are not used need none)
   sum = 0.f;
 #pragma unroll 1
   for (int i = 0; i < st.count; ++i) {
     const int at = (st.tile0 + i * st.step) * kTile;
     ok = ok && warp_wait(&sm.sfull[s], i & 1);
+    if (!ok) break;
     tc_after();
     if (at + kTile > w.free_to) {
-      const int n = lim - at - 64 * hf;      // scores that the row attends
+      const int n = lim - at;                // scores that the row attends
 #pragma unroll 1
-      for (int c = 0; c < 64; c += 16) {
+      for (int c = 0; c < 128; c += 16) {
         float x[16];
         tmem_load16(scol + c, reinterpret_cast<uint32_t*>(x));
         tq::tmem_wait_ld();
@@ -218,75 +238,54 @@ __device__ __forceinline__ bool softmax_stream(const PromptArgs& a, Smem& sm, co
       }
       tq::tmem_wait_st();
     }
-    float top = -INFINITY;
 #pragma unroll 1
-    for (int c = 0; c < 64; c += 32) {
-      float x[32];
-      tq::tmem_ld_32x32b_x32(scol + c, reinterpret_cast<uint32_t*>(x));
+    for (int part = 0; part < 2; ++part) {
+      float x[64];
+      uint32_t p[32];
+      tq::tmem_ld_32x32b_x32(scol + 64 * part, reinterpret_cast<uint32_t*>(x));
+      tq::tmem_ld_32x32b_x32(scol + 64 * part + 32, reinterpret_cast<uint32_t*>(x) + 32);
       tq::tmem_wait_ld();
-      float m[4] = {x[0], x[1], x[2], x[3]};
+      float l = weights<kBf16>(x, scale2, ref, p);
+      const bool bad = there && (!(l <= kMost) || ref == -INFINITY);
+      if (__any_sync(0xffffffffu, bad)) {
+        float m[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-      for (int k = 4; k < 28; k += 8)
+        for (int c = 4; c < 60; c += 8)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) m[e] = max3(m[e], x[k + e], x[k + 4 + e]);
-      top = fmaxf(top, max3(max3(m[0], m[1], x[28]), max3(m[2], m[3], x[29]), fmaxf(x[30], x[31])));
-    }
-    top *= a.scale;
-    // (a wait that gave up ends both halves' loops here, together)
-    if (tq::named_sync_or(bar, 64, top - ref > kGrow + kLift || !ok)) {
-      if (!tq::named_sync_and(bar, 64, ok)) return false;
-      if (hf == 0) sm.top[s][r] = top;
-      tq::named_sync(bar, 64);
-      if (hf == 1) sm.top[s][r] = top = fmaxf(top, sm.top[s][r]);
-      tq::named_sync(bar, 64);
-      if (hf == 0) top = sm.top[s][r];
-      const float next = top - ref > kGrow + kLift ? top - kLift : ref;
-      if (i > 0) {
-        ok = warp_wait(&sm.odone[s], (i - 1) & 1);
-        tc_after();
-        const float corr = ref == -INFINITY ? 0.f : ex2(ref - next);
+          for (int k = 0; k < 4; ++k) m[k] = max3(m[k], x[c + k], x[c + 4 + k]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = fmaxf(m[k], x[60 + k]);
+        const float top = max3(m[0], m[1], fmaxf(m[2], m[3])) * a.scale - kLift;
+        const float next = bad && top > ref ? top : ref;
+        if (i > 0 || part > 0) {
+          ok = warp_wait(&sm.odone[s][part ^ 1], (part ? i : i - 1) & 1);      // (of the part before)
+          if (!ok) break;
+          tc_after();
+          const float corr = ref == -INFINITY ? 0.f : ex2(ref - next);
 #pragma unroll 1
-        for (int c = 0; c < 64; c += 16) {
-          uint32_t o[16];
-          tmem_load16(ocol + c, o);
-          tq::tmem_wait_ld();
+          for (int c = 0; c < 128; c += 16) {
+            uint32_t o[16];
+            tmem_load16(ocol + c, o);
+            tq::tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
-          tq::tmem_st_32x32b_x16(ocol + c, o);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
+            tq::tmem_st_32x32b_x16(ocol + c, o);
+          }
+          sum *= corr;
         }
-        sum *= corr;
+        ref = next;
+        l = weights<kBf16>(x, scale2, ref, p);
       }
-      ref = next;
+      tq::tmem_st_32x32b_x32(scol + 32 * part, p);
+      sum += l;
+      tq::tmem_wait_st();
+      tc_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.pfull[s][part]);
     }
-    const float off = ref == -INFINITY ? 0.f : -ref;
-    const tq::f32x2 off2 = tq::pack2(off, off);
-    tq::f32x2 l0 = tq::pack2(0.f, 0.f), l1 = l0;
-#pragma unroll 1
-    for (int c = 0; c < 64; c += 32) {
-      float x[32];
-      uint32_t p[16];
-      tq::tmem_ld_32x32b_x32(scol + c, reinterpret_cast<uint32_t*>(x));
-      tq::tmem_wait_ld();
-#pragma unroll
-      for (int k = 0; k < 32; k += 4) {
-        const float2 u = tq::unpack2(tq::fma2(tq::pack2(x[k], x[k + 1]), scale2, off2));
-        const float2 v = tq::unpack2(tq::fma2(tq::pack2(x[k + 2], x[k + 3]), scale2, off2));
-        const float w0 = ex2(u.x), w1 = ex2(u.y), w2 = ex2(v.x), w3 = ex2(v.y);
-        l0 = tq::add2(l0, tq::pack2(w0, w1));
-        l1 = tq::add2(l1, tq::pack2(w2, w3));
-        p[k / 2] = pack<kBf16>(w0, w1);
-        p[k / 2 + 1] = pack<kBf16>(w2, w3);
-      }
-      tq::tmem_st_32x32b_x16(scol + c / 2, p);
-    }
-    tq::tmem_wait_st();
-    tc_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.pfull[s]);
-    const float2 l = tq::unpack2(tq::add2(l0, l1));
-    sum += l.x + l.y;
+    if (!ok) break;
   }
-  if (st.count > 0) ok = ok && warp_wait(&sm.odone[s], (st.count - 1) & 1);
+  if (st.count > 0) ok = ok && warp_wait(&sm.odone[s][1], (st.count - 1) & 1);
   return ok;
 }
 
@@ -343,19 +342,24 @@ __device__ __forceinline__ bool issue_stream(Smem& sm, const Work& w) {
     if (weigh) wait(&sm.full[pv.stage], pv.phase);
     if (score) wait(&sm.full[pk.stage], pk.phase);
     if (w.pair) tq::named_sync(kBarTurn + s, 64);
-    if (weigh && t < live) wait(&sm.pfull[s], i & 1);
+    if (weigh && t < live) {
+      // in two parts of 64 keys, as their weights come
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        wait(&sm.pfull[s][part], i & 1);
+        tc_after();
+        if (ok && elect_one()) {
+#pragma unroll
+          for (int ks = 4 * part; ks < 4 * part + 4; ++ks)
+            tq::mma_ts(kOCol + 128 * s, kSCol + 128 * s + 8 * ks, v + ks * (2048 >> 4), kIdescO, ks ? 1u : (uint32_t)(i > 0));
+          tq::mma_commit(&sm.odone[s][part]);
+        }
+        __syncwarp();
+      }
+    }
     tc_after();
     if (ok && elect_one()) {
-      if (weigh) {
-        if (t < live) {
-          tq::mma_ts(kOCol + 128 * s, kSCol + 128 * s, v, kIdescO, i > 0);
-#pragma unroll
-          for (int ks = 1; ks < 8; ++ks)
-            tq::mma_ts(kOCol + 128 * s, kSCol + 128 * s + 8 * ks + (ks >= 4 ? 32 : 0), v + ks * (2048 >> 4), kIdescO, 1u);
-          tq::mma_commit(&sm.odone[s]);
-        }
-        tq::mma_commit(&sm.empty[pv.stage]);
-      }
+      if (weigh) tq::mma_commit(&sm.empty[pv.stage]);
       if (score) {
         if (t + step < live) {
 #pragma unroll
@@ -433,8 +437,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
     for (int i = 0; i < kMaxGuarded; ++i) tq::mbar_init(&sm.gfull[i], 1);
     for (int i = 0; i < 2; ++i) {
       tq::mbar_init(&sm.sfull[i], 1);
-      tq::mbar_init(&sm.pfull[i], 8);
-      tq::mbar_init(&sm.odone[i], 1);
+      tq::mbar_init(&sm.pfull[i][0], 4);
+      tq::mbar_init(&sm.pfull[i][1], 4);
+      tq::mbar_init(&sm.odone[i][0], 1);
+      tq::mbar_init(&sm.odone[i][1], 1);
     }
     tq::mbar_init(&sm.drain, 2);
     sm.poison = 0;
@@ -446,11 +452,11 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
   bool ok = sm.tmem == 0;   // all 512 columns: they begin at address 0
   if (warp < kLoadWarp) {
     // ================================================================ softmax
-    const int s = warp >> 3, hf = (warp >> 2) & 1, warp4 = warp & 3, r = 32 * warp4 + lane;
+    const int s = warp >> 2, warp4 = warp & 3, r = 32 * warp4 + lane;
     float ref, sum;
-    ok = softmax_stream<kBf16>(a, sm, w, s, hf, warp4, lane, ref, sum) && ok;
+    ok = softmax_stream<kBf16>(a, sm, w, s, warp4, lane, ref, sum) && ok;
     if (guarded) ok = ok && warp_wait(&sm.gdone, 0);
-    ok = tq::named_sync_and(kBarSoftmax, 512, ok);
+    ok = tq::named_sync_and(kBarSoftmax, 256, ok);
     if (ok) {
       tc_after();
       const bool poison = guarded && *reinterpret_cast<volatile int*>(&sm.poison);
@@ -458,46 +464,45 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
       const int token = st.tok0 + r / a.G;
       const bool there = r < a.tokens * a.G && token < w.tok0 + w.ntok;
       const long long row = (long long)(w.q0 + token) * a.Hq + w.h * a.G + r % a.G;
-      const uint32_t ocol = ((uint32_t)(32 * warp4) << 16) + kOCol + 128 * s + 64 * hf;
+      const uint32_t ocol = ((uint32_t)(32 * warp4) << 16) + kOCol + 128 * s;
       float* part = reinterpret_cast<float*>(sm.kv[0]) + r * kRecFloats;      // (the ring is done with)
-      // Σw of a row's halves [stream][half][row]
-      float* sums = reinterpret_cast<float*>(sm.kv[0]) + kTile * kRecFloats;
-      sums[(2 * s + hf) * kTile + r] = sum;
-      if (!w.pair && s == 1) {
-#pragma unroll 1
-        for (int c = 0; c < 64; c += 16) {
-          float o[16];
-          if (st.count > 0) {
-            tmem_load16(ocol + c, reinterpret_cast<uint32_t*>(o));
-            tq::tmem_wait_ld();
-          }
-#pragma unroll
-          for (int k = 0; k < 16; k += 4)
-            *reinterpret_cast<float4*>(part + 64 * hf + c + k) =
-                st.count > 0 ? make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        if (hf == 0) part[128] = ref;
-      }
-      tq::named_sync(kBarSoftmax, 512);
-      sum += sums[(2 * s + (hf ^ 1)) * kTile + r];
       float mine = 1.f, other = 0.f;       // factors of the two streams' parts of a row
-      if (!w.pair && s == 0) {
-        const float ref1 = part[128], both = fmaxf(ref, ref1);
-        mine = ref == -INFINITY ? 0.f : ex2(ref - both);
-        other = ref1 == -INFINITY ? 0.f : ex2(ref1 - both);
-        sum = sum * mine + (sums[2 * kTile + r] + sums[3 * kTile + r]) * other;     // (a NaN sum stays)
-        ref = both;
+      if (!w.pair) {
+        if (s == 1) {
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 16) {
+            float o[16];
+            if (st.count > 0) {
+              tmem_load16(ocol + c, reinterpret_cast<uint32_t*>(o));
+              tq::tmem_wait_ld();
+            }
+#pragma unroll
+            for (int k = 0; k < 16; k += 4)
+              *reinterpret_cast<float4*>(part + c + k) =
+                  st.count > 0 ? make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          *reinterpret_cast<float2*>(part + 128) = make_float2(ref, sum);
+        }
+        tq::named_sync(kBarSoftmax, 256);
+        if (s == 0) {
+          const float2 rs = *reinterpret_cast<const float2*>(part + 128);
+          const float both = fmaxf(ref, rs.x);
+          mine = ref == -INFINITY ? 0.f : ex2(ref - both);
+          other = rs.x == -INFINITY ? 0.f : ex2(rs.x - both);
+          sum = sum * mine + rs.y * other;     // (a NaN sum stays)
+          ref = both;
+        }
       }
       if (w.pair || s == 0) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         float* rec = a.rec + ((long long)w.split * a.total_q * a.Hq + row) * kRecFloats;
 #pragma unroll 1
-        for (int c = 64 * hf; c < 64 * hf + 64; c += 16) {
+        for (int c = 0; c < 128; c += 16) {
           float o[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) o[k] = 0.f;
           if (st.count > 0) {
-            tmem_load16(ocol + c - 64 * hf, reinterpret_cast<uint32_t*>(o));
+            tmem_load16(ocol + c, reinterpret_cast<uint32_t*>(o));
             tq::tmem_wait_ld();
           }
           if (!w.pair) {
@@ -525,7 +530,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
             put16<kBf16>(a, row, o, inv, c);
           }
         }
-        if (there && a.splits > 1 && hf == 0) *reinterpret_cast<float2*>(rec + 128) = make_float2(ref, sum);
+        if (there && a.splits > 1) *reinterpret_cast<float2*>(rec + 128) = make_float2(ref, sum);
       }
     }
   } else {
