@@ -88,6 +88,21 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity) {
   return __all_sync(0xffffffffu, tq::mbar_wait(bar, parity));
 }
+// Bounded wait of one thread in short suspensions (2 us at most each; 10^6 of them take between 20 ms
+// and 2 s).  It wakes sooner than one long suspension and is little code.
+__device__ __forceinline__ bool poll(uint64_t* bar, unsigned parity) {
+#pragma unroll 1
+  for (int i = 0; i < 1000000; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(s32(bar)), "r"(parity), "r"(2000u)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -289,6 +304,29 @@ __device__ __forceinline__ bool softmax_stream(const PromptArgs& a, Smem& sm, co
   return ok;
 }
 
+// Four records (reference, Σw; O) joined to a running one.  A record with a sum of 0 attends nothing; a
+// NaN sum has no reference and stays.
+__device__ __forceinline__ void join4(const float2 (&ml)[4], const float4 (&x)[4], float& m, float& l, float4& o) {
+  float top = m;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (ml[k].y != 0.f) top = fmaxf(top, ml[k].x);
+  const float mine = m == -INFINITY ? 1.f : ex2(m - top);
+  l *= mine;
+  o.x *= mine; o.y *= mine; o.z *= mine; o.w *= mine;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (ml[k].y == 0.f) continue;
+    const float f = ml[k].x == -INFINITY ? 1.f : ex2(ml[k].x - top);
+    l = fmaf(ml[k].y, f, l);
+    o.x = fmaf(x[k].x, f, o.x);
+    o.y = fmaf(x[k].y, f, o.y);
+    o.z = fmaf(x[k].z, f, o.z);
+    o.w = fmaf(x[k].w, f, o.w);
+  }
+  m = top;
+}
+
 // A channel's values that the guard took out of n keys (v: the first one's, `stride` elements apart),
 // given back to a row that attends them: O and so the row become what they are, infinite or NaN.
 // Rare and slow.
@@ -329,7 +367,8 @@ __device__ __forceinline__ bool issue_stream(Smem& sm, const Work& w) {
   const int step = w.pair ? 1 : 2, first = w.pair ? 0 : s;
   const int live = w.pair && !s ? w.n0 : w.n;              // tiles before this one are this stream's too
   bool ok = true;
-  auto wait = [&](uint64_t* bar, unsigned parity) { ok = ok && warp_wait(bar, parity); };
+  auto wait = [&](uint64_t* bar, unsigned parity) { ok = ok && poll(bar, parity); };
+  auto agree = [&] { ok = __all_sync(0xffffffffu, ok); };
   if (s == 1 && w.pair) tq::named_arrive(kBarTurn, 64);
   if (first < w.n) wait(&sm.qfull, 0);
   // (a wait that gave up stops the issues, not the turns: both issuers take the same number of them)
@@ -342,11 +381,14 @@ __device__ __forceinline__ bool issue_stream(Smem& sm, const Work& w) {
     if (weigh) wait(&sm.full[pv.stage], pv.phase);
     if (score) wait(&sm.full[pk.stage], pk.phase);
     if (w.pair) tq::named_sync(kBarTurn + s, 64);
-    if (weigh && t < live) {
+    if (!weigh || t >= live) {
+      agree();
+    } else {
       // in two parts of 64 keys, as their weights come
 #pragma unroll
       for (int part = 0; part < 2; ++part) {
         wait(&sm.pfull[s][part], i & 1);
+        agree();
         tc_after();
         if (ok && elect_one()) {
 #pragma unroll
@@ -354,7 +396,6 @@ __device__ __forceinline__ bool issue_stream(Smem& sm, const Work& w) {
             tq::mma_ts(kOCol + 128 * s, kSCol + 128 * s + 8 * ks, v + ks * (2048 >> 4), kIdescO, ks ? 1u : (uint32_t)(i > 0));
           tq::mma_commit(&sm.odone[s][part]);
         }
-        __syncwarp();
       }
     }
     tc_after();
@@ -388,6 +429,14 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
   extern __shared__ unsigned char smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  if (tid < 3) {
+    const CUtensorMap* map = tid == 0 ? &qmap : tid == 1 ? &kmap : &vmap;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+  }
+  // What runs before may have written everything that is read from here on; what comes after waits
+  // for this kernel's end in the same way.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- the CTA's work.  Sequence b's CTAs are numbered from ⌊q_starts[b] / per_cta⌋ + b on, which
   // leaves each enough numbers; the last tokens of a sequence, which attend most, come first
@@ -618,34 +667,49 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
   if (warp == kIssueWarp) tq::tmem_dealloc(sm.tmem, 512);
 }
 
-// Records of a row joined with their log-sum-exp weights: a warp per row.
+// Records of a row joined with their log-sum-exp weights: four warps a row, each every fourth record.
 template <bool kBf16>
-__global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptArgs a) {
-  const long long rows = (long long)a.total_q * a.Hq, row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(128) prompt_merge_kernel(const PromptArgs a) {
+  __shared__ float4 acc[4][32];
+  __shared__ float2 part[4];
+  const long long rows = (long long)a.total_q * a.Hq, row = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // rows of no sequence are left as they are
-  if (row >= rows || row / a.Hq < a.q_starts[0] || row / a.Hq >= a.q_starts[a.batch]) return;
+  if (row / a.Hq < a.q_starts[0] || row / a.Hq >= a.q_starts[a.batch]) return;
   const float* rec = a.rec + row * kRecFloats;
-  float m = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) {
-    const float2 ml = *reinterpret_cast<const float2*>(rec + s * rows * kRecFloats + 128);
-    if (ml.y != 0.f) m = fmaxf(m, ml.x);
-  }
-  float l = 0.f;
+  float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int s = 0; s < a.splits; ++s) {
-    const float* r = rec + s * rows * kRecFloats;
-    const float2 ml = *reinterpret_cast<const float2*>(r + 128);
-    const float4 x = *reinterpret_cast<const float4*>(r + 4 * lane);
-    if (ml.y == 0.f) continue;             // (attends nothing there)
-    const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
-    l = fmaf(ml.y, f, l);
-    o.x = fmaf(x.x, f, o.x);
-    o.y = fmaf(x.y, f, o.y);
-    o.z = fmaf(x.z, f, o.z);
-    o.w = fmaf(x.w, f, o.w);
+  for (int s0 = warp; s0 < a.splits; s0 += 16) {
+    float2 ml[4];
+    float4 x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.f);
+      x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float* r = rec + (s0 + 4 * k) * rows * kRecFloats;
+      if (s0 + 4 * k < a.splits) {
+        ml[k] = *reinterpret_cast<const float2*>(r + 128);
+        x[k] = *reinterpret_cast<const float4*>(r + 4 * lane);
+      }
+    }
+    join4(ml, x, m, l, o);
   }
+  acc[warp][lane] = o;
+  if (lane == 0) part[warp] = make_float2(m, l);
+  __syncthreads();
+  if (warp) return;
+  float2 ml[4];
+  float4 x[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    ml[k] = part[k];
+    x[k] = acc[k][lane];
+  }
+  m = -INFINITY, l = 0.f;
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+  join4(ml, x, m, l, o);
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * TQ_D) + lane;
   *dst = make_uint2(pack<kBf16>(o.x * inv, o.y * inv), pack<kBf16>(o.z * inv, o.w * inv));
@@ -734,11 +798,22 @@ tq_status launch(const CUtensorMap (&maps)[3], const PromptArgs& a, long long gr
       return TQ_ERR_CUDA;
     configured[dev] = true;
   }
-  prompt_kernel<kBf16><<<(unsigned)grid, kThreads, smem, stream>>>(maps[0], maps[1], maps[2], a);
-  if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, prompt_kernel<kBf16>, maps[0], maps[1], maps[2], a) != cudaSuccess) return TQ_ERR_CUDA;
   if (a.splits > 1) {
-    const long long rows = (long long)a.total_q * a.Hq;
-    prompt_merge_kernel<kBf16><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(a);
+    cfg.gridDim = dim3((unsigned)((long long)a.total_q * a.Hq));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    if (cudaLaunchKernelEx(&cfg, prompt_merge_kernel<kBf16>, a) != cudaSuccess) return TQ_ERR_CUDA;
   }
   return tq_cuda_status(cudaGetLastError());
 }
