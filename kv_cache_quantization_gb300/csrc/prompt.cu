@@ -204,10 +204,10 @@ __device__ __forceinline__ Stream stream_of(const PromptArgs& a, const Work& w, 
 }
 
 template <bool kBf16>
-__device__ __forceinline__ void put16(const PromptArgs& a, long long row, const float (&o)[16], float inv, int c) {
+__device__ __forceinline__ void put32(const PromptArgs& a, long long row, const float (&o)[32], float inv, int c) {
   uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * TQ_D + c);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < 4; ++i)
     dst[i] = make_uint4(pack<kBf16>(o[8 * i] * inv, o[8 * i + 1] * inv), pack<kBf16>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
                         pack<kBf16>(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack<kBf16>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
 }
@@ -468,8 +468,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
   w.pair = w.ntok > a.tokens;
   w.free_to = w.limit(a, w.tok0);
   const int total = (w.limit(a, w.tok0 + w.ntok - 1) + kTile - 1) / kTile;
-  w.j0 = (int)((long long)total * w.split / a.splits);
-  w.n = (int)((long long)total * (w.split + 1) / a.splits) - w.j0;
+  // (2^21 tiles and 2^10 parts at most: 32 bits hold the products)
+  w.j0 = (int)((uint32_t)total * w.split / a.splits);
+  w.n = (int)((uint32_t)total * (w.split + 1) / a.splits) - w.j0;
   // (pairs: stream 0's tokens come first and attend fewer tiles)
   w.n0 = w.pair ? min(max((w.limit(a, w.tok0 + a.tokens - 1) + kTile - 1) / kTile - w.j0, 0), w.n) : w.n;
   // tiles that some row does not attend in full: the last `guarded` ones
@@ -514,73 +515,75 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
       const bool there = r < a.tokens * a.G && token < w.tok0 + w.ntok;
       const long long row = (long long)(w.q0 + token) * a.Hq + w.h * a.G + r % a.G;
       const uint32_t ocol = ((uint32_t)(32 * warp4) << 16) + kOCol + 128 * s;
-      float* part = reinterpret_cast<float*>(sm.kv[0]) + r * kRecFloats;      // (the ring is done with)
-      float mine = 1.f, other = 0.f;       // factors of the two streams' parts of a row
+      // Columns [c0, c1) of the row are this thread's.  Alternating streams hold parts of the same rows:
+      // each gives the other one half of its columns (through the ring, which is done with) and keeps
+      // the other half.
+      int c0 = 0, c1 = 128;
+      float mine = 1.f, other = 0.f;       // factors of its own part and the other one's
+      float4* given = reinterpret_cast<float4*>(sm.kv[0]) + r;               // [stream][16][row]
+      float2* stats = reinterpret_cast<float2*>(sm.kv[2]) + r;               // [stream][row]
       if (!w.pair) {
-        if (s == 1) {
+        if (w.n > 1) {
+          c0 = 64 * s;
+          c1 = c0 + 64;
+          stats[kTile * s] = make_float2(ref, sum);
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 16) {
-            float o[16];
-            if (st.count > 0) {
-              tmem_load16(ocol + c, reinterpret_cast<uint32_t*>(o));
-              tq::tmem_wait_ld();
-            }
+          for (int c = 0; c < 64; c += 32) {
+            float o[32];
+            tq::tmem_ld_32x32b_x32(ocol + (64 - c0) + c, reinterpret_cast<uint32_t*>(o));
+            tq::tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 16; k += 4)
-              *reinterpret_cast<float4*>(part + c + k) =
-                  st.count > 0 ? make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < 32; k += 4)
+              given[(16 * s + (c + k) / 4) * kTile] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
           }
-          *reinterpret_cast<float2*>(part + 128) = make_float2(ref, sum);
-        }
-        tq::named_sync(kBarSoftmax, 256);
-        if (s == 0) {
-          const float2 rs = *reinterpret_cast<const float2*>(part + 128);
+          tq::named_sync(kBarSoftmax, 256);
+          const float2 rs = stats[kTile * (s ^ 1)];
           const float both = fmaxf(ref, rs.x);
           mine = ref == -INFINITY ? 0.f : ex2(ref - both);
           other = rs.x == -INFINITY ? 0.f : ex2(rs.x - both);
           sum = sum * mine + rs.y * other;     // (a NaN sum stays)
           ref = both;
+        } else if (s == 1) {
+          c1 = 0;                              // (one tile: stream 0's)
         }
       }
-      if (w.pair || s == 0) {
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        float* rec = a.rec + ((long long)w.split * a.total_q * a.Hq + row) * kRecFloats;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      float* rec = a.rec + ((long long)w.split * a.total_q * a.Hq + row) * kRecFloats;
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 16) {
-          float o[16];
+      for (int c = c0; c < c1; c += 32) {
+        float o[32];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = 0.f;
-          if (st.count > 0) {
-            tmem_load16(ocol + c, reinterpret_cast<uint32_t*>(o));
-            tq::tmem_wait_ld();
-          }
-          if (!w.pair) {
+        for (int k = 0; k < 32; ++k) o[k] = 0.f;
+        if (st.count > 0) {
+          tq::tmem_ld_32x32b_x32(ocol + c, reinterpret_cast<uint32_t*>(o));
+          tq::tmem_wait_ld();
+        }
+        if (!there) continue;
+        if (!w.pair && w.n > 1) {
 #pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-              const float4 x = *reinterpret_cast<const float4*>(part + c + k);
-              o[k] = fmaf(o[k], mine, x.x * other);
-              o[k + 1] = fmaf(o[k + 1], mine, x.y * other);
-              o[k + 2] = fmaf(o[k + 2], mine, x.z * other);
-              o[k + 3] = fmaf(o[k + 3], mine, x.w * other);
-            }
-          }
-          if (!there) continue;
-          if (poison) {
-            const int first = max(w.free_to, w.j0 * kTile), n = min(w.limit(a, token), (w.j0 + w.n) * kTile) - first;
-            const uint16_t* v = a.v + (long long)(w.k0 + first) * a.v_t + w.h * a.v_h + c;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = give_back<kBf16>(v + k, a.v_t, n, o[k]);
-          }
-          if (a.splits > 1) {
-#pragma unroll
-            for (int k = 0; k < 16; k += 4)
-              *reinterpret_cast<float4*>(rec + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-          } else {
-            put16<kBf16>(a, row, o, inv, c);
+          for (int k = 0; k < 32; k += 4) {
+            const float4 x = given[(16 * (s ^ 1) + (c - c0 + k) / 4) * kTile];
+            o[k] = fmaf(o[k], mine, x.x * other);
+            o[k + 1] = fmaf(o[k + 1], mine, x.y * other);
+            o[k + 2] = fmaf(o[k + 2], mine, x.z * other);
+            o[k + 3] = fmaf(o[k + 3], mine, x.w * other);
           }
         }
-        if (there && a.splits > 1) *reinterpret_cast<float2*>(rec + 128) = make_float2(ref, sum);
+        if (poison) {
+          const int first = max(w.free_to, w.j0 * kTile), n = min(w.limit(a, token), (w.j0 + w.n) * kTile) - first;
+          const uint16_t* v = a.v + (long long)(w.k0 + first) * a.v_t + w.h * a.v_h + c;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = give_back<kBf16>(v + k, a.v_t, n, o[k]);
+        }
+        if (a.splits > 1) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<float4*>(rec + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+        } else {
+          put32<kBf16>(a, row, o, inv, c);
+        }
       }
+      if (there && a.splits > 1 && c0 == 0 && c1) *reinterpret_cast<float2*>(rec + 128) = make_float2(ref, sum);
     }
   } else {
     if (warp == kLoadWarp) {
@@ -735,14 +738,18 @@ tq_status make_plan(const tq_prompt_desc* d, Plan* p) {
   p->tokens = kTile / p->G;
   const int n = tq_num_sms();
   const long long sms = n > 0 ? n : 152;
-  auto ctas = [&](long long per) { return (d->total_q / per + d->batch) * d->kv_heads; };
+  // CTAs for sequences of about the same length (the lengths lie on the device; the grid is for any).
+  const long long each = d->batch ? (d->total_q + d->batch - 1) / d->batch : 0;
+  auto ctas = [&](long long per) { return std::max<long long>(1, d->batch * ((each + per - 1) / per) * d->kv_heads); };
   // Two blocks of rows a CTA where that fills the GPU, else one.
   p->per_cta = ctas(2 * p->tokens) >= sms ? 2 * p->tokens : p->tokens;
-  p->tiles = (int)(ctas(p->per_cta) / d->kv_heads);
-  const long long units = std::max<long long>(ctas(p->per_cta), 1);
-  // Keys split so that the CTAs fill the GPU once, each with at least four tiles.
+  p->tiles = d->total_q / p->per_cta + d->batch;
+  // Keys split so that the CTAs fill the GPU once, each with at least two tiles: a second CTA costs an
+  // SM its start and end again, about 5 us (one token of 8 sequences behind 8192 keys, 32 units of 64
+  // tiles: 4 parts 32 us, 5 parts 45, 9 parts 36; 2 sequences and 4096 keys: 16 parts 11.4 us, 8 parts 13).
   const long long key_tiles = ((long long)d->max_k_len + kTile - 1) / kTile;
-  p->splits = (int)std::max<long long>(1, std::min<long long>(sms / units, key_tiles / 4));
+  p->splits = (int)std::max<long long>(1, std::min<long long>(std::min<long long>(sms / ctas(p->per_cta), key_tiles / 2), 1023));
+  const long long units = (long long)p->tiles * d->kv_heads;
   if (units * p->splits > 0x7fffffffLL) return TQ_ERR_UNSUPPORTED;
   p->bytes = 256;
   if (p->splits > 1) p->bytes += (size_t)p->splits * d->total_q * d->q_heads * kRecFloats * sizeof(float);
