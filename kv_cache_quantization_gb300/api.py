@@ -650,12 +650,6 @@ class PrefixPlan:
 
 # ------------------------------------------------------------------ rotary positions
 
-def _span(t: torch.Tensor):
-    """First byte and the one behind the last that a tensor without negative strides reaches."""
-    n = sum((d - 1) * s for d, s in zip(t.shape, t.stride())) + 1
-    return t.data_ptr(), t.data_ptr() + n * t.element_size()
-
-
 class Rotary:
     """Rotary positions (include/tq.h, tq_rotary): angles position · f_i on pairs of the first
     rotary_dim coordinates, neighbouring ones (interleaved) or halves.  Frequencies are
@@ -679,43 +673,34 @@ class Rotary:
 
     @staticmethod
     def _io(x, y, name, batch, tokens, dtype):
-        sx, sy = x.stride(), y.stride()
-        shape = x.shape
+        sx, sy, shape = x.stride(), y.stride(), x.shape
         if len(shape) != 4 or shape[0] != batch or shape[2] != tokens or shape[3] != HEAD_DIM or x.dtype != dtype or \
                 y.shape != shape or y.dtype != dtype or sx[3] != 1 or sy[3] != 1:
             raise ValueError(f"{name} must be [{batch}, heads, {tokens}, {HEAD_DIM}] of {dtype} with contiguous "
                              f"last dim, and its output the same, got {x.dtype} {list(shape)} and {y.dtype} "
                              f"{list(y.shape)}")
-        if y is not x and (x.data_ptr() != y.data_ptr() or sx != sy):
-            (a, b), (c, d) = _span(x), _span(y)
-            if a < d and c < b:
-                raise ValueError(f"the output of {name} must be {name} itself or memory apart from it")
-        # every vector has a place of its own: dims by stride, none inside another's
-        at = HEAD_DIM
-        for s, n in sorted(zip(sy[:3], shape[:3])):
-            if n > 1:
-                if s < at:
-                    raise ValueError(f"vectors of the output of {name} overlap")
-                at = s * n
         return B.tq_rotary_io(x.data_ptr(), y.data_ptr(), shape[1], sx[0], sx[1], sx[2], sy[0], sy[1], sy[2])
 
     def apply(self, q, k, positions, q_out=None, k_out=None, stream=None):
         """Turns q and k [batch, heads, tokens, 128] (any strides, k may be None) by their positions,
-        int32 [batch, tokens], in one launch; into q_out and k_out, or in place.  Returns both."""
-        q_out = q if q_out is None else q_out
+        int32 [batch, tokens], in one launch; into q_out and k_out, memory apart from the inputs, or in
+        place.  Returns both."""
+        if q_out is None:
+            q_out = q
         batch, tokens = positions.shape
-        if positions.dtype != torch.int32 or (tokens > 1 and positions.stride(1) != 1):
+        ps, dtype = positions.stride(), q.dtype
+        if positions.dtype != torch.int32 or (tokens > 1 and ps[1] != 1):
             raise ValueError("positions must be int32 [batch, tokens] with contiguous rows")
-        io_q = self._io(q, q_out, "q", batch, tokens, q.dtype)
         io_k = None
         if k is None:
             d = _device(q, positions, q_out)
         else:
-            k_out = k if k_out is None else k_out
+            if k_out is None:
+                k_out = k
             d = _device(q, k, positions, q_out, k_out)
-            io_k = self._io(k, k_out, "k", batch, tokens, q.dtype)
-        st = B.load().tq_rotary_apply(self._c, tq_dtype(q.dtype), batch, tokens, positions.data_ptr(),
-                                      positions.stride(0), io_q, io_k, _on(stream, d))
+            io_k = self._io(k, k_out, "k", batch, tokens, dtype)
+        st = B.load().tq_rotary_apply(self._c, tq_dtype(dtype), batch, tokens, positions.data_ptr(), ps[0],
+                                      self._io(q, q_out, "q", batch, tokens, dtype), io_k, _on(stream, d))
         if st:
             B.check(st, "tq_rotary_apply")
         return q_out, k_out
@@ -811,18 +796,19 @@ def keep_tokens(k: ProdCache, v: MSECache, pos, keep, stream=None):
     """Keeps tokens of those behind pos[b] (int32 [batch]): for each entry j ≥ 0 of keep, int32 [batch,
     at most 64], the codes of token pos[b] + j become those of token pos[b] + i, i the entry's index
     (include/tq.h, tq_keep_tokens)."""
-    (batch,) = pos.shape
     kl, vl, slots = k._layout or k.layout(), v._layout or v.layout(), k.capacity
-    if not (_fits(kl, k.pages, batch, kl[1], slots) and _fits(vl, v.pages, batch, kl[1], slots)) or kl[4] != vl[4]:
+    n = keep.shape
+    if len(n) != 2:
+        raise ValueError("keep must be int32 [batch, tokens]")
+    batch, heads = n[0], kl[1]
+    if not (_fits(kl, k.pages, batch, heads, slots) and _fits(vl, v.pages, batch, heads, slots)) or kl[4] != vl[4]:
         raise ValueError(f"expected caches of {batch} sequences or block tables for them, of the same heads and "
                          f"slots on one device, got keys {list(k.xnorm.shape)} and values {list(v.xnorm.shape)}")
     _expect(pos, (batch,), torch.int32, "pos")
-    if keep.dim() != 2:
-        raise ValueError("keep must be int32 [batch, tokens]")
-    _expect(keep, (batch, keep.shape[1]), torch.int32, "keep")
+    _expect(keep, n, torch.int32, "keep")
     d = _device(k.idx, pos, keep)
-    st = B.load().tq_keep_tokens(k.c(), kl[3] + 1, v.c(), vl[3], batch, kl[1], slots, pos.data_ptr(),
-                                 keep.data_ptr(), keep.shape[1], _on(stream, d))
+    st = B.load().tq_keep_tokens(k.c(), kl[3] + 1, v.c(), vl[3], batch, heads, slots, pos.data_ptr(),
+                                 keep.data_ptr(), n[1], _on(stream, d))
     if st:
         B.check(st, "tq_keep_tokens")
 
@@ -832,26 +818,35 @@ def copy_pages(src, dst, k: Optional[ProdCache] = None, v: Optional[MSECache] = 
     """Copies page src[i] to page dst[i] (int32 [n], −1: passed over) of a pool in every array given: its
     keys, values and block bounds (include/tq.h, tq_copy_pages).  Of a flat cache the sequences are
     the pages."""
-    kl = k and (k._layout or k.layout())
-    vl = v and (v._layout or v.layout())
-    shapes = {x[:3] + x[4:] for x in (kl, vl) if x}
+    pools, kc, vc, bc, kbits, vbits = [], None, None, None, 0, 0      # (pages, heads, slots, device) of each
+    if k is not None:
+        pages, heads, slots, bits, at = k._layout or k.layout()
+        pools.append((pages, heads, slots, at))
+        kc, kbits = k.c(), bits + 1
+    if v is not None:
+        pages, heads, slots, vbits, at = v._layout or v.layout()
+        pools.append((pages, heads, slots, at))
+        vc = v.c()
     if blocks is not None:
-        s, t = blocks.bounds.shape, blocks.bounds
-        if len(s) != 5 or s[3:] != (2, HEAD_DIM) or t.dtype != torch.bfloat16 or not t.is_contiguous():
+        t = blocks.bounds
+        s = t.shape
+        if len(s) != 5 or s[3] != 2 or s[4] != HEAD_DIM or t.dtype != torch.bfloat16 or not t.is_contiguous():
             raise ValueError(f"bounds must be contiguous bfloat16 [pages, heads, blocks, 2, 128], got {t.dtype} {list(s)}")
-        shapes.add((s[0], s[1], s[2] * B.TQ_BLOCK_TOKENS, t.get_device()))
-    if len(shapes) != 1:
+        pools.append((s[0], s[1], s[2] * B.TQ_BLOCK_TOKENS, t.get_device()))
+        bc = blocks.c()
+    if not pools or any(p != pools[0] for p in pools):
         raise ValueError("expected keys, values or bounds of pools of one shape on one device, got "
-                         + (", ".join(str(list(x[:3])) for x in sorted(shapes)) or "none"))
-    ((pages, heads, slots, where),) = shapes
-    n = len(src)
-    _expect(src, (n,), torch.int32, "src")
-    _expect(dst, (n,), torch.int32, "dst")
+                         + (", ".join(str(list(p[:3])) for p in pools) or "none"))
+    pages, heads, slots, at = pools[0]
+    n = src.shape
+    if len(n) != 1:
+        raise ValueError("src must be int32 [n]")
+    _expect(src, n, torch.int32, "src")
+    _expect(dst, n, torch.int32, "dst")
     d = _device(src, dst)
-    if where != d:
+    if at != d:
         raise ValueError(f"expected a pool on the current device cuda:{d}")
-    st = B.load().tq_copy_pages(k and k.c(), kl[3] + 1 if k else 0, v and v.c(), vl[3] if v else 0,
-                                blocks and blocks.c(), heads, pages, slots, src.data_ptr(), dst.data_ptr(), n,
+    st = B.load().tq_copy_pages(kc, kbits, vc, vbits, bc, heads, pages, slots, src.data_ptr(), dst.data_ptr(), n[0],
                                 _on(stream, d))
     if st:
         B.check(st, "tq_copy_pages")

@@ -180,8 +180,9 @@ __global__ void __launch_bounds__(256) rotary_any_kernel(const __grid_constant__
   }
 }
 
-// One side of a call in bytes; false for a bad one.
-bool side_of(const tq_rotary_io* io, int elem, Side* s, bool* vec) {
+// One side of a call in bytes; false for a bad one: among others an output whose vectors overlap each
+// other (no dimension may lie inside another one's step) or the input without being the input.
+bool side_of(const tq_rotary_io* io, int batch, int tokens, int elem, Side* s, bool* vec) {
   *s = Side{};
   if (!io || io->heads == 0) return true;
   if (io->heads < 0 || !io->x || !io->y) return false;
@@ -193,8 +194,20 @@ bool side_of(const tq_rotary_io* io, int elem, Side* s, bool* vec) {
     if (x < 0) return false;
     low |= (uintptr_t)(x * elem);
   }
-  if (io->x == io->y && (strides[0] != strides[3] || strides[1] != strides[4] || strides[2] != strides[5]))
-    return false;
+  const int64_t n[3] = {batch, io->heads, tokens};
+  int64_t x_span = TQ_D, y_span = TQ_D;       // elements from the first to behind the last
+  bool same = io->x == io->y;
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int a, int b) { return strides[3 + a] < strides[3 + b]; });
+  for (int d : order) {
+    if (n[d] == 1) continue;
+    if (strides[3 + d] < y_span) return false;
+    same = same && strides[d] == strides[3 + d];
+    x_span += (n[d] - 1) * strides[d];
+    y_span += (n[d] - 1) * strides[3 + d];
+  }
+  const char *x0 = static_cast<const char*>(io->x), *y0 = static_cast<const char*>(io->y);
+  if (!same && x0 < y0 + y_span * elem && y0 < x0 + x_span * elem) return false;
   *vec = *vec && low % 16 == 0;
   *s = Side{static_cast<const char*>(io->x), static_cast<char*>(io->y), strides[0] * elem, strides[1] * elem,
             strides[2] * elem, strides[3] * elem, strides[4] * elem, strides[5] * elem};
@@ -265,7 +278,7 @@ extern "C" tq_status tq_rotary_apply(const tq_rotary* r, tq_dtype dtype, int32_t
   RotaryArgs a{};
   bool vec = r->rotary_dim % 16 == 0;
   const int elem = dtype == TQ_F32 ? 4 : 2;
-  if (!side_of(q, elem, &a.q, &vec) || !side_of(k, elem, &a.k, &vec)) return TQ_ERR_INVALID_ARG;
+  if (!side_of(q, batch, tokens, elem, &a.q, &vec) || !side_of(k, batch, tokens, elem, &a.k, &vec)) return TQ_ERR_INVALID_ARG;
   const long long qh = q ? q->heads : 0, heads = qh + (k ? k->heads : 0);
   if (heads > (1 << 20)) return TQ_ERR_UNSUPPORTED;
   a.rows = (long long)batch * tokens;

@@ -198,5 +198,5 @@ def test_refusals_on_the_gpu():
                 lambda: r.apply(x[:, :3], None, at, x[:, 1:]),                       # shifted by a head
                 lambda: r.apply(x, None, at, room[:, :1].expand(-1, 4, -1, -1)),     # all heads in one place
                 lambda: r.apply(x.transpose(-1, -2).contiguous().transpose(-1, -2), None, at)):
-        with pytest.raises((ValueError, TypeError)):
+        with pytest.raises((ValueError, TypeError, B.TQError)):
             bad()

@@ -68,7 +68,7 @@ def test_rotary_refuses(kw):
         api.Rotary(**kw)
 
 
-def io(x=OK16, y=OK16 + 65536, heads=2, xs=(1024, 512, 128), ys=(1024, 512, 128)):
+def io(x=OK16, y=OK16 + 65536, heads=2, xs=(1024, 512, 128), ys=(1024, 512, 128)):      # [1][2][4][128] in the calls
     return B.tq_rotary_io(x, y, heads, *xs, *ys)
 
 
@@ -87,15 +87,18 @@ def test_rotary_apply_refuses():
     call(INVALID, r=B.tq_rotary())
     call(INVALID, r=B.tq_rotary(130, 0, 1.0))
     for bad in (io(x=0), io(y=0), io(x=OK16 + 1), io(y=OK16 + 65537), io(heads=-1), io(xs=(1024, -1, 128)), io(ys=(1024, 512, -128)),
-                io(y=OK16, ys=(1024, 512, 256))):
+                io(y=OK16, ys=(1024, 512, 256)),                      # the input with other strides
+                io(y=OK16 + 256), io(y=OK16 + 1984), io(x=OK16 + 1984, y=OK16),          # overlapping the input
+                io(ys=(1024, 512, 64)), io(ys=(1024, 0, 128)), io(ys=(1024, 256, 128))):  # vectors over each other
         call(INVALID, q=bad)
         call(INVALID, k=bad)
     call(INVALID, dtype=B.TQ_F32, q=io(x=OK16 + 2))
-    call(UNSUPPORTED, q=io(heads=1 << 20))
+    call(UNSUPPORTED, q=io(y=1 << 40, heads=1 << 20))
     call(B.TQ_OK, q=None, k=None)               # nothing to do
     call(B.TQ_OK, batch=0)
     call(B.TQ_OK, tokens=0)
     call(B.TQ_OK, q=io(x=0, y=0, heads=0), k=None)
+    call(INVALID, q=io(y=OK16 + 2046), k=None)          # one coordinate short of apart
 
 
 def test_rotary_python_layer_refuses():
