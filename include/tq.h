@@ -442,7 +442,8 @@ tq_status tq_prefix_attention(const tq_attn_desc* desc, const tq_codec* kc, cons
  * seq_lens[b] tokens and those drafted tokens j whose bit j is set in its mask (its ancestors and
  * itself; any mask is allowed), in one softmax of the estimator scores ([QJL] §五, §六).  The
  * drafted keys and values were appended behind the history: node j is token seq_lens[b] + j.
- *   q, out   : device [batch][n_nodes][q_heads][128] of desc->q_dtype / desc->out_dtype.
+ *   q, out   : device [batch][n_nodes][q_heads][128] of desc->q_dtype / desc->out_dtype; out 16-byte
+ *              aligned.
  *   tree     : device uint64 [batch][n_nodes], rows tree_stride_b elements apart (0: one tree for
  *              all sequences); bits n_nodes and above are not read.
  *   desc->max_seq_len bounds seq_lens[b] + n_nodes (longer histories are clamped and flagged).

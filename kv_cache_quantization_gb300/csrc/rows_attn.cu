@@ -87,7 +87,8 @@ constexpr int kThreads = 768;
 constexpr int kRegsLaunch = 80;
 template <bool kFine>
 struct Regs {
-  static constexpr int softmax = kFine ? 96 : 80, expand = kFine ? 72 : 88, issue = kFine ? 72 : 56;
+  static constexpr bool kWide = kFine || kTree;      // (trees hold 32 scores a thread)
+  static constexpr int softmax = kWide ? 96 : 80, expand = kWide ? 72 : 88, issue = kWide ? 72 : 56;
 };
 constexpr int kRecFloats = 132;         // acc[128], m, l, padding
 constexpr int kLBO = 2048;              // bytes between 8-position chunks of an operand image
@@ -561,8 +562,9 @@ __device__ __forceinline__ int clamp_len(int len, int most) {
   return len < 0 ? 0 : len;
 }
 
-// Which drafted tokens a row attends (trees): token t is the item's token j0 + t of them, the ones
-// before them (the history) are all attended, and those past the length have no weight anyway.
+#ifdef TQ_ROWS_TREE
+// Which drafted tokens a row attends: token t is the item's token j0 + t of them, the ones before them
+// (the history) are all attended, and those past the length have no weight anyway.
 struct RowMask {
   unsigned long long seen;
   int j0;
@@ -575,12 +577,165 @@ struct RowMask {
     return j < TQ_TREE_NODES ? (uint32_t)(seen >> j) : 0u;
   }
 };
+#endif
 
 // What a softmax thread ends with.
 struct Stats {
   float m, l;
   bool ok;
 };
+
+#ifdef TQ_ROWS_TREE
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// The softmax of every tile by 8 warps: thread (lane group wl, half hf) of TMEM lane 32·wl + lane, rows
+// in one, two or four lane groups (reps) as below.  A thread's scores go kN at a time, 32 where it has
+// as many, so that an item of at most 64 rows keeps them in registers between the passes and one of
+// 128 rows goes twice: a pass waits for TMEM and shared memory once for each.
+template <bool kFine, int kN>
+__device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int reps, int wl, int hf, int lane,
+                                               float f, const RowMask& mask) {
+  const int rep = wl / (4 / reps), groups = 4 / reps;       // groups of 16 tokens per thread
+  const int group0 = (2 * rep + hf) * groups;
+  const uint32_t lane_base = (uint32_t)(32 * wl) << 16;
+  const int r = 32 * wl + lane;
+  const tq::f32x2 f2 = tq::pack2(f, f);
+  Stats z{-INFINITY, 0.f, true};
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, unsigned parity) { return ok = ok && warp_wait(bar, parity); };
+#pragma unroll 1
+  for (int t = 0; t < tiles; ++t) {
+    const int buf = kFine ? 0 : t & 1;
+    wait(&sm.ffull[t % kFacSlots], (t / kFacSlots) & 1);
+    wait(&sm.sfull[buf], (kFine ? t : t >> 1) & 1);
+    tc_after();
+    const uint32_t dcol = lane_base + kDCol + 128 * buf + 16 * group0;
+    const float* fx = sm.fac[t % kFacSlots][0] + 16 * group0;
+    float mt = -INFINITY;
+    uint32_t d[kN];      // the last scores stay here, the others go back to TMEM
+#pragma unroll 1
+    for (int c = 0;; c += kN) {
+      tmem_load<kN>(dcol + c, d);
+      tq::tmem_wait_ld();
+      float* e = reinterpret_cast<float*>(d);
+#pragma unroll
+      for (int i = 0; i < kN; i += 4) {
+        const float4 xn = *reinterpret_cast<const float4*>(fx + c + i);
+        const float4 lv = *reinterpret_cast<const float4*>(fx + kTile + c + i);
+        const float2 x = tq::unpack2(tq::fma2(tq::mul2(tq::pack2(e[i], e[i + 1]), f2),
+                                              tq::pack2(xn.x, xn.y), tq::pack2(lv.x, lv.y)));
+        const float2 y = tq::unpack2(tq::fma2(tq::mul2(tq::pack2(e[i + 2], e[i + 3]), f2),
+                                              tq::pack2(xn.z, xn.w), tq::pack2(lv.z, lv.w)));
+        e[i] = x.x; e[i + 1] = x.y; e[i + 2] = y.x; e[i + 3] = y.y;
+      }
+      // (uniform: the same tokens for all rows of an item)
+      const int token = t * kTile + 16 * group0 + c;
+      if (mask.j0 + token > -kN) {
+#pragma unroll
+        for (int g = 0; g < kN; g += 16) {
+          const uint32_t seen = mask.at(token + g);
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (!(seen >> k & 1u)) e[g + k] = -INFINITY;
+        }
+      }
+      float m0 = e[0], m1 = e[1];
+#pragma unroll
+      for (int k = 2; k < kN - 2; k += 4) {
+        m0 = max3(m0, e[k], e[k + 2]);
+        m1 = max3(m1, e[k + 1], e[k + 3]);
+      }
+      mt = max3(mt, max3(m0, e[kN - 2], m1), e[kN - 1]);
+      if (c + kN >= 16 * groups) break;
+      tmem_store<kN>(dcol + c, d);
+    }
+    sm.tmax[t & 1][hf][r] = mt;
+    // A wait that gave up ends both halves' loops here, together (neither then waits for the
+    // other)
+    if (!tq::named_sync_and(1 + wl, 64, ok)) {
+      z.ok = false;
+      return z;
+    }
+    mt = fmaxf(mt, sm.tmax[t & 1][hf ^ 1][r]);
+    const float m_new = mt - z.m > kGrow + kLift ? mt - kLift : z.m;
+    if (t > 0 && __any_sync(0xffffffffu, m_new != z.m)) {
+      // as below: O follows the reference, once O += W(t − 1)·V(t − 1) is done
+      wait(&sm.vempty[(t - 1) & 1], ((t - 1) >> 1) & 1);
+      tc_after();
+      const float corr = z.m == -INFINITY ? 0.f : ex2(z.m - m_new);
+#pragma unroll 1
+      for (int c = 0; c < 64; c += 16) {
+        uint32_t o[16];
+        const uint32_t at = lane_base + kOCol + 64 * hf + c;
+        tmem_load<16>(at, o);
+        tq::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
+        tmem_store<16>(at, o);
+      }
+      z.l *= corr;
+    }
+    z.m = m_new;
+    const float ref = m_new == -INFINITY ? 0.f : m_new;
+    const tq::f32x2 ref2 = tq::pack2(-ref, -ref);
+    tq::f32x2 l2 = tq::pack2(0.f, 0.f), l3 = l2;
+    tq::tmem_wait_st();
+#pragma unroll 1
+    for (int c = 16 * groups - kN;; c -= kN) {
+#pragma unroll
+      for (int g = 0; g < kN; g += 16) {
+        uint32_t w[kFine ? 16 : 8];      // fine: then what the rounding left
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          const float4 iv = *reinterpret_cast<const float4*>(fx + 2 * kTile + c + g + i);
+          const float* e = reinterpret_cast<const float*>(d) + g + i;
+          const float2 x = tq::unpack2(tq::add2(tq::pack2(e[0], e[1]), ref2));
+          const float2 y = tq::unpack2(tq::add2(tq::pack2(e[2], e[3]), ref2));
+          const float w0 = ex2(x.x), w1 = ex2(x.y), w2 = ex2(y.x), w3 = ex2(y.y);
+          l2 = tq::fma2(tq::pack2(w0, w1), tq::pack2(iv.x, iv.y), l2);
+          l3 = tq::fma2(tq::pack2(w2, w3), tq::pack2(iv.z, iv.w), l3);
+          const __half2 p0 = __floats2half2_rn(w0, w1), p1 = __floats2half2_rn(w2, w3);
+          w[i / 2] = *reinterpret_cast<const uint32_t*>(&p0);
+          w[i / 2 + 1] = *reinterpret_cast<const uint32_t*>(&p1);
+          if constexpr (kFine) {
+            const float2 h0 = __half22float2(p0), h1 = __half22float2(p1);
+            const __half2 r0 = __floats2half2_rn(w0 - h0.x, w1 - h0.y);
+            const __half2 r1 = __floats2half2_rn(w2 - h1.x, w3 - h1.y);
+            w[8 + i / 2] = *reinterpret_cast<const uint32_t*>(&r0);
+            w[8 + i / 2 + 1] = *reinterpret_cast<const uint32_t*>(&r1);
+          }
+        }
+        tmem_store<kFine ? 16 : 8>(dcol + c + g, w);
+      }
+      if (c == 0) break;
+      tmem_load<kN>(dcol + c - kN, d);
+      tq::tmem_wait_ld();
+    }
+    const float2 lp = tq::unpack2(tq::add2(l2, l3));
+    z.l += lp.x + lp.y;
+    if (reps > 1) {
+      // the other replicas' groups, every other one by each half
+      const uint32_t none[kFine ? 16 : 8] = {};
+#pragma unroll 1
+      for (int g = hf; g < 8; g += 2)
+        if (g / (2 * groups) != rep) tmem_store<kFine ? 16 : 8>(lane_base + kDCol + 128 * buf + 16 * g, none);
+    }
+    tq::tmem_wait_st();
+    tc_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.pfull[buf]);
+  }
+  wait(&sm.vempty[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1);
+  z.ok = ok;
+  return z;
+}
+
+#else
 
 // The softmax of every tile by 8 warps: thread (lane group wl, half hf) of TMEM lane 32·wl + lane.
 // An item of at most 32 (64) rows holds each row in 4 (2) lane groups, the `reps` replicas of a
@@ -594,7 +749,7 @@ struct Stats {
 // 16 tokens are stored over the first half of its scores, which no other thread reads.
 template <bool kFine>
 __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int reps, int wl, int hf, int lane,
-                                               float f, const RowMask& mask) {
+                                               float f) {
   const int rep = wl / (4 / reps), groups = 4 / reps;       // groups of 16 tokens per thread
   const int group0 = (2 * rep + hf) * groups;
   const uint32_t lane_base = (uint32_t)(32 * wl) << 16;
@@ -615,10 +770,6 @@ __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int reps, in
 #pragma unroll 1
     for (int c = 0;; c += 16) {
       tmem_load<16>(dcol + c, d);
-      // (uniform: the tile's groups of 16 tokens are the same for all rows of an item)
-      const int token = t * kTile + 16 * group0 + c;
-      const bool drafted = kTree && mask.j0 + token > -16;
-      const uint32_t seen = kTree && drafted ? mask.at(token) : 0u;
       tq::tmem_wait_ld();
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
@@ -630,13 +781,7 @@ __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int reps, in
         const float2 y = tq::unpack2(tq::fma2(tq::mul2(tq::pack2(e[2], e[3]), f2),
                                               tq::pack2(xn.z, xn.w), tq::pack2(lv.z, lv.w)));
         e[0] = x.x; e[1] = x.y; e[2] = y.x; e[3] = y.y;
-        if (kTree && drafted) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (!(seen >> (i + k) & 1u)) e[k] = -INFINITY;
-        }
-        mt = kTree ? fmaxf(mt, fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])))
-                   : fmaxf(mt, fmaxf(fmaxf(x.x, x.y), fmaxf(y.x, y.y)));
+        mt = fmaxf(mt, fmaxf(fmaxf(x.x, x.y), fmaxf(y.x, y.y)));
       }
       if (c + 16 >= 16 * groups) break;
       tmem_store<16>(dcol + c, d);
@@ -724,6 +869,8 @@ __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int reps, in
   z.ok = ok;
   return z;
 }
+
+#endif
 
 // Lengths, lists, block tables and codes are read before this kernel's wait: it starts only when all
 // of rows_prep_kernel is past its own wait, so whatever ran before that has ended and been flushed.
@@ -833,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
 
   if (warp < kKeyWarp) {
     // ================================================================ softmax
-    if (kFine) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::softmax));
+    if (R::kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::softmax));
     const int wl = warp & 3, hf = warp >> 2;
     const int per = kTile / reps;              // rows per replica
     const int r = (32 * wl + lane) & (per - 1);
@@ -859,12 +1006,14 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
     tc_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.qfull);
-    RowMask mask{0, 0};
 #ifdef TQ_ROWS_TREE
-    mask.j0 = t0 * kTile - hist;
+    RowMask mask{0, t0 * kTile - hist};
     if (r < rows) mask.seen = a.tree[b * a.tree_b + (rt * kTile + r) / a.G];
+    const Stats z = reps < 4 ? softmax_tiles<kFine, 32>(sm, tiles, reps, wl, hf, lane, f, mask)
+                             : softmax_tiles<kFine, 16>(sm, tiles, reps, wl, hf, lane, f, mask);
+#else
+    const Stats z = softmax_tiles<kFine>(sm, tiles, reps, wl, hf, lane, f);
 #endif
-    const Stats z = softmax_tiles<kFine>(sm, tiles, reps, wl, hf, lane, f, mask);
     // ---- the item's record: lanes' parts through shared memory (the operands are done with),
     // replicas of a row added up with their log-sum-exp weights
     ok = ok && tq::named_sync_and(5, 256, z.ok);
@@ -907,7 +1056,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
     }
   } else if (warp < kIssueWarp) {
     // ================================================================ expanders
-    if (kFine) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::expand));
+    if (R::kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::expand));
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::expand));
     const Item it{t0, tiles, len, nblk, b, h, list};
     if (pre) ok = expand<IB, VB, kFine, false>(a, a.pre, sm, it, warp, lane);
@@ -1158,6 +1307,193 @@ rows_merge_kernel(const float* rec, int nrec, int nrows, const float* __restrict
   }
 }
 
+#ifdef TQ_ROWS_TREE
+// ---------------------------------------------------------------- many rows
+// Trees have 16 and 64 times the rows of a decode step, and the two kernels above then take as long as
+// the attention itself (7168 rows: 28 and 30 us): a CTA reads its matrix for 4 or 8 rows, and its
+// threads get 16 bytes from shared memory for every four products.  These keep a matrix in the
+// registers of 256 threads, several columns a thread, for as many rows as there are (8 at a time), and
+// take the sums of the first kernel in the same order.
+constexpr int kManyThreads = 256, kManyRows = 8;
+
+__global__ void __launch_bounds__(kManyThreads, 1)
+rows_prep_many_kernel(const void* q, int q_dtype, int nrows, int fine, const float* __restrict__ piT,
+                      const float* __restrict__ sT, float factor, __half* qop, float* qf) {
+  __shared__ float qs[kManyRows][TQ_D];
+  __shared__ float part[4][kManyRows][256];
+  __shared__ float scale[kManyRows];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, p = tid & 63, kq = tid >> 6;
+  float w[4][32];   // positions p + 64·o, a quarter of k (the codec's matrices: not of the launch before)
+#pragma unroll
+  for (int o = 0; o < 4; ++o) {
+    const int c = p + 64 * o;
+    const float* mat = (c < 128 ? piT + plane_coord(c) : sT + sign_coord(c - 128)) + 32 * kq * TQ_D;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) w[o][k] = __ldg(mat + k * TQ_D);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // not before the wait: rows_attn_kernel reads lengths and codes before it waits for this one
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int step = gridDim.x * kManyRows;
+  float next[kManyRows * TQ_D / kManyThreads];     // the next rows' queries are in flight meanwhile
+  auto load = [&](int row0) {
+#pragma unroll
+    for (int i = 0; i < kManyRows * TQ_D / kManyThreads; ++i) {
+      const int e = tid + i * kManyThreads;
+      next[i] = row0 + e / TQ_D < nrows ? load_elem(q, q_dtype, (long long)row0 * TQ_D + e) : 0.f;
+    }
+  };
+  load(blockIdx.x * kManyRows);
+  for (int row0 = blockIdx.x * kManyRows; row0 < nrows; row0 += step) {
+#pragma unroll
+    for (int i = 0; i < kManyRows * TQ_D / kManyThreads; ++i) (&qs[0][0])[tid + i * kManyThreads] = next[i];
+    __syncthreads();
+    load(row0 + step < nrows ? row0 + step : row0);
+    {
+      const int r = warp;
+      float m = 0.f;
+      for (int j = lane; j < TQ_D; j += 32) m = fmaxf(m, fabsf(qs[r][j]));
+#pragma unroll
+      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (lane == 0) {
+        int e = 0;      // as above
+        if (m > 0.f && m < INFINITY) frexpf(m, &e);
+        e = min(max(e + 4, -110), 120);
+        scale[r] = ldexpf(1.f, -e);
+        if (row0 + r < nrows) qf[row0 + r] = ldexpf(factor, e);
+      }
+    }
+#pragma unroll 1
+    for (int r = 0; r < kManyRows; ++r) {
+      float s[4] = {};
+#pragma unroll
+      for (int k = 0; k < 32; k += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(&qs[r][32 * kq + k]);
+#pragma unroll
+        for (int o = 0; o < 4; ++o) {
+          s[o] = fmaf(w[o][k], x.x, s[o]);
+          s[o] = fmaf(w[o][k + 1], x.y, s[o]);
+          s[o] = fmaf(w[o][k + 2], x.z, s[o]);
+          s[o] = fmaf(w[o][k + 3], x.w, s[o]);
+        }
+      }
+#pragma unroll
+      for (int o = 0; o < 4; ++o) part[kq][r][p + 64 * o] = s[o];
+    }
+    __syncthreads();
+    // two neighbouring positions a thread, half of the rows each
+    const int c = 2 * (tid & 127);
+#pragma unroll
+    for (int r = tid >> 7; r < kManyRows; r += 2) {
+      if (row0 + r >= nrows) break;
+      const float2 a = *reinterpret_cast<const float2*>(&part[0][r][c]), b = *reinterpret_cast<const float2*>(&part[1][r][c]);
+      const float2 d = *reinterpret_cast<const float2*>(&part[2][r][c]), e = *reinterpret_cast<const float2*>(&part[3][r][c]);
+      const float by = c < 128 ? kAlpha : kBeta;
+      const float x = ((a.x + b.x) + (d.x + e.x)) * scale[r] * by, y = ((a.y + b.y) + (d.y + e.y)) * scale[r] * by;
+      const __half2 h = __floats2half2_rn(x, y);
+      __half2* row = reinterpret_cast<__half2*>(qop + (long long)(row0 + r) * (fine ? 512 : 256) + c);
+      row[0] = h;
+      if (fine) row[128] = __floats2half2_rn(x - __low2float(h), y - __high2float(h));
+    }
+    __syncthreads();
+  }
+}
+
+__global__ void __launch_bounds__(kManyThreads, 2)
+rows_merge_many_kernel(const float* rec, int nrec, int nrows, const float* __restrict__ pi, int nibbles,
+                       float unscale, void* out, int out_dtype) {
+  __shared__ float sum[kManyRows][TQ_D];
+  __shared__ float weight[kManyRows][kMaxRecs];
+  __shared__ float prod[4][kManyRows][TQ_D];
+  __shared__ float total[kManyRows];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, j = tid & 63, kq = tid >> 6;
+  float w[2][32];   // columns j and j + 64 of Π, a quarter of k
+#pragma unroll
+  for (int o = 0; o < 2; ++o)
+#pragma unroll
+    for (int k = 0; k < 32; ++k) w[o][k] = __ldg(pi + (32 * kq + k) * TQ_D + j + 64 * o);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long stride = (long long)nrows * kRecFloats;
+  for (int row0 = blockIdx.x * kManyRows; row0 < nrows; row0 += gridDim.x * kManyRows) {
+    // a warp per row: the records' weights, then their sum, eight reads in flight
+    const float* p = rec + (long long)min(row0 + warp, nrows - 1) * kRecFloats;
+    float m = -INFINITY;
+    for (int s = lane; s < nrec; s += 32) {
+      const float2 ml = *reinterpret_cast<const float2*>(p + s * stride + 128);
+      // an empty record weighs nothing; a NaN sum (a NaN query) makes the row NaN
+      weight[warp][s] = ml.y != ml.y ? ml.y : ml.y != 0.f ? ml.x : -INFINITY;
+      if (ml.y != 0.f) m = fmaxf(m, ml.x);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f;
+    for (int s = lane; s < nrec; s += 32) {
+      const float ls = p[s * stride + 129], ms = weight[warp][s];
+      const float ws = ms == -INFINITY ? 0.f : ex2(ms - m);
+      weight[warp][s] = ws;
+      if (ws != 0.f) l = fmaf(ls, ws, l);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) total[warp] = l;
+    __syncwarp();
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < nrec; i0 += 8) {
+      float4 x[8];
+      float ws[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + k;
+        ws[k] = i < nrec ? weight[warp][i] : 0.f;
+        x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (ws[k] != 0.f) x[k] = *reinterpret_cast<const float4*>(p + i * stride + 4 * lane);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        a.x = fmaf(x[k].x, ws[k], a.x);
+        a.y = fmaf(x[k].y, ws[k], a.y);
+        a.z = fmaf(x[k].z, ws[k], a.z);
+        a.w = fmaf(x[k].w, ws[k], a.w);
+      }
+    }
+    const float v[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum[warp][nibbles ? 4 * lane + k : plane_coord(4 * lane + k)] = v[k];
+    __syncthreads();
+#pragma unroll 1
+    for (int r = 0; r < kManyRows; ++r) {
+      float s[2] = {};
+#pragma unroll
+      for (int k = 0; k < 32; k += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(&sum[r][32 * kq + k]);
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          s[o] = fmaf(w[o][k], x.x, s[o]);
+          s[o] = fmaf(w[o][k + 1], x.y, s[o]);
+          s[o] = fmaf(w[o][k + 2], x.z, s[o]);
+          s[o] = fmaf(w[o][k + 3], x.w, s[o]);
+        }
+      }
+      prod[kq][r][j] = s[0];
+      prod[kq][r][j + 64] = s[1];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = tid; i < kManyRows * TQ_D / 2; i += kManyThreads) {
+      const int r = i >> 6, c = 2 * (i & 63);
+      if (row0 + r >= nrows) continue;
+      const float inv = total[r] == 0.f ? 0.f : unscale / total[r];
+      const float x = ((prod[0][r][c] + prod[1][r][c]) + (prod[2][r][c] + prod[3][r][c])) * inv;
+      const float y = ((prod[0][r][c + 1] + prod[1][r][c + 1]) + (prod[2][r][c + 1] + prod[3][r][c + 1])) * inv;
+      const long long at = (long long)(row0 + r) * TQ_D + c;
+      if (out_dtype == TQ_BF16) *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(out) + at) = __floats2bfloat162_rn(x, y);
+      else *reinterpret_cast<__half2*>(static_cast<__half*>(out) + at) = __floats2half2_rn(x, y);
+    }
+    __syncthreads();
+  }
+}
+#endif
+
 // ---------------------------------------------------------------- host
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -1374,8 +1710,22 @@ int rows_per_cta(int rows, int most) {
   return most;
 }
 
+#ifdef TQ_ROWS_TREE
+// Rows from which on the kernels for many are faster.
+int many_rows() { return 8 * std::max(tq_num_sms(), 1); }
+#endif
+
 tq_status launch_prep(const void* q, int q_dtype, int rows, int fine, const tq_codec* kc, float factor,
                       void* qop, float* qf, cudaStream_t stream) {
+#ifdef TQ_ROWS_TREE
+  if (rows > many_rows()) {
+    const int grid = std::min((rows + kManyRows - 1) / kManyRows, std::max(tq_num_sms(), 1));
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = config(grid, kManyThreads, 0, stream, attr);
+    return tq_cuda_status(cudaLaunchKernelEx(&cfg, rows_prep_many_kernel, q, q_dtype, rows, fine, (const float*)kc->d_piT,
+                                             (const float*)kc->d_sT, factor, static_cast<__half*>(qop), qf));
+  }
+#endif
   const int rp = rows_per_cta(rows, 8);
   auto kern = rp == 1 ? rows_prep_kernel<1> : rp == 2 ? rows_prep_kernel<2>
             : rp == 4 ? rows_prep_kernel<4> : rows_prep_kernel<8>;
@@ -1388,6 +1738,15 @@ tq_status launch_prep(const void* q, int q_dtype, int rows, int fine, const tq_c
 
 tq_status launch_merge(const float* rec, int nrec, int rows, const tq_codec* vc, void* out,
                        int out_dtype, cudaStream_t stream) {
+#ifdef TQ_ROWS_TREE
+  if (rows > many_rows()) {
+    const int grid = std::min((rows + kManyRows - 1) / kManyRows, 2 * std::max(tq_num_sms(), 1));
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = config(grid, kManyThreads, 0, stream, attr);
+    return tq_cuda_status(cudaLaunchKernelEx(&cfg, rows_merge_many_kernel, rec, nrec, rows, (const float*)vc->d_pi,
+                                             vc->ibits == 4 ? 1 : 0, 1.f / vc->lut_scale, out, out_dtype));
+  }
+#endif
   const int rp = rows_per_cta(rows, 4);
   auto kern = rp == 1 ? rows_merge_kernel<1> : rp == 2 ? rows_merge_kernel<2> : rows_merge_kernel<4>;
   cudaLaunchAttribute attr[1];
@@ -1482,6 +1841,7 @@ extern "C" tq_status tq_tree_attention(const tq_attn_desc* desc, int32_t n_nodes
   if (st != TQ_OK) return st;
   RowsArgs a{};
   if (!tree || reinterpret_cast<uintptr_t>(tree) % 8 || tree_stride_b < 0) return TQ_ERR_INVALID_ARG;
+  if (!aligned16(out)) return TQ_ERR_INVALID_ARG;
   if ((st = cache_side(k, v, desc->capacity, &a.own)) != TQ_OK) return st;
   a.seq_lens = seq_lens;
   a.tree = reinterpret_cast<const unsigned long long*>(tree);

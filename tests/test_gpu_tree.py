@@ -115,6 +115,17 @@ def test_tree_types(q_dtype, out_dtype):
     run_tree(4, 2, 2, 2, 4, [9, 70], 7, trees(2, 7, "tree"), 0, q_dtype, out_dtype, seed=7, scale=0.05)
 
 
+@pytest.mark.parametrize("batch,kv,group,nodes,kbits,vbits", [(29, 1, 5, 9, 3, 4), (30, 2, 7, 9, 4, 2), (3, 8, 8, 64, 2, 1)])
+@pytest.mark.parametrize("q_dtype,out_dtype", [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.float16),
+                                               (torch.float16, torch.bfloat16)])
+def test_many_rows(batch, kv, group, nodes, kbits, vbits, q_dtype, out_dtype):
+    """More rows than 8 for each SM: kernels of their own before and after the attention (1305 rows is no
+    multiple of 8)."""
+    lens = [(37 * b) % 150 for b in range(batch)]
+    run_tree(kbits, vbits, batch, kv, group, lens, nodes, trees(batch, nodes, "any", batch), 0, q_dtype, out_dtype, seed=batch)
+    assert flags() == 0
+
+
 @pytest.mark.parametrize("nodes", [15, 16, 17, 31, 32, 33, 48, 63, 64])
 @pytest.mark.parametrize("first", [0, 1, 15, 16, 17, 111, 112, 113, 127])
 def test_every_place_of_the_drafted_tokens_in_a_tile(first, nodes):

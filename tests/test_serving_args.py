@@ -130,6 +130,8 @@ def test_tree_refuses():
     call(INVALID, tree=0)
     call(INVALID, tree=OK16 + 4)
     call(INVALID, tree_b=-1)
+    call(INVALID, out=OK16 + 2)
+    call(INVALID, out=0)
     call(INVALID, d=desc(mx=3))                           # no room for four drafted tokens
     call(UNSUPPORTED, d=desc(out=B.TQ_F32))
     call(UNSUPPORTED, d=desc(batch=1 << 18))              # 28 · 4 · 2^18 query rows
