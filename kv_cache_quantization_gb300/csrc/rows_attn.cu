@@ -224,6 +224,12 @@ __host__ __device__ constexpr int sign_coord(int p) {
   return (p & ~31) + 4 * ((p >> 3) & 3) + ((p & 7) >> 1) + 16 * (p & 1);
 }
 
+// The position of a coordinate: the inverses of these.
+__host__ __device__ constexpr int plane_position(int j) { return (j & ~31) + ((j >> 2) & 7) + 8 * (j & 3); }
+__host__ __device__ constexpr int sign_position(int j) {
+  return (j & ~31) + ((j >> 4) & 1) + 2 * (j & 3) + 8 * ((j >> 2) & 3);
+}
+
 // Eight fp16 levels of eight 3-bit indices (one per nibble of s; with 16 levels `top` holds the
 // fourth bit, 8 | bit per nibble: a permute in sign-replicating mode makes it a byte mask).
 template <bool k16>
@@ -1323,11 +1329,13 @@ rows_prep_many_kernel(const void* q, int q_dtype, int nrows, int fine, const flo
   __shared__ float part[4][kManyRows][256];
   __shared__ float scale[kManyRows];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, p = tid & 63, kq = tid >> 6;
-  float w[4][32];   // positions p + 64·o, a quarter of k (the codec's matrices: not of the launch before)
+  float w[4][32];   // coordinates p and p + 64 of y and of z, a quarter of k (matrices of the codec's)
+  int at[4];        // and their positions in the operand
 #pragma unroll
   for (int o = 0; o < 4; ++o) {
-    const int c = p + 64 * o;
-    const float* mat = (c < 128 ? piT + plane_coord(c) : sT + sign_coord(c - 128)) + 32 * kq * TQ_D;
+    const int c = p + 64 * (o & 1);
+    at[o] = o < 2 ? plane_position(c) : 128 + sign_position(c);
+    const float* mat = (o < 2 ? piT : sT) + 32 * kq * TQ_D + c;
 #pragma unroll
     for (int k = 0; k < 32; ++k) w[o][k] = __ldg(mat + k * TQ_D);
   }
@@ -1356,11 +1364,12 @@ rows_prep_many_kernel(const void* q, int q_dtype, int nrows, int fine, const flo
 #pragma unroll
       for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       if (lane == 0) {
-        int e = 0;      // as above
-        if (m > 0.f && m < INFINITY) frexpf(m, &e);
+        // as above, from the exponent's bits (those of a subnormal m are below −110 anyway)
+        int e = 0;
+        if (m > 0.f && m < INFINITY) e = (int)(__float_as_uint(m) >> 23) - 126;
         e = min(max(e + 4, -110), 120);
-        scale[r] = ldexpf(1.f, -e);
-        if (row0 + r < nrows) qf[row0 + r] = ldexpf(factor, e);
+        scale[r] = __uint_as_float((uint32_t)(127 - e) << 23);
+        if (row0 + r < nrows) qf[row0 + r] = factor * __uint_as_float((uint32_t)(127 + e) << 23);
       }
     }
 #pragma unroll 1
@@ -1378,7 +1387,7 @@ rows_prep_many_kernel(const void* q, int q_dtype, int nrows, int fine, const flo
         }
       }
 #pragma unroll
-      for (int o = 0; o < 4; ++o) part[kq][r][p + 64 * o] = s[o];
+      for (int o = 0; o < 4; ++o) part[kq][r][at[o]] = s[o];
     }
     __syncthreads();
     // two neighbouring positions a thread, half of the rows each
@@ -1403,7 +1412,6 @@ __global__ void __launch_bounds__(kManyThreads, 2)
 rows_merge_many_kernel(const float* rec, int nrec, int nrows, const float* __restrict__ pi, int nibbles,
                        float unscale, void* out, int out_dtype) {
   __shared__ float sum[kManyRows][TQ_D];
-  __shared__ float weight[kManyRows][kMaxRecs];
   __shared__ float prod[4][kManyRows][TQ_D];
   __shared__ float total[kManyRows];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, j = tid & 63, kq = tid >> 6;
@@ -1415,47 +1423,51 @@ rows_merge_many_kernel(const float* rec, int nrec, int nrows, const float* __res
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long stride = (long long)nrows * kRecFloats;
   for (int row0 = blockIdx.x * kManyRows; row0 < nrows; row0 += gridDim.x * kManyRows) {
-    // a warp per row: the records' weights, then their sum, eight reads in flight
+    // a warp per row: the records' statistics and eight of their vectors are in flight together; 32
+    // records at a time, joined to a running sum
     const float* p = rec + (long long)min(row0 + warp, nrows - 1) * kRecFloats;
-    float m = -INFINITY;
-    for (int s = lane; s < nrec; s += 32) {
-      const float2 ml = *reinterpret_cast<const float2*>(p + s * stride + 128);
-      // an empty record weighs nothing; a NaN sum (a NaN query) makes the row NaN
-      weight[warp][s] = ml.y != ml.y ? ml.y : ml.y != 0.f ? ml.x : -INFINITY;
-      if (ml.y != 0.f) m = fmaxf(m, ml.x);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f;
-    for (int s = lane; s < nrec; s += 32) {
-      const float ls = p[s * stride + 129], ms = weight[warp][s];
-      const float ws = ms == -INFINITY ? 0.f : ex2(ms - m);
-      weight[warp][s] = ws;
-      if (ws != 0.f) l = fmaf(ls, ws, l);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (lane == 0) total[warp] = l;
-    __syncwarp();
+    float m = -INFINITY, l = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < nrec; i0 += 8) {
+    for (int s0 = 0; s0 < nrec; s0 += 32) {
+      const float2 ml = s0 + lane < nrec ? *reinterpret_cast<const float2*>(p + (s0 + lane) * stride + 128)
+                                         : make_float2(-INFINITY, 0.f);
       float4 x[8];
-      float ws[8];
+      auto load = [&](int i0) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int i = i0 + k;
-        ws[k] = i < nrec ? weight[warp][i] : 0.f;
-        x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (ws[k] != 0.f) x[k] = *reinterpret_cast<const float4*>(p + i * stride + 4 * lane);
-      }
+        for (int k = 0; k < 8; ++k)
+          x[k] = s0 + i0 + k < nrec ? *reinterpret_cast<const float4*>(p + (s0 + i0 + k) * stride + 4 * lane)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+      };
+      load(0);
+      // an empty record weighs nothing (its vector is not written); a NaN sum (a NaN query) makes the row NaN
+      float top = ml.y != 0.f ? ml.x : -INFINITY;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        a.x = fmaf(x[k].x, ws[k], a.x);
-        a.y = fmaf(x[k].y, ws[k], a.y);
-        a.z = fmaf(x[k].z, ws[k], a.z);
-        a.w = fmaf(x[k].w, ws[k], a.w);
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      top = fmaxf(top, m);
+      const float mine = m == -INFINITY ? 1.f : ex2(m - top);      // (no record so far: sums of 0, or NaN)
+      l *= mine;
+      a.x *= mine; a.y *= mine; a.z *= mine; a.w *= mine;
+      m = top;
+      const float ws = ml.y != ml.y ? ml.y : ml.y == 0.f ? 0.f : ex2(ml.x - m);
+      float sum_l = ws == 0.f ? 0.f : ml.y * ws;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum_l += __shfl_xor_sync(0xffffffffu, sum_l, o);
+      l += sum_l;
+      const int n = min(nrec - s0, 32);
+      for (int i0 = 0; i0 < n; i0 += 8) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float f = __shfl_sync(0xffffffffu, ws, (i0 + k) & 31);
+          if (i0 + k >= n || f == 0.f) continue;
+          a.x = fmaf(x[k].x, f, a.x);
+          a.y = fmaf(x[k].y, f, a.y);
+          a.z = fmaf(x[k].z, f, a.z);
+          a.w = fmaf(x[k].w, f, a.w);
+        }
+        if (i0 + 8 < n) load(i0 + 8);
       }
     }
+    if (lane == 0) total[warp] = l;
     const float v[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) sum[warp][nibbles ? 4 * lane + k : plane_coord(4 * lane + k)] = v[k];
