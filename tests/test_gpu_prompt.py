@@ -277,6 +277,28 @@ def test_starts_that_do_not_ascend_are_clamped_and_flagged():
     assert flags() == B.TQ_FLAG_LEN_OVERFLOW
 
 
+def test_no_keys_at_all_and_no_queries():
+    q, k, v = inputs([5, 3], [0, 0], 2, 3, torch.bfloat16, 19)
+    assert len(k) == 0
+    out = torch.full((8, 6, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    api.PromptPlan(2, 6, 2, 8, 0, 0).run(q, k, v, i32([0, 5, 8]), i32([0, 0, 0]), out)
+    assert not out.any()
+    q, k, v = inputs([0, 0], [5, 3], 2, 3, torch.bfloat16, 19)
+    plan = api.PromptPlan(2, 6, 2, 0, 8, 5)
+    plan.run(q, k, v, i32([0, 0, 0]), i32([0, 5, 8]), plan.new_out())
+    assert flags() == 0
+
+
+def test_queries_and_output_in_one_place():
+    """A CTA reads its rows' queries before it writes them."""
+    for nq, nk in (([300, 40], [300, 40]), ([1, 1], [5000, 70])):
+        q, k, v = inputs(nq, nk, 2, 4, torch.float16, 20)
+        plan = api.PromptPlan(2, 8, 2, sum(nq), sum(nk), max(nk), dtype=torch.float16)
+        n = (i32(starts(nq)), i32(starts(nk)))
+        want = plan.run(q, k, v, *n, plan.new_out())
+        assert torch.equal(plan.run(q, k, v, *n, q), want)
+
+
 def test_many_sequences():
     """More sequences than threads a block; all of one token, and none in most."""
     run([1] * 1000, [3] * 1000, 1, 2, torch.bfloat16, seed=13)

@@ -75,7 +75,7 @@ def io(x=OK16, y=OK16 + 65536, heads=2, xs=(1024, 512, 128), ys=(1024, 512, 128)
 def test_rotary_apply_refuses():
     r = api.Rotary(128)._c
 
-    def call(status, r=r, dtype=B.TQ_BF16, batch=1, tokens=4, at=OK16, at_b=4, q=io(), k=io()):
+    def call(status, r=r, dtype=B.TQ_BF16, batch=1, tokens=4, at=OK16, at_b=4, q=io(), k=io(x=1 << 20, y=1 << 24)):
         assert B.tq_rotary_apply(r, dtype, batch, tokens, at, at_b, q, k, None) == status
 
     call(UNSUPPORTED, dtype=7)
@@ -93,7 +93,10 @@ def test_rotary_apply_refuses():
         call(INVALID, q=bad)
         call(INVALID, k=bad)
     call(INVALID, dtype=B.TQ_F32, q=io(x=OK16 + 2))
-    call(UNSUPPORTED, q=io(y=1 << 40, heads=1 << 20))
+    call(INVALID, q=io(), k=io())                                       # both sides' outputs in one place
+    call(INVALID, q=io(), k=io(x=1 << 30, y=OK16))                      # over the other side's vectors
+    call(INVALID, q=io(y=1 << 30), k=io(x=1 << 30, y=1 << 35))
+    call(UNSUPPORTED, q=io(y=1 << 40, heads=(1 << 20) + 1), k=None)
     call(B.TQ_OK, q=None, k=None)               # nothing to do
     call(B.TQ_OK, batch=0)
     call(B.TQ_OK, tokens=0)
