@@ -72,7 +72,9 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
 
 // ---------------------------------------------------------------- tokens
 // A CTA moves the tokens of one (sequence, head): all are read before any is written, so a list may
-// be in any order.  An item is 16 bytes of a token's codes or one of its norms.
+// be in any order.  An item is 16 bytes of a token's codes or one of its norms; a block has as many
+// threads as items up to kKeepThreads (short lists with 256 threads a block: 10.2 us for 6.4, 512
+// sequences of 8 heads and 16 entries).
 constexpr int kKeepThreads = 256, kMaxItems = 12;         // 4 + 1 + 4 vectors, 3 norms
 constexpr int kPerThread = TQ_TREE_NODES * kMaxItems / kKeepThreads;
 
@@ -105,7 +107,7 @@ __device__ __forceinline__ char* item_at(const KeepArgs& a, int j, long long kr,
 }
 
 // Bound by latency: list, block table, codes, one after the other, and the launch (32 sequences of 4
-// heads and 5 entries: 3.0 us; 512 of 8 heads and 16: 10 us).
+// heads and 5 entries: 3.0 us; 512 of 8 heads and 16: 6.4 us).
 __global__ void __launch_bounds__(kKeepThreads) keep_tokens_kernel(const __grid_constant__ KeepArgs a) {
   const int h = blockIdx.x % a.heads, b = blockIdx.x / a.heads;
   const int per = a.kplanes + 1 + a.vparts + 3, wide = per - 3;
@@ -115,7 +117,7 @@ __global__ void __launch_bounds__(kKeepThreads) keep_tokens_kernel(const __grid_
   char* to[kPerThread];
 #pragma unroll
   for (int n = 0; n < kPerThread; ++n) {
-    const int x = threadIdx.x + n * kKeepThreads, i = x / per, j = x % per;
+    const int x = threadIdx.x + n * blockDim.x, i = x / per, j = x % per;
     to[n] = nullptr;
     const int from = i < a.max_keep ? keep[i] : -1;
     if (from < 0) continue;
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(kKeepThreads) keep_tokens_kernel(const __grid_
   __syncthreads();
 #pragma unroll
   for (int n = 0; n < kPerThread; ++n) {
-    const int j = (threadIdx.x + n * kKeepThreads) % per;
+    const int j = (threadIdx.x + n * blockDim.x) % per;
     if (!to[n]) continue;
     if (j < wide) *reinterpret_cast<uint4*>(to[n]) = v[n];
     else *reinterpret_cast<uint32_t*>(to[n]) = v[n].x;
@@ -229,7 +231,9 @@ extern "C" tq_status tq_keep_tokens(tq_prod_cache k, int32_t key_bits, tq_mse_ca
   a.max_keep = max_keep;
   a.pos = pos;
   a.keep = keep;
-  keep_tokens_kernel<<<(unsigned)(batch * heads), kKeepThreads, 0,
+  const int items = max_keep * (a.kplanes + 1 + a.vparts + 3);
+  const int threads = std::min(kKeepThreads, (items + 31) / 32 * 32);      // (more items: three a thread at most)
+  keep_tokens_kernel<<<(unsigned)(batch * heads), threads, 0,
                        reinterpret_cast<cudaStream_t>(stream_)>>>(a);
   return tq_cuda_status(cudaGetLastError());
 }
