@@ -878,6 +878,82 @@ __device__ __forceinline__ Stats softmax_tiles(Smem& sm, int tiles, int reps, in
 
 #endif
 
+#ifdef TQ_ROWS_TREE
+// An item's row operands into TMEM (halves hf of a row's positions, all reads in flight at once) and its
+// record out of it.  Functions of their own, so that the registers they take are not the loops'.
+template <bool kFine>
+__device__ __noinline__ void tree_rows_in(const uint4* row, bool there, uint32_t lane_base, int hf) {
+#pragma unroll 1
+  for (int c = 0; c < (kFine ? 2 : 1); ++c) {
+    uint32_t q[64];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint4 x = there ? row[32 * c + 16 * hf + i] : make_uint4(0, 0, 0, 0);
+      q[4 * i] = x.x; q[4 * i + 1] = x.y; q[4 * i + 2] = x.z; q[4 * i + 3] = x.w;
+    }
+    const uint32_t at = lane_base + (c ? kQLowCol : kQCol) + 64 * hf;
+    tmem_store<32>(at, q);
+    tmem_store<32>(at + 32, q + 32);
+  }
+  tq::tmem_wait_st();
+}
+
+__device__ __noinline__ void tree_record(float* part, float* recs, int nodes_row0, int G, int Hq, int rows, int reps,
+                                         int wl, int hf, int lane, float m_mine, float l_mine) {
+  // lanes' parts through shared memory [128 lanes][kRecFloats] (the operands are done with)
+  float* mine = part + (32 * wl + lane) * kRecFloats;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    float o[32];
+    tmem_load<32>(((uint32_t)(32 * wl) << 16) + kOCol + 64 * hf + 32 * c, reinterpret_cast<uint32_t*>(o));
+    tq::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<float4*>(mine + 64 * hf + 32 * c + 4 * i) =
+          make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+  }
+  *reinterpret_cast<float2*>(mine + 128 + 2 * hf) = make_float2(m_mine, l_mine);      // (one reference for both halves)
+  tq::named_sync(5, 256);
+  // replicas of a row added up with their log-sum-exp weights, four rows of a warp side by side
+  const int per = kTile / reps;
+  for (int row0 = wl + 4 * hf; row0 < rows; row0 += 32) {
+    const float* p[4];
+    float m[4], l[4] = {};
+    float4 acc[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      p[i] = part + min(row0 + 8 * i, rows - 1) * kRecFloats;
+      m[i] = -INFINITY;
+      acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int k = 0; k < reps; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], p[i][k * per * kRecFloats + 128]);
+    for (int k = 0; k < reps; ++k) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 st = *reinterpret_cast<const float4*>(p[i] + k * per * kRecFloats + 128);   // m, l of both halves
+        const float w = st.x == -INFINITY ? 0.f : ex2(st.x - m[i]);
+        const float4 x = *reinterpret_cast<const float4*>(p[i] + k * per * kRecFloats + 4 * lane);
+        acc[i].x = fmaf(w, x.x, acc[i].x);
+        acc[i].y = fmaf(w, x.y, acc[i].y);
+        acc[i].z = fmaf(w, x.z, acc[i].z);
+        acc[i].w = fmaf(w, x.w, acc[i].w);
+        l[i] = fmaf(w, st.y + st.w, l[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (row0 + 8 * i >= rows) break;
+      const int nr = nodes_row0 + row0 + 8 * i;
+      float* rec = recs + ((long long)(nr / G) * Hq + nr % G) * kRecFloats;
+      *reinterpret_cast<float4*>(rec + 4 * lane) = acc[i];
+      if (lane == 0) *reinterpret_cast<float2*>(rec + 128) = make_float2(m[i], l[i]);
+    }
+  }
+}
+#endif
+
 // Lengths, lists, block tables and codes are read before this kernel's wait: it starts only when all
 // of rows_prep_kernel is past its own wait, so whatever ran before that has ended and been flushed.
 template <int IB, int VB, bool kFine>
@@ -996,6 +1072,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
     // (plain loads: the kernel before writes the operands while this one runs, so they must not go
     // through the read-only path, which the wait does not order)
     const float f = r < rows ? a.qf[qr] : 0.f;
+#ifdef TQ_ROWS_TREE
+    tree_rows_in<kFine>(a.qop + qr * (kFine ? 64 : 32), r < rows, lane_base, hf);
+#else
     // (fine: the row's second 512 bytes are what the first ones' rounding left)
 #pragma unroll 1
     for (int c = 0; c < (kFine ? 4 : 2); ++c) {
@@ -1009,6 +1088,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
       tmem_store<32>(lane_base + (c >> 1 ? kQLowCol : kQCol) + 64 * hf + 32 * (c & 1), q);
     }
     tq::tmem_wait_st();
+#endif
     tc_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.qfull);
@@ -1025,6 +1105,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
     ok = ok && tq::named_sync_and(5, 256, z.ok);
     if (ok) {
       tc_after();
+#ifdef TQ_ROWS_TREE
+      float* recs = a.rec + (rec_split * nrows + (long long)b * a.nodes * a.Hq + h * a.G) * kRecFloats;
+      tree_record(reinterpret_cast<float*>(sm.k[0]), recs, rt * kTile, a.G, a.Hq, rows, reps, wl, hf, lane, z.m, z.l);
+#else
       float* part = reinterpret_cast<float*>(sm.k[0]);      // [128 lanes][kRecFloats]
       float* mine = part + (32 * wl + lane) * kRecFloats;
 #pragma unroll
@@ -1059,6 +1143,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
         *reinterpret_cast<float4*>(rec + 4 * lane) = acc;
         if (lane == 0) *reinterpret_cast<float2*>(rec + 128) = make_float2(m, l);
       }
+#endif
     }
   } else if (warp < kIssueWarp) {
     // ================================================================ expanders
