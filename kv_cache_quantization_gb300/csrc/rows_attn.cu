@@ -977,14 +977,18 @@ __global__ void __launch_bounds__(kThreads, 1) rows_attn_kernel(const __grid_con
     h = item / a.row_tiles % a.Hkv;
     split = item / (a.row_tiles * a.Hkv);
   } else {
+#ifdef TQ_ROWS_TREE
+    // one sequence's items side by side (by split first: 233 for 228 us in 32 sequences of 4096 to 16384)
+    rt = item % a.row_tiles;
+    split = item / a.row_tiles % a.own_splits;
+    h = item / (a.row_tiles * a.own_splits) % a.Hkv;
+    b = item / (a.row_tiles * a.own_splits * a.Hkv);
+#else
     item -= npre;
-    if (kTree) {
-      rt = item % a.row_tiles;
-      item /= a.row_tiles;
-    }
     h = item % a.Hkv;
     b = item / a.Hkv % a.B;
     split = item / (a.Hkv * a.B);
+#endif
   }
 #ifdef TQ_ROWS_TREE
   const int rows = min(kTile, a.nodes * a.G - rt * kTile);
@@ -1401,7 +1405,7 @@ rows_merge_kernel(const float* rec, int nrec, int nrows, const float* __restrict
 #ifdef TQ_ROWS_TREE
 // ---------------------------------------------------------------- many rows
 // Trees have 16 and 64 times the rows of a decode step, and the two kernels above then take as long as
-// the attention itself (7168 rows: 28 and 30 us): a CTA reads its matrix for 4 or 8 rows, and its
+// the attention itself (7168 rows: 28 and 30 us, these 20 and 16): a CTA reads its matrix for 4 or 8 rows, and its
 // threads get 16 bytes from shared memory for every four products.  These keep a matrix in the
 // registers of 256 threads, several columns a thread, for as many rows as there are (8 at a time), and
 // take the sums of the first kernel in the same order.
@@ -1600,6 +1604,7 @@ struct Plan {
   size_t qf_off, rec_off, bytes;
 };
 
+#ifndef TQ_ROWS_TREE
 // Time of a grid of n1 items of c1 tiles each and then n2 items of c2, taken in order by `sms` SMs
 // that each work on one (in tiles).
 double makespan(long long n1, double c1, long long n2, double c2, long long sms) {
@@ -1676,6 +1681,8 @@ void find_splits(Splits* x) {
   }
 }
 
+#endif
+
 tq_status check_desc(const tq_attn_desc* d, long long pre_tiles, long long own_tiles) {
   if (!d) return TQ_ERR_INVALID_ARG;
   if (d->head_dim != TQ_HEAD_DIM) return TQ_ERR_UNSUPPORTED;
@@ -1700,6 +1707,7 @@ void lay_out(const tq_attn_desc* d, Plan* p) {
   p->bytes = p->rec_off + (size_t)(p->pre_splits + p->own_splits) * p->rows * kRecFloats * sizeof(float);
 }
 
+#ifndef TQ_ROWS_TREE
 tq_status make_plan(const tq_attn_desc* d, long long pre_tiles, long long own_tiles, Plan* p) {
   const tq_status st = check_desc(d, pre_tiles, own_tiles);
   if (st != TQ_OK) return st;
@@ -1717,6 +1725,7 @@ tq_status make_plan(const tq_attn_desc* d, long long pre_tiles, long long own_ti
   lay_out(d, p);
   return TQ_OK;
 }
+#endif
 
 LevelBytes level_bytes(const tq_codec* c) {
   LevelBytes t{};
@@ -1900,6 +1909,33 @@ long long tiles_of(long long tokens) { return (tokens + kTile - 1) / kTile; }
 #ifdef TQ_ROWS_TREE
 
 // Splits as a prefix has them: row_tiles items of up to 128 rows for each (sequence, KV head).
+// Splits of a sequence's tiles that make the estimated time least, in tiles.  An item costs its tiles
+// and about three more for its start and end (8 us; a tile 2.4 us with 56 rows, 3.1 with 112), and a
+// record 2 times 528 bytes of the merge (of 5 bytes a picosecond, a tile 2.4 us).  Items that all have an
+// SM take the time of one; one sequence's items are alike and go in waves; those of a batch differ with
+// its lengths, which the host does not know (taken: half of the longest to all of it, three quarters of
+// it on average), and what bounds them is every SM's share of the work and then the longest item.
+// Against one search for both as in decode steps: 64 nodes behind 262144 tokens 447 for 465 us, 8 nodes
+// of 32 sequences 225 for 233.
+int tree_splits(long long units, long long tiles, long long rows, long long sms, bool alike) {
+  constexpr double kItem = 3.0, kRecord = 2 * 528 / 12e6;
+  const long long most = std::min(std::max(tiles, 1LL), std::min<long long>(kMaxRecs, 8 * sms / units + 8));
+  double best = 0;
+  int splits = 1;
+  for (long long s = 1; s <= most; ++s) {
+    const long long items = units * s, waves = (items + sms - 1) / sms;
+    const double item = (double)((tiles + s - 1) / s) + kItem;
+    const double t = (items <= sms || alike ? (double)waves * item
+                                            : (double)units * (0.75 * (double)tiles + kItem * (double)s) / (double)sms + item) +
+                     kRecord * (double)(rows * s);
+    if (s == 1 || t < best) {
+      best = t;
+      splits = (int)s;
+    }
+  }
+  return splits;
+}
+
 tq_status plan_tree(const tq_attn_desc* d, int nodes, Plan* p) {
   if (!d || nodes <= 0) return TQ_ERR_INVALID_ARG;
   const long long tiles = tiles_of(d->max_seq_len);
@@ -1912,10 +1948,8 @@ tq_status plan_tree(const tq_attn_desc* d, int nodes, Plan* p) {
   p->row_tiles = (nodes * p->G + kTile - 1) / kTile;
   const int n = tq_num_sms();
   const long long units = (long long)d->batch * d->kv_heads * p->row_tiles;
-  Splits want{units, tiles, 0, 0, n > 0 ? n : 152, nodes * p->G <= kTile / 2, 0, 0};
-  find_splits(&want);
   p->pre_splits = 0;
-  p->own_splits = want.sp;
+  p->own_splits = tree_splits(units, tiles, p->rows, n > 0 ? n : 152, d->batch == 1);
   if (units * p->own_splits > 0x7fffffffLL) return TQ_ERR_UNSUPPORTED;
   lay_out(d, p);
   return TQ_OK;

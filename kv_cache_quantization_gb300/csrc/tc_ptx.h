@@ -121,17 +121,6 @@ __device__ __forceinline__ bool named_sync_and(int id, int threads, bool p) {
       : "memory");
   return r != 0;
 }
-// the same with OR
-__device__ __forceinline__ bool named_sync_or(int id, int threads, bool p) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n bar.red.or.pred b, %2, %3, a;\n"
-      " selp.u32 %0, 1, 0, b;\n}\n"
-      : "=r"(r)
-      : "r"((uint32_t)p), "r"(id), "r"(threads)
-      : "memory");
-  return r != 0;
-}
 
 // ---------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tc_before() {
