@@ -1405,7 +1405,7 @@ rows_merge_kernel(const float* rec, int nrec, int nrows, const float* __restrict
 #ifdef TQ_ROWS_TREE
 // ---------------------------------------------------------------- many rows
 // Trees have 16 and 64 times the rows of a decode step, and the two kernels above then take as long as
-// the attention itself (7168 rows: 28 and 30 us, these 20 and 16): a CTA reads its matrix for 4 or 8 rows, and its
+// the attention itself (7168 rows: 28 and 30 us; these take 20 and 16): a CTA reads its matrix for 4 or 8 rows, and its
 // threads get 16 bytes from shared memory for every four products.  These keep a matrix in the
 // registers of 256 threads, several columns a thread, for as many rows as there are (8 at a time), and
 // take the sums of the first kernel in the same order.

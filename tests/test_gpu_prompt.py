@@ -339,6 +339,22 @@ def test_graph_stream_and_two_plans():
     assert flags() == 0
 
 
+def test_heads_before_tokens():
+    """Views whose heads lie further apart than their tokens, of one sequence and of a step."""
+    for nq, nk in (([300], [300]), ([1, 1], [2000, 700])):
+        q, k, v, qs, ks, plan, out = run(nq, nk, 2, 3, torch.float16, seed=21)
+        views = [t.transpose(0, 1).contiguous().transpose(0, 1) for t in (q, k, v)]
+        assert all(t.stride(1) > t.stride(0) for t in views)
+        assert torch.equal(plan.run(*views, i32(qs), i32(ks), plan.new_out()), out)
+    assert flags() == 0
+
+
+def test_two_blocks_of_rows_without_keys():
+    """Long prompts, some of them without a key, in CTAs of two blocks of rows."""
+    run([700, 700, 700, 40], [0, 700, 129, 0], 8, 7, torch.bfloat16, seed=22)
+    run([700, 700, 700, 40], [0, 700, 129, 0], 8, 7, torch.float16, causal=False, seed=23)
+
+
 def test_prompt_then_codes_then_decode():
     """A prompt as a program takes it in: positions, attention on exact keys, codes; then a decode step
     on the codes is near attention on the exact keys (as near as 5-bit keys and 4-bit values are)."""
