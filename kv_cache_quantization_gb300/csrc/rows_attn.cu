@@ -1908,7 +1908,6 @@ long long tiles_of(long long tokens) { return (tokens + kTile - 1) / kTile; }
 
 #ifdef TQ_ROWS_TREE
 
-// Splits as a prefix has them: row_tiles items of up to 128 rows for each (sequence, KV head).
 // Splits of a sequence's tiles that make the estimated time least, in tiles.  An item costs its tiles
 // and about three more for its start and end (8 us; a tile 2.4 us with 56 rows, 3.1 with 112), and a
 // record 2 times 528 bytes of the merge (of 5 bytes a picosecond, a tile 2.4 us).  Items that all have an
@@ -1919,7 +1918,7 @@ long long tiles_of(long long tokens) { return (tokens + kTile - 1) / kTile; }
 // of 32 sequences 225 for 233.
 int tree_splits(long long units, long long tiles, long long rows, long long sms, bool alike) {
   constexpr double kItem = 3.0, kRecord = 2 * 528 / 12e6;
-  const long long most = std::min(std::max(tiles, 1LL), std::min<long long>(kMaxRecs, 8 * sms / units + 8));
+  const long long most = std::min(std::max(tiles, 1LL), std::min<long long>(kMaxRecs, 8 * sms / std::max(units, 1LL) + 8));
   double best = 0;
   int splits = 1;
   for (long long s = 1; s <= most; ++s) {

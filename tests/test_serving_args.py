@@ -146,6 +146,8 @@ def test_tree_refuses():
         call(INVALID, k=key(p=pages(**p)))
         call(INVALID, v=value(p=pages(**p)))
     assert B.tq_tree_workspace_bytes(d, 64) > B.tq_tree_workspace_bytes(d, 1) > 0
+    call(INVALID, d=desc(batch=0))                        # (the codecs; no sequences are nothing to split)
+    assert B.tq_tree_workspace_bytes(desc(batch=0), 4) == B.tq_prefix_workspace_bytes(desc(batch=0), 128)
     with pytest.raises(ValueError):
         api.TreePlan(1, 65, 4, 4, 128, 128, device="cpu")
     with pytest.raises(ValueError):
