@@ -126,6 +126,32 @@ def test_many_rows(batch, kv, group, nodes, kbits, vbits, q_dtype, out_dtype):
     assert flags() == 0
 
 
+@pytest.mark.parametrize("batch,group", [(300, 8), (257, 5), (2, 8)])
+def test_ragged_batches_are_taken_by_length(batch, group):
+    """Large batches' items are taken by length: equal lengths, none at all, one much longer than the
+    others; then the same call replayed with other lengths."""
+    nodes, kv = (2, 1) if batch > 2 else (64, 8)
+    lens = [(61 * b) % 7 * 40 for b in range(batch)]
+    lens[batch // 2] = 3000
+    rows = trees(batch, nodes, "any", batch)
+    kc, vc, q, k, v, plan, out = run_tree(3, 2, batch, kv, group, lens, nodes, rows, seed=batch)
+    tree, n, side = masks(rows), i32(lens), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o = plan.new_out()
+    with torch.cuda.stream(side):
+        g = capture(lambda: plan.run(kc, vc, q, k, v, n, tree, o), side)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, out)
+    other = [x // (1 + b % 3) for b, x in enumerate(lens)]
+    n.copy_(i32(other))
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    check_tree(kc, vc, q, k, v, other, rows, o, group)
+    assert flags() == 0
+
+
 @pytest.mark.parametrize("nodes", [15, 16, 17, 31, 32, 33, 48, 63, 64])
 @pytest.mark.parametrize("first", [0, 1, 15, 16, 17, 111, 112, 113, 127])
 def test_every_place_of_the_drafted_tokens_in_a_tile(first, nodes):
