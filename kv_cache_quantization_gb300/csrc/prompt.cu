@@ -735,6 +735,32 @@ struct Plan {
   size_t bytes;
 };
 
+// Parts of the keys of sequences with one block of rows each that make the estimated time least, in
+// tiles (1.5 us each where all SMs read).  A part costs its tiles and about 3.5 more for its start and end (5
+// us), a record 2 times 528 bytes of the join (of 5 bytes a picosecond).  Parts that all have an SM take
+// the time of one; one sequence's are alike and go in waves; those of a batch differ with its lengths,
+// which the host does not know (taken: half of the longest to all of it, three quarters of it on average),
+// and take an SM's share of the work and half of the longest part.  Within 6% of the best number of parts in
+// twelve batches of 2 to 100 sequences, alike or from 1% of the longest on.
+int key_parts(long long units, long long tiles, long long rows, long long sms, bool alike) {
+  constexpr double kPart = 3.5, kRecord = 2 * 528 / 7.5e6;
+  const long long most = std::min(std::max(tiles / 2, 1LL), std::min<long long>(1023, 8 * sms / units + 8));
+  double best = 0;
+  int parts = 1;
+  for (long long s = 1; s <= most; ++s) {
+    const long long items = units * s, waves = (items + sms - 1) / sms;
+    const double item = (double)((tiles + s - 1) / s) + kPart;
+    const double t = (items <= sms || alike ? (double)waves * item
+                                            : (double)units * (0.75 * (double)tiles + kPart * (double)s) / (double)sms + item / 2) +
+                     (s > 1 ? kRecord * (double)(rows * s) : 0.0);
+    if (s == 1 || t < best) {
+      best = t;
+      parts = (int)s;
+    }
+  }
+  return parts;
+}
+
 tq_status make_plan(const tq_prompt_desc* d, Plan* p) {
   if (!d) return TQ_ERR_INVALID_ARG;
   if (d->head_dim != TQ_HEAD_DIM) return TQ_ERR_UNSUPPORTED;
@@ -755,12 +781,18 @@ tq_status make_plan(const tq_prompt_desc* d, Plan* p) {
   // and ends twice (28/4 heads: 8 prompts of 100 tokens 11.1 us for 14.8, 1000 tokens behind 8000
   // keys 107 for 136; 700 tokens, 156 CTAs of one block, 14.7 us and 18.1 with two).
   p->per_cta = ctas(p->tokens) * 10 <= sms * 11 ? p->tokens : 2 * p->tokens;
-  p->tiles = d->total_q / p->per_cta + d->batch;
-  // Keys split so that the CTAs fill the GPU once, each with at least two tiles: a second CTA costs an
-  // SM its start and end again, about 5 us (one token of 8 sequences behind 8192 keys, 32 units of 64
-  // tiles: 4 parts 32 us, 5 parts 45, 9 parts 36; 2 sequences and 4096 keys: 16 parts 11.4 us, 8 parts 13).
+  // Keys split, each part with at least two tiles: with several blocks of rows a sequence so that the CTAs
+  // fill the GPU once, else by an estimate, in single blocks (one token of 8 sequences behind 8192 keys, 32
+  // units of 64 tiles: 4 parts 31 us, 5 parts 45, 8 parts 35; 8 sequences of 8 heads behind 1600 to 21000 keys:
+  // 90 us, unsplit, two parts 106 and 176).
   const long long key_tiles = ((long long)d->max_k_len + kTile - 1) / kTile;
-  p->splits = (int)std::max<long long>(1, std::min<long long>(std::min<long long>(sms / ctas(p->per_cta), key_tiles / 2), 1023));
+  if (d->batch && each <= p->tokens) {
+    p->splits = key_parts((long long)d->batch * d->kv_heads, key_tiles, (long long)d->total_q * d->q_heads, sms, d->batch == 1);
+    if (p->splits > 1) p->per_cta = p->tokens;
+  } else {
+    p->splits = (int)std::max<long long>(1, std::min<long long>(std::min<long long>(sms / ctas(p->per_cta), key_tiles / 2), 1023));
+  }
+  p->tiles = d->total_q / p->per_cta + d->batch;
   const long long units = (long long)p->tiles * d->kv_heads;
   if (units * p->splits > 0x7fffffffLL) return TQ_ERR_UNSUPPORTED;
   p->bytes = 256;

@@ -349,6 +349,21 @@ def test_heads_before_tokens():
     assert flags() == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("batch,kv,group", [(40, 4, 7), (60, 4, 8), (9, 8, 5)])
+def test_ragged_batches_of_few_rows(batch, kv, group, dtype):
+    """More parts of keys than SMs, many of them empty: histories of 0 to 9000 keys, one of which is long;
+    some sequences have more rows than a block."""
+    g = torch.Generator().manual_seed(batch)
+    nk = torch.randint(0, 900, (batch,), generator=g).tolist()
+    nq = torch.randint(0, 4, (batch,), generator=g).tolist()
+    nk[batch // 2] = 9000
+    nq[batch // 2] = 2
+    nk[1], nq[1] = 700, 50
+    run(nq, nk, kv, group, dtype, seed=batch, before=2, behind=3)
+    run(nq, nk, kv, group, dtype, causal=False, seed=batch + 1)
+
+
 def test_two_blocks_of_rows_without_keys():
     """Long prompts, some of them without a key, in CTAs of two blocks of rows."""
     run([700, 700, 700, 40], [0, 700, 129, 0], 8, 7, torch.bfloat16, seed=22)
