@@ -225,8 +225,8 @@ typedef struct {
  *   positions : device int32 [batch][tokens], rows pos_stride_b apart (0: one row for all); any
  *               number, negative ones turn backwards.
  * Angles are right to 2^-32 turns at any position; products and sums are 32 bits, rounded once.
- * Vectors at multiples of 16 bytes and a rotary_dim that is a multiple of 16 take 16-byte accesses;
- * others work and are slower. */
+ * Vectors at multiples of 16 bytes take 16-byte accesses where the pairs are neighbours or rotary_dim
+ * is a multiple of 16; others work and are slower. */
 tq_status tq_rotary_apply(const tq_rotary* r, tq_dtype dtype, int32_t batch, int32_t tokens,
                           const int32_t* positions, int64_t pos_stride_b, const tq_rotary_io* q,
                           const tq_rotary_io* k, tq_stream_t stream);
