@@ -17,6 +17,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "tq_internal.h"
 
@@ -75,6 +76,24 @@ __device__ __forceinline__ void turn(float a, float b, float c, float s, float& 
   yb = fmaf(a, s, b * c);
 }
 
+// Two 16-bit numbers of a word.  (Rounded two at a time: one bf16 number at a time, 40000 tokens of 40 heads
+// took 161 us for 131.)
+template <typename T>
+__device__ __forceinline__ float2 widen2(uint32_t w) {
+  if constexpr (std::is_same_v<T, __half>) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  else return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t narrow2(float x, float y) {
+  if constexpr (std::is_same_v<T, __half>) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
 // kPer = 16 bytes of T.  Lane l of a vector's eight holds pairs 8l..8l + 7 of the turned
 // coordinates: neighbouring ones are the 16 coordinates from 16l, halves are 8 from 8l and the 8
 // that lie rotary_dim/2 behind; lanes past the turned coordinates copy 16 of the others.
@@ -125,16 +144,37 @@ __global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ Rot
       if (!turned && x.x == x.y) continue;
       char* p = x.y + b * x.yb + (hf - (key ? a.q_heads : 0)) * x.yh + t * x.yt;
       if (turned) {
-        T* e[2] = {reinterpret_cast<T*>(v[f][0]), reinterpret_cast<T*>(v[f][1])};
+        uint32_t* wa = reinterpret_cast<uint32_t*>(v[f][0]);
+        uint32_t* wb = reinterpret_cast<uint32_t*>(v[f][1]);
+        float ya[2], yb[2];
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (kInterleaved && 16 * unit + 2 * i >= a.r.rotary_dim) continue;       // (copied as it is)
-          T* ea = kInterleaved ? &e[i >> 2][2 * (i & 3)] : &e[0][i];
-          T* eb = kInterleaved ? ea + 1 : &e[1][i];
-          float ya, yb;
-          turn(to_float<T>(*ea), to_float<T>(*eb), c[i], s[i], ya, yb);
-          *ea = from_float<T>(ya);
-          *eb = from_float<T>(yb);
+          for (int i = 0; i < 8; ++i) {
+            if (kInterleaved && 16 * unit + 2 * i >= a.r.rotary_dim) continue;       // (copied as it is)
+            uint32_t* ea = kInterleaved ? (i < 4 ? wa : wb) + 2 * (i & 3) : wa + i;
+            uint32_t* eb = kInterleaved ? ea + 1 : wb + i;
+            turn(__uint_as_float(*ea), __uint_as_float(*eb), c[i], s[i], ya[0], yb[0]);
+            *ea = __float_as_uint(ya[0]);
+            *eb = __float_as_uint(yb[0]);
+          }
+        } else if constexpr (kInterleaved) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (16 * unit + 2 * i >= a.r.rotary_dim) continue;
+            uint32_t* w = (i < 4 ? wa : wb) + (i & 3);
+            const float2 x = widen2<T>(*w);
+            turn(x.x, x.y, c[i], s[i], ya[0], yb[0]);
+            *w = narrow2<T>(ya[0], yb[0]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 xa = widen2<T>(wa[i]), xb = widen2<T>(wb[i]);
+            turn(xa.x, xb.x, c[2 * i], s[2 * i], ya[0], yb[0]);
+            turn(xa.y, xb.y, c[2 * i + 1], s[2 * i + 1], ya[1], yb[1]);
+            wa[i] = narrow2<T>(ya[0], ya[1]);
+            wb[i] = narrow2<T>(yb[0], yb[1]);
+          }
         }
       }
 #pragma unroll
