@@ -266,6 +266,7 @@ __device__ __forceinline__ bool softmax_stream(const PromptArgs& a, Smem& sm, co
     for (int part = 0; part < 2; ++part) {
       float x[64];
       uint32_t p[32];
+      __syncwarp();       // (lane 0 arrived alone)
       tq::tmem_ld_32x32b_x32(scol + 64 * part, reinterpret_cast<uint32_t*>(x));
       tq::tmem_ld_32x32b_x32(scol + 64 * part + 32, reinterpret_cast<uint32_t*>(x) + 32);
       tq::tmem_wait_ld();
@@ -389,6 +390,7 @@ __device__ __forceinline__ bool issue_stream(Smem& sm, const Work& w) {
     // (the weights come last: the rest is there before them)
     if (weigh) wait(&sm.full[pv.stage], pv.phase);
     if (score) wait(&sm.full[pk.stage], pk.phase);
+    __syncwarp();         // (lanes leave their waits one by one; a barrier takes the warp as one)
     if (w.pair) tq::named_sync(kBarTurn + s, 64);
     if (!weigh || t >= live) {
       agree();
@@ -560,6 +562,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
       float* rec = a.rec + ((long long)w.split * a.total_q * a.Hq + row) * kRecFloats;
 #pragma unroll 1
       for (int c = c0; c < c1; c += 32) {
+        // Rows that are not there skip the body and rows with values given back loop in it, each lane as
+        // often as it has to: the warp meets before the load, which takes all of its lanes at once.
+        __syncwarp();
         float o[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) o[k] = 0.f;
@@ -567,31 +572,33 @@ prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
           tq::tmem_ld_32x32b_x32(ocol + c, reinterpret_cast<uint32_t*>(o));
           tq::tmem_wait_ld();
         }
-        if (!there) continue;
-        if (!w.pair && w.n > 1) {
+        if (there) {
+          if (!w.pair && w.n > 1) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            const float4 x = given[(16 * (s ^ 1) + (c - c0 + k) / 4) * kTile];
-            o[k] = fmaf(o[k], mine, x.x * other);
-            o[k + 1] = fmaf(o[k + 1], mine, x.y * other);
-            o[k + 2] = fmaf(o[k + 2], mine, x.z * other);
-            o[k + 3] = fmaf(o[k + 3], mine, x.w * other);
+            for (int k = 0; k < 32; k += 4) {
+              const float4 x = given[(16 * (s ^ 1) + (c - c0 + k) / 4) * kTile];
+              o[k] = fmaf(o[k], mine, x.x * other);
+              o[k + 1] = fmaf(o[k + 1], mine, x.y * other);
+              o[k + 2] = fmaf(o[k + 2], mine, x.z * other);
+              o[k + 3] = fmaf(o[k + 3], mine, x.w * other);
+            }
+          }
+          if (poison) {
+            const int first = max(w.free_to, w.j0 * kTile), n = min(w.limit(a, token), (w.j0 + w.n) * kTile) - first;
+            const uint16_t* v = a.v + (long long)(w.k0 + first) * a.v_t + w.h * a.v_h + c;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = give_back<kBf16>(v + k, a.v_t, n, o[k]);
+          }
+          if (a.splits > 1) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<float4*>(rec + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          } else {
+            put32<kBf16>(a, row, o, inv, c);
           }
         }
-        if (poison) {
-          const int first = max(w.free_to, w.j0 * kTile), n = min(w.limit(a, token), (w.j0 + w.n) * kTile) - first;
-          const uint16_t* v = a.v + (long long)(w.k0 + first) * a.v_t + w.h * a.v_h + c;
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = give_back<kBf16>(v + k, a.v_t, n, o[k]);
-        }
-        if (a.splits > 1) {
-#pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<float4*>(rec + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-        } else {
-          put32<kBf16>(a, row, o, inv, c);
-        }
       }
+      __syncwarp();
       if (there && a.splits > 1 && c0 == 0 && c1) *reinterpret_cast<float2*>(rec + 128) = make_float2(ref, sum);
     }
   } else {

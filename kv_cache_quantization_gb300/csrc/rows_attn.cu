@@ -894,6 +894,7 @@ __device__ __noinline__ void tree_rows_in(const uint4* row, bool there, uint32_t
       q[4 * i] = x.x; q[4 * i + 1] = x.y; q[4 * i + 2] = x.z; q[4 * i + 3] = x.w;
     }
     const uint32_t at = lane_base + (c ? kQLowCol : kQCol) + 64 * hf;
+    __syncwarp();         // (lanes without a row read nothing)
     tmem_store<32>(at, q);
     tmem_store<32>(at + 32, q + 32);
   }

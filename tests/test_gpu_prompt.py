@@ -423,3 +423,32 @@ def test_refusals_on_the_gpu():
         with pytest.raises((ValueError, B.TQError)):
             bad()
     assert flags() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("nq,nk,group", [
+    ([19, 3, 100], [60, 3, 100], 7),               # blocks of rows that are not full, rows 126 and 127 never are
+    ([2, 18], [9000, 700], 7),                     # keys in parts
+    ([5, 11], [5, 300], 3),                        # one tile, two streams of tiles
+    ([700, 37, 600], [700, 37, 640], 5),           # two blocks of rows a CTA, the last of them in part
+    ([1], [1], 8),
+])
+def test_values_given_back_in_blocks_that_are_not_full(nq, nk, group, dtype):
+    """Infinite values at the ends of the sequences, in every quarter of the channels, which rows attend in
+    different numbers: a row has those of the keys that it attends and keeps every other bit."""
+    kv = 2 if sum(nq) < 500 else 8
+    q, k, v = inputs(nq, nk, kv, group, dtype, 24, behind=2)
+    qs, ks = starts(nq), starts(nk)
+    plan = api.PromptPlan(len(nq), kv * group, kv, len(q), len(k), max(nk), True, dtype)
+    n = (i32(qs), i32(ks))
+    want = plan.run(q, k, v, *n, plan.new_out().fill_(7))
+    check(q, k, v, qs, ks, want, True)
+    for b, (m, rows) in enumerate(zip(nk, nq)):
+        for i, c in enumerate((0, 31, 32, 50, 77, 95, 96, 127)):
+            j = m - 1 - (5 * i) % min(rows, m)     # the last rows attend it
+            v[ks[b] + j, 1, c] = math.inf
+            for row in range(rows):
+                if row + m - rows >= j:
+                    want[qs[b] + row, group:2 * group, c] = math.inf
+    assert torch.equal(plan.run(q, k, v, *n, plan.new_out().fill_(7)), want)
+    assert flags() == 0
