@@ -1,5 +1,6 @@
 // Host-side part of the library: status strings, the Lloyd-Max codebook solver, the QR
 // rotation, and codec creation (device copies of Π, Πᵀ, Sᵀ and M = S Πᵀ).
+#include <algorithm>
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
@@ -174,6 +175,59 @@ int tq_num_sms() {
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
   return n;
+}
+
+namespace {
+
+typedef __int128 Wide;      // (strides are the caller's: their products with counts may pass 64 bits)
+
+// Multiples of a stride: from lo to hi of it.
+struct Term {
+  Wide stride, lo, hi;
+};
+
+Wide floor_div(Wide a, Wide b) { return a / b - (a % b != 0 && (a < 0) != (b < 0)); }
+
+// Whether terms k.. of `t` have a sum in (low, high), where the sums of terms k.. lie in [lo[k], hi[k]].
+// The largest strides come first, so that in arrays each leaves one or two multiples to look at;
+// after `budget` of them the answer is yes.
+bool sum_within(const Term* t, const Wide* lo, const Wide* hi, int k, int n, Wide low, Wide high, int* budget) {
+  if (hi[k] <= low || lo[k] >= high) return false;
+  if (k == n || --*budget < 0) return true;
+  const Wide s = t[k].stride;
+  const Wide first = std::max(t[k].lo, floor_div(low - hi[k + 1], s) + 1);
+  const Wide last = std::min(t[k].hi, -floor_div(lo[k + 1] - high, s) - 1);
+  for (Wide m = first; m <= last; ++m)
+    if (sum_within(t, lo, hi, k + 1, n, low - m * s, high - m * s, budget)) return true;
+  return false;
+}
+
+}  // namespace
+
+// x's vector i and y's vector j overlap where Σ i_d·x_d − Σ j_d·y_d lies within their lengths of the
+// distance of the first ones; equal strides are one term.
+bool tq_vectors_meet(const tq_vectors& x, const tq_vectors& y) {
+  Term t[6];
+  int n = 0;
+  for (int side = 0; side < 2; ++side)
+    for (int d = 0; d < 3; ++d) {
+      const tq_vectors& v = side ? y : x;
+      if (v.n[d] <= 0) return false;
+      if (v.n[d] == 1 || v.stride[d] == 0) continue;
+      int k = 0;
+      while (k < n && t[k].stride != v.stride[d]) ++k;
+      if (k == n) t[n++] = Term{v.stride[d], 0, 0};
+      (side ? t[k].lo : t[k].hi) += (side ? -1 : 1) * (Wide)(v.n[d] - 1);
+    }
+  std::sort(t, t + n, [](const Term& a, const Term& b) { return a.stride > b.stride; });
+  Wide lo[7] = {}, hi[7] = {};
+  for (int k = n - 1; k >= 0; --k) {
+    lo[k] = lo[k + 1] + t[k].stride * t[k].lo;
+    hi[k] = hi[k + 1] + t[k].stride * t[k].hi;
+  }
+  const Wide apart = (Wide)reinterpret_cast<uintptr_t>(y.at) - (Wide)reinterpret_cast<uintptr_t>(x.at);
+  int budget = 4096;
+  return sum_within(t, lo, hi, 0, n, apart - x.bytes, apart + y.bytes, &budget);
 }
 
 tq_status tq_check_codec(const tq_codec* c, tq_kind kind) {

@@ -250,6 +250,13 @@ __global__ void __launch_bounds__(256) rotary_any_kernel(const __grid_constant__
   }
 }
 
+tq_vectors inputs(const Side& s, int batch, int heads, int tokens, int elem) {
+  return tq_vectors{s.x, {batch, heads, tokens}, {s.xb, s.xh, s.xt}, TQ_D * elem};
+}
+tq_vectors outputs(const Side& s, int batch, int heads, int tokens, int elem) {
+  return tq_vectors{s.y, {batch, heads, tokens}, {s.yb, s.yh, s.yt}, TQ_D * elem};
+}
+
 // One side of a call in bytes; false for a bad one: among others an output whose vectors overlap each
 // other (no dimension may lie inside another one's step) or the input without being the input.
 bool side_of(const tq_rotary_io* io, int batch, int tokens, int elem, Side* s, bool* vec) {
@@ -265,7 +272,7 @@ bool side_of(const tq_rotary_io* io, int batch, int tokens, int elem, Side* s, b
     low |= (uintptr_t)(x * elem);
   }
   const int64_t n[3] = {batch, io->heads, tokens};
-  int64_t x_span = TQ_D, y_span = TQ_D;       // elements from the first to behind the last
+  int64_t y_span = TQ_D;                      // elements from the first to behind the last
   bool same = io->x == io->y;
   int order[3] = {0, 1, 2};
   std::sort(order, order + 3, [&](int a, int b) { return strides[3 + a] < strides[3 + b]; });
@@ -273,15 +280,12 @@ bool side_of(const tq_rotary_io* io, int batch, int tokens, int elem, Side* s, b
     if (n[d] == 1) continue;
     if (strides[3 + d] < y_span) return false;
     same = same && strides[d] == strides[3 + d];
-    x_span += (n[d] - 1) * strides[d];
     y_span += (n[d] - 1) * strides[3 + d];
   }
-  const char *x0 = static_cast<const char*>(io->x), *y0 = static_cast<const char*>(io->y);
-  if (!same && x0 < y0 + y_span * elem && y0 < x0 + x_span * elem) return false;
   *vec = *vec && low % 16 == 0;
   *s = Side{static_cast<const char*>(io->x), static_cast<char*>(io->y), strides[0] * elem, strides[1] * elem,
             strides[2] * elem, strides[3] * elem, strides[4] * elem, strides[5] * elem};
-  return true;
+  return same || !tq_vectors_meet(inputs(*s, batch, io->heads, tokens, elem), outputs(*s, batch, io->heads, tokens, elem));
 }
 
 template <typename T>
@@ -349,8 +353,12 @@ extern "C" tq_status tq_rotary_apply(const tq_rotary* r, tq_dtype dtype, int32_t
   bool vec = r->interleaved || r->rotary_dim % 16 == 0;
   const int elem = dtype == TQ_F32 ? 4 : 2;
   if (!side_of(q, batch, tokens, elem, &a.q, &vec) || !side_of(k, batch, tokens, elem, &a.k, &vec)) return TQ_ERR_INVALID_ARG;
-  // (one side's output in place of the other side's vectors)
-  if (q && k && q->heads && k->heads && (q->y == k->y || q->x == k->y || q->y == k->x)) return TQ_ERR_INVALID_ARG;
+  // one side's output over the other side's vectors: warps would read what others write
+  if (a.q.x && a.k.x) {
+    const tq_vectors qx = inputs(a.q, batch, q->heads, tokens, elem), qy = outputs(a.q, batch, q->heads, tokens, elem);
+    const tq_vectors kx = inputs(a.k, batch, k->heads, tokens, elem), ky = outputs(a.k, batch, k->heads, tokens, elem);
+    if (tq_vectors_meet(qy, ky) || tq_vectors_meet(qx, ky) || tq_vectors_meet(qy, kx)) return TQ_ERR_INVALID_ARG;
+  }
   const long long qh = q ? q->heads : 0, heads = qh + (k ? k->heads : 0);
   if (heads > (1 << 20)) return TQ_ERR_UNSUPPORTED;
   a.rows = (long long)batch * tokens;

@@ -110,6 +110,15 @@ static inline tq_status tq_cuda_status(cudaError_t e) {
 tq_status tq_check_codec(const tq_codec* c, tq_kind kind);
 int tq_num_sms();
 
+// Vectors of `bytes` bytes at at + Σ_d i_d·stride[d], 0 ≤ i_d < n[d] (strides in bytes, ≥ 0).
+struct tq_vectors {
+  const void* at;
+  long long n[3], stride[3], bytes;
+};
+// Whether a vector of one overlaps a vector of the other.  Views of one array whose vectors lie
+// between each other's are told apart.
+bool tq_vectors_meet(const tq_vectors& x, const tq_vectors& y);
+
 // Launch helpers implemented in the .cu files
 tq_levels tq_make_levels(const tq_codec* c);
 // Tensor-core quantiser (quantize_tc.cu)

@@ -200,3 +200,32 @@ def test_refusals_on_the_gpu():
                 lambda: r.apply(x.transpose(-1, -2).contiguous().transpose(-1, -2), None, at)):
         with pytest.raises((ValueError, TypeError, B.TQError)):
             bad()
+
+
+@pytest.mark.parametrize("layout", ["grouped", "alternating", "heads first"])
+def test_sides_between_each_other_in_one_array(layout):
+    """Queries, keys and outputs that are views of one array and apart: each is what separate arrays give,
+    and the rest of the array stays."""
+    r = api.Rotary(128)
+    tokens = 9
+    if layout == "grouped":          # the heads of a token: queries, keys, values, then room
+        x = torch.randn(2, tokens, 20, D, generator=gen(1), device="cuda").bfloat16().transpose(1, 2)
+        at = [slice(0, 6), slice(6, 8), slice(10, 16), slice(16, 18)]
+    elif layout == "alternating":    # a query, a key and a value for each head, then their outputs
+        x = torch.randn(2, tokens, 4, 5, D, generator=gen(1), device="cuda").bfloat16().view(2, tokens, 20, D).transpose(1, 2)
+        at = [slice(i, None, 5) for i in (0, 1, 3, 4)]
+    else:
+        x = torch.randn(2, 20, tokens, D, generator=gen(1), device="cuda").bfloat16()
+        at = [slice(0, 6), slice(6, 8), slice(12, 18), slice(18, 20)]
+    pos = i32([list(range(5, 5 + tokens)), list(range(70, 70 + tokens))])
+    q, k, qo, ko = (x[:, s] for s in at)
+    want = x.clone()
+    a, b = r.apply(q, k, pos, torch.empty_like(q, memory_format=torch.contiguous_format), torch.empty_like(k))
+    want[:, at[2]], want[:, at[3]] = a, b
+    r.apply(q, k, pos, qo, ko)
+    assert torch.equal(x, want)
+    want[:, at[0]], want[:, at[1]] = a, b
+    r.apply(q, k, pos)
+    assert torch.equal(x, want)
+    with pytest.raises(B.TQError):   # the last query head is the keys' first
+        r.apply(q, x[:, 5:7] if layout != "alternating" else x[:, 15:17], pos)

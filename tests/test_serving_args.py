@@ -104,6 +104,37 @@ def test_rotary_apply_refuses():
     call(INVALID, q=io(y=OK16 + 2046), k=None)          # one coordinate short of apart
 
 
+def test_rotary_apply_refuses_one_side_over_part_of_the_other():
+    """Outputs that share some heads with the other side's vectors, in place and out of place, in every
+    layout of projections; [2][heads][4][128], strides in elements."""
+    r = api.Rotary(128)._c
+    row = 14 * 128                                                     # a fused row of 14 heads
+    fused, heads_first = (4 * row, 128, row), (14 * 512, 512, 128)     # [2][4][14][128] and [2][14][4][128]
+
+    def view(at, heads, s, y=None, ys=None):
+        x = OK16 + 2 * at
+        return io(x, x if y is None else y, heads, s, ys or s)
+
+    def call(q, k, batch=2, tokens=4):
+        assert B.tq_rotary_apply(r, B.TQ_BF16, batch, tokens, OK16, tokens, q, k, None) == INVALID
+
+    for s in (fused, heads_first):
+        h = s[1]
+        call(view(0, 8, s), view(7 * h, 2, s))                         # one head of both
+        call(view(2 * h, 8, s), view(0, 3, s))
+        call(view(0, 8, s), view(7 * h + 64, 2, s))                    # half a head
+        call(view(0, 8, s), view(8 * h, 2, s, OK16 + 14 * h))          # k's output over q's last heads
+        call(view(0, 8, s, 1 << 30), view(0, 2, s, (1 << 30) + 14 * h))
+        call(view(0, 8, s, 1 << 30), view(9 * h, 2, s, OK16 + 6 * h))
+        call(view(0, 8, s, OK16 + 18 * h), view(9 * h, 2, s, 1 << 30))
+        call(view(0, 8, s), view(7 * h, 2, s), batch=1)
+    call(view(0, 8, fused), view(3 * row + 512, 2, (4 * row, 128, row)), tokens=4)       # q's row 3 from k's row 0
+    # other strides: k's output, packed, among q's rows
+    call(view(0, 8, fused), view(1 << 20, 2, (1024, 512, 128), OK16 + 2 * row, (1024, 512, 128)))
+    # a side's own output over its input by one head of another token
+    call(view(0, 8, fused, OK16 + 2 * 7 * 128), None)
+
+
 def test_rotary_python_layer_refuses():
     r = api.Rotary(128)
     x, at = torch.zeros(2, 4, 5, 128), torch.zeros(2, 5, dtype=torch.int32)
