@@ -258,7 +258,8 @@ typedef struct {
  *              q_starts[b] .. q_starts[b + 1] − 1 of q, its keys those of k and v (the same array for
  *              whole prompts).  Rows of no sequence are neither read into anything nor written.
  *              Entries outside [0, total] are clamped and TQ_FLAG_LEN_OVERFLOW is raised.
- *   out      : device [total_q][q_heads][128], contiguous.
+ *   out      : device [total_q][q_heads][128], contiguous; q itself, where that is contiguous, or memory
+ *              apart from q, k and v.
  *   workspace: ≥ tq_prompt_workspace_bytes(desc) bytes, 256-byte aligned, no initialisation needed;
  *              calls that share it must be serialised on one stream.
  * Scores, sums and accumulators are 32 bits; softmax weights are rounded to the inputs' type and held

@@ -899,6 +899,15 @@ extern "C" tq_status tq_prompt_attention(const tq_prompt_desc* d, const void* q,
       reinterpret_cast<uintptr_t>(k_starts) % 4)
     return TQ_ERR_INVALID_ARG;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < p.bytes) return TQ_ERR_INVALID_ARG;
+  // A CTA writes rows while others read keys, values and their own queries; its own queries it has read by then.
+  const tq_vectors o{out, {1, 1, 1}, {}, (long long)d->total_q * d->q_heads * TQ_D * 2};
+  auto over = [&](const void* x, int tokens, int heads, int64_t stride_t, int64_t stride_h) {
+    return tq_vectors_meet(o, tq_vectors{x, {tokens, heads, 1}, {stride_t * 2, stride_h * 2, 0}, TQ_D * 2});
+  };
+  const bool in_place = q == out && (d->total_q == 1 || q_stride_t == (int64_t)d->q_heads * TQ_D) && (d->q_heads == 1 || q_stride_h == TQ_D);
+  if (over(k, d->total_k, d->kv_heads, k_stride_t, k_stride_h) || over(v, d->total_k, d->kv_heads, v_stride_t, v_stride_h) ||
+      (!in_place && over(q, d->total_q, d->q_heads, q_stride_t, q_stride_h)))
+    return TQ_ERR_INVALID_ARG;
   const bool bf16 = d->dtype == TQ_BF16;
   CUtensorMap maps[3];
   // (without keys nothing is loaded; the maps need some address all the same)

@@ -452,3 +452,21 @@ def test_values_given_back_in_blocks_that_are_not_full(nq, nk, group, dtype):
                     want[qs[b] + row, group:2 * group, c] = math.inf
     assert torch.equal(plan.run(q, k, v, *n, plan.new_out().fill_(7)), want)
     assert flags() == 0
+
+
+def test_output_beside_the_inputs_in_one_array():
+    """An output in the room between two rows of keys is apart from them."""
+    q, k, v = inputs([1], [90], 2, 4, torch.bfloat16, 25)
+    n = (i32([0, 1]), i32([0, 90]))
+    plan = api.PromptPlan(1, 8, 2, 1, 90, 90)
+    want = plan.run(q, k, v, *n, plan.new_out())
+    x = torch.full((90, 13, D), 3.0, dtype=torch.bfloat16, device="cuda")
+    x[:, :2], x[:, 2:4] = k, v
+    out = x[40, 5:13].view(1, 8, D)
+    plan.run(q, x[:, :2], x[:, 2:4], *n, out)
+    assert torch.equal(out, want)
+    with pytest.raises(B.TQError):
+        plan.run(q, x[:, :2], x[:, 2:4], *n, x[40, 3:11].view(1, 8, D))
+    with pytest.raises(B.TQError):
+        plan.run(x[40, 4:12].view(1, 8, D), k, v, *n, out)
+    assert flags() == 0

@@ -262,3 +262,23 @@ def test_prompt_workspaces():
         api.PromptPlan(1, 28, 4, 10, 10, 10, dtype=torch.float32, device="cpu")
     with pytest.raises(ValueError):
         api.PromptPlan(1, 27, 4, 10, 10, 10, device="cpu")
+
+
+def test_prompt_refuses_outputs_over_inputs():
+    """Keys, values, and queries that are not the output themselves; [1000][28 or 4][128] rows in bytes
+    from their starts."""
+    def call(q=1 << 30, k=1 << 31, v=1 << 32, out=1 << 33, qt=3584, kt=512, vt=512, kh=128, d=prompt(tq=1000, tk=2000)):
+        assert B.tq_prompt_attention(d, q, qt, 128, k, kt, kh, v, vt, 128, OK16, OK16, out, OK256, 1 << 40, None) == INVALID
+
+    size = 1000 * 28 * 256
+    call(k=1 << 33)
+    call(v=1 << 33)
+    call(k=(1 << 33) + size - 16)
+    call(v=(1 << 33) - 2000 * 1024 + 16)
+    call(q=(1 << 33) + 16)
+    call(q=(1 << 33) + size - 256)
+    call(q=1 << 33, qt=3712)                          # rows further apart than the output's
+    call(k=(1 << 33) - 4096 * 255, kh=2000 * 128, kt=128, d=prompt(tq=1, tk=2000))    # heads first; one token into them
+    fused = dict(qt=36 * 128, kt=36 * 128, vt=36 * 128, d=prompt(tq=1000, tk=1000))
+    call(q=1 << 33, k=(1 << 33) + 28 * 256, v=(1 << 33) + 32 * 256, **fused)
+    call(q=1 << 30, k=(1 << 30) + 28 * 256, v=(1 << 30) + 32 * 256, out=(1 << 30) + 999 * 36 * 256, **fused)
