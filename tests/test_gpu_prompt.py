@@ -470,3 +470,32 @@ def test_output_beside_the_inputs_in_one_array():
     with pytest.raises(B.TQError):
         plan.run(x[40, 4:12].view(1, 8, D), k, v, *n, out)
     assert flags() == 0
+
+
+@pytest.mark.parametrize("batch", [384, 385, 20000, 160000])
+def test_more_sequences_than_a_block_looks_at_at_once(batch):
+    """Single tokens that attend their one key are its value, bit for bit; the last sequence has none."""
+    v = torch.randn(batch - 1, 1, D, generator=gen(26), device="cuda").bfloat16()
+    q = torch.randn(batch - 1, 2, D, generator=gen(27), device="cuda").bfloat16()
+    n = torch.arange(batch + 1, dtype=torch.int32, device="cuda").clamp(max=batch - 1)
+    plan = api.PromptPlan(batch, 2, 1, batch - 1, batch - 1, 1)
+    assert torch.equal(plan.run(q, v, v, n, n, plan.new_out()), v.expand(-1, 2, -1))
+    # starts that do not ascend, anywhere in a long list
+    n[batch - 5] = batch
+    plan.run(q, v, v, n, n, plan.new_out())
+    assert flags() == B.TQ_FLAG_LEN_OVERFLOW
+
+
+def test_few_sequences_with_tokens_among_many():
+    batch = 150000
+    at = [0, 1, 383, 384, 390, 391, 392, 1000, 77777, 77778, batch - 392, batch - 1]
+    lens = [0] * batch
+    for i, b in enumerate(at):
+        lens[b] = (3, 300, 1, 40, 18, 19)[i % 6]
+    total = sum(lens)
+    q, k, v = inputs([total], [total], 1, 7, torch.bfloat16, 28, before=2, behind=1)
+    n = i32(starts(lens, 2))
+    plan = api.PromptPlan(batch, 7, 1, len(q), len(k), 300)
+    out = plan.run(q, k, v, n, n, plan.new_out().fill_(7))
+    check(q, k, v, *[starts([lens[b] for b in at], 2)] * 2, out, True)
+    assert (out[:2] == 7).all() and (out[-1:] == 7).all() and flags() == 0
