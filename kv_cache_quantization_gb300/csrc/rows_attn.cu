@@ -1441,7 +1441,7 @@ rows_prep_many_kernel(const void* q, int q_dtype, int nrows, int fine, const flo
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // Ranks of the sequences by length, the lower number of equal ones first: the attention takes long items
   // first, so that its last ones are short (16 drafted tokens of 20 sequences of 100 to 30000: 300 us for
-  // 344, 8 of 32 of 4096 to 16384: 206 for 215; both with the best splits).
+  // 344, 8 of 32 of 4096 to 16384: 206 for 215; both with the best splits).  Batches of at most kMostOrdered.
   for (int b = order ? blockIdx.x : batch; b < batch; b += gridDim.x) {
     const int len = seq_lens[b];
     int rank = 0;
@@ -1840,6 +1840,11 @@ int rows_per_cta(int rows, int most) {
 #ifdef TQ_ROWS_TREE
 // Rows from which on the kernels for many are faster.
 int many_rows() { return 8 * std::max(tq_num_sms(), 1); }
+
+// Sequences up to which they are ranked: ranking costs their square, and an item is a small part of what an SM
+// has of larger batches (2 drafted tokens of 8 heads; 2048 sequences, 11 of them of 4096 tokens and the others
+// of up to 512: 286 us ranked, 311 not; 8192 of up to 1024 tokens: 1350 and 1220).
+constexpr int kMostOrdered = 2048;
 #endif
 
 tq_status launch_prep(const void* q, int q_dtype, int rows, int fine, const tq_codec* kc, float factor,
@@ -1973,11 +1978,12 @@ tq_status plan_tree(const tq_attn_desc* d, int nodes, Plan* p) {
   const int n = tq_num_sms();
   const long long units = (long long)d->batch * d->kv_heads * p->row_tiles;
   p->pre_splits = 0;
-  p->own_splits = tree_splits(units, tiles, p->rows, n > 0 ? n : 152, d->batch == 1, p->rows > many_rows());
+  // (rows_prep_many_kernel writes the order)
+  const bool ordered = p->rows > many_rows() && d->batch > 1 && d->batch <= kMostOrdered;
+  p->own_splits = tree_splits(units, tiles, p->rows, n > 0 ? n : 152, d->batch == 1, ordered);
   if (units * p->own_splits > 0x7fffffffLL) return TQ_ERR_UNSUPPORTED;
   lay_out(d, p);
-  // (rows_prep_many_kernel writes the order)
-  if (p->rows > many_rows() && d->batch > 1 && units * p->own_splits > (n > 0 ? n : 152)) {
+  if (ordered && units * p->own_splits > (n > 0 ? n : 152)) {
     p->order_off = p->bytes;
     p->bytes += (size_t)d->batch * sizeof(int);
   }

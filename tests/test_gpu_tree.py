@@ -152,6 +152,30 @@ def test_ragged_batches_are_taken_by_length(batch, group):
     assert flags() == 0
 
 
+@pytest.mark.parametrize("batch", [2048, 2049, 5000])
+def test_more_sequences_than_are_ranked(batch):
+    """Large ragged batches with one long sequence, ranked by length and not."""
+    kc, vc = codec("k", 3), codec("v", 2)
+    lens = [(61 * b) % 11 * 6 for b in range(batch)]
+    lens[batch // 3] = 1500
+    cap = up64(1502)
+    some = [0, 1, batch // 3 - 1, batch // 3, batch // 3 + 1, 2047, batch - 1] + list(range(5, batch, batch // 20))
+    k, v = api.ProdCache.empty(batch, 1, cap, 3), api.MSECache.empty(batch, 1, cap, 2)
+    few = caches(len(some), 1, cap, 3, 2, 5)
+    for c, f in ((k, few[0]), (v, few[1])):
+        for t, x in ((c.idx, f.idx), (c.xnorm, f.xnorm)) + (((c.sgn, f.sgn), (c.rnorm, f.rnorm)) if c is k else ()):
+            t.zero_()
+            t[some] = x
+    q = queries(batch, 2, 8, torch.bfloat16, 6)
+    rows = trees(batch, 2, "any", batch)
+    plan = api.TreePlan(batch, 2, 8, 1, cap, 1502, out_dtype=torch.bfloat16)
+    out = plan.run(kc, vc, q, k, v, i32(lens), masks(rows), plan.new_out())
+    pick = lambda c: type(c)(*[t[some] for t in ((c.idx, c.sgn, c.xnorm, c.rnorm) if c is k else (c.idx, c.xnorm))],
+                             *(() if c is k else (2,)))
+    check_tree(kc, vc, q[some], pick(k), pick(v), [lens[b] for b in some], [rows[b] for b in some], out[some], 8)
+    assert out.isfinite().all() and flags() == 0
+
+
 @pytest.mark.parametrize("nodes", [15, 16, 17, 31, 32, 33, 48, 63, 64])
 @pytest.mark.parametrize("first", [0, 1, 15, 16, 17, 111, 112, 113, 127])
 def test_every_place_of_the_drafted_tokens_in_a_tile(first, nodes):

@@ -187,6 +187,16 @@ def test_tree_refuses():
         api.TreePlan(1, 8, 4, 4, 128, 128, out_dtype=torch.float32, device="cpu")
 
 
+def test_tree_batches_that_are_ranked_hold_an_order():
+    """Ranks cost the square of the sequences: above 2048 there are none.  (The rest of the workspace is
+    256-byte aligned row operands, and records of 528 bytes.)"""
+    for batch, ranked in ((2, False), (2048, True), (2049, False), (1 << 18, False)):
+        rows = batch * 8 * 2
+        front = -(-(rows * 516) // 256) * 256
+        n = B.tq_tree_workspace_bytes(desc(batch=batch, hq=8, hkv=1, mx=1024, out=B.TQ_BF16), 2) - front
+        assert n % (rows * 528) == (4 * batch if ranked else 0)
+
+
 # ------------------------------------------------------------------ moving codes
 
 def test_copy_pages_refuses():
