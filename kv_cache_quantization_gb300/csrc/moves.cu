@@ -70,6 +70,92 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
   }
 }
 
+// Long lists.  Above, each of n CTAs looks at all n pairs, which is most of the time from some thousand small
+// pages on.  Here two CTAs an SM hold up to kManyPairs pairs each, their destinations in a hash table, so that
+// a CTA looks at the list once for all of them; then its warps take its pages' pieces of kWarpPiece vectors in
+// turn: 65536 pages of 6 KB (64 tokens of one head, 3-bit keys, 2-bit values) 222 us, 3.5 TB/s.
+constexpr int kManyThreads = 512, kManyPairs = 256, kSlots = 1024, kWarpPiece = 32 * kFlight;
+
+__global__ void __launch_bounds__(kManyThreads, 2) copy_many_pages_kernel(const __grid_constant__ CopyArgs a, int per_cta) {
+  __shared__ int src[kManyPairs], dst[kManyPairs], slot[kSlots], left_out[kManyPairs];
+  const int tid = threadIdx.x, i0 = blockIdx.x * per_cta, pairs = min(per_cta, a.n - i0);
+  for (int i = tid; i < kSlots; i += kManyThreads) slot[i] = 0;
+  auto first_slot = [](int page) { return (int)(((uint32_t)page * 2654435761u) >> 22); };      // (spreads runs of pages)
+  bool bad = false, mine = false;
+  if (tid < pairs) {
+    const int s = a.src[i0 + tid], d = a.dst[i0 + tid];
+    src[tid] = s;
+    dst[tid] = d;
+    if (s < 0 || d < 0) bad = s < -1 || d < -1;
+    else bad = s >= a.num_pages || d >= a.num_pages;
+    mine = s >= 0 && d >= 0 && !bad && s != d;
+    left_out[tid] = !mine;
+  }
+  __syncthreads();
+  if (mine)
+    for (int h = first_slot(dst[tid]);; h = (h + 1) % kSlots) {      // (at most a quarter of the slots are taken)
+      const int there = atomicCAS(&slot[h], 0, tid + 1);
+      if (there == 0) break;
+      if (dst[there - 1] == dst[tid]) {
+        left_out[there - 1] = left_out[tid] = 2;
+        break;
+      }
+    }
+  __syncthreads();
+  auto find = [&](int page) {       // the pair here that has this destination, or −1
+    for (int h = first_slot(page);; h = (h + 1) % kSlots) {
+      const int k = slot[h] - 1;
+      if (k < 0 || dst[k] == page) return k;
+    }
+  };
+#pragma unroll 4
+  for (int j = tid; j < a.n; j += kManyThreads) {
+    const int s = a.src[j], d = a.dst[j];
+    if (s < 0 || d < 0 || s == d) continue;
+    const int ks = find(s), kd = find(d);
+    if (ks >= 0) left_out[ks] = 2;
+    if (kd >= 0 && i0 + kd != j) left_out[kd] = 2;
+  }
+  __syncthreads();
+  bad = bad || (mine && left_out[tid] == 2);
+  if (bad) atomicOr(&g_tq_flags, TQ_FLAG_PAGE);
+  uint32_t before[kArrays + 1] = {};        // vectors before each array's
+#pragma unroll
+  for (int k = 0; k < kArrays; ++k) before[k + 1] = before[k] + (k < a.arrays ? a.vecs[k] : 0u);
+  const uint32_t total = before[kArrays], pieces = (total + kWarpPiece - 1) / kWarpPiece;
+  uint32_t piece = tid >> 5;
+  for (int i = 0;; piece += kManyThreads / 32) {
+    while (piece >= pieces) {
+      piece -= pieces;
+      ++i;
+    }
+    if (i >= pairs) break;
+    if (left_out[i]) continue;
+    const long long from = src[i], to = dst[i];
+    uint4 v[kFlight];
+    uint4* at[kFlight];
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      const uint32_t e = piece * kWarpPiece + f * 32 + (tid & 31);
+      at[f] = nullptr;
+      if (e >= total) continue;
+      int k = 0;
+      uint32_t x = e;
+#pragma unroll
+      for (int m = 1; m < kArrays; ++m)
+        if (e >= before[m] && m < a.arrays) {
+          k = m;
+          x = e - before[m];
+        }
+      at[f] = a.base[k] + to * a.vecs[k] + x;
+      v[f] = a.base[k][from * a.vecs[k] + x];
+    }
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f)
+      if (at[f]) *at[f] = v[f];
+  }
+}
+
 // ---------------------------------------------------------------- tokens
 // A CTA moves the tokens of one (sequence, head): all are read before any is written, so a list may
 // be in any order.  An item is 16 bytes of a token's codes or one of its norms; a block has as many
@@ -192,6 +278,17 @@ extern "C" tq_status tq_copy_pages(const tq_prod_cache* k, int32_t key_bits, con
   a.num_pages = num_pages;
   a.src = src;
   a.dst = dst;
+  // Which kernel: a CTA of the first reads a list of 8n bytes for a page, which the copy hides (4096 pages of 47
+  // KB 66 us and 74, 16384 of 188 KB 918 and 994) until the list is twice as long as the page (16384 pages of 47
+  // KB 261 us and 269, 32768 of 94 KB 1117 and 996, 4096 of 12 KB 35 and 19, 65536 of 6 KB 2359 and 222).
+  long long page = 0;
+  for (int i = 0; i < a.arrays; ++i) page += a.vecs[i] * 16LL;
+  if (4LL * n > page) {
+    const int most = std::max(2 * tq_num_sms(), (n + kManyPairs - 1) / kManyPairs), per_cta = (n + most - 1) / most;
+    copy_many_pages_kernel<<<(unsigned)((n + per_cta - 1) / per_cta), kManyThreads, 0, reinterpret_cast<cudaStream_t>(stream_)>>>(
+        a, per_cta);
+    return tq_cuda_status(cudaGetLastError());
+  }
   // CTAs that share a page: as many as give each SM about eight, up to one for each piece
   const int want = std::max(tq_num_sms(), 1) * 8;
   a.ways = std::min(a.pieces[a.arrays], std::max(1, (want + n - 1) / n));

@@ -106,6 +106,64 @@ def test_copy_finds_a_clash_anywhere_in_a_long_list(at):
     assert flags() == B.TQ_FLAG_PAGE
 
 
+@pytest.mark.parametrize("n,heads,page", [(2000, 1, 64), (2100, 2, 64), (2300, 2, 64), (7000, 2, 192), (65536, 1, 64)])
+def test_copy_long_lists(n, heads, page):
+    """Clashes between pairs that lie far apart or side by side, bad pages, pairs that are passed over and
+    pages onto themselves, in lists up to the longest; sources may repeat."""
+    pages = 2 * n + 7
+    k, v = caches(pages, heads, page, 2, 1, 1)
+    b = bounds(pages, heads, page, 2)
+    rng = np.random.default_rng(n)
+    order = rng.permutation(pages)
+    src, dst = order[:n].astype(np.int64), order[n:2 * n].astype(np.int64)
+    src[rng.integers(0, n, n // 3)] = src[0]                # (a repeated source)
+    used = rng.permutation(n)[:590]
+    for i, j in zip(used[:100], used[100:200]):
+        dst[i] = dst[j]                                     # two write one page
+    for i in range(0, n - 1, max(n // 50, 2)):
+        dst[i] = dst[i + 1]                                 # neighbours in the list
+    for i, j in zip(used[200:300], used[300:400]):
+        src[i] = dst[j]                                     # one reads what another writes
+    dst[used[400:450]] = src[used[400:450]]                 # onto itself
+    src[used[450:500]], dst[used[500:550]] = -1, -1
+    src[used[550:560]], dst[used[560:570]], dst[used[570:580]], src[used[580:590]] = pages, pages + 5, -2, -2 ** 31
+    moves = (src >= 0) & (dst >= 0) & (src != dst)
+    writes = np.bincount(dst[moves & (dst < pages)], minlength=pages)
+    reads = np.bincount(src[moves & (src < pages)], minlength=pages)
+    good = [i for i in range(n) if moves[i] and src[i] < pages and dst[i] < pages and writes[dst[i]] == 1 and not reads[dst[i]]]
+    assert n // 2 < len(good) < n - 300
+    every = arrays(k, v) + [b.bounds]
+    want = [t.clone() for t in every]
+    at = torch.tensor(good, device="cuda")
+    s, d = (torch.tensor(x, device="cuda") for x in (src, dst))
+    for w, t in zip(want, every):
+        w[d[at]] = t[s[at]]
+    api.copy_pages(s.int(), d.int(), k, v, b)
+    assert all(torch.equal(t, w) for t, w in zip(every, want))
+    assert flags() == B.TQ_FLAG_PAGE
+    # the good pairs alone, and into themselves again: nothing changes, nothing is flagged
+    api.copy_pages(s[at].int(), d[at].int(), k, v, b)
+    assert all(torch.equal(t, w) for t, w in zip(every, want))
+    assert flags() == 0
+
+
+def test_copy_long_lists_of_parts_of_a_cache():
+    n = 5000
+    order = np.random.default_rng(5).permutation(2 * n)
+    src, dst = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (order[:n], order[n:]))
+    k, v = caches(2 * n, 3, 64, 5, 4, 3)
+    b = bounds(2 * n, 3, 64, 4)
+    for which in range(3):
+        every = arrays(k, v) + [b.bounds]
+        want = [t.clone() for t in every]
+        for i, t in enumerate(want):
+            if (0 if i < 4 else 1 if i < 6 else 2) == which:
+                t[dst.long()] = t[src.long()]
+        api.copy_pages(src, dst, *[x if i == which else None for i, x in enumerate((k, v, b))])
+        assert all(torch.equal(t, w) for t, w in zip(every, want))
+    assert flags() == 0
+
+
 def test_copy_offsets_past_32_bits():
     """A pool of more than 4 GiB of value codes."""
     n = 40000
