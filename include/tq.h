@@ -224,7 +224,7 @@ typedef struct {
 /* Turns q and k (either may be NULL or have no heads) of `dtype` (F32, F16 or BF16) in one launch.
  *   positions : device int32 [batch][tokens], rows pos_stride_b apart (0: one row for all); any
  *               number, negative ones turn backwards.
- * Angles are right to 2^-32 turns at any position; products and sums are 32 bits, rounded once.
+ * Angles are off by less than 2^-25 radians at any position; products and sums are 32 bits, rounded once.
  * Vectors at multiples of 16 bytes take 16-byte accesses where the pairs are neighbours or rotary_dim
  * is a multiple of 16; others work and are slower. */
 tq_status tq_rotary_apply(const tq_rotary* r, tq_dtype dtype, int32_t batch, int32_t tokens,

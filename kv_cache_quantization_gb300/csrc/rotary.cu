@@ -3,10 +3,11 @@
 // Mathematics.  Pair i of a vector at position p turns by θ = p·f_i and is scaled by m:
 //   y_a = m·(a·cos θ − b·sin θ),   y_b = m·(a·sin θ + b·cos θ).
 // f_i/2π is held as a fraction of 2^64 (turns per position), so that p·f_i is one 64-bit
-// multiplication whose overflow drops whole turns: the angle is as good at position 2^31 as at 1
-// (2^-33 turns).  The nearest quarter turn is taken out in integers; what is left, at most an
-// eighth of a turn, is exact in 32 bits to 2^-27 radians or so.  Products and sums are 32 bits,
-// rounded once to the output's type.
+// multiplication whose overflow drops whole turns: the angle is as good at position 2^31 as at 1.  It
+// is cut to 32 bits (2^-31 turns in all) and the nearest quarter turn is taken out in integers; what is
+// left, at most an eighth of a turn, is rounded to the 24 bits of a float, by at most 2^-28 turns.
+// Together less than 2^-25 radians, which is below what rounding the vectors to 32 bits takes.
+// Products and sums are 32 bits, rounded once to the output's type.
 //
 // Bound by reading and writing the vectors: 131072 tokens of 32/8 fp16 heads take 402 us, 6.68 TB/s, the
 // copy rate; a step's 32 tokens of 28/4 heads 3.5 us, a launch.  A warp takes four heads of a token at a
