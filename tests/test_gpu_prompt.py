@@ -8,7 +8,7 @@ import torch
 import longctx_ref as ref
 from kv_cache_quantization_gb300 import _binding as B
 from kv_cache_quantization_gb300 import api
-from test_gpu_longctx import capture, flags, gen, i32
+from test_gpu_longctx import capture, flags, gen, i32, parts
 
 pytestmark = pytest.mark.gpu
 
@@ -393,6 +393,44 @@ def test_prompt_then_codes_then_decode():
     got = dec.run(kc, vc, last, kcache, vcache, i32(lens), dec.new_out())
     want = torch.stack([out[e - 1] for e in qs[1:]]).float()
     assert float((got - want).norm() / want.norm()) < 0.5
+    assert flags() == 0
+
+
+def test_prompt_codes_and_the_step_behind_them():
+    """A prompt whose keys were turned where they lie is coded as the turned keys are by themselves, and a
+    drafted token behind it attends those codes as their definition says."""
+    lens, kv, group = [200, 75], 2, 4
+    q, k, v = inputs(lens, lens, kv, group, torch.bfloat16, 29, fused=True)
+    qs, rot = starts(lens), api.Rotary(128)
+    at = i32([i for n in lens for i in range(n)])[None]
+    raw_k = k.clone()
+    rot.apply(q.transpose(0, 1)[None], k.transpose(0, 1)[None], at)
+    plan = api.PromptPlan(2, 8, 2, len(q), len(k), 200)
+    out = plan.run(q, k, v, i32(qs), i32(qs), plan.new_out())
+    check(q, k, v, qs, qs, out, True)
+    kc, vc = api.Codec.prod(4), api.Codec.mse(4)
+    kcache, vcache = api.ProdCache.empty(2, kv, 256, 4), api.MSECache.empty(2, kv, 256, 4)
+    for b, n in enumerate(lens):
+        turned = torch.empty(1, kv, n, D, dtype=k.dtype, device="cuda")
+        rot.apply(raw_k[qs[b]:qs[b + 1]].transpose(0, 1)[None], None, i32([list(range(n))]), turned)
+        assert torch.equal(turned[0].transpose(0, 1), k[qs[b]:qs[b + 1]])
+        one = api.ProdCache(*[t[b:b + 1] for t in (kcache.idx, kcache.sgn, kcache.xnorm, kcache.rnorm)])
+        api.quantize_prod(kc, k[qs[b]:qs[b + 1]].transpose(0, 1)[None], one)
+        api.quantize_mse(vc, v[qs[b]:qs[b + 1]].transpose(0, 1)[None], api.MSECache(vcache.idx[b:b + 1], vcache.xnorm[b:b + 1], 4))
+        alone = api.ProdCache.empty(1, kv, 256, 4)
+        api.quantize_prod(kc, turned, alone)
+        for x, y, dim in ((alone.idx, one.idx, 3), (alone.sgn, one.sgn, 2), (alone.xnorm, one.xnorm, 2), (alone.rnorm, one.rnorm, 2)):
+            assert torch.equal(x.narrow(dim, 0, n), y.narrow(dim, 0, n))
+    # the last token of each prompt, as the one drafted token behind the others
+    last = torch.stack([q[e - 1] for e in qs[1:]])[:, None].contiguous()
+    step = api.TreePlan(2, 1, 8, 2, 256, 256, out_dtype=torch.float16)
+    one = torch.ones(2, 1, dtype=torch.int64, device="cuda")
+    got = step.run(kc, vc, last, kcache, vcache, i32([n - 1 for n in lens]), one, step.new_out())
+    for b, n in enumerate(lens):
+        for h in range(kv):
+            p = parts(kcache, vcache, kc, vc, b, h, torch.arange(n, device="cuda"))
+            r, err = ref.attend(last[b, 0, h * group:(h + 1) * group], p, kc, vc, None, True)
+            ref.check_rows(got[b, 0, h * group:(h + 1) * group], r, err, f"sequence {b}, KV head {h}")
     assert flags() == 0
 
 

@@ -346,6 +346,47 @@ def test_graph_stream_and_two_plans():
     flags()
 
 
+def test_replays_and_streams_raise_no_flags():
+    """A captured call replayed with other lengths and trees is right in every sequence; neither that nor
+    calls of two plans on two streams raise a flag; histories past the plan's bound raise theirs."""
+    lens, nodes, other = [700, 64, 1], 7, [333, 600, 0]
+    kc, vc, q, k, v, plan, out = run_tree(3, 2, 3, 2, 4, [700] * 3, nodes, trees(3, nodes, "tree"), seed=31)
+    rows, new = trees(3, nodes, "tree", 1), trees(3, nodes, "any", 2)
+    tree, n, o = masks(rows), i32(lens), plan.new_out()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        g = capture(lambda: plan.run(kc, vc, q, k, v, n, tree, o), side)
+    assert flags() == 0
+    q.copy_(queries(3, nodes, 8, q.dtype, 32))
+    n.copy_(i32(other))
+    tree.copy_(masks(new))
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    check_tree(kc, vc, q, k, v, other, new, o, 4)
+    assert flags() == 0
+    n.copy_(i32(lens))
+    tree.copy_(masks(rows))
+    plans = [plan, api.TreePlan(3, nodes, 8, 2, k.capacity, 700 + nodes, out_dtype=torch.float16)]
+    alone = plan.run(kc, vc, q, k, v, n, tree, plan.new_out()).clone()
+    streams = [torch.cuda.Stream() for _ in plans]
+    outs = [[plan.new_out() for _ in range(10)] for _ in plans]
+    torch.cuda.synchronize()
+    for i in range(10):
+        for p, s, os in zip(plans, streams, outs):
+            p.run(kc, vc, q, k, v, n, tree, os[i], stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, alone) for os in outs for x in os)
+    assert flags() == 0
+    n.copy_(i32([700, 701, 0]))
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    check_tree(kc, vc, q, k, v, [700, 700, 0], rows, o, 4)
+    assert flags() == B.TQ_FLAG_LEN_OVERFLOW
+
+
 def test_offsets_past_32_bits():
     """Value codes of more than 4 GiB, drafted tokens at their end."""
     kc, vc = codec("k", 2), codec("v", 4)

@@ -71,3 +71,16 @@ def test_inputs_of_waiting_kernels_are_not_read_through_the_read_only_path():
     text = source("append_small.h")
     begin = text.index("void append_load8")
     assert "__ldg" not in text[begin:text.index("__device__", begin)]
+
+
+def test_warps_meet_before_loads_of_tensor_memory_and_turns():
+    """Loads of tensor memory and barriers take the warp as one: after branches that differ between its lanes
+    (rows that are not there, lanes that arrive alone, waits that lanes leave one by one) it has to meet."""
+    text = source("prompt.cu")
+    body = dict(kernels(text))["prompt_kernel"]
+    columns = body[body.rindex("#pragma unroll 1", 0, body.index("give_back")):]
+    assert columns.index("__syncwarp()") < columns.index("tmem_ld_32x32b_x32") < columns.index("if (there)")
+    assert "continue" not in columns[:columns.index("put32")]
+    for first, then in (("for (int part = 0; part < 2; ++part)", "tmem_ld_32x32b_x32"), ("wait(&sm.full[pk.stage]", "named_sync(kBarTurn + s")):
+        at = text.index(first)
+        assert "__syncwarp()" in text[at:text.index(then, at)]
