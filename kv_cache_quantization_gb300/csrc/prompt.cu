@@ -914,10 +914,11 @@ extern "C" tq_status tq_prompt_attention(const tq_prompt_desc* d, const void* q,
     return TQ_ERR_INVALID_ARG;
   const bool bf16 = d->dtype == TQ_BF16;
   CUtensorMap maps[3];
-  // (without keys nothing is loaded; the maps need some address all the same)
+  // (without keys nothing is loaded; the maps need some address all the same, and no strides)
+  const int kv_heads = d->total_k ? d->kv_heads : 1;
   if (!encode(&maps[0], bf16, q, d->total_q, d->q_heads, q_stride_t, q_stride_h, p.G, p.tokens) ||
-      !encode(&maps[1], bf16, d->total_k ? k : q, d->total_k, d->kv_heads, k_stride_t, k_stride_h, 1, kTile) ||
-      !encode(&maps[2], bf16, d->total_k ? v : q, d->total_k, d->kv_heads, v_stride_t, v_stride_h, 1, kTile))
+      !encode(&maps[1], bf16, d->total_k ? k : q, d->total_k, kv_heads, k_stride_t, k_stride_h, 1, kTile) ||
+      !encode(&maps[2], bf16, d->total_k ? v : q, d->total_k, kv_heads, v_stride_t, v_stride_h, 1, kTile))
     return TQ_ERR_CUDA;
   PromptArgs a{};
   a.q_starts = q_starts;

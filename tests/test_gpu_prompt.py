@@ -537,3 +537,12 @@ def test_few_sequences_with_tokens_among_many():
     out = plan.run(q, k, v, n, n, plan.new_out().fill_(7))
     check(q, k, v, *[starts([lens[b] for b in at], 2)] * 2, out, True)
     assert (out[:2] == 7).all() and (out[-1:] == 7).all() and flags() == 0
+
+
+def test_no_keys_in_arrays_of_any_strides():
+    """Keys and values that are not there have no strides to be refused."""
+    q, _, _ = inputs([5, 3], [0, 0], 2, 3, torch.bfloat16, 30)
+    none = torch.empty(0, 2, 132, dtype=torch.bfloat16, device="cuda")[..., :D]
+    out = torch.full((8, 6, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    api.PromptPlan(2, 6, 2, 8, 0, 0).run(q, none, none, i32([0, 5, 8]), i32([0, 0, 0]), out)
+    assert not out.any() and flags() == 0
