@@ -730,8 +730,9 @@ class PromptPlan:
 
     def run(self, q, k, v, q_starts, k_starts, out, stream=None):
         """Attention of q [total_q, q_heads, 128] over k and v [total_k, kv_heads, 128] (views with any
-        strides of multiples of 8 elements), into out [total_q, q_heads, 128]; q_starts and k_starts,
-        int32 [batch + 1], are where each sequence's rows begin (the same for whole prompts)."""
+        strides of multiples of 8 elements), into out [total_q, q_heads, 128], q itself or memory apart from
+        the inputs; q_starts and k_starts, int32 [batch + 1], are where each sequence's rows begin (the
+        same for whole prompts)."""
         d = _device(q, k, v, q_starts, k_starts, out, self.workspace)
         sq, sk, sv = q.stride(), k.stride(), v.stride()
         for t, s, shape, name in ((q, sq, self.shape, "q"), (k, sk, self.k_shape, "k"), (v, sv, self.k_shape, "v")):
