@@ -25,7 +25,8 @@
 // prompt_merge_kernel joins.
 //
 // Measured: 32768 causal tokens of 28/4 bf16 heads 4.49 ms (1713 TFLOP/s, 90% of a large library
-// product's rate; 4.95 ms, 1556 TFLOP/s, in runs of seconds under the power limit), 8192 × 8192 without a mask 583 us (1651); one token each of 32 sequences behind 8192
+// product's rate; 4.95 ms, 1556 TFLOP/s, in runs of seconds under the power limit), 8192 × 8192 without
+// a mask 583 us (1651); one token each of 32 sequences behind 8192
 // keys of 8 heads 175 us (6.1 TB/s of keys and values); one token behind 128 keys 6.0 us.  What bounds long
 // prompts is the chain of a tile (weights 500 cycles and more, their hand-over, 1024 of products, S back:
 // about 2700 for both streams, where the products take 2048), then the shared memory that S = Q·Kᵀ reads:
